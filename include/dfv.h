@@ -19,6 +19,10 @@
  * plus dfv_kv_quantize_rows, the same Q4_0 quantiser used to fill a cache
  * from float rows (prefill).
  *
+ * Beside them, for the same loop: a cache held in 8 bits with one scale per
+ * 64 positions and head (dfv_kv8_append, dfv_kv8_commit, dfv_kv8_read,
+ * dfv_kv8_attn), and dfv_token_logprobs, log probabilities of given tokens.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - All tensor pointers are DEVICE pointers owned by the caller. The library
@@ -85,6 +89,8 @@ typedef enum dfv_status {
                                /* committed; attention uses it clamped       */
 #define DFV_DEV_BAD_PATH 0x10u /* path entry outside [0, n_nodes): no write   */
 #define DFV_DEV_TIMEOUT 0x20u  /* a bounded wait gave up; outputs undefined   */
+#define DFV_DEV_NONFINITE 0x40u /* a K/V value was infinite, NaN or >= 2^40  */
+#define DFV_DEV_BAD_TOKEN 0x80u /* a token outside the vocabulary            */
 /* Every wait of a kernel (on a copy, an MMA, or another CTA of the step)
  * gives up after 100 ms of the GPU's global timer and sets DFV_DEV_TIMEOUT;
  * the kernel then skips what depended on the wait (a walker that timed out
@@ -348,6 +354,126 @@ dfv_status dfv_workspace_clear(void* workspace, size_t bytes, dfv_stream_t strea
 #define DFV_MASK_WORDS ((DFV_MAX_NODES + 31) / 32) /* 3 */
 dfv_status dfv_build_tree_mask(int n_nodes, const int32_t* parent, int32_t* depth,
                                uint32_t* anc_mask, uint32_t* status, dfv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit cache: K and V of one sequence as signed 8-bit codes with one
+ * f32 scale for each block of 64 positions and head.
+ *
+ * Position p lies in block b = p / 64. A block is quantised once, when all of
+ * its positions have been written, from their bf16 values (float32 rows are
+ * rounded to bf16 first, nearest even):
+ *
+ *   amax = max |x| over the block's 64 * D values of the head
+ *   scale = amax / 127,  code = round-half-even(127 x / amax)
+ *
+ * The open block, and the one before it, are kept as bf16 rows in the tail,
+ * so a write can start up to one whole block back (rollback). The content
+ * does not depend on how the rows were split into calls. Values of 2^40 or
+ * more (also infinities and NaN) enter as zeros and set DFV_DEV_NONFINITE; a
+ * block whose largest magnitude is below 2^-40 is stored as zeros.
+ *
+ * nblk = (capacity + 63) / 64 blocks per head. All pointers are device
+ * memory; the struct itself is read by the host during the call.
+ *   state    int32[4]: [0] the committed length; [1] a counter the library
+ *            keeps at zero between calls; [2] the first block whose bf16 rows
+ *            the tail still holds; [3] unused. Zero it for an empty cache.
+ *   k_codes  int8 [n_kv_heads][nblk][D / 16][64][16]: byte (position t of
+ *            block b, dim c) at (((h * nblk + b) * (D / 16) + c / 16) * 64 + t)
+ *            * 16 + c % 16. 128-byte aligned.
+ *   v_codes  int8 [n_kv_heads][nblk][4][D][16]: byte (t, c) at
+ *            (((h * nblk + b) * 4 + t / 16) * D + c) * 16 + t % 16
+ *   k_scale, v_scale  f32 [n_kv_heads][nblk]
+ *   k_tail, v_tail    bf16 [n_kv_heads][2][64][D]: block b in slot b % 2
+ * Calls on one cache must be ordered (one stream, or events); D in
+ * {64, 128, 256}.
+ * ---------------------------------------------------------------------- */
+typedef struct dfv_kv8_cache {
+  int32_t n_kv_heads, head_dim, capacity, reserved;
+  int32_t* state;
+  int8_t *k_codes, *v_codes;
+  float *k_scale, *v_scale;
+  void *k_tail, *v_tail;
+} dfv_kv8_cache;
+
+/* dfv_kv8_append -- write rows [at, at + n_rows) of every head and set the
+ * committed length to at + n_rows (the counterpart of dfv_kv_quantize_rows).
+ *   at       first position, or -1 for the committed length. It must not lie
+ *            behind that length, and has to be a multiple of 64 or lie in a
+ *            block that the tail still holds (DFV_DEV_CTX otherwise, nothing
+ *            written). n_rows = 0 truncates to `at`.
+ *   k_src, v_src  device f32 or bf16 (src_dtype); element (row r, head h, dim
+ *            c) at src[r * stride_row + h * stride_head + c] (elements)
+ * at + n_rows > capacity: DFV_ERR_INVALID where the host can see it, else
+ * DFV_DEV_CAPACITY and nothing written. */
+dfv_status dfv_kv8_append(const dfv_kv8_cache* cache, int at, int n_rows, const void* k_src,
+                          const void* v_src, int src_dtype, int64_t k_stride_row,
+                          int64_t k_stride_head, int64_t v_stride_row, int64_t v_stride_head,
+                          uint32_t* status, dfv_stream_t stream);
+
+/* dfv_kv8_commit -- append the accepted rows tree_k[path[k]], k < *accept_len
+ * (and tree_v), as dfv_kv_commit does for the other formats; same arguments,
+ * checks and status bits. */
+dfv_status dfv_kv8_commit(const dfv_kv8_cache* cache, int n_nodes, const int32_t* accept_len,
+                          const int32_t* path, const void* tree_k, const void* tree_v,
+                          uint32_t* status, dfv_stream_t stream);
+
+/* dfv_kv8_read -- cached rows [pos0, pos0 + n_rows) as values: code * scale
+ * for complete blocks, the bf16 rows of the open one.
+ *   k_dst, v_dst  device f32 or bf16 (dst_dtype, nearest even); element (row
+ *            r, head h, dim c) at dst[r * stride_row + h * stride_head + c]
+ * Rows behind the committed length are left as they were (DFV_DEV_CTX). */
+dfv_status dfv_kv8_read(const dfv_kv8_cache* cache, int pos0, int n_rows, void* k_dst,
+                        void* v_dst, int dst_dtype, int64_t stride_row, int64_t stride_head,
+                        uint32_t* status, dfv_stream_t stream);
+
+/* dfv_kv8_attn -- dfv_tree_verify_attn over the 8-bit cache: complete blocks
+ * as code * scale, the open block and the tree rows as their bf16 values.
+ * Arguments as there, except
+ *   out        device f32 or bf16 (out_dtype) [N][Hq][D], 16-byte aligned
+ *   workspace  device scratch, >= dfv_kv8_attn_workspace_bytes() bytes,
+ *              256-byte aligned; it needs no clearing and holds nothing
+ *              between calls. Calls sharing one must not overlap.
+ * n_nodes = 1 is plain decode. q may have any finite bf16 magnitude; a
+ * non-finite q row gives a non-finite result for that row alone. A node that
+ * sees a tree row holding a value of 2^40 or more, an infinity or a NaN gets
+ * NaN for that head (DFV_DEV_NONFINITE); the others are not affected. */
+size_t dfv_kv8_attn_workspace_bytes(int n_nodes, int n_q_heads, int n_kv_heads, int head_dim,
+                                    int window, int cache_capacity);
+
+dfv_status dfv_kv8_attn(const dfv_kv8_cache* cache, int n_nodes, int max_depth, int n_q_heads,
+                        int window, const void* q, const void* tree_k, const void* tree_v,
+                        const int32_t* parent, float scale, void* out, int out_dtype, float* lse,
+                        void* workspace, size_t workspace_bytes, uint32_t* status,
+                        dfv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dfv_token_logprobs -- for each row of logits x: the natural-log probability
+ * of a given token, the entropy (nats) and the `top` most probable tokens.
+ *
+ *   logprob[i] = x[t_i] - lse(x),  entropy[i] = -sum p log p
+ *   top_ids[i][k] the index of the k-th largest logit, ties to the lowest
+ *   index (-0.0 equals +0.0); top_logprobs[i][k] its log probability
+ *
+ * Logits of -inf (or of the type's lowest value beside larger ones) have
+ * probability zero and add nothing to the entropy. A row that is -inf
+ * throughout, or holds a NaN or +inf, has NaN results (its top_ids lie in
+ * range).
+ *
+ *   logits        device f32 or bf16 (logits_dtype), row i at logits +
+ *                 i * stride_row elements, any alignment of the type
+ *   tokens        device int32 [n_rows]; may be NULL without logprob. A token
+ *                 outside [0, vocab): NaN and DFV_DEV_BAD_TOKEN
+ *   top           0..min(DFV_MAX_TOP, vocab)
+ *   logprob, entropy  device f32 [n_rows], each may be NULL
+ *   top_ids       device int32 [n_rows][top], top_logprobs f32 [n_rows][top],
+ *                 one of them may be NULL
+ * One launch, no workspace.
+ * ---------------------------------------------------------------------- */
+#define DFV_MAX_TOP 32
+dfv_status dfv_token_logprobs(int n_rows, int vocab, int logits_dtype, const void* logits,
+                              int64_t stride_row, const int32_t* tokens, int top, float* logprob,
+                              float* entropy, int32_t* top_ids, float* top_logprobs,
+                              uint32_t* status, dfv_stream_t stream);
 
 #ifdef __cplusplus
 }

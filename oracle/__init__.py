@@ -32,6 +32,8 @@ Module map:
 * ``accept``    -- per-node argmax and the greedy tree walk.
 * ``commit``    -- commit of the accepted rows into the cache (Q4_0 or F16).
 * ``step``      -- the whole verify step composed from the above.
+* ``int8``      -- the 8-bit cache with a scale per 64 positions and head.
+* ``logprobs``  -- log probabilities of given tokens, entropy, alternatives.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against brute force, closed forms, invariants or library routines. Parity
@@ -39,4 +41,4 @@ with the pages' own implementation is unpinned: the pages print no worked
 example and no kernel output.
 """
 
-from . import q4_0, f16, tree, attention, accept, commit, step  # noqa: F401
+from . import q4_0, f16, tree, attention, accept, commit, step, int8, logprobs  # noqa: F401

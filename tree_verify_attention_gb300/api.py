@@ -5,6 +5,8 @@ dtypes/shapes, passes raw pointers to the C ABI and raises DfvError on a
 non-OK status. No compute happens here.
 """
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -25,6 +27,11 @@ DEV_CAPACITY = 0x4
 DEV_CTX = 0x8
 DEV_BAD_PATH = 0x10
 DEV_TIMEOUT = 0x20
+DEV_NONFINITE = 0x40
+DEV_BAD_TOKEN = 0x80
+
+KV8_BLOCK = 64       # positions that share a scale in an Int8Cache
+MAX_TOP = 32         # alternatives token_logprobs can return
 
 
 class DfvError(RuntimeError):
@@ -116,6 +123,143 @@ class Q4Cache(KVCache):
         super().__init__(n_kv_heads, head_dim, capacity, device=device, fmt="q4_0")
 
 
+def _same_device(device, **tensors):
+    """All of ``tensors`` (None allowed) on ``device``, which is the current
+    one: the library launches on the current device."""
+    if device.index != torch.cuda.current_device():
+        raise DfvError(f"tensors on {device}, but the current device is "
+                       f"cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise DfvError(f"{name} is on {t.device}, expected {device}")
+
+
+def _float_rows(t, name, shape, dtypes=(torch.float32, torch.bfloat16)):
+    if t is None or not t.is_cuda or t.dtype not in dtypes:
+        raise DfvError(f"{name} must be a CUDA f32 or bf16 tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise DfvError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.numel() and t.stride(-1) != 1:
+        raise DfvError(f"{name} rows must be contiguous")
+    return t
+
+
+class Int8Cache:
+    """Device KV cache of one sequence held in 8 bits: signed codes with one
+    float32 scale for each block of 64 positions and head; the open block and
+    the one before it are also kept as bf16 rows (``k_tail``, ``v_tail``), so a
+    block is quantised once, when it is complete. The layouts are those of
+    ``dfv_kv8_cache`` (include/dfv.h).
+
+    Every method is asynchronous on ``stream`` (the current one by default);
+    problems that only the device can see are OR-ed into ``status`` (int32[1],
+    DEV_* bits; :attr:`status` of the cache by default)."""
+
+    fmt = "int8"
+
+    def __init__(self, n_kv_heads, head_dim, capacity, device="cuda"):
+        if head_dim not in (64, 128, 256):
+            raise DfvError(f"head_dim {head_dim} is not one of 64, 128, 256")
+        if not (1 <= n_kv_heads <= 65535 and 1 <= capacity <= 1 << 30):
+            raise DfvError(f"bad cache shape ({n_kv_heads} heads, capacity {capacity})")
+        self.n_kv_heads, self.head_dim, self.capacity = n_kv_heads, head_dim, capacity
+        nblk = -(-capacity // KV8_BLOCK)
+        h, d = n_kv_heads, head_dim
+        self.k = torch.zeros(h, nblk, d // 16, KV8_BLOCK, 16, dtype=torch.int8, device=device)
+        self.v = torch.zeros(h, nblk, KV8_BLOCK // 16, d, 16, dtype=torch.int8, device=device)
+        self.k_scale = torch.zeros(h, nblk, device=device)
+        self.v_scale = torch.zeros(h, nblk, device=device)
+        self.k_tail = torch.zeros(h, 2, KV8_BLOCK, d, dtype=torch.bfloat16, device=device)
+        self.v_tail = torch.zeros_like(self.k_tail)
+        self.state = torch.zeros(4, dtype=torch.int32, device=device)
+        self.ctx_len = self.state[:1]
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._struct = _lib.Kv8CacheStruct(
+            h, d, capacity, 0, self.state.data_ptr(), self.k.data_ptr(), self.v.data_ptr(),
+            self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.k_tail.data_ptr(),
+            self.v_tail.data_ptr())
+        self.handle = ctypes.addressof(self._struct)
+
+    def append(self, k_rows, v_rows, at=None, head_major=False, stream=None, status=None):
+        """Write float rows [n, Hkv, D] (or [Hkv, n, D] with head_major=True;
+        f32 or bf16, last axis contiguous) at positions [at, at + n), and set
+        the committed length to at + n. ``at=None`` appends at the committed
+        length. An ``at`` behind that length, or inside a block whose bf16
+        rows are no longer held, writes nothing and sets DEV_CTX."""
+        h, d = self.n_kv_heads, self.head_dim
+        n = k_rows.shape[1 if head_major else 0]
+        shape = (h, n, d) if head_major else (n, h, d)
+        _float_rows(k_rows, "k_rows", shape)
+        _float_rows(v_rows, "v_rows", shape, (k_rows.dtype,))
+        status = self.status if status is None else status
+        _same_device(self.state.device, k_rows=k_rows, v_rows=v_rows, status=status)
+        r, hd = (1, 0) if head_major else (0, 1)
+        _check(lib().dfv_kv8_append(
+            self.handle, -1 if at is None else at, n, k_rows.data_ptr(), v_rows.data_ptr(),
+            DTYPE_F32 if k_rows.dtype == torch.float32 else DTYPE_BF16, k_rows.stride(r),
+            k_rows.stride(hd), v_rows.stride(r), v_rows.stride(hd), status.data_ptr(),
+            _stream(stream)), "dfv_kv8_append")
+
+    def fill(self, k_rows, v_rows, pos0=0, stream=None):
+        """Rows [Hkv, n, D] at positions [pos0, pos0 + n), as KVCache.fill."""
+        self.append(k_rows, v_rows, at=pos0, head_major=True, stream=stream)
+
+    def truncate(self, length, stream=None, status=None):
+        """Set the committed length back to ``length`` (the same rule as
+        :meth:`append`'s ``at``)."""
+        none = self.k_tail.new_empty(0, self.n_kv_heads, self.head_dim)
+        self.append(none, none, at=length, stream=stream, status=status)
+
+    def read(self, pos0, n, k_out, v_out, head_major=False, stream=None, status=None):
+        """The values of rows [pos0, pos0 + n) into k_out and v_out, [n, Hkv,
+        D] (or [Hkv, n, D]) f32 or bf16 with equal strides. Rows behind the
+        committed length are left as they were (DEV_CTX)."""
+        h, d = self.n_kv_heads, self.head_dim
+        shape = (h, n, d) if head_major else (n, h, d)
+        _float_rows(k_out, "k_out", shape)
+        _float_rows(v_out, "v_out", shape, (k_out.dtype,))
+        if k_out.stride() != v_out.stride():
+            raise DfvError("k_out and v_out must have the same strides")
+        status = self.status if status is None else status
+        _same_device(self.state.device, k_out=k_out, v_out=v_out, status=status)
+        r, hd = (1, 0) if head_major else (0, 1)
+        _check(lib().dfv_kv8_read(
+            self.handle, pos0, n, k_out.data_ptr(), v_out.data_ptr(),
+            DTYPE_F32 if k_out.dtype == torch.float32 else DTYPE_BF16, k_out.stride(r),
+            k_out.stride(hd), status.data_ptr(), _stream(stream)), "dfv_kv8_read")
+
+
+def int8_attn_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity):
+    return lib().dfv_kv8_attn_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window,
+                                              capacity)
+
+
+def _int8_attn(cache, q, tree_k, tree_v, parent, window, max_depth, out, lse, ws, scale, status,
+               stream):
+    n, hq, d = q.shape
+    hkv = cache.n_kv_heads
+    if d != cache.head_dim:
+        raise DfvError(f"q has head_dim {d}, the cache {cache.head_dim}")
+    _dev(q, "q", _BF16)
+    for t, name in ((tree_k, "tree_k"), (tree_v, "tree_v")):
+        _dev(t, name, _BF16)
+        if tuple(t.shape) != (n, hkv, d):
+            raise DfvError(f"{name} has shape {tuple(t.shape)}, expected {(n, hkv, d)}")
+    _dev(parent, "parent", _I32, n)
+    _dev(out, "out", (torch.float32, torch.bfloat16), n * hq * d)
+    if lse is not None:
+        _dev(lse, "lse", _F32, n * hq)
+    _dev(ws, "workspace", (torch.uint8,))
+    status = cache.status if status is None else status
+    _same_device(cache.state.device, q=q, tree_k=tree_k, tree_v=tree_v, parent=parent, out=out,
+                 lse=lse, workspace=ws, status=status)
+    _check(lib().dfv_kv8_attn(
+        cache.handle, n, max_depth, hq, window, q.data_ptr(), tree_k.data_ptr(),
+        tree_v.data_ptr(), parent.data_ptr(), float(scale), out.data_ptr(),
+        DTYPE_F32 if out.dtype == torch.float32 else DTYPE_BF16, _p(lse), ws.data_ptr(),
+        ws.numel(), status.data_ptr(), _stream(stream)), "dfv_kv8_attn")
+
+
 def kv_quantize_rows(cache, src, pos0, n_kv_heads, head_dim, capacity, head_major=False,
                      stream=None, fmt="q4_0"):
     """Encode rows of ``src`` into ``cache`` positions [pos0, pos0 + n) in
@@ -174,6 +318,15 @@ def clear_workspace(ws, stream=None):
 
 def tree_verify_attn(cache, q, tree_k, tree_v, parent, window, max_depth, out, lse, ws,
                      scale=0.0, status=None, stream=None, tree_as_cache=False, pipelined=False):
+    """Tree-masked attention over ``cache`` (KVCache, Q4Cache or Int8Cache).
+    With an Int8Cache, ``out`` may be f32 or bf16, the workspace comes from
+    :func:`int8_attn_workspace_bytes`, and ``tree_as_cache`` and ``pipelined``
+    are not available."""
+    if isinstance(cache, Int8Cache):
+        if tree_as_cache or pipelined:
+            raise DfvError("tree_as_cache and pipelined are not available with an Int8Cache")
+        return _int8_attn(cache, q, tree_k, tree_v, parent, window, max_depth, out, lse, ws,
+                          scale, status, stream)
     n, hq, d = q.shape
     hkv = tree_k.shape[1]
     _dev(q, "q", _BF16)
@@ -218,12 +371,60 @@ def greedy_accept(logits, parent, tokens, argmax, accept_len, path, out_tokens, 
         _p(status), _stream(stream)), "dfv_greedy_accept")
 
 
+def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None,
+                   status=None, stream=None):
+    """Log probability of ``tokens`` [N] (int32) under each row of ``logits``
+    [N, V] (f32 or bf16, rows may be strided) into ``logprob`` [N], the
+    entropy of each row into ``entropy`` [N], and its most probable tokens
+    into ``top_ids`` / ``top_logprobs`` [N, K], K <= MAX_TOP (either may be
+    None). Ties go to the lowest index."""
+    if logits is None or not logits.is_cuda or logits.dim() != 2 or \
+            logits.dtype not in (torch.float32, torch.bfloat16):
+        raise DfvError("logits must be a CUDA f32 or bf16 tensor [N, V]")
+    n, vocab = logits.shape
+    if n and vocab > 1 and logits.stride(1) != 1:
+        raise DfvError("logits rows must be contiguous")
+    if logprob is not None:
+        _dev(tokens, "tokens", _I32, n)
+        _dev(logprob, "logprob", _F32, n)
+    if entropy is not None:
+        _dev(entropy, "entropy", _F32, n)
+    top = 0
+    for t, name, dt in ((top_ids, "top_ids", _I32), (top_logprobs, "top_logprobs", _F32)):
+        if t is None:
+            continue
+        _dev(t, name, dt)
+        if t.dim() != 2 or t.shape[0] != n or (top and t.shape[1] != top):
+            raise DfvError(f"{name} must be [{n}, K], the same K for ids and log probabilities")
+        top = t.shape[1]
+    if top > min(MAX_TOP, vocab):
+        raise DfvError(f"{top} alternatives asked for, at most {min(MAX_TOP, vocab)}")
+    _same_device(logits.device, tokens=tokens, logprob=logprob, entropy=entropy, top_ids=top_ids,
+                 top_logprobs=top_logprobs, status=status)
+    _check(lib().dfv_token_logprobs(
+        n, vocab, DTYPE_F32 if logits.dtype == torch.float32 else DTYPE_BF16, logits.data_ptr(),
+        logits.stride(0) if n > 1 else vocab, _p(tokens), top, _p(logprob), _p(entropy),
+        _p(top_ids), _p(top_logprobs), _p(status), _stream(stream)), "dfv_token_logprobs")
+
+
 def kv_commit(cache, accept_len, path, tree_k, tree_v, status=None, stream=None):
     n = tree_k.shape[0]
     _dev(tree_k, "tree_k", _BF16)
     _dev(tree_v, "tree_v", _BF16)
     _dev(accept_len, "accept_len", _I32, 1)
     _dev(path, "path", _I32)
+    if isinstance(cache, Int8Cache):
+        if tuple(tree_k.shape) != (n, cache.n_kv_heads, cache.head_dim) or \
+                tree_v.shape != tree_k.shape:
+            raise DfvError("tree_k and tree_v must be [N, Hkv, D] of the cache")
+        _dev(path, "path", _I32, n)
+        status = cache.status if status is None else status
+        _same_device(cache.state.device, accept_len=accept_len, path=path, tree_k=tree_k,
+                     tree_v=tree_v, status=status)
+        _check(lib().dfv_kv8_commit(
+            cache.handle, n, accept_len.data_ptr(), path.data_ptr(), tree_k.data_ptr(),
+            tree_v.data_ptr(), status.data_ptr(), _stream(stream)), "dfv_kv8_commit")
+        return
     _check(lib().dfv_kv_commit(
         n, cache.n_kv_heads, cache.head_dim, cache.kv_format, cache.capacity, cache.ctx_len.data_ptr(),
         accept_len.data_ptr(), path.data_ptr(), tree_k.data_ptr(), tree_v.data_ptr(),

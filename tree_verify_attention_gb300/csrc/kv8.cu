@@ -1,0 +1,549 @@
+// Writing the 8-bit cache (rows appended, accepted rows committed) and
+// reading it back.
+//
+// A block is quantised once, when its 64 positions are complete, from their
+// bf16 values:
+//
+//   amax = max |x| over the block's 64 * D values,  scale = amax / 127,
+//   code = round-half-even(127 x / amax)
+//
+// so the cache's content does not depend on how the rows arrived (one prompt,
+// single tokens, accepted rows of a tree). 127 x is exact in f32 for a bf16
+// x, and one correctly rounded division of it cannot turn a quotient that is
+// no tie into a tie or the reverse (with 8-bit significands a quotient that
+// misses a half-way point misses it by 2^-17 at least), so the rule is the
+// exact rounding of the real quotient. The kernel multiplies by 127 / amax
+// (an error below 2^-15) and divides only where the product is that near to
+// a half-way point.
+//
+// Both kernels are bound by memory: 2 (4 for f32) bytes in and 1 out a value,
+// 1 in and 2 (4) out. One CTA of D threads takes one block of K or V of one
+// head, 64 values a thread in registers, so every value is read once and the
+// block's maximum needs no second pass. A K thread holds four pieces of 16
+// dims of one position, a V thread 4 dims of 16 positions: the piece of the
+// layout that it writes is then whole in its registers.
+
+#include "kv8.cuh"
+
+namespace dfv {
+
+struct Kv8AppendParams {
+  dfv_kv8_cache c;
+  int nblk;            // blocks a head has room for
+  int at, n;           // at < 0: the committed length
+  const void* src[2];
+  int64_t s_row[2], s_head[2];
+  const int32_t* path;        // with accept_len: row k of the write is src row path[k]
+  const int32_t* accept_len;
+  int n_nodes;
+  uint32_t* status;
+};
+
+// The rows of a write, agreed on by every CTA.
+struct Kv8Span {
+  int at, end;     // positions written
+  int b0, open;    // first block touched, block that is open afterwards
+};
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// kN values from global memory as packed bf16 (f32: rounded to nearest even).
+template <typename T, int kN, bool kVec>
+__device__ __forceinline__ void load_bf16(const T* s, uint32_t* w) {
+  if constexpr (!kVec) {
+#pragma unroll
+    for (int k = 0; k < kN / 2; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        w[k] = bf16x2_bits(s[2 * k], s[2 * k + 1]);
+      } else {
+        const uint16_t* u = reinterpret_cast<const uint16_t*>(s);
+        w[k] = u[2 * k] | (static_cast<uint32_t>(u[2 * k + 1]) << 16);
+      }
+    }
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < kN / 4; ++k) {
+      const float4 v = reinterpret_cast<const float4*>(s)[k];
+      w[2 * k] = bf16x2_bits(v.x, v.y);
+      w[2 * k + 1] = bf16x2_bits(v.z, v.w);
+    }
+  } else if constexpr (kN % 8 == 0) {
+#pragma unroll
+    for (int k = 0; k < kN / 8; ++k) {
+      const uint4 v = reinterpret_cast<const uint4*>(s)[k];
+      w[4 * k] = v.x;
+      w[4 * k + 1] = v.y;
+      w[4 * k + 2] = v.z;
+      w[4 * k + 3] = v.w;
+    }
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(s);
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+}
+
+// Four values as codes, lowest byte first.
+__device__ __forceinline__ uint32_t quantise4(float a, float b, float c, float d, float inv,
+                                              float amax) {
+  const float x[4] = {a, b, c, d};
+  int q[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float t = x[k] * inv;
+    float r = rintf(t);
+    if (fabsf(t - r) > 0.4998f) r = rintf(__fdiv_rn(x[k] * 127.0f, amax));
+    q[k] = static_cast<int>(r);
+  }
+  return (q[0] & 0xFF) | ((q[1] & 0xFF) << 8) | ((q[2] & 0xFF) << 16) |
+         (static_cast<uint32_t>(q[3] & 0xFF) << 24);
+}
+
+// The 64 values of one thread: 32 packed words. K: piece j of 16 dims at w[8 j]; V: position i of
+// 16 at w[2 i].
+template <typename T, int D, bool kVec>
+struct BlockIo {
+  static constexpr int kTpt = D / 64;      // K: threads per position
+  static constexpr int kVt = D / 4;        // V: threads per 16 positions
+
+  // Row of position p: its tail row, its source row, or none.
+  template <bool kV, int kN>
+  static __device__ __forceinline__ void load_row(const Kv8AppendParams& p, const Kv8Span& s,
+                                                  const int* path, int h, int pos, int dim,
+                                                  uint32_t* w) {
+    if (pos >= s.end) {
+#pragma unroll
+      for (int k = 0; k < kN / 2; ++k) w[k] = 0u;
+    } else if (pos < s.at) {
+      const __nv_bfloat16* tail =
+          static_cast<const __nv_bfloat16*>(kV ? p.c.v_tail : p.c.k_tail) +
+          ((static_cast<int64_t>(h) * 2 + ((pos / kBlk) & 1)) * kBlk + pos % kBlk) * D + dim;
+      load_bf16<__nv_bfloat16, kN, true>(tail, w);
+    } else {
+      const int64_t r = path ? path[pos - s.at] : pos - s.at;
+      const T* src = static_cast<const T*>(p.src[kV]) + r * p.s_row[kV] + h * p.s_head[kV] + dim;
+      load_bf16<T, kN, kVec>(src, w);
+    }
+  }
+
+  template <bool kV>
+  static __device__ __forceinline__ void load(const Kv8AppendParams& p, const Kv8Span& s,
+                                              const int* path, int h, int b, uint32_t* w) {
+    const int tid = threadIdx.x;
+    if constexpr (!kV) {
+      const int pos = b * kBlk + tid / kTpt;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        load_row<false, 16>(p, s, path, h, pos, (tid % kTpt + j * kTpt) * 16, w + 8 * j);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        load_row<true, 4>(p, s, path, h, b * kBlk + tid / kVt * 16 + i, tid % kVt * 4, w + 2 * i);
+    }
+  }
+
+  // Rows of block b written by this call, into their tail slot.
+  template <bool kV>
+  static __device__ __forceinline__ void store_tail(const Kv8AppendParams& p, const Kv8Span& s,
+                                                    int h, int b, const uint32_t* w) {
+    const int tid = threadIdx.x;
+    __nv_bfloat16* slot = static_cast<__nv_bfloat16*>(kV ? p.c.v_tail : p.c.k_tail) +
+                          (static_cast<int64_t>(h) * 2 + (b & 1)) * kBlk * D;
+    if constexpr (!kV) {
+      const int t = tid / kTpt, pos = b * kBlk + t;
+      if (pos < s.at || pos >= s.end) return;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4* dst = reinterpret_cast<uint4*>(slot + t * D + (tid % kTpt + j * kTpt) * 16);
+        dst[0] = make_uint4(w[8 * j], w[8 * j + 1], w[8 * j + 2], w[8 * j + 3]);
+        dst[1] = make_uint4(w[8 * j + 4], w[8 * j + 5], w[8 * j + 6], w[8 * j + 7]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int t = tid / kVt * 16 + i, pos = b * kBlk + t;
+        if (pos >= s.at && pos < s.end)
+          *reinterpret_cast<uint2*>(slot + t * D + tid % kVt * 4) =
+              make_uint2(w[2 * i], w[2 * i + 1]);
+      }
+    }
+  }
+
+  template <bool kV>
+  static __device__ __forceinline__ void store_codes(const Kv8AppendParams& p, int h, int b,
+                                                     const uint32_t* w, uint32_t amax_bits) {
+    const int tid = threadIdx.x;
+    const bool zero = amax_bits < kSmallBits;
+    const float amax = __uint_as_float(amax_bits << 16);
+    const float inv = zero ? 0.0f : __fdiv_rn(127.0f, amax);
+    if (tid == 0)
+      (kV ? p.c.v_scale : p.c.k_scale)[static_cast<int64_t>(h) * p.nblk + b] =
+          zero ? 0.0f : __fdiv_rn(amax, 127.0f);
+    int8_t* base = (kV ? p.c.v_codes : p.c.k_codes) + static_cast<int64_t>(h) * p.nblk * kBlk * D;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t q[4];
+      int64_t off;
+      if constexpr (!kV) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t a = w[8 * j + 2 * e], c = w[8 * j + 2 * e + 1];
+          q[e] = quantise4(bf16_lo(a), bf16_hi(a), bf16_lo(c), bf16_hi(c), inv, amax);
+        }
+        off = kv8_k_piece(b, tid / kTpt, tid % kTpt + j * kTpt, D);
+      } else {   // dim j of the thread's four, 16 positions
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a = w[2 * (4 * e + i) + j / 2];
+            x[i] = j & 1 ? bf16_hi(a) : bf16_lo(a);
+          }
+          q[e] = quantise4(x[0], x[1], x[2], x[3], inv, amax);
+        }
+        off = kv8_v_piece(b, tid / kVt, tid % kVt * 4 + j, D);
+      }
+      *reinterpret_cast<uint4*>(base + off) = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+  }
+};
+
+// Values that are not stored become zeros; returns whether there were any.
+__device__ __forceinline__ bool drop_big(uint32_t* w) {
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+    if (lo >= kBigBits) { w[k] &= 0xFFFF0000u; any = true; }
+    if (hi >= kBigBits) { w[k] &= 0x0000FFFFu; any = true; }
+  }
+  return any;
+}
+
+template <typename T, int D, bool kVec, bool kV>
+__device__ __forceinline__ void append_block(const Kv8AppendParams& p, const Kv8Span& s,
+                                             const int* path, uint32_t* s_max) {
+  using Io = BlockIo<T, D, kVec>;
+  const int h = blockIdx.y, b = s.b0 + blockIdx.x;
+  const int tid = threadIdx.x;
+  uint32_t w[32];
+  Io::template load<kV>(p, s, path, h, b, w);
+  if (drop_big(w)) report(p.status, DFV_DEV_NONFINITE);
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((tid & 31) == 0) s_max[tid >> 5] = m;
+  __syncthreads();   // also: the block's tail rows have been read
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) m = max(m, s_max[k]);
+  if (s.end >= (b + 1) * kBlk) Io::template store_codes<kV>(p, h, b, w, m);
+  // The blocks that the tail keeps afterwards are the open one and the one
+  // before. Their slots may hold rows that block b0 still needs (its own
+  // slot has the same parity every second block); b0's CTA then writes them.
+  const bool shared = s.at % kBlk != 0;   // b0 reads its slot
+  if (b >= s.open - 1 && (b == s.b0 || !shared || ((b - s.b0) & 1)))
+    Io::template store_tail<kV>(p, s, h, b, w);
+  if (b == s.b0 && shared) {
+    const int other = ((s.open - s.b0) & 1) ? s.open - 1 : s.open;
+    if (other > b) {
+      Io::template load<kV>(p, s, path, h, other, w);
+      drop_big(w);
+      Io::template store_tail<kV>(p, s, h, other, w);
+    }
+  }
+}
+
+template <typename T, int D, bool kVec>
+__global__ void __launch_bounds__(D) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
+  __shared__ uint32_t s_max[D / 32];
+  __shared__ int s_path[kMaxNodes];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x;
+  const int C = *static_cast<volatile int32_t*>(p.c.state);
+  int n = p.n;
+  uint32_t bad = 0;
+  if (C < 0 || C > p.c.capacity) bad = DFV_DEV_CTX;
+  if (p.accept_len) {
+    n = *p.accept_len;
+    if (n < 1 || n > p.n_nodes) bad |= DFV_DEV_BAD_PATH;
+  }
+  const int at = p.at < 0 ? C : p.at;
+  // the rows of at's block before it have to be in the tail
+  const int held = static_cast<volatile int32_t*>(p.c.state)[2];
+  if (!bad && (at > C || (at % kBlk != 0 && at / kBlk < held))) bad = DFV_DEV_CTX;
+  if (!bad && at + n > p.c.capacity) bad = DFV_DEV_CAPACITY;
+  if (p.accept_len) {
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    if (!bad)
+      for (int k = tid; k < n; k += D) {
+        const int node = p.path[k];
+        s_path[k] = node;
+        if (node < 0 || node >= p.n_nodes) s_bad = 1;
+      }
+    __syncthreads();
+    if (s_bad) bad |= DFV_DEV_BAD_PATH;
+  }
+  if (bad) {   // the same for every CTA: nothing is written
+    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) report(p.status, bad);
+    return;
+  }
+  Kv8Span s;
+  s.at = at;
+  s.end = at + n;
+  s.b0 = at / kBlk;
+  s.open = s.end / kBlk;
+  if ((s.b0 + static_cast<int>(blockIdx.x)) * kBlk < s.end) {
+    const int* path = p.accept_len ? s_path : nullptr;
+    if (blockIdx.z == 0) append_block<T, D, kVec, false>(p, s, path, s_max);
+    else append_block<T, D, kVec, true>(p, s, path, s_max);
+  }
+  // the last CTA to finish advances the committed length, which the others
+  // have read; the counter beside it is left at zero
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    const unsigned total = gridDim.x * gridDim.y * gridDim.z;
+    if (atomicAdd(reinterpret_cast<unsigned*>(p.c.state) + 1, 1u) == total - 1) {
+      p.c.state[1] = 0;
+      p.c.state[0] = s.end;
+      // the first block whose bf16 rows the tail now has
+      p.c.state[2] = s.open > s.b0 ? s.open - 1 : s.b0 < held ? s.b0 : max(held, s.b0 - 1);
+    }
+  }
+}
+
+template <typename T, bool kVec>
+dfv_status append_launch_t(const Kv8AppendParams& p, int rows, cudaStream_t stream) {
+  const dim3 grid((rows + kBlk - 2) / kBlk + 1, p.c.n_kv_heads, 2);   // blocks that `rows` can touch
+  switch (p.c.head_dim) {
+    case 64: kv8_append_kernel<T, 64, kVec><<<grid, 64, 0, stream>>>(p); break;
+    case 128: kv8_append_kernel<T, 128, kVec><<<grid, 128, 0, stream>>>(p); break;
+    default: kv8_append_kernel<T, 256, kVec><<<grid, 256, 0, stream>>>(p); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
+}
+
+dfv_status kv8_append_launch(Kv8AppendParams& p, int rows, int dtype, cudaStream_t stream) {
+  p.nblk = kv8_blocks(p.c.capacity);
+  const int e = dtype == DFV_DTYPE_F32 ? 4 : 2;
+  bool vec = true;
+  for (int k = 0; k < 2; ++k)
+    vec = vec && aligned(p.src[k], 16) && (p.s_row[k] * e) % 16 == 0 && (p.s_head[k] * e) % 16 == 0;
+  if (dtype == DFV_DTYPE_F32)
+    return vec ? append_launch_t<float, true>(p, rows, stream)
+               : append_launch_t<float, false>(p, rows, stream);
+  return vec ? append_launch_t<__nv_bfloat16, true>(p, rows, stream)
+             : append_launch_t<__nv_bfloat16, false>(p, rows, stream);
+}
+
+// ---------------------------------------------------------------- read back
+
+struct Kv8ReadParams {
+  dfv_kv8_cache c;
+  int nblk;
+  int pos0, end;
+  void* dst[2];
+  int64_t s_row, s_head;
+  uint32_t* status;
+};
+
+template <typename T, int kN, bool kVec>
+__device__ __forceinline__ void store_values(T* dst, const float* x) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int k = 0; k < kN / 4; ++k)
+        reinterpret_cast<float4*>(dst)[k] =
+            make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kN; ++k) dst[k] = x[k];
+    }
+  } else if constexpr (!kVec) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) dst[k] = __float2bfloat16_rn(x[k]);
+  } else if constexpr (kN % 8 == 0) {
+#pragma unroll
+    for (int k = 0; k < kN / 8; ++k)
+      reinterpret_cast<uint4*>(dst)[k] =
+          make_uint4(bf16x2_bits(x[8 * k], x[8 * k + 1]), bf16x2_bits(x[8 * k + 2], x[8 * k + 3]),
+                     bf16x2_bits(x[8 * k + 4], x[8 * k + 5]),
+                     bf16x2_bits(x[8 * k + 6], x[8 * k + 7]));
+  } else {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]));
+  }
+}
+
+__device__ __forceinline__ float code_at(const uint4& v, int i) {
+  const uint32_t w = i < 4 ? v.x : i < 8 ? v.y : i < 12 ? v.z : v.w;
+  return static_cast<float>(static_cast<int8_t>((w >> (8 * (i & 3))) & 0xFF));
+}
+
+template <typename T, int D, bool kVec>
+__global__ void __launch_bounds__(D) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
+  constexpr int kTpt = D / 64, kVt = D / 4;
+  const int C = *p.c.state;
+  const int tid = threadIdx.x, h = blockIdx.y, kv = blockIdx.z;
+  int end = p.end;
+  if (C < 0 || C > p.c.capacity || end > C) {   // rows behind the committed ones stay as they are
+    if (tid == 0 && blockIdx.x == 0 && h == 0 && kv == 0) report(p.status, DFV_DEV_CTX);
+    end = C < 0 || C > p.c.capacity ? 0 : min(end, C);
+  }
+  const int b = p.pos0 / kBlk + blockIdx.x;
+  const int first = max(p.pos0, b * kBlk), last = min(end, (b + 1) * kBlk);
+  if (first >= last) return;
+  T* dst = static_cast<T*>(p.dst[kv]) + h * p.s_head;
+  if (b == C / kBlk) {   // the open block: bf16 rows
+    const __nv_bfloat16* tail = static_cast<const __nv_bfloat16*>(kv ? p.c.v_tail : p.c.k_tail) +
+                                (static_cast<int64_t>(h) * 2 + (b & 1)) * kBlk * D;
+    for (int pos = first; pos < last; ++pos) {
+      const float x = __bfloat162float(tail[(pos % kBlk) * D + tid]);
+      T* o = dst + (pos - p.pos0) * p.s_row + tid;
+      if constexpr (sizeof(T) == 4) *o = x;
+      else *o = __float2bfloat16_rn(x);
+    }
+    return;
+  }
+  const float scale = (kv ? p.c.v_scale : p.c.k_scale)[static_cast<int64_t>(h) * p.nblk + b];
+  const int8_t* codes =
+      (kv ? p.c.v_codes : p.c.k_codes) + static_cast<int64_t>(h) * p.nblk * kBlk * D;
+  if (kv == 0) {
+    const int pos = b * kBlk + tid / kTpt;
+    if (pos < first || pos >= last) return;
+    uint4 q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      q[j] = *reinterpret_cast<const uint4*>(
+          codes + kv8_k_piece(b, tid / kTpt, tid % kTpt + j * kTpt, D));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = code_at(q[j], i) * scale;
+      store_values<T, 16, kVec>(dst + (pos - p.pos0) * p.s_row + (tid % kTpt + j * kTpt) * 16, x);
+    }
+  } else {
+    uint4 q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      q[j] = *reinterpret_cast<const uint4*>(
+          codes + kv8_v_piece(b, tid / kVt, tid % kVt * 4 + j, D));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int pos = b * kBlk + tid / kVt * 16 + i;
+      if (pos < first || pos >= last) continue;
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = code_at(q[j], i) * scale;
+      store_values<T, 4, kVec>(dst + (pos - p.pos0) * p.s_row + tid % kVt * 4, x);
+    }
+  }
+}
+
+template <typename T, bool kVec>
+dfv_status read_launch_t(const Kv8ReadParams& p, cudaStream_t stream) {
+  const dim3 grid((p.end - 1) / kBlk - p.pos0 / kBlk + 1, p.c.n_kv_heads, 2);
+  switch (p.c.head_dim) {
+    case 64: kv8_read_kernel<T, 64, kVec><<<grid, 64, 0, stream>>>(p); break;
+    case 128: kv8_read_kernel<T, 128, kVec><<<grid, 128, 0, stream>>>(p); break;
+    default: kv8_read_kernel<T, 256, kVec><<<grid, 256, 0, stream>>>(p); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
+}
+
+}  // namespace dfv
+
+extern "C" dfv_status dfv_kv8_append(const dfv_kv8_cache* cache, int at, int n_rows,
+                                     const void* k_src, const void* v_src, int src_dtype,
+                                     int64_t k_stride_row, int64_t k_stride_head,
+                                     int64_t v_stride_row, int64_t v_stride_head,
+                                     uint32_t* status, dfv_stream_t stream) {
+  using namespace dfv;
+  if (!kv8_cache_ok(cache)) return DFV_ERR_INVALID;
+  if (!kv8_dim_ok(cache->head_dim)) return DFV_ERR_UNSUPPORTED;
+  if (src_dtype != DFV_DTYPE_F32 && src_dtype != DFV_DTYPE_BF16) return DFV_ERR_UNSUPPORTED;
+  const size_t size = src_dtype == DFV_DTYPE_F32 ? 4 : 2;
+  if (at < -1 || n_rows < 0 || n_rows > cache->capacity ||
+      static_cast<int64_t>(at < 0 ? 0 : at) + n_rows > cache->capacity)
+    return DFV_ERR_INVALID;
+  if (n_rows > 0 && (!k_src || !v_src || !aligned(k_src, size) || !aligned(v_src, size)))
+    return DFV_ERR_INVALID;
+  if (n_rows == 0 && at < 0) return DFV_OK;
+  Kv8AppendParams p = {};
+  p.c = *cache;
+  p.at = at;
+  p.n = n_rows;
+  p.src[0] = k_src;
+  p.src[1] = v_src;
+  p.s_row[0] = k_stride_row;
+  p.s_head[0] = k_stride_head;
+  p.s_row[1] = v_stride_row;
+  p.s_head[1] = v_stride_head;
+  p.status = status;
+  return kv8_append_launch(p, n_rows, src_dtype, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dfv_status dfv_kv8_commit(const dfv_kv8_cache* cache, int n_nodes,
+                                     const int32_t* accept_len, const int32_t* path,
+                                     const void* tree_k, const void* tree_v, uint32_t* status,
+                                     dfv_stream_t stream) {
+  using namespace dfv;
+  if (!kv8_cache_ok(cache)) return DFV_ERR_INVALID;
+  if (!kv8_dim_ok(cache->head_dim)) return DFV_ERR_UNSUPPORTED;
+  if (n_nodes < 1 || n_nodes > kMaxNodes || !accept_len || !path || !tree_k || !tree_v ||
+      !aligned(tree_k, 16) || !aligned(tree_v, 16))
+    return DFV_ERR_INVALID;
+  Kv8AppendParams p = {};
+  p.c = *cache;
+  p.at = -1;
+  for (int k = 0; k < 2; ++k) {
+    p.s_row[k] = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
+    p.s_head[k] = cache->head_dim;
+  }
+  p.src[0] = tree_k;
+  p.src[1] = tree_v;
+  p.path = path;
+  p.accept_len = accept_len;
+  p.n_nodes = n_nodes;
+  p.status = status;
+  return kv8_append_launch(p, n_nodes, DFV_DTYPE_BF16, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dfv_status dfv_kv8_read(const dfv_kv8_cache* cache, int pos0, int n_rows, void* k_dst,
+                                   void* v_dst, int dst_dtype, int64_t stride_row,
+                                   int64_t stride_head, uint32_t* status, dfv_stream_t stream) {
+  using namespace dfv;
+  if (!kv8_cache_ok(cache)) return DFV_ERR_INVALID;
+  if (!kv8_dim_ok(cache->head_dim)) return DFV_ERR_UNSUPPORTED;
+  if (dst_dtype != DFV_DTYPE_F32 && dst_dtype != DFV_DTYPE_BF16) return DFV_ERR_UNSUPPORTED;
+  if (pos0 < 0 || n_rows < 0 || static_cast<int64_t>(pos0) + n_rows > cache->capacity)
+    return DFV_ERR_INVALID;
+  if (n_rows == 0) return DFV_OK;
+  const int e = dst_dtype == DFV_DTYPE_F32 ? 4 : 2;
+  if (!k_dst || !v_dst || !aligned(k_dst, e) || !aligned(v_dst, e)) return DFV_ERR_INVALID;
+  Kv8ReadParams p = {};
+  p.c = *cache;
+  p.nblk = kv8_blocks(cache->capacity);
+  p.pos0 = pos0;
+  p.end = pos0 + n_rows;
+  p.dst[0] = k_dst;
+  p.dst[1] = v_dst;
+  p.s_row = stride_row;
+  p.s_head = stride_head;
+  p.status = status;
+  const bool vec = aligned(k_dst, 16) && aligned(v_dst, 16) && (stride_row * e) % 16 == 0 &&
+                   (stride_head * e) % 16 == 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dst_dtype == DFV_DTYPE_F32)
+    return vec ? read_launch_t<float, true>(p, s) : read_launch_t<float, false>(p, s);
+  return vec ? read_launch_t<__nv_bfloat16, true>(p, s) : read_launch_t<__nv_bfloat16, false>(p, s);
+}

@@ -1,0 +1,451 @@
+// Log probabilities of given tokens, the entropy of each row of logits and
+// its top alternatives.
+//
+//   m = max_i x_i, z_i = x_i - m, s = sum exp(z_i)
+//   log p(t) = z_t - log s
+//   entropy  = log s - (sum exp(z_i) z_i) / s
+//   top      = the `top` largest x, ties to the lowest index
+//
+// Everything comes from one pass over the row: each thread carries a running
+// (m, s, sum exp(z) z), rescaled when its maximum moves, and the partial
+// triples are merged in a fixed order. The kernel is bound by memory for many
+// rows and by latency for few, so a row belongs to a cluster of 1 to 8 CTAs
+// (the fewer the rows, the more) whose results meet through distributed
+// shared memory: one launch, no workspace, nothing to reset.
+//
+// The alternatives cost next to nothing beside that pass. The first chunk of
+// a slice (its values stay in registers) is cut into 64 groups; the top-th
+// largest of the group maxima is a lower bound of the slice's top-th value,
+// and whatever reaches that bound is collected in shared memory: for a row
+// in random order some top * slice / chunk candidates. Rows that collect more
+// than the buffer holds (many equal values, ascending values) are read once
+// more by a path that cuts the buffer back to the best `top` as it fills.
+// Candidates are ordered by a 64-bit key (value, then lower index), which is
+// unique, so the result does not depend on the order of collection.
+
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+
+namespace dfv {
+
+namespace cg = cooperative_groups;
+
+constexpr int kLpThreads = 256;
+constexpr int kLpGroups = 64;       // >= DFV_MAX_TOP
+constexpr int kLpCap = 2048;        // candidates a CTA can hold
+constexpr int kLpVecs = 4;          // 16-byte loads per thread and chunk
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct LogprobParams {
+  int vocab, top;
+  const void* logits;
+  int64_t stride;
+  const int32_t* tokens;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ float lp_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Orders like (value, lower index first); -0 equals +0.
+__device__ __forceinline__ uint64_t lp_key(float x, int idx) {
+  uint32_t u = __float_as_uint(x + 0.0f);
+  u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return (static_cast<uint64_t>(u) << 32) | static_cast<uint32_t>(~idx);
+}
+__device__ __forceinline__ float lp_value(uint64_t key) {
+  const uint32_t u = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+__device__ __forceinline__ int lp_index(uint64_t key) {
+  return static_cast<int>(~static_cast<uint32_t>(key));
+}
+
+// Running maximum, sum of exp(x - m) and of exp(x - m) (x - m).
+struct LpStats {
+  float m, s, t;
+  __device__ __forceinline__ void init() {
+    m = -INFINITY;
+    s = 0.0f;
+    t = 0.0f;
+  }
+  __device__ __forceinline__ void raise(float to) {   // to > m
+    const float d = fmaxf(m - to, -200.0f);           // exp(-200) is zero; 0 * -inf is not
+    const float f = lp_ex2(d * kLog2e);
+    t = f * fmaf(d, s, t);
+    s *= f;
+    m = to;
+  }
+  __device__ __forceinline__ void merge(const LpStats& o) {
+    if (o.m != o.m || m != m) {
+      m = s = t = NAN;
+      return;
+    }
+    LpStats b = o;
+    if (b.m > m) raise(b.m);
+    else if (m > b.m) b.raise(m);
+    s += b.s;
+    t += b.t;
+  }
+};
+
+template <typename T> struct LpVec;   // one 16-byte load
+template <> struct LpVec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ float at(const uint4& v, int i) {
+    return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  }
+};
+template <> struct LpVec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ float at(const uint4& v, int i) {
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
+
+__device__ __forceinline__ float lp_to_f32(float x) { return x; }
+__device__ __forceinline__ float lp_to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+struct LpSmem {
+  uint64_t buf[kLpCap];
+  uint64_t gkey[kLpGroups];
+  uint64_t best[DFV_MAX_TOP];   // the slice's, in order
+  float gmax[kLpThreads];
+  LpStats wst[kLpThreads / 32];
+  LpStats st;
+  uint64_t cut;
+  float bound;
+  int count, n_best;
+};
+
+// Adds n values (all of one thread) to its statistics.
+template <int kN, typename F>
+__device__ __forceinline__ void lp_add(LpStats& st, float vm, F value) {
+  if (!(vm <= st.m)) {
+    if (vm == vm) st.raise(vm);
+    else st.m = st.s = st.t = NAN;   // NaN stays: comparisons with it fail
+  }
+  if (st.m == -INFINITY) return;     // nothing but -inf so far
+  float s0 = 0.0f, s1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    // exp(-200) is zero; the limit keeps 0 * -inf out of the sum
+    const float z = fmaxf(value(i) - st.m, -200.0f);
+    const float e = lp_ex2(z * kLog2e);
+    if (i & 1) {
+      s1 += e;
+      t1 = fmaf(e, z, t1);
+    } else {
+      s0 += e;
+      t0 = fmaf(e, z, t0);
+    }
+  }
+  st.s += s0 + s1;
+  st.t += t0 + t1;
+}
+
+__device__ __forceinline__ void lp_push(LpSmem& sm, float x, int idx) {
+  const int k = atomicAdd(&sm.count, 1);
+  if (k < kLpCap) sm.buf[k] = lp_key(x, idx);
+}
+
+// The best `top` of buf[0, c), in order, into sm.best (n_best of them).
+// All threads; c <= kLpCap. Large sets are cut first: at least `top` keys
+// reach the top-th largest of the group maxima.
+__device__ void lp_select(LpSmem& sm, int c, int top) {
+  const int tid = threadIdx.x;
+  while (c > kLpThreads) {
+    uint64_t mine = 0;
+    for (int i = tid; i < c; i += kLpThreads) mine = max(mine, sm.buf[i]);
+    // threads tid, tid ^ 64, ... form a group
+    uint64_t* all = sm.gkey;
+    if (tid < kLpGroups) all[tid] = 0;
+    __syncthreads();
+    atomicMax(reinterpret_cast<unsigned long long*>(&all[tid % kLpGroups]),
+              static_cast<unsigned long long>(mine));
+    __syncthreads();
+    if (tid < kLpGroups) {
+      int above = 0;
+      for (int i = 0; i < kLpGroups; ++i) above += all[i] > all[tid];
+      if (above == top - 1) sm.cut = all[tid];
+    }
+    __syncthreads();
+    const uint64_t cut = sm.cut;
+    uint64_t keep[kLpCap / kLpThreads];
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < kLpCap / kLpThreads; ++j) {
+      const int i = tid + j * kLpThreads;
+      keep[j] = i < c ? sm.buf[i] : 0;
+      n += keep[j] >= cut && keep[j] != 0;
+    }
+    if (tid == 0) sm.count = 0;
+    __syncthreads();
+    int at = n ? atomicAdd(&sm.count, n) : 0;
+#pragma unroll
+    for (int j = 0; j < kLpCap / kLpThreads; ++j)
+      if (keep[j] >= cut && keep[j] != 0) sm.buf[at++] = keep[j];
+    __syncthreads();
+    const int left = sm.count;
+    __syncthreads();
+    if (left == c) break;
+    c = left;
+  }
+  const int n_best = min(c, top);
+  for (int i = tid; i < c; i += kLpThreads) {
+    const uint64_t mine = sm.buf[i];
+    int above = 0;
+    for (int k = 0; k < c; ++k) above += sm.buf[k] > mine;
+    if (above < top) sm.best[above] = mine;
+  }
+  if (tid == 0) sm.n_best = n_best;
+  __syncthreads();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_constant__ LogprobParams p) {
+  __shared__ LpSmem sm;
+  constexpr int kV = LpVec<T>::kN;
+  cg::cluster_group cl = cg::this_cluster();
+  const int cs = cl.num_blocks(), rank = cl.block_rank();
+  const int row = blockIdx.x / cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const T* x = static_cast<const T*>(p.logits) + row * p.stride;
+  // The row: a head before the first 16-byte boundary, whole vectors, a
+  // tail. The vectors are dealt in equal runs; the first CTA of the cluster
+  // has the head too, the last one the tail.
+  const int head = min(p.vocab, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
+  const int nv = (p.vocab - head) / kV;
+  const int v0 = static_cast<int>(static_cast<int64_t>(nv) * rank / cs);
+  const int v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / cs);
+  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+  int extra = -1;   // this thread's element outside the vectors
+  if (rank == 0 && tid < head) extra = tid;
+  if (rank == cs - 1 && tid >= 32 && tid - 32 < p.vocab - head - nv * kV)
+    extra = head + nv * kV + tid - 32;
+  const int slice_n = (v1 - v0) * kV + (rank == 0 ? head : 0) +
+                      (rank == cs - 1 ? p.vocab - head - nv * kV : 0);
+  const int top = p.top;
+  if (tid == 0) sm.count = 0;
+
+  LpStats st;
+  st.init();
+  constexpr int kStep = kLpThreads * kLpVecs;
+  uint4 v[kLpVecs];
+  const uint32_t lowest = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;   // -inf
+  const uint4 none = make_uint4(lowest, lowest, lowest, lowest);
+  auto load = [&](int base) {
+#pragma unroll
+    for (int j = 0; j < kLpVecs; ++j) {
+      const int i = base + j * kLpThreads + tid;
+      v[j] = i < v1 ? __ldg(xv + i) : none;
+    }
+  };
+  auto value = [&](int i) { return LpVec<T>::at(v[i / kV], i % kV); };
+  auto chunk_max = [&]() {
+    float vm = value(0);
+#pragma unroll
+    for (int i = 1; i < kV * kLpVecs; ++i) vm = max_nan(vm, value(i));
+    return vm;
+  };
+  auto push_from = [&](int base, float bound) {
+#pragma unroll
+    for (int j = 0; j < kLpVecs; ++j) {
+      const int i = base + j * kLpThreads + tid;
+#pragma unroll
+      for (int e = 0; e < kV; ++e) {
+        const float w = LpVec<T>::at(v[j], e);
+        if (w >= bound && i < v1) lp_push(sm, w, head + i * kV + e);
+      }
+    }
+  };
+
+  // ---- first chunk: statistics, and the bound for the alternatives
+  load(v0);
+  const float xe = extra >= 0 ? lp_to_f32(x[extra]) : -INFINITY;
+  float vm = chunk_max();
+  lp_add<kV * kLpVecs>(st, vm, value);
+  if (extra >= 0) lp_add<1>(st, xe, [&](int) { return xe; });
+  float bound = INFINITY;
+  if (top > 0) {
+    sm.gmax[tid] = fmaxf(vm, xe);
+    __syncthreads();
+    float g = 0.0f;
+    if (tid < kLpGroups) {
+      g = sm.gmax[tid];
+#pragma unroll
+      for (int k = 1; k < kLpThreads / kLpGroups; ++k) g = fmaxf(g, sm.gmax[tid + k * kLpGroups]);
+    }
+    __syncthreads();
+    if (tid < kLpGroups) sm.gmax[tid] = g;
+    __syncthreads();
+    if (tid < kLpGroups) {
+      int above = 0, same = 0;
+#pragma unroll 8
+      for (int k = 0; k < kLpGroups; ++k) {
+        above += sm.gmax[k] > g;
+        same += sm.gmax[k] >= g;
+      }
+      if (above < top && same >= top) sm.bound = g;   // the same value from each such thread
+    }
+    __syncthreads();
+    // -inf is no bound: what is above it is collected, the rest if that is too little
+    bound = fmaxf(sm.bound, -3.4028235e38f);
+    push_from(v0, bound);
+    if (extra >= 0 && xe >= bound) lp_push(sm, xe, extra);
+  }
+  // ---- the rest of the slice
+  for (int base = v0 + kStep; base < v1; base += kStep) {
+    load(base);
+    vm = chunk_max();
+    lp_add<kV * kLpVecs>(st, vm, value);
+    if (vm >= bound) push_from(base, bound);
+  }
+  // ---- statistics of the CTA: lanes, then warps in order
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    LpStats b;
+    b.m = __shfl_down_sync(0xFFFFFFFFu, st.m, o);
+    b.s = __shfl_down_sync(0xFFFFFFFFu, st.s, o);
+    b.t = __shfl_down_sync(0xFFFFFFFFu, st.t, o);
+    st.merge(b);
+  }
+  if (lane == 0) sm.wst[warp] = st;
+  __syncthreads();
+  if (tid == 0) {
+    LpStats a = sm.wst[0];
+    for (int w = 1; w < kLpThreads / 32; ++w) a.merge(sm.wst[w]);
+    sm.st = a;
+  }
+  // ---- alternatives of the slice
+  if (top > 0) {
+    int c = sm.count;
+    if (c > kLpCap || c < min(top, slice_n)) {
+      // Once more, with keys: the buffer is cut back to the best `top`
+      // whenever the next round might not fit.
+      constexpr int kRound = kLpCap / 2;   // elements a round can add
+      const int lo = rank == 0 ? 0 : head + v0 * kV;
+      const int hi = rank == cs - 1 ? p.vocab : head + v1 * kV;
+      uint64_t cut = 0;
+      __syncthreads();
+      if (tid == 0) sm.count = 0;
+      __syncthreads();
+      for (int base = lo; base < hi; base += kRound) {
+        for (int i = base + tid; i < min(hi, base + kRound); i += kLpThreads) {
+          const float w = lp_to_f32(x[i]);
+          if (lp_key(w, i) > cut) lp_push(sm, w, i);
+        }
+        __syncthreads();
+        c = sm.count;
+        __syncthreads();
+        if (c > kLpCap - kRound) {
+          lp_select(sm, c, top);
+          c = sm.n_best;
+          cut = c == top ? sm.best[top - 1] : 0;
+          if (tid < c) sm.buf[tid] = sm.best[tid];
+          if (tid == 0) sm.count = c;
+          __syncthreads();
+        }
+      }
+    }
+    lp_select(sm, c, top);
+  } else {
+    __syncthreads();
+  }
+  // ---- the cluster's CTAs in order, by the first one
+  if (cs > 1) cl.sync();
+  if (rank == 0) {
+    LpStats a = sm.st;
+    for (int r = 1; r < cs; ++r) a.merge(*cl.map_shared_rank(&sm.st, r));
+    const float logs = logf(a.s);
+    if (tid == 0) {
+      if (p.logprob) {
+        const int t = p.tokens[row];
+        const bool in = t >= 0 && t < p.vocab;
+        if (!in) report(p.status, DFV_DEV_BAD_TOKEN);
+        p.logprob[row] = in ? (lp_to_f32(x[t]) - a.m) - logs : NAN;
+      }
+      if (p.entropy) p.entropy[row] = logs - a.t / a.s;
+    }
+    if (top > 0) {
+      int c = sm.n_best;
+      if (cs > 1) {
+        __syncthreads();
+        if (tid < c) sm.buf[tid] = sm.best[tid];
+        for (int r = 1; r < cs; ++r) {
+          const LpSmem* o = cl.map_shared_rank(&sm, r);
+          const int n = o->n_best;
+          if (tid < n) sm.buf[c + tid] = o->best[tid];
+          c += n;
+        }
+        __syncthreads();
+        lp_select(sm, c, top);
+      }
+      if (tid < top) {
+        const uint64_t key = sm.best[tid];
+        const int64_t at = static_cast<int64_t>(row) * top + tid;
+        if (p.top_ids) p.top_ids[at] = lp_index(key);
+        if (p.top_logprobs) p.top_logprobs[at] = (lp_value(key) - a.m) - logs;
+      }
+    }
+  }
+  if (cs > 1) cl.sync();   // the others' shared memory is read until here
+}
+
+template <typename T>
+dfv_status logprob_launch(const LogprobParams& p, int rows, cudaStream_t stream) {
+  // CTAs per row: about four per SM in all
+  const int slots = sm_count() * 4;
+  int cs = 8;
+  while (cs > 1 && static_cast<int64_t>(rows) * cs > slots) cs >>= 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows) * cs);
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<T>, p) == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
+}
+
+}  // namespace dfv
+
+extern "C" dfv_status dfv_token_logprobs(int n_rows, int vocab, int logits_dtype,
+                                         const void* logits, int64_t stride_row,
+                                         const int32_t* tokens, int top, float* logprob,
+                                         float* entropy, int32_t* top_ids, float* top_logprobs,
+                                         uint32_t* status, dfv_stream_t stream) {
+  using namespace dfv;
+  if (logits_dtype != DFV_DTYPE_F32 && logits_dtype != DFV_DTYPE_BF16) return DFV_ERR_UNSUPPORTED;
+  const size_t size = logits_dtype == DFV_DTYPE_F32 ? 4 : 2;
+  if (n_rows < 0 || n_rows > (1 << 27) || vocab < 1 || vocab > (1 << 30) || top < 0 ||
+      top > DFV_MAX_TOP || top > vocab || (n_rows > 1 && stride_row < vocab))
+    return DFV_ERR_INVALID;
+  if (n_rows == 0) return DFV_OK;
+  if (!logits || !aligned(logits, size) || (logprob && !tokens)) return DFV_ERR_INVALID;
+  if (top > 0 && !top_ids && !top_logprobs) return DFV_ERR_INVALID;
+  LogprobParams p = {vocab, top, logits, stride_row, tokens, logprob, entropy, top_ids,
+                     top_logprobs, status};
+  return logits_dtype == DFV_DTYPE_F32
+             ? logprob_launch<float>(p, n_rows, static_cast<cudaStream_t>(stream))
+             : logprob_launch<__nv_bfloat16>(p, n_rows, static_cast<cudaStream_t>(stream));
+}
