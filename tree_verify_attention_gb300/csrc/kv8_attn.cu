@@ -58,13 +58,17 @@ constexpr float kLn2F = 0.6931471805599453f;
 template <int D, int R>
 struct AttnShape {
   static constexpr int kHalves = D == 256 ? 2 : 1;      // 128-lane parts of V^T
+  static constexpr int kKSub = D / 64, kVSub = 2 * kHalves;   // 32-column parts of K^ and V^
   static constexpr int kRaw = kAtKeys * D;              // bytes of a chunk's K (V) codes
+  static constexpr int kRowB = D * 2 + 16;              // a staged bf16 row (padded: banks)
   static constexpr int kPBlk = (R + 63) / 64;
   static constexpr int kPBytes = kPBlk * kAtKeys * 128;
   static constexpr int kPBufs = R <= 64 || D < 256 ? 2 : 1;
   static constexpr int kStages = D == 256 ? 2 : 4;
   static constexpr int kQBytes = R * D * 2;
-  static constexpr int kOffQ = kStages * 2 * kRaw;
+  static constexpr int kRing = kStages * 2 * kRaw;
+  static constexpr int kRows = 2 * kAtKeys * kRowB;
+  static constexpr int kOffQ = ((kRing > kRows ? kRing : kRows) + 1023) / 1024 * 1024;
   static constexpr int kOffP = (kOffQ + kQBytes + 1023) / 1024 * 1024;
   static constexpr int kBytes = kOffP + kPBufs * kPBytes + 1024;
   // TMEM columns
@@ -73,24 +77,22 @@ struct AttnShape {
   static constexpr uint32_t kTS = kTV + 64 * kHalves;
   static constexpr uint32_t kTO = kTS + R;
   static_assert(kTO + R * kHalves <= 512, "TMEM columns");
-  static_assert(kBytes <= 227 * 1024, "shared memory");
+  static_assert(kBytes <= 219 * 1024, "shared memory");
 };
 
 struct AttnParams {
   dfv_kv8_cache c;
   int nblk;
   int n_nodes, max_depth, hq, group, window;
-  int tiles, rows_tile, rows, splits;   // rows: of one KV head
+  uint32_t group_m;                 // ceil(2^32 / group): r / group = umulhi(r, group_m)
+  int rows_tile, rows;              // query rows of a tile, of a KV head
   const __nv_bfloat16* q;
   const __nv_bfloat16* tree_k;
   const __nv_bfloat16* tree_v;
   const int32_t* parent;
   float scale;
-  void* out;
-  int out_bf16;
-  float* lse;
-  float* part_o;     // [split][node][query head][D], normalised (splits > 1)
-  float* part_lse;   // [split][node][query head], base 2
+  float* part_o;     // [head][tile][split][R][D], normalised
+  float* part_lse;   // [head][tile][split][R], base 2
   uint32_t* status;
 };
 
@@ -99,8 +101,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 // Bounded wait that also gives up when another role has.
-__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool role_wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead) {
   bool there = false;
   const bool ended = wait_bounded([&]() {
     there = mbar_try_wait(bar, parity);
@@ -108,6 +109,9 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volati
   });
   if (!ended) *dead = 1;
   return there;
+}
+__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  return mbar_try_wait(bar, parity) || role_wait_slow(bar, parity, dead);
 }
 
 // 16 codes as 8 words of binary16 pairs: 0x6400 | u is 1024 + u, and u = code + 128.
@@ -130,11 +134,22 @@ __device__ __forceinline__ float pow2i(int e) {   // e in [-126, 127]
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Byte offset of the 16-byte piece j (8 dims) of key k in a staged bf16-chunk
-// operand: consecutive keys are adjacent, and the exclusive or keeps both a
-// row's pieces and a dim's keys off one another's banks.
-__device__ __forceinline__ int stage_piece(int j, int k) {
-  return (j * kAtKeys + (k ^ (j & 7))) * 16;
+// A packed pair of bf16 values times f, as a pair of binary16 values.
+__device__ __forceinline__ uint32_t scaled_half2(uint32_t bf, float f) {
+  return pack_half2(__uint_as_float(bf << 16) * f, __uint_as_float(bf & 0xFFFF0000u) * f);
+}
+
+// Largest magnitude (bf16 bits) of a staged row of D values.
+template <int D>
+__device__ __forceinline__ uint32_t row_max(const uint8_t* row) {
+  uint32_t m = 0;
+#pragma unroll 8
+  for (int j = 0; j < D / 8; ++j) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + j * 16);
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                             __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  }
+  return max(m & 0xFFFFu, m >> 16);
 }
 
 template <int D, int R>
@@ -146,26 +161,36 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem + A::kOffQ;
   uint8_t* sP = smem + A::kOffP;
-  __shared__ uint64_t b_kfull[4], b_kfree[4], b_vfull[4], b_vfree[4];
-  __shared__ uint64_t b_khat, b_vhat, b_sfull, b_sfree, b_q, b_end, b_p[2], b_pv[2];
+  // raw codes landed / read (per stage); operand part written / read by the
+  // products; scores written / read; P written / read; bf16 rows landed
+  __shared__ uint64_t b_kraw[4], b_kdone[4], b_vraw[4], b_vdone[4];
+  __shared__ uint64_t b_khat[4], b_kfree[4], b_vhat[4], b_vfree[4];
+  __shared__ uint64_t b_sfull, b_sfree, b_q, b_end, b_krow, b_vrow, b_p[2], b_pv[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_dead;
   __shared__ int s_parent[kMaxNodes], s_maxdepth;
-  __shared__ uint32_t s_anc[kMaskWords][R];
-  __shared__ int s_lo[R], s_row[R];   // first visible position; row of the output
-  __shared__ __align__(16) float s_m[R], s_f[R];
+  // columns (of each half) that see a tree node; columns by depth, and up to a depth
+  __shared__ unsigned long long s_see[kMaxNodes][2], s_dep[kMaxNodes][2], s_upto[kMaxNodes][2];
+  __shared__ __align__(16) float s_m[R], s_f[R], s_zero[R];
   __shared__ float s_red[4][R];
-  __shared__ float s_ksc[kAtKeys];
-  __shared__ int s_vexp[kAtKeys];
-  __shared__ int s_badk[kAtKeys], s_badv[kAtKeys];
+  __shared__ float s_ksc[kAtKeys], s_vfac[kAtKeys];
+  __shared__ int s_vexp[kAtKeys], s_bad[2][kAtKeys];
   __shared__ uint32_t s_qmax;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_dep_launch_dependents();   // the merge may be set up meanwhile
-  const int split = blockIdx.x % p.splits, unit = blockIdx.x / p.splits;
-  const int tile = unit % p.tiles, h = unit / p.tiles;
-  const int row0 = tile * p.rows_tile, n_rows = min(p.rows_tile, p.rows - row0);
   int C = *p.c.state;
+  grid_dep_launch_dependents();   // the merge may be set up meanwhile
+  const int split = blockIdx.x, splits = gridDim.x, tile = blockIdx.y, h = blockIdx.z;
+  const int row0 = tile * p.rows_tile, n_rows = min(p.rows_tile, p.rows - row0);
+  for (int i = tid; i < p.n_nodes; i += kAtThreads) {
+    int pa = i == 0 ? -1 : p.parent[i];
+    if (i > 0 && (pa < 0 || pa >= i)) {
+      report(p.status, DFV_DEV_BAD_TREE);
+      pa = 0;
+    }
+    s_parent[i] = pa;
+    s_see[i][0] = s_see[i][1] = s_dep[i][0] = s_dep[i][1] = 0;
+  }
   if (C < 0 || C > p.c.capacity) {
     if (tid == 0) report(p.status, DFV_DEV_CTX);
     C = max(0, min(C, p.c.capacity));
@@ -175,42 +200,95 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const int lo_min = p.window > 0 ? max(0, C - p.window + 1) : 0;
   const int fb = min(lo_min / kBlk, open);
   const int nq = (open - fb + 1) / 2, nch = nq + 1;
-  const int c0 = static_cast<int>(static_cast<int64_t>(nch) * split / p.splits);
-  const int c1 = static_cast<int>(static_cast<int64_t>(nch) * (split + 1) / p.splits);
+  const int per = nch / splits, rem = nch - per * splits;
+  const int c0 = split * per + split * rem / splits;
+  const int c1 = (split + 1) * per + (split + 1) * rem / splits;
   const int n = c1 - c0;
   const bool has_tree = c1 == nch && n > 0;     // its last chunk is the bf16 one
   const int n8 = n - (has_tree ? 1 : 0);
+  const int live_rows = T + p.n_nodes;          // keys of the bf16 chunk
 
+  // raw codes of chunk i into its stage (one thread)
+  auto copy_codes = [&](int i) {
+    const int s = i % A::kStages, b = fb + 2 * (c0 + i);
+    const uint32_t bytes = static_cast<uint32_t>(min(2, open - b) * kBlk * D);
+    const int64_t off = (static_cast<int64_t>(h) * p.nblk + b) * kBlk * D;
+    uint8_t* raw = smem + s * 2 * A::kRaw;
+    mbar_arrive_expect_tx(&b_kraw[s], bytes);
+    bulk_g2s(raw, p.c.k_codes + off, bytes, &b_kraw[s]);
+    mbar_arrive_expect_tx(&b_vraw[s], bytes);
+    bulk_g2s(raw + A::kRaw, p.c.v_codes + off, bytes, &b_vraw[s]);
+  };
+  // rows of the bf16 chunk over the ring (one warp)
+  auto copy_rows = [&]() {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&b_krow, static_cast<uint32_t>(live_rows * D * 2));
+      mbar_arrive_expect_tx(&b_vrow, static_cast<uint32_t>(live_rows * D * 2));
+    }
+    __syncwarp();
+    const int64_t t0 = (static_cast<int64_t>(h) * 2 + (open & 1)) * kBlk * D;
+    for (int k = lane; k < live_rows; k += 32) {
+      const int64_t n0 = (static_cast<int64_t>(k - T) * p.c.n_kv_heads + h) * D;
+      const __nv_bfloat16* ks = k < T ? static_cast<const __nv_bfloat16*>(p.c.k_tail) + t0 + k * D
+                                      : p.tree_k + n0;
+      const __nv_bfloat16* vs = k < T ? static_cast<const __nv_bfloat16*>(p.c.v_tail) + t0 + k * D
+                                      : p.tree_v + n0;
+      bulk_g2s(smem + k * A::kRowB, ks, D * 2, &b_krow);
+      bulk_g2s(smem + (kAtKeys + k) * A::kRowB, vs, D * 2, &b_vrow);
+    }
+  };
+
+  const int first_copies = min(n8, A::kStages);
+  if (warp == 17) {   // the first copies wait for nothing
+    if (lane == 0) {
+      for (int s = 0; s < 4; ++s) {
+        mbar_init(&b_kraw[s], 1);
+        mbar_init(&b_vraw[s], 1);
+        mbar_init(&b_kdone[s], 4);
+        mbar_init(&b_vdone[s], 4);
+        mbar_init(&b_khat[s], 4);
+        mbar_init(&b_vhat[s], 4);
+        mbar_init(&b_kfree[s], 1);
+        mbar_init(&b_vfree[s], 1);
+      }
+      mbar_init(&b_sfull, 1);
+      mbar_init(&b_sfree, 8);
+      mbar_init(&b_q, 8);
+      mbar_init(&b_end, 1);
+      mbar_init(&b_krow, 1);
+      mbar_init(&b_vrow, 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&b_p[k], 8);
+        mbar_init(&b_pv[k], 1);
+      }
+      fence_mbar_init();
+      for (int i = 0; i < first_copies; ++i) copy_codes(i);
+    }
+    __syncwarp();
+    if (has_tree && n8 == 0) copy_rows();
+  } else if (warp == 16) {
+    tc::tmem_alloc(&s_tmem, 512);
+  }
   if (tid == 0) {
     s_dead = 0;
     s_qmax = 0;
     s_maxdepth = 0;
-    for (int s = 0; s < A::kStages; ++s) {
-      mbar_init(&b_kfull[s], 1);
-      mbar_init(&b_vfull[s], 1);
-      mbar_init(&b_kfree[s], 4);
-      mbar_init(&b_vfree[s], 4);
-    }
-    mbar_init(&b_khat, 4);
-    mbar_init(&b_vhat, 4);
-    mbar_init(&b_sfull, 1);
-    mbar_init(&b_sfree, 8);
-    mbar_init(&b_q, 8);
-    mbar_init(&b_end, 1);
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(&b_p[k], 8);
-      mbar_init(&b_pv[k], 1);
-    }
-    fence_mbar_init();
   }
-  if (warp == 16) tc::tmem_alloc(&s_tmem, 512);
-  for (int i = tid; i < p.n_nodes; i += kAtThreads) {
-    int pa = i == 0 ? -1 : p.parent[i];
-    if (i > 0 && (pa < 0 || pa >= i)) {
-      report(p.status, DFV_DEV_BAD_TREE);
-      pa = 0;
+  // Q rows of the tile, into registers meanwhile (softmax warps)
+  constexpr int kQSteps = (R * D / 8 + 255) / 256;
+  uint4 qv[kQSteps];
+  uint32_t qm = 0;
+  if (warp < 8) {
+#pragma unroll
+    for (int k = 0; k < kQSteps; ++k) {
+      const int it = tid + k * 256, r = it / (D / 8), j = it % (D / 8);
+      qv[k] = make_uint4(0, 0, 0, 0);
+      if (r < n_rows) {
+        const int node = static_cast<int>(p.group == 1 ? row0 + r : __umulhi(row0 + r, p.group_m));
+        const int row = node * p.hq + h * p.group + (row0 + r - node * p.group);
+        qv[k] = *reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(row) * D + j * 8);
+      }
     }
-    s_parent[i] = pa;
   }
   __syncthreads();
   tc::fence_after_sync();
@@ -219,30 +297,35 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
   if (warp == 17) {
     // ------------------------------------------------------ bulk copies
-    if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < n8; ++i) {
-        const int s = i % A::kStages, use = i / A::kStages;
-        if (use > 0 && (!role_wait(&b_kfree[s], (use - 1) & 1, &s_dead) ||
-                        !role_wait(&b_vfree[s], (use - 1) & 1, &s_dead)))
-          break;
-        const int b = fb + 2 * (c0 + i);
-        const uint32_t bytes = static_cast<uint32_t>(min(2, open - b) * kBlk * D);
-        const int64_t off = (static_cast<int64_t>(h) * p.nblk + b) * kBlk * D;
-        uint8_t* raw = smem + s * 2 * A::kRaw;
-        mbar_arrive_expect_tx(&b_kfull[s], bytes);
-        bulk_g2s(raw, p.c.k_codes + off, bytes, &b_kfull[s]);
-        mbar_arrive_expect_tx(&b_vfull[s], bytes);
-        bulk_g2s(raw + A::kRaw, p.c.v_codes + off, bytes, &b_vfull[s]);
-        issued = i + 1;
-      }
-      // copies that nobody will wait for any more must still land
-      for (int i = max(0, issued - A::kStages); i < issued; ++i) {
+    bool ok = true;
+    int issued = first_copies;
+    for (int i = first_copies; ok && i < n8; ++i) {
+      const int s = i % A::kStages;
+      const uint32_t ph = (i / A::kStages - 1) & 1;
+      ok = role_wait(&b_kdone[s], ph, &s_dead) && role_wait(&b_vdone[s], ph, &s_dead);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      if (lane == 0) copy_codes(i);
+      issued = i + 1;
+    }
+    if (has_tree && n8 > 0) {
+      for (int i = max(0, n8 - A::kStages); ok && i < n8; ++i) {   // the ring has been read
         const uint32_t ph = (i / A::kStages) & 1;
-        if (s_dead) {
-          mbar_wait_bounded(&b_kfull[i % A::kStages], ph);
-          mbar_wait_bounded(&b_vfull[i % A::kStages], ph);
-        }
+        ok = role_wait(&b_kdone[i % A::kStages], ph, &s_dead) &&
+             role_wait(&b_vdone[i % A::kStages], ph, &s_dead);
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (ok) copy_rows();
+    }
+    // copies that nobody waits for any more must still land
+    if (s_dead) {
+      for (int i = max(0, issued - A::kStages); i < issued; ++i) {
+        mbar_wait_bounded(&b_kraw[i % A::kStages], (i / A::kStages) & 1);
+        mbar_wait_bounded(&b_vraw[i % A::kStages], (i / A::kStages) & 1);
+      }
+      if (has_tree && ok) {
+        mbar_wait_bounded(&b_krow, 0);
+        mbar_wait_bounded(&b_vrow, 0);
       }
     }
   } else if (warp == 16) {
@@ -251,15 +334,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       constexpr uint32_t id_s = tc::idesc_f16(128, R);
       constexpr uint32_t id_o = tc::idesc_f16(128, R, true);
       const uint64_t qd = tc::smem_desc_sw128(smem_u32(sQ), 1024);
+      // S^T of chunk i, part by part as K^ arrives (64 dims each)
       auto issue_s = [&](int i) {
-        if (!role_wait(&b_khat, i & 1, &s_dead)) return false;
         if (i > 0 && !role_wait(&b_sfree, (i - 1) & 1, &s_dead)) return false;
-        tc::fence_after_sync();
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_f16_ts(tmem + A::kTS, tmem + A::kTK + kk * 8,
-                         qd + static_cast<uint64_t>(((kk >> 2) * R * 128 + (kk & 3) * 32) >> 4),
-                         id_s, kk > 0 ? 1u : 0u);
+        for (int c = 0; c < A::kKSub; ++c) {
+          if (!role_wait(&b_khat[c], i & 1, &s_dead)) return false;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_f16_ts(tmem + A::kTS, tmem + A::kTK + c * 32 + kk * 8,
+                           qd + static_cast<uint64_t>((c * R * 128 + kk * 32) >> 4), id_s,
+                           c + kk > 0 ? 1u : 0u);
+          tc::commit(&b_kfree[c]);
+        }
         tc::commit(&b_sfull);
         return true;
       };
@@ -267,20 +355,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       for (int i = 0; ok && i < n; ++i) {
         if (i + 1 < n) ok = issue_s(i + 1);
         const int pb = i & 1;
-        ok = ok && role_wait(&b_vhat, i & 1, &s_dead) &&
-             role_wait(&b_p[pb], (i >> 1) & 1, &s_dead);
-        if (!ok) break;
-        tc::fence_after_sync();
+        ok = ok && role_wait(&b_p[pb], (i >> 1) & 1, &s_dead);
         const uint64_t pd = tc::smem_desc_sw128_mn(
             smem_u32(sP + (A::kPBufs == 2 ? pb : 0) * A::kPBytes), kAtKeys * 128, 1024);
+        // O^T: parts (half of the dims, block of 64 keys)
 #pragma unroll
-        for (int hh = 0; hh < A::kHalves; ++hh)
+        for (int c = 0; c < A::kVSub; ++c) {
+          ok = ok && role_wait(&b_vhat[c], i & 1, &s_dead);
+          if (!ok) break;
+          tc::fence_after_sync();
 #pragma unroll
-          for (int kk = 0; kk < kAtKeys / 16; ++kk)
-            tc::mma_f16_ts(tmem + A::kTO + hh * R, tmem + A::kTV + hh * 64 + kk * 8,
-                           pd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_o,
-                           i > 0 || kk > 0 ? 1u : 0u);
-        tc::commit(&b_pv[pb]);
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_f16_ts(tmem + A::kTO + (c >> 1) * R, tmem + A::kTV + c * 32 + kk * 8,
+                           pd + static_cast<uint64_t>((((c & 1) * 4 + kk) * 16 * 128) >> 4), id_o,
+                           i > 0 || (c & 1) + kk > 0 ? 1u : 0u);
+          tc::commit(&b_vfree[c]);
+        }
+        if (ok) tc::commit(&b_pv[pb]);
       }
       if (!ok) {
         s_dead = 1;
@@ -290,154 +381,113 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       }
     }
   } else if (warp >= 8) {
-    // ------------------------------------------------------ codes to TMEM
+    // ------------------------------------------------------ operands to TMEM
     const bool is_v = warp >= 12;
     const int slot = (warp & 3) * 32 + lane;   // key (K) or dim of a half (V)
-    uint64_t* full = is_v ? b_vfull : b_kfull;
-    uint64_t* free_ = is_v ? b_vfree : b_kfree;
+    uint64_t* raw_full = is_v ? b_vraw : b_kraw;
+    uint64_t* raw_done = is_v ? b_vdone : b_kdone;
+    uint64_t* hat = is_v ? b_vhat : b_khat;
+    uint64_t* hat_free = is_v ? b_vfree : b_kfree;
+    const uint32_t t_op = tmem + lanes + (is_v ? A::kTV : A::kTK);
+    const int subs = is_v ? A::kVSub : A::kKSub;
+    const bool works = !is_v || D >= 128 || slot < D;   // D = 64: V^T has 64 lanes
+    // the bytes of one part, for this thread: K 64 dims of its key (pieces
+    // 64 * 16 apart), V 64 keys of its dim (pieces D * 16 apart)
+    const int base0 = is_v ? A::kRaw + slot * 16 : (slot >> 6) * kBlk * D + (slot & 63) * 16;
+    const int step = is_v ? D * 16 : kBlk * 16;
     bool ok = true;
-    // the operand's columns are free once the products that read them end
-    auto operand_free = [&](int i) {
-      if (i == 0) return true;
-      return is_v ? role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead)
-                  : role_wait(&b_sfull, (i - 1) & 1, &s_dead);
-    };
-    for (int i = 0; ok && i < n8; ++i) {
-      const int s = i % A::kStages;
-      const uint8_t* raw = smem + s * 2 * A::kRaw + (is_v ? A::kRaw : 0);
-      ok = role_wait(&full[s], (i / A::kStages) & 1, &s_dead) && operand_free(i);
+    // part c of chunk i, converted and waiting in registers, into TMEM
+    auto put = [&](int i, int c, const uint32_t* w) {
+      if (i > 0) ok = role_wait(&hat_free[c], (i - 1) & 1, &s_dead);
       ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
+      if (!ok) return;
       tc::fence_after_sync();
-      if (!is_v) {
-        const uint8_t* mine = raw + (slot >> 6) * kBlk * D + (slot & 63) * 16;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t w[32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            codes_to_half(*reinterpret_cast<const uint4*>(mine + (c * 4 + j) * kBlk * 16), w + 8 * j);
-          tc::TmemIo<32>::store(tmem + lanes + A::kTK + c * 32, w);
-        }
-      } else if (D >= 128 || slot < D) {   // whole warps
-#pragma unroll
-        for (int hh = 0; hh < A::kHalves; ++hh)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {    // the chunk's blocks
-            const uint8_t* mine = raw + c * kBlk * D + (hh * 128 + slot) * 16;
-            uint32_t w[32];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              codes_to_half(*reinterpret_cast<const uint4*>(mine + j * D * 16), w + 8 * j);
-            tc::TmemIo<32>::store(tmem + lanes + A::kTV + hh * 64 + c * 32, w);
-          }
-      }
+      if (works) tc::TmemIo<32>::store(t_op + c * 32, w);
       tc::store_wait();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&free_[s]);
-        mbar_arrive(is_v ? &b_vhat : &b_khat);
+      if (lane == 0) mbar_arrive(&hat[c]);
+    };
+    for (int i = 0; ok && i < n8; ++i) {
+      const int s = i % A::kStages;
+      ok = role_wait(&raw_full[s], (i / A::kStages) & 1, &s_dead);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      const uint8_t* raw = smem + s * 2 * A::kRaw + base0;
+#pragma unroll 1
+      for (int c = 0; c < subs; ++c) {
+        // V part (half, block): dims 128 on, keys of the second block
+        const uint8_t* mine = raw + (is_v ? (c >> 1) * 128 * 16 + (c & 1) * kBlk * D
+                                          : c * 4 * kBlk * 16);
+        uint32_t w[32];
+        if (works) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            codes_to_half(*reinterpret_cast<const uint4*>(mine + j * step), w + 8 * j);
+        }
+        if (c == subs - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_done[s]);
+        }
+        put(i, c, w);
+        if (!ok) break;
       }
     }
     if (has_tree) {
       // The bf16 chunk: key slots [0, T) are the open block's rows, then the
-      // tree nodes. Rows are read whole, scaled to binary16 by a power of two
-      // (largest magnitude in [64, 128)) and staged over the raw codes, K
-      // over the first stage and V over the second.
-      ok = named_sync_and(1, 256, ok);   // all earlier codes have been read
-      constexpr int LPK = D / 8, KPI = 32 / LPK;   // lanes per key, keys per step
-      constexpr int NS = 32 / KPI;                 // steps for the warp's 32 keys
-      constexpr int NB = NS < 16 ? NS : 16;        // loads in flight
-      uint8_t* stage = smem + (is_v ? 2 * A::kRaw : 0);
-      const int j = lane % LPK;
+      // tree nodes. Each key is scaled to binary16 by a power of two (largest
+      // magnitude in [64, 128)).
+      ok = ok && role_wait(is_v ? &b_vrow : &b_krow, 0, &s_dead);
+      ok = named_sync_and(is_v ? 3 : 2, 128, ok);
       if (ok) {
-#pragma unroll 1
-        for (int st = 0; st < NS; st += NB) {
-          uint4 v[NB];
-#pragma unroll
-          for (int u = 0; u < NB; ++u) {
-            const int k = (warp & 3) * 32 + (st + u) * KPI + lane / LPK;
-            const __nv_bfloat16* src = nullptr;
-            if (k < T)
-              src = static_cast<const __nv_bfloat16*>(is_v ? p.c.v_tail : p.c.k_tail) +
-                    ((static_cast<int64_t>(h) * 2 + (open & 1)) * kBlk + k) * D;
-            else if (k < T + p.n_nodes)
-              src = (is_v ? p.tree_v : p.tree_k) +
-                    (static_cast<int64_t>(k - T) * p.c.n_kv_heads + h) * D;
-            v[u] = src ? *reinterpret_cast<const uint4*>(src + j * 8) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int u = 0; u < NB; ++u) {
-            const int k = (warp & 3) * 32 + (st + u) * KPI + lane / LPK;
-            uint32_t in[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-            uint32_t m = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m = __vmaxu2(m, in[e] & 0x7FFF7FFFu);
-            m = max(m & 0xFFFFu, m >> 16);
-#pragma unroll
-            for (int o = LPK / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const bool bad = m >= kBigBits;   // infinite, NaN or out of range
-            const int e = max(static_cast<int>(m >> 7), 86);
-            const float f = bad ? 0.0f : pow2i(133 - e);
-            uint32_t o[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              o[q] = bad ? 0u
-                         : pack_half2(__uint_as_float(in[q] << 16) * f,
-                                      __uint_as_float(in[q] & 0xFFFF0000u) * f);
-            *reinterpret_cast<uint4*>(stage + stage_piece(j, k)) = make_uint4(o[0], o[1], o[2], o[3]);
-            if (j == 0) {
-              if (is_v) {
-                s_vexp[k] = bad ? 0 : e - 133;
-                s_badv[k] = bad;
-              } else {
-                s_ksc[k] = bad ? 0.0f : pow2i(e - 133);
-                s_badk[k] = bad;
-              }
-            }
-            if (bad && k < T + p.n_nodes && j == 0) report(p.status, DFV_DEV_NONFINITE);
-          }
-        }
-      }
-      ok = ok && operand_free(n8);
-      ok = named_sync_and(is_v ? 3 : 2, 128, ok);   // this operand's rows are staged
-      if (ok) {
-        tc::fence_after_sync();
+        uint8_t* rows = smem + (is_v ? kAtKeys * A::kRowB : 0);
+        uint8_t* row = rows + slot * A::kRowB;
+        const bool live = slot < live_rows;
+        const uint32_t m = live ? row_max<D>(row) : 0u;
+        const bool bad = m >= kBigBits;   // infinite, NaN or out of range
+        const int e = max(static_cast<int>(m >> 7), 86);
+        const float f = bad || !live ? 0.0f : pow2i(133 - e);
+        s_bad[is_v][slot] = bad;
+        if (bad) report(p.status, DFV_DEV_NONFINITE);
         if (!is_v) {
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t w[32];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const uint4 x = *reinterpret_cast<const uint4*>(stage + stage_piece(c * 8 + q, slot));
-              w[4 * q] = x.x;
-              w[4 * q + 1] = x.y;
-              w[4 * q + 2] = x.z;
-              w[4 * q + 3] = x.w;
-            }
-            tc::TmemIo<32>::store(tmem + lanes + A::kTK + c * 32, w);
-          }
-        } else if (D >= 128 || slot < D) {
+          s_ksc[slot] = bad ? 0.0f : pow2i(e - 133);
+        } else {
+          s_vexp[slot] = bad ? 0 : e - 133;
+          s_vfac[slot] = f;
+        }
+        if (bad || !live) {   // no 0 * inf below
 #pragma unroll 1
-          for (int hc = 0; hc < 2 * A::kHalves; ++hc) {
-            const int d = (hc >> 1) * 128 + slot, kb = (hc & 1) * 64;
-            uint32_t w[32];
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<uint4*>(row + j * 16) = make_uint4(0, 0, 0, 0);
+        }
+        if (is_v) named_sync(3, 128);
+#pragma unroll 1
+        for (int c = 0; c < subs; ++c) {
+          uint32_t w[32];
+          if (!is_v) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint4 x = *reinterpret_cast<const uint4*>(row + (c * 8 + j) * 16);
+              w[4 * j] = scaled_half2(x.x, f);
+              w[4 * j + 1] = scaled_half2(x.y, f);
+              w[4 * j + 2] = scaled_half2(x.z, f);
+              w[4 * j + 3] = scaled_half2(x.w, f);
+            }
+          } else if (works) {
+            const int d = (c >> 1) * 128 + slot, kb = (c & 1) * 64;
+            const uint8_t* col = rows + kb * A::kRowB + d * 2;
+            const float2* fac = reinterpret_cast<const float2*>(s_vfac + kb);
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
-              const uint16_t a = *reinterpret_cast<const uint16_t*>(
-                  stage + stage_piece(d >> 3, kb + 2 * q) + (d & 7) * 2);
-              const uint16_t b = *reinterpret_cast<const uint16_t*>(
-                  stage + stage_piece(d >> 3, kb + 2 * q + 1) + (d & 7) * 2);
-              w[q] = a | (static_cast<uint32_t>(b) << 16);
+              const uint32_t a = *reinterpret_cast<const uint16_t*>(col + 2 * q * A::kRowB);
+              const uint32_t b = *reinterpret_cast<const uint16_t*>(col + (2 * q + 1) * A::kRowB);
+              const float2 g = fac[q];
+              w[q] = pack_half2(__uint_as_float(a << 16) * g.x, __uint_as_float(b << 16) * g.y);
             }
-            tc::TmemIo<32>::store(tmem + lanes + A::kTV + (hc >> 1) * 64 + (hc & 1) * 32, w);
           }
+          put(n8, c, w);
+          if (!ok) break;
         }
-        tc::store_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(is_v ? &b_vhat : &b_khat);
       }
     }
   } else {
@@ -445,190 +495,183 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int cg = warp >> 2;                  // column half
     const int key = (warp & 3) * 32 + lane;
     bool ok = true;
-    // Q rows of the tile, scaled so that the largest magnitude is in [2^14, 2^15)
-    constexpr int kQSteps = (R * D / 8 + 255) / 256;
-    float qs;
-    {
-      uint4 v[kQSteps];
-      uint32_t m = 0;
+    // Q scaled so that the tile's largest magnitude is in [2^14, 2^15)
 #pragma unroll
-      for (int k = 0; k < kQSteps; ++k) {
-        const int it = tid + k * 256, r = it / (D / 8), j = it % (D / 8);
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (r < n_rows) {
-          const int g = (row0 + r) % p.group, node = (row0 + r) / p.group;
-          v[k] = *reinterpret_cast<const uint4*>(
-              p.q + (static_cast<int64_t>(node) * p.hq + h * p.group + g) * D + j * 8);
-        }
-        const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    for (int k = 0; k < kQSteps; ++k) {
+      const uint32_t in[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t lo = in[e] & 0x7FFFu, hi = (in[e] >> 16) & 0x7FFFu;
-          if (lo < 0x7F80u) m = max(m, lo);   // infinities and NaN stay in their row
-          if (hi < 0x7F80u) m = max(m, hi);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = in[e] & 0x7FFFu, hi = (in[e] >> 16) & 0x7FFFu;
+        if (lo < 0x7F80u) qm = max(qm, lo);   // infinities and NaN stay in their row
+        if (hi < 0x7F80u) qm = max(qm, hi);
       }
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
-      if (lane == 0) atomicMax(&s_qmax, m);
-      named_sync(4, 256);
-      const int e = max(static_cast<int>(s_qmax >> 7), 20);
-      const float f = pow2i(min(141 - e, 126));
-      qs = pow2i(max(e - 141, -126));
-#pragma unroll
-      for (int k = 0; k < kQSteps; ++k) {
-        const int it = tid + k * 256, r = it / (D / 8), j = it % (D / 8);
-        if (r >= R) continue;
-        const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          o[q] = pack_half2(__uint_as_float(in[q] << 16) * f,
-                            __uint_as_float(in[q] & 0xFFFF0000u) * f);
-        *reinterpret_cast<uint4*>(sQ + tc::sw128_offset(r, j, R)) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b_q);
     }
-    // columns: what each row sees of the tree and of the window
+    qm = __reduce_max_sync(0xFFFFFFFFu, qm);
+    if (lane == 0) atomicMax(&s_qmax, qm);
+    // columns: what each row sees of the tree, and its depth
     if (tid < R) {
-      uint32_t a[kMaskWords] = {};
-      int depth = 0, node;
       if (tid < n_rows) {
-        node = (row0 + tid) / p.group;
-        s_row[tid] = node * p.hq + h * p.group + (row0 + tid) % p.group;
-        for (int x = node; x >= 0; x = s_parent[x]) {
-#pragma unroll
-          for (int w = 0; w < kMaskWords; ++w)
-            if ((x >> 5) == w) a[w] |= 1u << (x & 31);
+        const int half = tid / HC;
+        const unsigned long long bit = 1ull << (tid - half * HC);
+        int depth = -1;
+        for (int x = p.group == 1 ? row0 + tid : static_cast<int>(__umulhi(row0 + tid, p.group_m));
+             x >= 0; x = s_parent[x]) {
+          atomicOr(&s_see[x][half], bit);
           ++depth;
         }
-        --depth;
         if (depth > p.max_depth) report(p.status, DFV_DEV_DEPTH);
+        atomicOr(&s_dep[depth][half], bit);
         atomicMax(&s_maxdepth, depth);
       }
-#pragma unroll
-      for (int w = 0; w < kMaskWords; ++w) s_anc[w][tid] = a[w];
-      s_lo[tid] = p.window > 0 ? C + depth - p.window + 1 : INT32_MIN;
       s_m[tid] = kNoRef;
+      s_zero[tid] = 0.0f;
     }
     named_sync(4, 256);
-    const int lo_all = p.window > 0 ? C + s_maxdepth - p.window + 1 : INT32_MIN;
-    const float sc = p.scale * kLog2eF * qs;
+    const int qe = max(static_cast<int>(s_qmax >> 7), 20);
+    const float qf = pow2i(min(141 - qe, 126));
+#pragma unroll
+    for (int k = 0; k < kQSteps; ++k) {
+      const int it = tid + k * 256, r = it / (D / 8), j = it % (D / 8);
+      if (r < R)
+        *reinterpret_cast<uint4*>(sQ + tc::sw128_offset(r, j, R)) =
+            make_uint4(scaled_half2(qv[k].x, qf), scaled_half2(qv[k].y, qf),
+                       scaled_half2(qv[k].z, qf), scaled_half2(qv[k].w, qf));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b_q);
+    const int maxdepth = s_maxdepth;
+    for (int k = tid; k < 2 * (maxdepth + 1); k += 256) {
+      unsigned long long m = 0;
+      for (int x = 0; x <= k >> 1; ++x) m |= s_dep[x][k & 1];
+      s_upto[k >> 1][k & 1] = m;
+    }
+    named_sync(4, 256);
+    const int lo_all = p.window > 0 ? C + maxdepth - p.window + 1 : INT32_MIN;
+    const float sc = p.scale * kLog2eF * pow2i(max(qe - 141, -126));
     float l[HC];
 #pragma unroll
     for (int c = 0; c < HC; ++c) l[c] = 0.0f;
     const uint32_t t_s = tmem + lanes + A::kTS + cg * HC;
     const uint32_t t_o = tmem + lanes + A::kTO + cg * HC;
     const float4* m4 = reinterpret_cast<const float4*>(s_m + cg * HC);
+    const float4* zero4 = reinterpret_cast<const float4*>(s_zero + cg * HC);
 
     for (int i = 0; i < n; ++i) {
       // this lane's key
       const bool bf = has_tree && i == n - 1;
       const int b = fb + 2 * (c0 + i);
       float a = 0.0f, lv = 0.0f, iv = 0.0f;
-      int pos;
-      bool live;
-      if (!bf) {
-        const int kb = b + (key >> 6);
-        live = kb < open;
-        pos = kb * kBlk + (key & 63);
-        if (live) {
+      unsigned long long vis = ~0ull;   // columns that see it
+      bool bad = false;
+      const bool masked = bf || b + 2 > open || b * kBlk < lo_all;
+      {
+        const int kb = bf ? open + (key >= T) : b + (key >> 6);
+        const int pos = bf ? open * kBlk + key : kb * kBlk + (key & 63);
+        const bool live = bf ? key < live_rows : kb < open;
+        if (live && !bf) {
           const int64_t at = static_cast<int64_t>(h) * p.nblk + kb;
           a = __ldg(p.c.k_scale + at) * sc;
           const float sv = fmaxf(__ldg(p.c.v_scale + at), 7.1054274e-15f);   // 2^-47
           lv = log2f(sv);
           iv = __fdividef(1.0f, sv);
         }
-      } else {
-        live = key < T + p.n_nodes;
-        pos = key < T ? open * kBlk + key : INT32_MAX;
+        if (masked) {
+          if (!live) vis = 0;
+          else if (bf && key >= T) vis = s_see[key - T][cg];
+          else if (p.window > 0) {
+            const int dd = pos - C + p.window - 1;   // deepest node that sees it
+            vis = dd < 0 ? 0ull : s_upto[min(dd, maxdepth)][cg];
+          }
+        }
       }
       ok = ok && role_wait(&b_sfull, i & 1, &s_dead);
-      ok = __all_sync(0xFFFFFFFFu, ok);   // the TMEM loads are warp-wide
-      tc::fence_after_sync();
-      bool bad = false;
       if (bf) {   // the key's scales were written with the operands
-        ok = ok && role_wait(&b_khat, i & 1, &s_dead) && role_wait(&b_vhat, i & 1, &s_dead);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok && live) {
+        ok = ok && role_wait(&b_khat[A::kKSub - 1], i & 1, &s_dead) &&
+             role_wait(&b_vhat[0], i & 1, &s_dead);
+        if (ok && key < live_rows) {
           a = s_ksc[key] * sc;
           lv = static_cast<float>(s_vexp[key]);
           iv = pow2i(-s_vexp[key]);
-          bad = s_badk[key] || s_badv[key];
+          bad = s_bad[0][key] || s_bad[1][key];
         }
       }
+      ok = __all_sync(0xFFFFFFFFu, ok);   // the TMEM loads are warp-wide
+      tc::fence_after_sync();
       float x[HC];
-      if (ok) tc::TmemIo<HC>::load(t_s, reinterpret_cast<uint32_t*>(x));
-      const bool masked = bf || b + 2 > open || b * kBlk < lo_all;
-      // keys this lane's column may not see
-      auto mask = [&]() {
-        if (!masked) return;
-        const int t = key - T;   // tree node of the slot
-#pragma unroll
-        for (int c = 0; c < HC; ++c) {
-          bool see = live && pos >= s_lo[cg * HC + c];
-          if (bf && t >= 0) see = live && ((s_anc[t >> 5][cg * HC + c] >> (t & 31)) & 1u);
-          if (!see) x[c] = -INFINITY;
+      // Exponents against the references (pass 0). Where one is too large, and
+      // in the first chunk: scores alone, columns' maxima, new references
+      // (pass 1), and the exponents again (pass 2).
+      bool alive = true;
+#pragma unroll 1
+      for (int pass = i == 0 ? 1 : 0; pass < 3; ++pass) {
+        if (pass == 1) {   // a wait gave up somewhere in the group?
+          ok = named_sync_and(5 + cg, 128, ok);
+          if (!ok) {
+            alive = false;
+            break;
+          }
         }
-      };
-      auto exponents = [&]() {
-        float top = -INFINITY;
+        if (ok) tc::TmemIo<HC>::load(t_s, reinterpret_cast<uint32_t*>(x));
+        const float4* ref = pass == 1 ? zero4 : m4;
 #pragma unroll
         for (int c = 0; c < HC; c += 4) {
-          const float4 m = m4[c / 4];
+          const float4 m = ref[c / 4];
           x[c] = fmaf(x[c], a, lv - m.x);
           x[c + 1] = fmaf(x[c + 1], a, lv - m.y);
           x[c + 2] = fmaf(x[c + 2], a, lv - m.z);
           x[c + 3] = fmaf(x[c + 3], a, lv - m.w);
         }
-        mask();
+        if (masked) {
+          const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
-        for (int c = 0; c < HC; ++c) top = fmaxf(top, x[c]);
-        return top;
-      };
-      if (!named_sync_and(5 + cg, 128, !(exponents() > kRaise) && ok)) {
-        // some column outgrew its reference (or a wait gave up)
-        if (!named_sync_and(5 + cg, 128, ok)) break;
-        tc::TmemIo<HC>::load(t_s, reinterpret_cast<uint32_t*>(x));
-#pragma unroll
-        for (int c = 0; c < HC; ++c) x[c] = fmaf(x[c], a, lv);
-        mask();
-#pragma unroll
-        for (int c = 0; c < HC; ++c) {
-          float m;
-          asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x[c]));
-          if (lane == 0) s_red[warp & 3][cg * HC + c] = m;
+          for (int c = 0; c < HC; ++c)
+            if (!((c < 32 ? v0 : v1) & (1u << (c & 31)))) x[c] = -INFINITY;
         }
-        named_sync(5 + cg, 128);
-        if ((warp & 3) == 0) {
-          for (int c = cg * HC + lane; c < (cg + 1) * HC; c += 32) {
-            const float was = s_m[c];
-            const float m = fmaxf(fmaxf(fmaxf(s_red[0][c], s_red[1][c]),
-                                        fmaxf(s_red[2][c], s_red[3][c])), was);
-            s_m[c] = m;
-            s_f[c] = tc::ex2(was - m);
+        if (pass == 0) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < HC; ++c) top = fmaxf(top, x[c]);
+          if (named_sync_and(5 + cg, 128, ok && !(top > kRaise))) break;
+        } else if (pass == 1) {
+#pragma unroll
+          for (int c = 0; c < HC; ++c) {
+            float m;
+            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x[c]));
+            if (lane == 0) s_red[warp & 3][cg * HC + c] = m;
+          }
+          named_sync(5 + cg, 128);
+          if ((warp & 3) == 0) {
+            for (int c = cg * HC + lane; c < (cg + 1) * HC; c += 32) {
+              const float was = s_m[c];
+              const float m = fmaxf(fmaxf(fmaxf(s_red[0][c], s_red[1][c]),
+                                          fmaxf(s_red[2][c], s_red[3][c])), was);
+              s_m[c] = m;
+              s_f[c] = tc::ex2(was - m);
+            }
+          }
+          if (i > 0) ok = role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead);
+          ok = named_sync_and(5 + cg, 128, ok);
+          if (!ok) {
+            alive = false;
+            break;
+          }
+          if (i > 0) {
+            tc::fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < HC; ++c) l[c] *= s_f[cg * HC + c];
+#pragma unroll 1
+            for (int hh = 0; hh < A::kHalves; ++hh) {
+              tc::TmemIo<HC>::load(t_o + hh * R, reinterpret_cast<uint32_t*>(x));
+#pragma unroll
+              for (int c = 0; c < HC; ++c) x[c] *= s_f[cg * HC + c];
+              tc::TmemIo<HC>::store(t_o + hh * R, reinterpret_cast<const uint32_t*>(x));
+              tc::store_wait();
+            }
           }
         }
-        if (i > 0) ok = role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead);
-        ok = named_sync_and(5 + cg, 128, ok);
-        if (!ok) break;
-        tc::fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < HC; ++c) l[c] *= s_f[cg * HC + c];
-        if (i > 0) {
-#pragma unroll
-          for (int hh = 0; hh < A::kHalves; ++hh) {
-            tc::TmemIo<HC>::load(t_o + hh * R, reinterpret_cast<uint32_t*>(x));
-#pragma unroll
-            for (int c = 0; c < HC; ++c) x[c] *= s_f[cg * HC + c];
-            tc::TmemIo<HC>::store(t_o + hh * R, reinterpret_cast<const uint32_t*>(x));
-            tc::store_wait();
-          }
-        }
-        tc::TmemIo<HC>::load(t_s, reinterpret_cast<uint32_t*>(x));
-        exponents();
       }
+      if (!alive) break;
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&b_sfree);
@@ -663,46 +706,54 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (__all_sync(0xFFFFFFFFu, ok) && lane == 0) mbar_arrive(&b_p[pb]);
     }
     // ---- the unit's result
-    if (ok && n > 0) ok = role_wait(&b_pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &s_dead);
-    ok = named_sync_and(5 + cg, 128, ok);
-    tc::fence_after_sync();
+    // sums over the lanes, eight columns at a time: three exchanges that
+    // halve the columns a lane holds, then two plain ones
 #pragma unroll
-    for (int c = 0; c < HC; ++c) {
-      float s = l[c];
+    for (int c = 0; c < HC; c += 8) {
+      float s4[4], s2[2], s;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      if (lane == 0) s_red[warp & 3][cg * HC + c] = s;
+      for (int k = 0; k < 4; ++k) {
+        const float send = lane & 16 ? l[c + k] : l[c + 4 + k];
+        s4[k] = (lane & 16 ? l[c + 4 + k] : l[c + k]) + __shfl_xor_sync(0xFFFFFFFFu, send, 16);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float send = lane & 8 ? s4[k] : s4[2 + k];
+        s2[k] = (lane & 8 ? s4[2 + k] : s4[k]) + __shfl_xor_sync(0xFFFFFFFFu, send, 8);
+      }
+      const float send = lane & 4 ? s2[0] : s2[1];
+      s = (lane & 4 ? s2[1] : s2[0]) + __shfl_xor_sync(0xFFFFFFFFu, send, 4);
+      s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+      s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+      if ((lane & 3) == 0) s_red[warp & 3][cg * HC + c + (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1)] = s;
     }
     named_sync(5 + cg, 128);
-    const int64_t all_rows = static_cast<int64_t>(p.n_nodes) * p.hq;
+    const int64_t slice = (static_cast<int64_t>(h) * gridDim.y + tile) * splits + split;
     if ((warp & 3) == 0) {
       for (int c = cg * HC + lane; c < (cg + 1) * HC; c += 32) {
         const float s = (s_red[0][c] + s_red[1][c]) + (s_red[2][c] + s_red[3][c]);
-        const float lse = s == 0.0f || !ok ? -INFINITY : s_m[c] + log2f(s);
         s_f[c] = s == 0.0f ? 0.0f : 1.0f / s;
-        if (c < n_rows) {
-          if (p.splits > 1) p.part_lse[split * all_rows + s_row[c]] = lse;
-          else if (p.lse) p.lse[s_row[c]] = lse * kLn2F;
-        }
+        p.part_lse[slice * R + c] = s == 0.0f ? -INFINITY : s_m[c] + log2f(s);
       }
     }
-    named_sync(5 + cg, 128);
+    if (ok && n > 0) ok = role_wait(&b_pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &s_dead);
+    ok = named_sync_and(5 + cg, 128, ok);
     if (ok && n > 0) {
-#pragma unroll
+      tc::fence_after_sync();
+      float* dst = p.part_o + (slice * R + cg * HC) * D + key;
+      const float4* f4 = reinterpret_cast<const float4*>(s_f + cg * HC);
+#pragma unroll 1
       for (int hh = 0; hh < A::kHalves; ++hh) {
         float x[HC];
         tc::TmemIo<HC>::load(t_o + hh * R, reinterpret_cast<uint32_t*>(x));
-        const int d = hh * 128 + key;
-        if (d < D) {
+        if (D >= 128 || key < D) {
 #pragma unroll
-          for (int c = 0; c < HC; ++c) {
-            const int col = cg * HC + c;
-            if (col >= n_rows) continue;
-            const float o = x[c] * s_f[col];
-            const int64_t at = static_cast<int64_t>(s_row[col]) * D + d;
-            if (p.splits > 1) p.part_o[split * all_rows * D + at] = o;
-            else if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
-            else static_cast<float*>(p.out)[at] = o;
+          for (int c = 0; c < HC; c += 4) {
+            const float4 f = f4[c / 4];
+            dst[hh * 128 + c * D] = x[c] * f.x;
+            dst[hh * 128 + (c + 1) * D] = x[c + 1] * f.y;
+            dst[hh * 128 + (c + 2) * D] = x[c + 2] * f.z;
+            dst[hh * 128 + (c + 3) * D] = x[c + 3] * f.w;
           }
         }
       }
@@ -724,23 +775,38 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 constexpr int kMergeThreads = 128;
 constexpr int kMaxSplits = 256;
 
+struct MergeParams {
+  int splits, r, tiles, rows_tile, hq, group;
+  const float* part_o;
+  const float* part_lse;
+  void* out;
+  int out_bf16;
+  float* lse;
+};
+
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
-    kv8_merge_kernel(int splits, const float* part_o, const float* part_lse, void* out,
-                     int out_bf16, float* lse) {
+    kv8_merge_kernel(const __grid_constant__ MergeParams p) {
   constexpr int kV = D / 4, kG = kMergeThreads / kV;   // float4 of a row; groups of splits
   __shared__ float s_w[kMaxSplits];
   __shared__ float4 s_o[kG][kV];
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t row = blockIdx.x, rows = gridDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, splits = p.splits;
+  const int head = blockIdx.x, node = blockIdx.y;
+  const int h = head / p.group, r = node * p.group + head - h * p.group;
+  const int tile = r / p.rows_tile;
+  const int64_t row = static_cast<int64_t>(node) * p.hq + head;
+  // this row of slice 0, and what lies between slices
+  const int64_t at = ((static_cast<int64_t>(h) * p.tiles + tile) * splits) * p.r + r - tile * p.rows_tile;
+  const float* part_lse = p.part_lse + at;
+  const float* part_o = p.part_o + at * D;
   grid_dep_wait();
   float m = -INFINITY;
-  for (int s = lane; s < splits; s += 32) m = fmaxf(m, part_lse[s * rows + row]);
+  for (int s = lane; s < splits; s += 32) m = fmaxf(m, part_lse[s * p.r]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   float total = 0.0f;
   for (int s = lane; s < splits; s += 32) {
-    const float v = part_lse[s * rows + row];
+    const float v = part_lse[s * p.r];
     const float w = v == -INFINITY ? 0.0f : tc::ex2(v - m);
     total += w;
     if (tid < 32) s_w[s] = w;
@@ -753,7 +819,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   for (int s = tid / kV; s < splits; s += kG) {
     const float w = s_w[s];
     if (w == 0.0f) continue;   // an empty slice has no row
-    const float4 v = reinterpret_cast<const float4*>(part_o + (s * rows + row) * D)[tid % kV];
+    const float4 v = reinterpret_cast<const float4*>(part_o + static_cast<int64_t>(s) * p.r * D)[tid % kV];
     a.x = fmaf(w, v.x, a.x);
     a.y = fmaf(w, v.y, a.y);
     a.z = fmaf(w, v.z, a.z);
@@ -774,16 +840,16 @@ __global__ void __launch_bounds__(kMergeThreads)
     a.y *= inv;
     a.z *= inv;
     a.w *= inv;
-    if (out_bf16) {
+    if (p.out_bf16) {
       const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
-      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + row * D)[tid] =
+      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D)[tid] =
           make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     } else {
-      reinterpret_cast<float4*>(static_cast<float*>(out) + row * D)[tid] = a;
+      reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D)[tid] = a;
     }
   }
-  if (tid == 0 && lse)
-    lse[row] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2F;
+  if (tid == 0 && p.lse)
+    p.lse[row] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2F;
 }
 
 // ---------------------------------------------------------------- host
@@ -826,13 +892,12 @@ static bool attn_shape_ok(int n_nodes, int hq, int hkv, int d, int window, int c
          hq <= 256 && kv8_dim_ok(d) && window >= 0 && capacity >= 1 && capacity <= (1 << 30);
 }
 
-static size_t attn_ws_bytes(const AttnPlan& pl, int n_nodes, int hq, int d) {
-  if (pl.splits == 1) return 256;
-  return static_cast<size_t>(pl.splits) * n_nodes * hq * (d + 4) * sizeof(float) + 256;
+static size_t attn_ws_bytes(const AttnPlan& pl, int hkv, int d) {
+  return static_cast<size_t>(hkv) * pl.tiles * pl.splits * pl.r * (d + 1) * sizeof(float);
 }
 
 template <int D, int R>
-static dfv_status attn_launch(const AttnParams& p, int units, cudaStream_t stream) {
+static dfv_status attn_launch(const AttnParams& p, const MergeParams& m, cudaStream_t stream) {
   using A = AttnShape<D, R>;
   static std::atomic<int> configured[64];
   int dev = 0;
@@ -843,11 +908,11 @@ static dfv_status attn_launch(const AttnParams& p, int units, cudaStream_t strea
       return DFV_ERR_CUDA;
     configured[dev].store(1, std::memory_order_release);
   }
-  kv8_attn_kernel<D, R><<<units * p.splits, kAtThreads, A::kBytes, stream>>>(p);
+  kv8_attn_kernel<D, R>
+      <<<dim3(m.splits, m.tiles, p.c.n_kv_heads), kAtThreads, A::kBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DFV_ERR_CUDA;
-  if (p.splits == 1) return DFV_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.n_nodes * p.hq);
+  cfg.gridDim = dim3(p.hq, p.n_nodes);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -855,22 +920,17 @@ static dfv_status attn_launch(const AttnParams& p, int units, cudaStream_t strea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D>, p.splits,
-                            static_cast<const float*>(p.part_o),
-                            static_cast<const float*>(p.part_lse), p.out, p.out_bf16,
-                            p.lse) == cudaSuccess
-             ? DFV_OK
-             : DFV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D>, m) == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
 }
 
 template <int D>
-static dfv_status attn_launch_r(const AttnParams& p, int r, int units, cudaStream_t stream) {
-  switch (r) {
-    case 16: return attn_launch<D, 16>(p, units, stream);
-    case 32: return attn_launch<D, 32>(p, units, stream);
-    case 48: return attn_launch<D, 48>(p, units, stream);
-    case 64: return attn_launch<D, 64>(p, units, stream);
-    default: return attn_launch<D, 80>(p, units, stream);
+static dfv_status attn_launch_r(const AttnParams& p, const MergeParams& m, cudaStream_t stream) {
+  switch (m.r) {
+    case 16: return attn_launch<D, 16>(p, m, stream);
+    case 32: return attn_launch<D, 32>(p, m, stream);
+    case 48: return attn_launch<D, 48>(p, m, stream);
+    case 64: return attn_launch<D, 64>(p, m, stream);
+    default: return attn_launch<D, 80>(p, m, stream);
   }
 }
 
@@ -880,8 +940,8 @@ extern "C" size_t dfv_kv8_attn_workspace_bytes(int n_nodes, int n_q_heads, int n
                                                int head_dim, int window, int cache_capacity) {
   using namespace dfv;
   if (!attn_shape_ok(n_nodes, n_q_heads, n_kv_heads, head_dim, window, cache_capacity)) return 0;
-  return attn_ws_bytes(attn_plan(n_nodes, n_q_heads, n_kv_heads, window, cache_capacity), n_nodes,
-                       n_q_heads, head_dim);
+  return attn_ws_bytes(attn_plan(n_nodes, n_q_heads, n_kv_heads, window, cache_capacity),
+                       n_kv_heads, head_dim);
 }
 
 extern "C" dfv_status dfv_kv8_attn(const dfv_kv8_cache* cache, int n_nodes, int max_depth,
@@ -900,10 +960,8 @@ extern "C" dfv_status dfv_kv8_attn(const dfv_kv8_cache* cache, int n_nodes, int 
       !aligned(tree_v, 16) || !aligned(out, 16))
     return DFV_ERR_INVALID;
   const AttnPlan pl = attn_plan(n_nodes, n_q_heads, hkv, window, cache->capacity);
-  if (pl.splits > 1) {
-    if (!workspace || !aligned(workspace, 256)) return DFV_ERR_INVALID;
-    if (workspace_bytes < attn_ws_bytes(pl, n_nodes, n_q_heads, d)) return DFV_ERR_WORKSPACE;
-  }
+  if (!workspace || !aligned(workspace, 256)) return DFV_ERR_INVALID;
+  if (workspace_bytes < attn_ws_bytes(pl, hkv, d)) return DFV_ERR_WORKSPACE;
   AttnParams p = {};
   p.c = *cache;
   p.nblk = kv8_blocks(cache->capacity);
@@ -912,26 +970,23 @@ extern "C" dfv_status dfv_kv8_attn(const dfv_kv8_cache* cache, int n_nodes, int 
   p.hq = n_q_heads;
   p.group = n_q_heads / hkv;
   p.window = window;
+  p.group_m = static_cast<uint32_t>(((1ull << 32) + p.group - 1) / p.group);   // exact below 2^24
   p.rows = n_nodes * p.group;
-  p.tiles = pl.tiles;
   p.rows_tile = pl.rows_tile;
-  p.splits = pl.splits;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.tree_k = static_cast<const __nv_bfloat16*>(tree_k);
   p.tree_v = static_cast<const __nv_bfloat16*>(tree_v);
   p.parent = parent;
   p.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(d));
-  p.out = out;
-  p.out_bf16 = out_dtype == DFV_DTYPE_BF16;
-  p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
-  p.part_lse = p.part_o + static_cast<size_t>(pl.splits) * n_nodes * n_q_heads * d;
+  p.part_lse = p.part_o + static_cast<size_t>(hkv) * pl.tiles * pl.splits * pl.r * d;
   p.status = status;
-  const int units = hkv * pl.tiles;
+  const MergeParams m = {pl.splits, pl.r, pl.tiles, pl.rows_tile, n_q_heads, p.group, p.part_o,
+                         p.part_lse, out, out_dtype == DFV_DTYPE_BF16, lse};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (d) {
-    case 64: return attn_launch_r<64>(p, pl.r, units, s);
-    case 128: return attn_launch_r<128>(p, pl.r, units, s);
-    default: return attn_launch_r<256>(p, pl.r, units, s);
+    case 64: return attn_launch_r<64>(p, m, s);
+    case 128: return attn_launch_r<128>(p, m, s);
+    default: return attn_launch_r<256>(p, m, s);
   }
 }
