@@ -330,53 +330,67 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
   } else if (warp == 16) {
     // ------------------------------------------------------ MMA issue
-    if (lane == 0 && n > 0) {
+    // The whole warp walks the loop and one elected lane issues: the compiler
+    // then keeps descriptors in uniform registers. One lane in a divergent
+    // branch took 45 to 56 cycles per MMA whatever its size; elected, an MMA
+    // takes its R / 2 cycles (11 at R = 16, 40 at R = 80).
+    if (n > 0) {
       constexpr uint32_t id_s = tc::idesc_f16(128, R);
       constexpr uint32_t id_o = tc::idesc_f16(128, R, true);
       const uint64_t qd = tc::smem_desc_sw128(smem_u32(sQ), 1024);
+      auto all_wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool got = __all_sync(0xFFFFFFFFu, role_wait(bar, parity, &s_dead));
+        tc::fence_after_sync();
+        return got;
+      };
       // S^T of chunk i, part by part as K^ arrives (64 dims each)
       auto issue_s = [&](int i) {
-        if (i > 0 && !role_wait(&b_sfree, (i - 1) & 1, &s_dead)) return false;
+        if (i > 0 && !all_wait(&b_sfree, (i - 1) & 1)) return false;
 #pragma unroll
         for (int c = 0; c < A::kKSub; ++c) {
-          if (!role_wait(&b_khat[c], i & 1, &s_dead)) return false;
-          tc::fence_after_sync();
+          if (!all_wait(&b_khat[c], i & 1)) return false;
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc::mma_f16_ts(tmem + A::kTS, tmem + A::kTK + c * 32 + kk * 8,
-                           qd + static_cast<uint64_t>((c * R * 128 + kk * 32) >> 4), id_s,
-                           c + kk > 0 ? 1u : 0u);
-          tc::commit(&b_kfree[c]);
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_f16_ts(tmem + A::kTS, tmem + A::kTK + c * 32 + kk * 8,
+                             qd + static_cast<uint64_t>((c * R * 128 + kk * 32) >> 4), id_s,
+                             c + kk > 0 ? 1u : 0u);
+            tc::commit(&b_kfree[c]);
+            if (c == A::kKSub - 1) tc::commit(&b_sfull);
+          }
+          __syncwarp();
         }
-        tc::commit(&b_sfull);
         return true;
       };
-      bool ok = role_wait(&b_q, 0, &s_dead) && issue_s(0);
+      bool ok = all_wait(&b_q, 0) && issue_s(0);
       for (int i = 0; ok && i < n; ++i) {
         if (i + 1 < n) ok = issue_s(i + 1);
         const int pb = i & 1;
-        ok = ok && role_wait(&b_p[pb], (i >> 1) & 1, &s_dead);
+        ok = ok && all_wait(&b_p[pb], (i >> 1) & 1);
         const uint64_t pd = tc::smem_desc_sw128_mn(
             smem_u32(sP + (A::kPBufs == 2 ? pb : 0) * A::kPBytes), kAtKeys * 128, 1024);
         // O^T: parts (half of the dims, block of 64 keys)
 #pragma unroll
         for (int c = 0; c < A::kVSub; ++c) {
-          ok = ok && role_wait(&b_vhat[c], i & 1, &s_dead);
+          ok = ok && all_wait(&b_vhat[c], i & 1);
           if (!ok) break;
-          tc::fence_after_sync();
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc::mma_f16_ts(tmem + A::kTO + (c >> 1) * R, tmem + A::kTV + c * 32 + kk * 8,
-                           pd + static_cast<uint64_t>((((c & 1) * 4 + kk) * 16 * 128) >> 4), id_o,
-                           i > 0 || (c & 1) + kk > 0 ? 1u : 0u);
-          tc::commit(&b_vfree[c]);
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_f16_ts(tmem + A::kTO + (c >> 1) * R, tmem + A::kTV + c * 32 + kk * 8,
+                             pd + static_cast<uint64_t>((((c & 1) * 4 + kk) * 16 * 128) >> 4),
+                             id_o, i > 0 || (c & 1) + kk > 0 ? 1u : 0u);
+            tc::commit(&b_vfree[c]);
+            if (c == A::kVSub - 1) tc::commit(&b_pv[pb]);
+          }
+          __syncwarp();
         }
-        if (ok) tc::commit(&b_pv[pb]);
       }
       if (!ok) {
         s_dead = 1;
         // MMAs in flight must end before TMEM is freed
-        tc::commit(&b_end);
+        if (tc::elect_one()) tc::commit(&b_end);
+        __syncwarp();
         mbar_wait_bounded(&b_end, 0);
       }
     }

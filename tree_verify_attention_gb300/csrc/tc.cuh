@@ -111,6 +111,17 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       : "memory");
 }
 
+// True in one lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- TMEM loads
 
 // 32 consecutive 32-bit columns of this thread's TMEM lane (32x32b shape).
