@@ -35,7 +35,7 @@
 //
 // Roles of a CTA (one per SM): warps 0-7 softmax (lane quadrant w % 4, column
 // half w / 4), warps 8-11 K codes to TMEM, warps 12-15 V codes, warp 16 issues
-// MMAs, warp 17 bulk copies. A unit is (KV head, tile of at most 80 query
+// MMAs, warps 17 and 18 bulk copies of K and V. A unit is (KV head, tile of at most 80 query
 // rows, slice of the chunks). Bound by HBM while a tile has few rows, by the
 // softmax and the decode for many.
 
@@ -48,7 +48,7 @@
 
 namespace dfv {
 
-constexpr int kAtThreads = 576;
+constexpr int kAtThreads = 608;
 constexpr int kAtKeys = 128;         // keys of a chunk
 constexpr float kRaise = 10.0f;      // a larger exponent moves the reference
 constexpr float kNoRef = -1e30f;     // reference of a column that has seen no key
@@ -208,39 +208,34 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const int n8 = n - (has_tree ? 1 : 0);
   const int live_rows = T + p.n_nodes;          // keys of the bf16 chunk
 
-  // raw codes of chunk i into its stage (one thread)
-  auto copy_codes = [&](int i) {
+  // raw K (V) codes of chunk i into its stage (one thread)
+  auto copy_codes = [&](int i, bool v) {
     const int s = i % A::kStages, b = fb + 2 * (c0 + i);
     const uint32_t bytes = static_cast<uint32_t>(min(2, open - b) * kBlk * D);
     const int64_t off = (static_cast<int64_t>(h) * p.nblk + b) * kBlk * D;
-    uint8_t* raw = smem + s * 2 * A::kRaw;
-    mbar_arrive_expect_tx(&b_kraw[s], bytes);
-    bulk_g2s(raw, p.c.k_codes + off, bytes, &b_kraw[s]);
-    mbar_arrive_expect_tx(&b_vraw[s], bytes);
-    bulk_g2s(raw + A::kRaw, p.c.v_codes + off, bytes, &b_vraw[s]);
+    uint64_t* bar = v ? &b_vraw[s] : &b_kraw[s];
+    mbar_arrive_expect_tx(bar, bytes);
+    bulk_g2s(smem + (s * 2 + v) * A::kRaw, (v ? p.c.v_codes : p.c.k_codes) + off, bytes, bar);
   };
-  // rows of the bf16 chunk over the ring (one warp)
-  auto copy_rows = [&]() {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&b_krow, static_cast<uint32_t>(live_rows * D * 2));
-      mbar_arrive_expect_tx(&b_vrow, static_cast<uint32_t>(live_rows * D * 2));
-    }
+  // K (V) rows of the bf16 chunk over the ring (one warp)
+  auto copy_rows = [&](bool v) {
+    uint64_t* bar = v ? &b_vrow : &b_krow;
+    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live_rows * D * 2));
     __syncwarp();
-    const int64_t t0 = (static_cast<int64_t>(h) * 2 + (open & 1)) * kBlk * D;
-    for (int k = lane; k < live_rows; k += 32) {
-      const int64_t n0 = (static_cast<int64_t>(k - T) * p.c.n_kv_heads + h) * D;
-      const __nv_bfloat16* ks = k < T ? static_cast<const __nv_bfloat16*>(p.c.k_tail) + t0 + k * D
-                                      : p.tree_k + n0;
-      const __nv_bfloat16* vs = k < T ? static_cast<const __nv_bfloat16*>(p.c.v_tail) + t0 + k * D
-                                      : p.tree_v + n0;
-      bulk_g2s(smem + k * A::kRowB, ks, D * 2, &b_krow);
-      bulk_g2s(smem + (kAtKeys + k) * A::kRowB, vs, D * 2, &b_vrow);
-    }
+    const __nv_bfloat16* tail = static_cast<const __nv_bfloat16*>(v ? p.c.v_tail : p.c.k_tail) +
+                                (static_cast<int64_t>(h) * 2 + (open & 1)) * kBlk * D;
+    const __nv_bfloat16* tree = (v ? p.tree_v : p.tree_k) + static_cast<int64_t>(h) * D;
+    for (int k = lane; k < live_rows; k += 32)
+      bulk_g2s(smem + ((v ? kAtKeys : 0) + k) * A::kRowB,
+               k < T ? tail + k * D
+                     : tree + static_cast<int64_t>(k - T) * p.c.n_kv_heads * D,
+               D * 2, bar);
   };
 
   const int first_copies = min(n8, A::kStages);
-  if (warp == 17) {   // the first copies wait for nothing
-    if (lane == 0) {
+  // warps 17 (K) and 18 (V): the first copies wait for nothing
+  if (warp >= 17) {
+    if (warp == 17 && lane == 0) {
       for (int s = 0; s < 4; ++s) {
         mbar_init(&b_kraw[s], 1);
         mbar_init(&b_vraw[s], 1);
@@ -262,10 +257,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mbar_init(&b_pv[k], 1);
       }
       fence_mbar_init();
-      for (int i = 0; i < first_copies; ++i) copy_codes(i);
     }
-    __syncwarp();
-    if (has_tree && n8 == 0) copy_rows();
+    named_sync(1, 64);
+    if (lane == 0)
+      for (int i = 0; i < first_copies; ++i) copy_codes(i, warp == 18);
+    if (has_tree && n8 == 0) copy_rows(warp == 18);
   } else if (warp == 16) {
     tc::tmem_alloc(&s_tmem, 512);
   }
@@ -295,38 +291,32 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const uint32_t tmem = s_tmem;
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // first lane of the quadrant << 16
 
-  if (warp == 17) {
+  if (warp >= 17) {
     // ------------------------------------------------------ bulk copies
+    const bool v = warp == 18;
+    uint64_t* raw_full = v ? b_vraw : b_kraw;
     bool ok = true;
     int issued = first_copies;
     for (int i = first_copies; ok && i < n8; ++i) {
-      const int s = i % A::kStages;
-      const uint32_t ph = (i / A::kStages - 1) & 1;
-      ok = role_wait(&b_kdone[s], ph, &s_dead) && role_wait(&b_vdone[s], ph, &s_dead);
+      ok = role_wait(v ? &b_vdone[i % A::kStages] : &b_kdone[i % A::kStages],
+                     (i / A::kStages - 1) & 1, &s_dead);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
-      if (lane == 0) copy_codes(i);
+      if (lane == 0) copy_codes(i, v);
       issued = i + 1;
     }
     if (has_tree && n8 > 0) {
-      for (int i = max(0, n8 - A::kStages); ok && i < n8; ++i) {   // the ring has been read
-        const uint32_t ph = (i / A::kStages) & 1;
-        ok = role_wait(&b_kdone[i % A::kStages], ph, &s_dead) &&
-             role_wait(&b_vdone[i % A::kStages], ph, &s_dead);
-      }
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (ok) copy_rows();
+      for (int i = max(0, n8 - A::kStages); ok && i < n8; ++i)
+        ok = role_wait(v ? &b_vdone[i % A::kStages] : &b_kdone[i % A::kStages],
+                       (i / A::kStages) & 1, &s_dead);
+      ok = named_sync_and(1, 64, ok);   // both rings have been read
+      if (ok) copy_rows(v);
     }
     // copies that nobody waits for any more must still land
     if (s_dead) {
-      for (int i = max(0, issued - A::kStages); i < issued; ++i) {
-        mbar_wait_bounded(&b_kraw[i % A::kStages], (i / A::kStages) & 1);
-        mbar_wait_bounded(&b_vraw[i % A::kStages], (i / A::kStages) & 1);
-      }
-      if (has_tree && ok) {
-        mbar_wait_bounded(&b_krow, 0);
-        mbar_wait_bounded(&b_vrow, 0);
-      }
+      for (int i = max(0, issued - A::kStages); i < issued; ++i)
+        mbar_wait_bounded(&raw_full[i % A::kStages], (i / A::kStages) & 1);
+      if (has_tree && ok) mbar_wait_bounded(v ? &b_vrow : &b_krow, 0);
     }
   } else if (warp == 16) {
     // ------------------------------------------------------ MMA issue
@@ -410,13 +400,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int base0 = is_v ? A::kRaw + slot * 16 : (slot >> 6) * kBlk * D + (slot & 63) * 16;
     const int step = is_v ? D * 16 : kBlk * 16;
     bool ok = true;
-    // part c of chunk i, converted and waiting in registers, into TMEM
+    // Part c of chunk i, converted and waiting in registers, into TMEM once
+    // the products have read the last chunk's; handed over by give().
     auto put = [&](int i, int c, const uint32_t* w) {
       if (i > 0) ok = role_wait(&hat_free[c], (i - 1) & 1, &s_dead);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) return;
       tc::fence_after_sync();
       if (works) tc::TmemIo<32>::store(t_op + c * 32, w);
+    };
+    auto give = [&](int c) {
       tc::store_wait();
       tc::fence_before_sync();
       __syncwarp();
@@ -428,24 +421,30 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       const uint8_t* raw = smem + s * 2 * A::kRaw + base0;
-#pragma unroll 1
-      for (int c = 0; c < subs; ++c) {
-        // V part (half, block): dims 128 on, keys of the second block
+      uint4 q[4];
+      // V part (half, block): dims 128 on, keys of the second block
+      auto fetch = [&](int c) {
         const uint8_t* mine = raw + (is_v ? (c >> 1) * 128 * 16 + (c & 1) * kBlk * D
                                           : c * 4 * kBlk * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const uint4*>(mine + j * step);
+      };
+      if (works) fetch(0);
+#pragma unroll 1
+      for (int c = 0; c < subs; ++c) {
         uint32_t w[32];
         if (works) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            codes_to_half(*reinterpret_cast<const uint4*>(mine + j * step), w + 8 * j);
+          for (int j = 0; j < 4; ++j) codes_to_half(q[j], w + 8 * j);
+          if (c + 1 < subs) fetch(c + 1);   // lands while this part is handed over
         }
-        if (c == subs - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&raw_done[s]);
-        }
+        if (c > 0) give(c - 1);
         put(i, c, w);
         if (!ok) break;
       }
+      if (!ok) break;
+      give(subs - 1);
+      if (lane == 0) mbar_arrive(&raw_done[s]);
     }
     if (has_tree) {
       // The bf16 chunk: key slots [0, T) are the open block's rows, then the
@@ -501,6 +500,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           put(n8, c, w);
           if (!ok) break;
+          give(c);
         }
       }
     }
