@@ -58,7 +58,11 @@ constexpr float kLn2F = 0.6931471805599453f;
 template <int D, int R>
 struct AttnShape {
   static constexpr int kHalves = D == 256 ? 2 : 1;      // 128-lane parts of V^T
-  static constexpr int kKSub = D / 64, kVSub = 2 * kHalves;   // 32-column parts of K^ and V^
+  // K^ and V^ are handed to the products in parts of kPart columns (two per
+  // operand at D = 256 and 128): the next chunk's part can be written while
+  // the products read the other
+  static constexpr int kPart = D == 256 ? 64 : 32;
+  static constexpr int kKSub = D / 2 / kPart, kVSub = 64 * kHalves / kPart;
   static constexpr int kRaw = kAtKeys * D;              // bytes of a chunk's K (V) codes
   static constexpr int kRowB = D * 2 + 16;              // a staged bf16 row (padded: banks)
   static constexpr int kPBlk = (R + 63) / 64;
@@ -162,10 +166,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   uint8_t* sQ = smem + A::kOffQ;
   uint8_t* sP = smem + A::kOffP;
   // raw codes landed / read (per stage); operand part written / read by the
-  // products; scores written / read; P written / read; bf16 rows landed
+  // products (K's last part read: the scores are there); scores read; P
+  // written and O there (two each, used in turn: a phase's parity tells it
+  // from its neighbours only, and the softmax may lag P V by two chunks);
+  // bf16 rows landed
   __shared__ uint64_t b_kraw[4], b_kdone[4], b_vraw[4], b_vdone[4];
   __shared__ uint64_t b_khat[4], b_kfree[4], b_vhat[4], b_vfree[4];
-  __shared__ uint64_t b_sfull, b_sfree, b_q, b_end, b_krow, b_vrow, b_p[2], b_pv[2];
+  __shared__ uint64_t b_sfree, b_q, b_end, b_krow, b_vrow, b_p[2], b_pv[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_dead;
   __shared__ int s_parent[kMaxNodes], s_maxdepth;
@@ -246,7 +253,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mbar_init(&b_kfree[s], 1);
         mbar_init(&b_vfree[s], 1);
       }
-      mbar_init(&b_sfull, 1);
       mbar_init(&b_sfree, 8);
       mbar_init(&b_q, 8);
       mbar_init(&b_end, 1);
@@ -333,7 +339,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         tc::fence_after_sync();
         return got;
       };
-      // S^T of chunk i, part by part as K^ arrives (64 dims each)
+      // S^T of chunk i, part by part as K^ arrives. A commit costs about as
+      // much as eight MMAs of 16 columns, so there is one for each part: the
+      // last one also tells that S is there and that all products before,
+      // P V of chunk i - 2 among them, have ended.
       auto issue_s = [&](int i) {
         if (i > 0 && !all_wait(&b_sfree, (i - 1) & 1)) return false;
 #pragma unroll
@@ -341,12 +350,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (!all_wait(&b_khat[c], i & 1)) return false;
           if (tc::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_f16_ts(tmem + A::kTS, tmem + A::kTK + c * 32 + kk * 8,
-                             qd + static_cast<uint64_t>((c * R * 128 + kk * 32) >> 4), id_s,
-                             c + kk > 0 ? 1u : 0u);
+            for (int kk = c * A::kPart / 8; kk < (c + 1) * A::kPart / 8; ++kk)
+              tc::mma_f16_ts(tmem + A::kTS, tmem + A::kTK + kk * 8,
+                             qd + static_cast<uint64_t>(((kk >> 2) * R * 128 + (kk & 3) * 32) >> 4),
+                             id_s, kk > 0 ? 1u : 0u);
             tc::commit(&b_kfree[c]);
-            if (c == A::kKSub - 1) tc::commit(&b_sfull);
           }
           __syncwarp();
         }
@@ -359,19 +367,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         ok = ok && all_wait(&b_p[pb], (i >> 1) & 1);
         const uint64_t pd = tc::smem_desc_sw128_mn(
             smem_u32(sP + (A::kPBufs == 2 ? pb : 0) * A::kPBytes), kAtKeys * 128, 1024);
-        // O^T: parts (half of the dims, block of 64 keys)
+        // O^T, eight steps of 16 keys for each half of the dims
 #pragma unroll
         for (int c = 0; c < A::kVSub; ++c) {
           ok = ok && all_wait(&b_vhat[c], i & 1);
           if (!ok) break;
           if (tc::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_f16_ts(tmem + A::kTO + (c >> 1) * R, tmem + A::kTV + c * 32 + kk * 8,
-                             pd + static_cast<uint64_t>((((c & 1) * 4 + kk) * 16 * 128) >> 4),
-                             id_o, i > 0 || (c & 1) + kk > 0 ? 1u : 0u);
-            tc::commit(&b_vfree[c]);
-            if (c == A::kVSub - 1) tc::commit(&b_pv[pb]);
+            for (int kk = c * A::kPart / 8; kk < (c + 1) * A::kPart / 8; ++kk)
+              tc::mma_f16_ts(tmem + A::kTO + (kk >> 3) * R, tmem + A::kTV + kk * 8,
+                             pd + static_cast<uint64_t>(((kk & 7) * 16 * 128) >> 4),
+                             id_o, i > 0 || (kk & 7) > 0 ? 1u : 0u);
+            tc::commit(c == A::kVSub - 1 ? &b_pv[pb] : &b_vfree[c]);
           }
           __syncwarp();
         }
@@ -393,27 +400,32 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     uint64_t* hat = is_v ? b_vhat : b_khat;
     uint64_t* hat_free = is_v ? b_vfree : b_kfree;
     const uint32_t t_op = tmem + lanes + (is_v ? A::kTV : A::kTK);
-    const int subs = is_v ? A::kVSub : A::kKSub;
+    const int subs = is_v ? 2 * A::kHalves : D / 64;   // pieces of 32 columns
     const bool works = !is_v || D >= 128 || slot < D;   // D = 64: V^T has 64 lanes
-    // the bytes of one part, for this thread: K 64 dims of its key (pieces
+    // the bytes of 32 columns, for this thread: K 64 dims of its key (pieces
     // 64 * 16 apart), V 64 keys of its dim (pieces D * 16 apart)
     const int base0 = is_v ? A::kRaw + slot * 16 : (slot >> 6) * kBlk * D + (slot & 63) * 16;
     const int step = is_v ? D * 16 : kBlk * 16;
     bool ok = true;
-    // Part c of chunk i, converted and waiting in registers, into TMEM once
-    // the products have read the last chunk's; handed over by give().
+    constexpr int kPer = A::kPart / 32;     // 32-column pieces of a part
+    // 32 columns of chunk i, converted and waiting in registers, into TMEM
+    // once the products have read the last chunk's part; give() hands it over.
     auto put = [&](int i, int c, const uint32_t* w) {
-      if (i > 0) ok = role_wait(&hat_free[c], (i - 1) & 1, &s_dead);
+      if (i > 0 && c % kPer == 0)
+        ok = is_v && c / kPer == A::kVSub - 1
+                 ? role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead)
+                 : role_wait(&hat_free[c / kPer], (i - 1) & 1, &s_dead);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) return;
       tc::fence_after_sync();
       if (works) tc::TmemIo<32>::store(t_op + c * 32, w);
     };
     auto give = [&](int c) {
+      if (c % kPer != kPer - 1) return;
       tc::store_wait();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&hat[c]);
+      if (lane == 0) mbar_arrive(&hat[c / kPer]);
     };
     for (int i = 0; ok && i < n8; ++i) {
       const int s = i % A::kStages;
@@ -422,7 +434,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (!ok) break;
       const uint8_t* raw = smem + s * 2 * A::kRaw + base0;
       uint4 q[4];
-      // V part (half, block): dims 128 on, keys of the second block
+      // V piece (half, block): dims 128 on, keys of the second block
       auto fetch = [&](int c) {
         const uint8_t* mine = raw + (is_v ? (c >> 1) * 128 * 16 + (c & 1) * kBlk * D
                                           : c * 4 * kBlk * 16);
@@ -430,9 +442,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const uint4*>(mine + j * step);
       };
       if (works) fetch(0);
-#pragma unroll 1
-      for (int c = 0; c < subs; ++c) {
-        uint32_t w[32];
+      // two sets of registers: the store of one part reads its own while the
+      // next part is converted
+      uint32_t w0[32], w1[32];
+      auto part = [&](int c, uint32_t* w) {
         if (works) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) codes_to_half(q[j], w + 8 * j);
@@ -440,6 +453,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         if (c > 0) give(c - 1);
         put(i, c, w);
+      };
+#pragma unroll 1
+      for (int c = 0; c < subs; c += 2) {
+        part(c, w0);
+        if (!ok) break;
+        if (c + 1 < subs) part(c + 1, w1);
         if (!ok) break;
       }
       if (!ok) break;
@@ -571,6 +590,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const float4* m4 = reinterpret_cast<const float4*>(s_m + cg * HC);
     const float4* zero4 = reinterpret_cast<const float4*>(s_zero + cg * HC);
 
+    // a chunk's scales, read one chunk ahead
+    float ks_next = 0.0f, vs_next = 0.0f;
+    auto fetch_scales = [&](int i) {
+      const int kb = fb + 2 * (c0 + i) + (key >> 6);
+      if (i < n8 && kb < open) {
+        const int64_t at = static_cast<int64_t>(h) * p.nblk + kb;
+        ks_next = __ldg(p.c.k_scale + at);
+        vs_next = __ldg(p.c.v_scale + at);
+      }
+    };
+    fetch_scales(0);
+
     for (int i = 0; i < n; ++i) {
       // this lane's key
       const bool bf = has_tree && i == n - 1;
@@ -584,9 +615,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const int pos = bf ? open * kBlk + key : kb * kBlk + (key & 63);
         const bool live = bf ? key < live_rows : kb < open;
         if (live && !bf) {
-          const int64_t at = static_cast<int64_t>(h) * p.nblk + kb;
-          a = __ldg(p.c.k_scale + at) * sc;
-          const float sv = fmaxf(__ldg(p.c.v_scale + at), 7.1054274e-15f);   // 2^-47
+          a = ks_next * sc;
+          const float sv = fmaxf(vs_next, 7.1054274e-15f);   // 2^-47
           lv = log2f(sv);
           iv = __fdividef(1.0f, sv);
         }
@@ -599,7 +629,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
         }
       }
-      ok = ok && role_wait(&b_sfull, i & 1, &s_dead);
+      fetch_scales(i + 1);
+      ok = ok && role_wait(&b_kfree[A::kKSub - 1], i & 1, &s_dead);
       if (bf) {   // the key's scales were written with the operands
         ok = ok && role_wait(&b_khat[A::kKSub - 1], i & 1, &s_dead) &&
              role_wait(&b_vhat[0], i & 1, &s_dead);
@@ -698,7 +729,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       }
       // P' as the B operand: 16-byte pieces of 8 columns of this key's row
       const int pb = i & 1;
-      if (A::kPBufs == 2 && i >= 2) ok = role_wait(&b_pv[pb], ((i - 2) >> 1) & 1, &s_dead);
       if (A::kPBufs == 1 && i >= 1) ok = role_wait(&b_pv[pb ^ 1], ((i - 1) >> 1) & 1, &s_dead);
       if (ok) {
         uint8_t* dst = sP + (A::kPBufs == 2 ? pb : 0) * A::kPBytes;
