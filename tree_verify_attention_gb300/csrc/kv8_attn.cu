@@ -51,7 +51,7 @@ namespace dfv {
 constexpr int kAtThreads = 608;
 constexpr int kAtKeys = 128;         // keys of a chunk
 constexpr float kRaise = 10.0f;      // a larger exponent moves the reference
-constexpr float kNoRef = -1e30f;     // reference of a column that has seen no key
+constexpr float kNoRef = 1e30f;      // -reference of a column that has seen no key
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kLn2F = 0.6931471805599453f;
 
@@ -138,6 +138,35 @@ __device__ __forceinline__ float pow2i(int e) {   // e in [-126, 127]
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
+                                     float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float lg2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // A packed pair of bf16 values times f, as a pair of binary16 values.
 __device__ __forceinline__ uint32_t scaled_half2(uint32_t bf, float f) {
   return pack_half2(__uint_as_float(bf << 16) * f, __uint_as_float(bf & 0xFFFF0000u) * f);
@@ -178,7 +207,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __shared__ int s_parent[kMaxNodes], s_maxdepth;
   // columns (of each half) that see a tree node; columns by depth, and up to a depth
   __shared__ unsigned long long s_see[kMaxNodes][2], s_dep[kMaxNodes][2], s_upto[kMaxNodes][2];
-  __shared__ __align__(16) float s_m[R], s_f[R], s_zero[R];
+  __shared__ __align__(16) float s_neg[R], s_f[R], s_zero[R];   // s_neg: -reference
   __shared__ float s_red[4][R];
   __shared__ float s_ksc[kAtKeys], s_vfac[kAtKeys];
   __shared__ int s_vexp[kAtKeys], s_bad[2][kAtKeys];
@@ -556,7 +585,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         atomicOr(&s_dep[depth][half], bit);
         atomicMax(&s_maxdepth, depth);
       }
-      s_m[tid] = kNoRef;
+      s_neg[tid] = kNoRef;
       s_zero[tid] = 0.0f;
     }
     named_sync(4, 256);
@@ -587,7 +616,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     for (int c = 0; c < HC; ++c) l[c] = 0.0f;
     const uint32_t t_s = tmem + lanes + A::kTS + cg * HC;
     const uint32_t t_o = tmem + lanes + A::kTO + cg * HC;
-    const float4* m4 = reinterpret_cast<const float4*>(s_m + cg * HC);
+    const float4* m4 = reinterpret_cast<const float4*>(s_neg + cg * HC);
     const float4* zero4 = reinterpret_cast<const float4*>(s_zero + cg * HC);
 
     // a chunk's scales, read one chunk ahead
@@ -617,8 +646,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (live && !bf) {
           a = ks_next * sc;
           const float sv = fmaxf(vs_next, 7.1054274e-15f);   // 2^-47
-          lv = log2f(sv);
-          iv = __fdividef(1.0f, sv);
+          lv = lg2_fast(sv);      // within 2^-20, in both
+          iv = tc::ex2(-lv);
         }
         if (masked) {
           if (!live) vis = 0;
@@ -661,11 +690,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const float4* ref = pass == 1 ? zero4 : m4;
 #pragma unroll
         for (int c = 0; c < HC; c += 4) {
-          const float4 m = ref[c / 4];
-          x[c] = fmaf(x[c], a, lv - m.x);
-          x[c + 1] = fmaf(x[c + 1], a, lv - m.y);
-          x[c + 2] = fmaf(x[c + 2], a, lv - m.z);
-          x[c + 3] = fmaf(x[c + 3], a, lv - m.w);
+          float4 m = ref[c / 4];
+          add2(m.x, m.y, m.x, m.y, lv, lv);
+          add2(m.z, m.w, m.z, m.w, lv, lv);
+          fma2(x[c], x[c + 1], x[c], x[c + 1], a, a, m.x, m.y);
+          fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], a, a, m.z, m.w);
         }
         if (masked) {
           const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
@@ -676,7 +705,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (pass == 0) {
           float top = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < HC; ++c) top = fmaxf(top, x[c]);
+          for (int c = 0; c < HC; c += 2) top = max3(top, x[c], x[c + 1]);
           if (named_sync_and(5 + cg, 128, ok && !(top > kRaise))) break;
         } else if (pass == 1) {
 #pragma unroll
@@ -688,10 +717,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           named_sync(5 + cg, 128);
           if ((warp & 3) == 0) {
             for (int c = cg * HC + lane; c < (cg + 1) * HC; c += 32) {
-              const float was = s_m[c];
+              const float was = -s_neg[c];
               const float m = fmaxf(fmaxf(fmaxf(s_red[0][c], s_red[1][c]),
                                           fmaxf(s_red[2][c], s_red[3][c])), was);
-              s_m[c] = m;
+              s_neg[c] = -m;
               s_f[c] = tc::ex2(was - m);
             }
           }
@@ -738,8 +767,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float p0 = tc::ex2(x[8 * j + 2 * e]), p1 = tc::ex2(x[8 * j + 2 * e + 1]);
-            l[8 * j + 2 * e] = fmaf(p0, iv, l[8 * j + 2 * e]);
-            l[8 * j + 2 * e + 1] = fmaf(p1, iv, l[8 * j + 2 * e + 1]);
+            fma2(l[8 * j + 2 * e], l[8 * j + 2 * e + 1], p0, p1, iv, iv, l[8 * j + 2 * e],
+                 l[8 * j + 2 * e + 1]);
             o[e] = pack_half2(p0, p1);
           }
           *reinterpret_cast<uint4*>(dst + tc::sw128_offset(key, cg * (HC / 8) + j, kAtKeys)) =
@@ -777,7 +806,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       for (int c = cg * HC + lane; c < (cg + 1) * HC; c += 32) {
         const float s = (s_red[0][c] + s_red[1][c]) + (s_red[2][c] + s_red[3][c]);
         s_f[c] = s == 0.0f ? 0.0f : 1.0f / s;
-        p.part_lse[slice * R + c] = s == 0.0f ? -INFINITY : s_m[c] + log2f(s);
+        p.part_lse[slice * R + c] = s == 0.0f ? -INFINITY : log2f(s) - s_neg[c];
       }
     }
     if (ok && n > 0) ok = role_wait(&b_pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &s_dead);
