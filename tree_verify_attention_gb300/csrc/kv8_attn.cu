@@ -33,11 +33,11 @@
 // power of two per tile. Every operand is then exact in binary16 except P',
 // whose rounding (2^-12) is below that of the bf16 output.
 //
-// Roles of a CTA (one per SM): warps 0-7 softmax (lane quadrant w % 4, column
-// half w / 4), warps 8-11 K codes to TMEM, warps 12-15 V codes, warp 16 issues
-// MMAs, warps 17 and 18 bulk copies of K and V. A unit is (KV head, tile of at most 80 query
-// rows, slice of the chunks). Bound by HBM while a tile has few rows, by the
-// softmax and the decode for many.
+// Roles of a CTA (one per SM): 8 or 16 softmax warps (lane quadrant w % 4,
+// column group w / 4), four warps that put K codes into TMEM, four for V, one
+// that issues MMAs, two that copy K and V. A unit is (KV head, tile of at
+// most 80 query rows, slice of the chunks). Bound by HBM while a tile has few
+// rows, by the softmax and the conversion of the codes for many.
 
 #include <atomic>
 #include <math.h>
@@ -48,7 +48,6 @@
 
 namespace dfv {
 
-constexpr int kAtThreads = 608;
 constexpr int kAtKeys = 128;         // keys of a chunk
 constexpr float kRaise = 10.0f;      // a larger exponent moves the reference
 constexpr float kNoRef = 1e30f;      // -reference of a column that has seen no key
@@ -57,6 +56,13 @@ constexpr float kLn2F = 0.6931471805599453f;
 
 template <int D, int R>
 struct AttnShape {
+  // Softmax warps: four lane quadrants times the column groups. The softmax
+  // of many columns is a long chain per warp; twice the warps, with half the
+  // columns each, shorten it (and leave 72 registers a thread).
+  static constexpr int kSoft = R >= 64 ? 16 : 8;
+  static constexpr int kGroups = kSoft / 4;
+  static constexpr int kCols = R / kGroups;             // columns of a softmax thread
+  static constexpr int kThreads = (kSoft + 11) * 32;
   static constexpr int kHalves = D == 256 ? 2 : 1;      // 128-lane parts of V^T
   // K^ and V^ are handed to the products in parts of kPart columns (two per
   // operand at D = 256 and 128): the next chunk's part can be written while
@@ -186,10 +192,10 @@ __device__ __forceinline__ uint32_t row_max(const uint8_t* row) {
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kAtThreads, 1)
+__global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     kv8_attn_kernel(const __grid_constant__ AttnParams p) {
   using A = AttnShape<D, R>;
-  constexpr int HC = R / 2;   // columns of a softmax thread
+  constexpr int HC = A::kCols, SW = A::kSoft, NG = A::kGroups;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem + A::kOffQ;
@@ -205,8 +211,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_dead;
   __shared__ int s_parent[kMaxNodes], s_maxdepth;
-  // columns (of each half) that see a tree node; columns by depth, and up to a depth
-  __shared__ unsigned long long s_see[kMaxNodes][2], s_dep[kMaxNodes][2], s_upto[kMaxNodes][2];
+  // columns (of each group) that see a tree node; columns by depth, and up to a depth
+  __shared__ uint32_t s_see[kMaxNodes][NG], s_dep[kMaxNodes][NG], s_upto[kMaxNodes][NG];
   __shared__ __align__(16) float s_neg[R], s_f[R], s_zero[R];   // s_neg: -reference
   __shared__ float s_red[4][R];
   __shared__ float s_ksc[kAtKeys], s_vfac[kAtKeys];
@@ -218,14 +224,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   grid_dep_launch_dependents();   // the merge may be set up meanwhile
   const int split = blockIdx.x, splits = gridDim.x, tile = blockIdx.y, h = blockIdx.z;
   const int row0 = tile * p.rows_tile, n_rows = min(p.rows_tile, p.rows - row0);
-  for (int i = tid; i < p.n_nodes; i += kAtThreads) {
+  for (int i = tid; i < p.n_nodes; i += A::kThreads) {
     int pa = i == 0 ? -1 : p.parent[i];
     if (i > 0 && (pa < 0 || pa >= i)) {
       report(p.status, DFV_DEV_BAD_TREE);
       pa = 0;
     }
     s_parent[i] = pa;
-    s_see[i][0] = s_see[i][1] = s_dep[i][0] = s_dep[i][1] = 0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) s_see[i][g] = s_dep[i][g] = 0;
   }
   if (C < 0 || C > p.c.capacity) {
     if (tid == 0) report(p.status, DFV_DEV_CTX);
@@ -269,9 +276,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   };
 
   const int first_copies = min(n8, A::kStages);
-  // warps 17 (K) and 18 (V): the first copies wait for nothing
-  if (warp >= 17) {
-    if (warp == 17 && lane == 0) {
+  // the copying warps, one for K and one for V: the first copies wait for nothing
+  if (warp >= SW + 9) {
+    if (warp == SW + 9 && lane == 0) {
       for (int s = 0; s < 4; ++s) {
         mbar_init(&b_kraw[s], 1);
         mbar_init(&b_vraw[s], 1);
@@ -282,22 +289,22 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mbar_init(&b_kfree[s], 1);
         mbar_init(&b_vfree[s], 1);
       }
-      mbar_init(&b_sfree, 8);
-      mbar_init(&b_q, 8);
+      mbar_init(&b_sfree, SW);
+      mbar_init(&b_q, SW);
       mbar_init(&b_end, 1);
       mbar_init(&b_krow, 1);
       mbar_init(&b_vrow, 1);
       for (int k = 0; k < 2; ++k) {
-        mbar_init(&b_p[k], 8);
+        mbar_init(&b_p[k], SW);
         mbar_init(&b_pv[k], 1);
       }
       fence_mbar_init();
     }
     named_sync(1, 64);
     if (lane == 0)
-      for (int i = 0; i < first_copies; ++i) copy_codes(i, warp == 18);
-    if (has_tree && n8 == 0) copy_rows(warp == 18);
-  } else if (warp == 16) {
+      for (int i = 0; i < first_copies; ++i) copy_codes(i, warp == SW + 10);
+    if (has_tree && n8 == 0) copy_rows(warp == SW + 10);
+  } else if (warp == SW + 8) {
     tc::tmem_alloc(&s_tmem, 512);
   }
   if (tid == 0) {
@@ -306,13 +313,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     s_maxdepth = 0;
   }
   // Q rows of the tile, into registers meanwhile (softmax warps)
-  constexpr int kQSteps = (R * D / 8 + 255) / 256;
+  constexpr int kQSteps = (R * D / 8 + SW * 32 - 1) / (SW * 32);
   uint4 qv[kQSteps];
   uint32_t qm = 0;
-  if (warp < 8) {
+  if (warp < SW) {
 #pragma unroll
     for (int k = 0; k < kQSteps; ++k) {
-      const int it = tid + k * 256, r = it / (D / 8), j = it % (D / 8);
+      const int it = tid + k * (SW * 32), r = it / (D / 8), j = it % (D / 8);
       qv[k] = make_uint4(0, 0, 0, 0);
       if (r < n_rows) {
         const int node = static_cast<int>(p.group == 1 ? row0 + r : __umulhi(row0 + r, p.group_m));
@@ -326,9 +333,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const uint32_t tmem = s_tmem;
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // first lane of the quadrant << 16
 
-  if (warp >= 17) {
+  if (warp >= SW + 9) {
     // ------------------------------------------------------ bulk copies
-    const bool v = warp == 18;
+    const bool v = warp == SW + 10;
     uint64_t* raw_full = v ? b_vraw : b_kraw;
     bool ok = true;
     int issued = first_copies;
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mbar_wait_bounded(&raw_full[i % A::kStages], (i / A::kStages) & 1);
       if (has_tree && ok) mbar_wait_bounded(v ? &b_vrow : &b_krow, 0);
     }
-  } else if (warp == 16) {
+  } else if (warp == SW + 8) {
     // ------------------------------------------------------ MMA issue
     // The whole warp walks the loop and one elected lane issues: the compiler
     // then keeps descriptors in uniform registers. One lane in a divergent
@@ -420,9 +427,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mbar_wait_bounded(&b_end, 0);
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= SW) {
     // ------------------------------------------------------ operands to TMEM
-    const bool is_v = warp >= 12;
+    const bool is_v = warp >= SW + 4;
     const int slot = (warp & 3) * 32 + lane;   // key (K) or dim of a half (V)
     uint64_t* raw_full = is_v ? b_vraw : b_kraw;
     uint64_t* raw_done = is_v ? b_vdone : b_kdone;
@@ -471,9 +478,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const uint4*>(mine + j * step);
       };
       if (works) fetch(0);
-      // two sets of registers: the store of one part reads its own while the
-      // next part is converted
-      uint32_t w0[32], w1[32];
+      // two sets of registers (where there are as many): the store of one
+      // part reads its own while the next part is converted
+      uint32_t w0[32], w1[SW == 8 ? 32 : 1];
       auto part = [&](int c, uint32_t* w) {
         if (works) {
 #pragma unroll
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       for (int c = 0; c < subs; c += 2) {
         part(c, w0);
         if (!ok) break;
-        if (c + 1 < subs) part(c + 1, w1);
+        if (c + 1 < subs) part(c + 1, SW == 8 ? w1 : w0);
         if (!ok) break;
       }
       if (!ok) break;
@@ -554,7 +561,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
   } else {
     // ------------------------------------------------------ Q, tree, softmax
-    const int cg = warp >> 2;                  // column half
+    const int cg = warp >> 2;                  // column group
     const int key = (warp & 3) * 32 + lane;
     bool ok = true;
     // Q scaled so that the tile's largest magnitude is in [2^14, 2^15)
@@ -573,27 +580,27 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     // columns: what each row sees of the tree, and its depth
     if (tid < R) {
       if (tid < n_rows) {
-        const int half = tid / HC;
-        const unsigned long long bit = 1ull << (tid - half * HC);
+        const int grp = tid / HC;
+        const uint32_t bit = 1u << (tid - grp * HC);
         int depth = -1;
         for (int x = p.group == 1 ? row0 + tid : static_cast<int>(__umulhi(row0 + tid, p.group_m));
              x >= 0; x = s_parent[x]) {
-          atomicOr(&s_see[x][half], bit);
+          atomicOr(&s_see[x][grp], bit);
           ++depth;
         }
         if (depth > p.max_depth) report(p.status, DFV_DEV_DEPTH);
-        atomicOr(&s_dep[depth][half], bit);
+        atomicOr(&s_dep[depth][grp], bit);
         atomicMax(&s_maxdepth, depth);
       }
       s_neg[tid] = kNoRef;
       s_zero[tid] = 0.0f;
     }
-    named_sync(4, 256);
+    named_sync(4, SW * 32);
     const int qe = max(static_cast<int>(s_qmax >> 7), 20);
     const float qf = pow2i(min(141 - qe, 126));
 #pragma unroll
     for (int k = 0; k < kQSteps; ++k) {
-      const int it = tid + k * 256, r = it / (D / 8), j = it % (D / 8);
+      const int it = tid + k * (SW * 32), r = it / (D / 8), j = it % (D / 8);
       if (r < R)
         *reinterpret_cast<uint4*>(sQ + tc::sw128_offset(r, j, R)) =
             make_uint4(scaled_half2(qv[k].x, qf), scaled_half2(qv[k].y, qf),
@@ -603,12 +610,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&b_q);
     const int maxdepth = s_maxdepth;
-    for (int k = tid; k < 2 * (maxdepth + 1); k += 256) {
-      unsigned long long m = 0;
-      for (int x = 0; x <= k >> 1; ++x) m |= s_dep[x][k & 1];
-      s_upto[k >> 1][k & 1] = m;
+    for (int k = tid; k < NG * (maxdepth + 1); k += SW * 32) {
+      uint32_t m = 0;
+      for (int x = 0; x <= k / NG; ++x) m |= s_dep[x][k % NG];
+      s_upto[k / NG][k % NG] = m;
     }
-    named_sync(4, 256);
+    named_sync(4, SW * 32);
     const int lo_all = p.window > 0 ? C + maxdepth - p.window + 1 : INT32_MIN;
     const float sc = p.scale * kLog2eF * pow2i(max(qe - 141, -126));
     float l[HC];
@@ -621,12 +628,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
     // a chunk's scales, read one chunk ahead
     float ks_next = 0.0f, vs_next = 0.0f;
+    const int kb0 = fb + 2 * c0 + (key >> 6);
+    const float* ks_at = p.c.k_scale + static_cast<int64_t>(h) * p.nblk + kb0;
+    const float* vs_at = p.c.v_scale + static_cast<int64_t>(h) * p.nblk + kb0;
     auto fetch_scales = [&](int i) {
-      const int kb = fb + 2 * (c0 + i) + (key >> 6);
-      if (i < n8 && kb < open) {
-        const int64_t at = static_cast<int64_t>(h) * p.nblk + kb;
-        ks_next = __ldg(p.c.k_scale + at);
-        vs_next = __ldg(p.c.v_scale + at);
+      if (i < n8 && kb0 + 2 * i < open) {
+        ks_next = __ldg(ks_at + 2 * i);
+        vs_next = __ldg(vs_at + 2 * i);
       }
     };
     fetch_scales(0);
@@ -636,7 +644,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const bool bf = has_tree && i == n - 1;
       const int b = fb + 2 * (c0 + i);
       float a = 0.0f, lv = 0.0f, iv = 0.0f;
-      unsigned long long vis = ~0ull;   // columns that see it
+      uint32_t vis = ~0u;   // columns that see it
       bool bad = false;
       const bool masked = bf || b + 2 > open || b * kBlk < lo_all;
       {
@@ -654,7 +662,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           else if (bf && key >= T) vis = s_see[key - T][cg];
           else if (p.window > 0) {
             const int dd = pos - C + p.window - 1;   // deepest node that sees it
-            vis = dd < 0 ? 0ull : s_upto[min(dd, maxdepth)][cg];
+            vis = dd < 0 ? 0u : s_upto[min(dd, maxdepth)][cg];
           }
         }
       }
@@ -697,10 +705,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], a, a, m.z, m.w);
         }
         if (masked) {
-          const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
           for (int c = 0; c < HC; ++c)
-            if (!((c < 32 ? v0 : v1) & (1u << (c & 31)))) x[c] = -INFINITY;
+            if (!(vis & (1u << c))) x[c] = -INFINITY;
         }
         if (pass == 0) {
           float top = -INFINITY;
@@ -761,44 +768,42 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (A::kPBufs == 1 && i >= 1) ok = role_wait(&b_pv[pb ^ 1], ((i - 1) >> 1) & 1, &s_dead);
       if (ok) {
         uint8_t* dst = sP + (A::kPBufs == 2 ? pb : 0) * A::kPBytes;
+        const uint32_t krow = static_cast<uint32_t>((key >> 3) * 1024 + (key & 7) * 128);
 #pragma unroll
-        for (int j = 0; j < HC / 8; ++j) {
-          uint32_t o[4];
+        for (int j = 0; j < HC / 4; ++j) {   // half a 16-byte piece
+          uint32_t o[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p0 = tc::ex2(x[8 * j + 2 * e]), p1 = tc::ex2(x[8 * j + 2 * e + 1]);
-            fma2(l[8 * j + 2 * e], l[8 * j + 2 * e + 1], p0, p1, iv, iv, l[8 * j + 2 * e],
-                 l[8 * j + 2 * e + 1]);
+          for (int e = 0; e < 2; ++e) {
+            const int c = 4 * j + 2 * e;
+            const float p0 = tc::ex2(x[c]), p1 = tc::ex2(x[c + 1]);
+            fma2(l[c], l[c + 1], p0, p1, iv, iv, l[c], l[c + 1]);
             o[e] = pack_half2(p0, p1);
           }
-          *reinterpret_cast<uint4*>(dst + tc::sw128_offset(key, cg * (HC / 8) + j, kAtKeys)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+          const int col = cg * HC + 4 * j, piece = col >> 3;
+          *reinterpret_cast<uint2*>(dst + (piece >> 3) * (kAtKeys * 128) + krow +
+                                    (((piece & 7) ^ (key & 7)) << 4) + (col & 4) * 2) =
+              make_uint2(o[0], o[1]);
         }
       }
       fence_proxy_async_smem();
       if (__all_sync(0xFFFFFFFFu, ok) && lane == 0) mbar_arrive(&b_p[pb]);
     }
     // ---- the unit's result
-    // sums over the lanes, eight columns at a time: three exchanges that
-    // halve the columns a lane holds, then two plain ones
+    // sums over the lanes, four columns at a time: two exchanges that halve
+    // the columns a lane holds, then three plain ones
 #pragma unroll
-    for (int c = 0; c < HC; c += 8) {
-      float s4[4], s2[2], s;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float send = lane & 16 ? l[c + k] : l[c + 4 + k];
-        s4[k] = (lane & 16 ? l[c + 4 + k] : l[c + k]) + __shfl_xor_sync(0xFFFFFFFFu, send, 16);
-      }
+    for (int c = 0; c < HC; c += 4) {
+      float s2[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float send = lane & 8 ? s4[k] : s4[2 + k];
-        s2[k] = (lane & 8 ? s4[2 + k] : s4[k]) + __shfl_xor_sync(0xFFFFFFFFu, send, 8);
+        const float send = lane & 16 ? l[c + k] : l[c + 2 + k];
+        s2[k] = (lane & 16 ? l[c + 2 + k] : l[c + k]) + __shfl_xor_sync(0xFFFFFFFFu, send, 16);
       }
-      const float send = lane & 4 ? s2[0] : s2[1];
-      s = (lane & 4 ? s2[1] : s2[0]) + __shfl_xor_sync(0xFFFFFFFFu, send, 4);
-      s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-      s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
-      if ((lane & 3) == 0) s_red[warp & 3][cg * HC + c + (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1)] = s;
+      const float send = lane & 8 ? s2[0] : s2[1];
+      float s = (lane & 8 ? s2[1] : s2[0]) + __shfl_xor_sync(0xFFFFFFFFu, send, 8);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      if ((lane & 7) == 0) s_red[warp & 3][cg * HC + c + (lane >> 4) * 2 + ((lane >> 3) & 1)] = s;
     }
     named_sync(5 + cg, 128);
     const int64_t slice = (static_cast<int64_t>(h) * gridDim.y + tile) * splits + split;
@@ -835,7 +840,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == SW + 8) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
@@ -982,7 +987,7 @@ static dfv_status attn_launch(const AttnParams& p, const MergeParams& m, cudaStr
     configured[dev].store(1, std::memory_order_release);
   }
   kv8_attn_kernel<D, R>
-      <<<dim3(m.splits, m.tiles, p.c.n_kv_heads), kAtThreads, A::kBytes, stream>>>(p);
+      <<<dim3(m.splits, m.tiles, p.c.n_kv_heads), A::kThreads, A::kBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DFV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.hq, p.n_nodes);

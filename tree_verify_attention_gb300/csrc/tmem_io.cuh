@@ -65,6 +65,40 @@ template <> struct TmemIo<16> {
   }
 };
 
+template <> struct TmemIo<20> {
+  static __device__ __forceinline__ void load(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%20];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 "
+        "{%16,%17,%18,%19}, [%21];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        :
+        "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
+        "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]),
+        "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]),
+        "=&r"(r[18]), "=&r"(r[19])
+        :
+        "r"(taddr + 0u), "r"(taddr + 16u)
+        : "memory");
+  }
+  // no wait: store_wait() before the columns are used
+  static __device__ __forceinline__ void store(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%20], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n\t"
+        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%21], "
+        "{%16,%17,%18,%19};\n\t"
+        :
+        :
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(taddr + 0u),
+        "r"(taddr + 16u)
+        : "memory");
+  }
+};
+
 template <> struct TmemIo<24> {
   static __device__ __forceinline__ void load(uint32_t taddr, uint32_t* r) {
     asm volatile(
@@ -130,47 +164,6 @@ template <> struct TmemIo<32> {
         "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr + 0u)
-        : "memory");
-  }
-};
-
-template <> struct TmemIo<40> {
-  static __device__ __forceinline__ void load(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%40];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 "
-        "{%32,%33,%34,%35,%36,%37,%38,%39}, [%41];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        :
-        "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
-        "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]),
-        "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]),
-        "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]),
-        "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]),
-        "=&r"(r[30]), "=&r"(r[31]), "=&r"(r[32]), "=&r"(r[33]), "=&r"(r[34]), "=&r"(r[35]),
-        "=&r"(r[36]), "=&r"(r[37]), "=&r"(r[38]), "=&r"(r[39])
-        :
-        "r"(taddr + 0u), "r"(taddr + 32u)
-        : "memory");
-  }
-  // no wait: store_wait() before the columns are used
-  static __device__ __forceinline__ void store(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%40], "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\t"
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%41], "
-        "{%32,%33,%34,%35,%36,%37,%38,%39};\n\t"
-        :
-        :
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(r[32]), "r"(r[33]), "r"(r[34]), "r"(r[35]),
-        "r"(r[36]), "r"(r[37]), "r"(r[38]), "r"(r[39]), "r"(taddr + 0u), "r"(taddr + 32u)
         : "memory");
   }
 };
