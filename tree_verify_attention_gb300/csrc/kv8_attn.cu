@@ -41,6 +41,7 @@
 
 #include <atomic>
 #include <math.h>
+#include <type_traits>
 
 #include "kv8.cuh"
 #include "tc.cuh"
@@ -215,7 +216,8 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   __shared__ uint32_t s_see[kMaxNodes][NG], s_dep[kMaxNodes][NG], s_upto[kMaxNodes][NG];
   __shared__ __align__(16) float s_neg[R], s_f[R], s_zero[R];   // s_neg: -reference
   __shared__ float s_red[4][R];
-  __shared__ float s_ksc[kAtKeys], s_vfac[kAtKeys];
+  __shared__ float s_ksc[kAtKeys];
+  __shared__ __align__(8) float s_vfac[kAtKeys];
   __shared__ int s_vexp[kAtKeys], s_bad[2][kAtKeys];
   __shared__ uint32_t s_qmax;
 
@@ -429,39 +431,35 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     }
   } else if (warp >= SW) {
     // ------------------------------------------------------ operands to TMEM
-    const bool is_v = warp >= SW + 4;
-    const int slot = (warp & 3) * 32 + lane;   // key (K) or dim of a half (V)
-    uint64_t* raw_full = is_v ? b_vraw : b_kraw;
-    uint64_t* raw_done = is_v ? b_vdone : b_kdone;
-    uint64_t* hat = is_v ? b_vhat : b_khat;
-    uint64_t* hat_free = is_v ? b_vfree : b_kfree;
-    const uint32_t t_op = tmem + lanes + (is_v ? A::kTV : A::kTK);
-    const int subs = is_v ? 2 * A::kHalves : D / 64;   // pieces of 32 columns
-    const bool works = !is_v || D >= 128 || slot < D;   // D = 64: V^T has 64 lanes
-    // the bytes of 32 columns, for this thread: K 64 dims of its key (pieces
-    // 64 * 16 apart), V 64 keys of its dim (pieces D * 16 apart)
-    const int base0 = is_v ? A::kRaw + slot * 16 : (slot >> 6) * kBlk * D + (slot & 63) * 16;
-    const int step = is_v ? D * 16 : kBlk * 16;
-    bool ok = true;
-    constexpr int kPer = A::kPart / 32;     // 32-column pieces of a part
-    // 32 columns of chunk i, converted and waiting in registers, into TMEM
-    // once the products have read the last chunk's part; give() hands it over.
-    auto put = [&](int i, int c, const uint32_t* w) {
-      if (i > 0 && c % kPer == 0)
-        ok = is_v && c / kPer == A::kVSub - 1
-                 ? role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead)
-                 : role_wait(&hat_free[c / kPer], (i - 1) & 1, &s_dead);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) return;
-      tc::fence_after_sync();
-      if (works) tc::TmemIo<32>::store(t_op + c * 32, w);
+    // One body for both operands, unrolled: what differs are constants.
+    auto convert = [&](auto tag) {
+      constexpr bool kV = decltype(tag)::value;
+      const int slot = (warp & 3) * 32 + lane;   // key (K) or dim of a half (V)
+      uint64_t* raw_full = kV ? b_vraw : b_kraw;
+      uint64_t* raw_done = kV ? b_vdone : b_kdone;
+      uint64_t* hat = kV ? b_vhat : b_khat;
+      const uint32_t t_op = tmem + lanes + (kV ? A::kTV : A::kTK);
+      constexpr int kParts = kV ? A::kVSub : A::kKSub, kPer = A::kPart / 32;   // of 32-column pieces
+      constexpr int kPieces = kParts * kPer;
+      const bool works = !kV || D >= 128 || slot < D;   // D = 64: V^T has 64 lanes
+      // the bytes of a piece, for this thread: K 64 dims of its key (16-byte
+      // pieces 64 * 16 apart), V 64 keys of its dim (D * 16 apart)
+      const int base0 = kV ? A::kRaw + slot * 16 : (slot >> 6) * kBlk * D + (slot & 63) * 16;
+      bool ok = true;
+      // A part's columns are free once the products have read the last chunk's.
+      auto take = [&](int i, int part) {
+        if (i > 0)
+          ok = kV && part == kParts - 1
+                   ? role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead)
+                   : role_wait(kV ? &b_vfree[part] : &b_kfree[part], (i - 1) & 1, &s_dead);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc::fence_after_sync();
     };
-    auto give = [&](int c) {
-      if (c % kPer != kPer - 1) return;
+    auto give = [&](int part) {
       tc::store_wait();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&hat[c / kPer]);
+      if (lane == 0) mbar_arrive(&hat[part]);
     };
     for (int i = 0; ok && i < n8; ++i) {
       const int s = i % A::kStages;
@@ -470,95 +468,99 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
       if (!ok) break;
       const uint8_t* raw = smem + s * 2 * A::kRaw + base0;
       uint4 q[4];
-      // V piece (half, block): dims 128 on, keys of the second block
-      auto fetch = [&](int c) {
-        const uint8_t* mine = raw + (is_v ? (c >> 1) * 128 * 16 + (c & 1) * kBlk * D
-                                          : c * 4 * kBlk * 16);
+      auto fetch = [&](int c) {   // V piece (half, block): dims 128 on, keys of the second block
+        const int at = kV ? (c >> 1) * 128 * 16 + (c & 1) * kBlk * D : c * 4 * kBlk * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const uint4*>(mine + j * step);
+        for (int j = 0; j < 4; ++j)
+          q[j] = *reinterpret_cast<const uint4*>(raw + at + j * (kV ? D : kBlk) * 16);
       };
       if (works) fetch(0);
-      // two sets of registers (where there are as many): the store of one
-      // part reads its own while the next part is converted
-      uint32_t w0[32], w1[SW == 8 ? 32 : 1];
-      auto part = [&](int c, uint32_t* w) {
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        uint32_t w[32];
         if (works) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) codes_to_half(q[j], w + 8 * j);
-          if (c + 1 < subs) fetch(c + 1);   // lands while this part is handed over
+          if (c + 1 < kPieces) fetch(c + 1);   // lands while this piece is handed over
         }
-        if (c > 0) give(c - 1);
-        put(i, c, w);
-      };
-#pragma unroll 1
-      for (int c = 0; c < subs; c += 2) {
-        part(c, w0);
-        if (!ok) break;
-        if (c + 1 < subs) part(c + 1, SW == 8 ? w1 : w0);
-        if (!ok) break;
+        if (c + 1 == kPieces) {   // every code is in registers
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_done[s]);
+        }
+        if (c % kPer == 0) {
+          // a store takes its time: waited for after the next conversion
+          if (c > 0) give(c / kPer - 1);
+          take(i, c / kPer);
+          if (!ok) break;
+        }
+        if (works) tc::TmemIo<32>::store(t_op + c * 32, w);
       }
       if (!ok) break;
-      give(subs - 1);
-      if (lane == 0) mbar_arrive(&raw_done[s]);
+      give(kParts - 1);
     }
     if (has_tree) {
       // The bf16 chunk: key slots [0, T) are the open block's rows, then the
       // tree nodes. Each key is scaled to binary16 by a power of two (largest
       // magnitude in [64, 128)).
-      ok = ok && role_wait(is_v ? &b_vrow : &b_krow, 0, &s_dead);
-      ok = named_sync_and(is_v ? 3 : 2, 128, ok);
-      if (ok) {
-        uint8_t* rows = smem + (is_v ? kAtKeys * A::kRowB : 0);
-        uint8_t* row = rows + slot * A::kRowB;
-        const bool live = slot < live_rows;
-        const uint32_t m = live ? row_max<D>(row) : 0u;
-        const bool bad = m >= kBigBits;   // infinite, NaN or out of range
-        const int e = max(static_cast<int>(m >> 7), 86);
-        const float f = bad || !live ? 0.0f : pow2i(133 - e);
-        s_bad[is_v][slot] = bad;
-        if (bad) report(p.status, DFV_DEV_NONFINITE);
-        if (!is_v) {
-          s_ksc[slot] = bad ? 0.0f : pow2i(e - 133);
-        } else {
-          s_vexp[slot] = bad ? 0 : e - 133;
-          s_vfac[slot] = f;
-        }
-        if (bad || !live) {   // no 0 * inf below
+      ok = ok && role_wait(kV ? &b_vrow : &b_krow, 0, &s_dead);
+      ok = named_sync_and(kV ? 3 : 2, 128, ok);
+      if (!ok) return;
+      uint8_t* rows = smem + (kV ? kAtKeys * A::kRowB : 0);
+      uint8_t* row = rows + slot * A::kRowB;
+      const bool live = slot < live_rows;
+      const uint32_t m = live ? row_max<D>(row) : 0u;
+      const bool bad = m >= kBigBits;   // infinite, NaN or out of range
+      const int e = max(static_cast<int>(m >> 7), 86);
+      const float f = bad || !live ? 0.0f : pow2i(133 - e);
+      s_bad[kV][slot] = bad;
+      if (bad) report(p.status, DFV_DEV_NONFINITE);
+      if (!kV) {
+        s_ksc[slot] = bad ? 0.0f : pow2i(e - 133);
+      } else {
+        s_vexp[slot] = bad ? 0 : e - 133;
+        s_vfac[slot] = f;
+      }
+      if (bad || !live) {   // no 0 * inf below
 #pragma unroll 1
-          for (int j = 0; j < D / 8; ++j)
-            *reinterpret_cast<uint4*>(row + j * 16) = make_uint4(0, 0, 0, 0);
-        }
-        if (is_v) named_sync(3, 128);
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<uint4*>(row + j * 16) = make_uint4(0, 0, 0, 0);
+      }
+      if (kV) named_sync(3, 128);
 #pragma unroll 1
-        for (int c = 0; c < subs; ++c) {
-          uint32_t w[32];
-          if (!is_v) {
+      for (int c = 0; c < kPieces; ++c) {
+        uint32_t w[32];
+        if (!kV) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint4 x = *reinterpret_cast<const uint4*>(row + (c * 8 + j) * 16);
-              w[4 * j] = scaled_half2(x.x, f);
-              w[4 * j + 1] = scaled_half2(x.y, f);
-              w[4 * j + 2] = scaled_half2(x.z, f);
-              w[4 * j + 3] = scaled_half2(x.w, f);
-            }
-          } else if (works) {
-            const int d = (c >> 1) * 128 + slot, kb = (c & 1) * 64;
-            const uint8_t* col = rows + kb * A::kRowB + d * 2;
-            const float2* fac = reinterpret_cast<const float2*>(s_vfac + kb);
-#pragma unroll
-            for (int q = 0; q < 32; ++q) {
-              const uint32_t a = *reinterpret_cast<const uint16_t*>(col + 2 * q * A::kRowB);
-              const uint32_t b = *reinterpret_cast<const uint16_t*>(col + (2 * q + 1) * A::kRowB);
-              const float2 g = fac[q];
-              w[q] = pack_half2(__uint_as_float(a << 16) * g.x, __uint_as_float(b << 16) * g.y);
-            }
+          for (int j = 0; j < 8; ++j) {
+            const uint4 x = *reinterpret_cast<const uint4*>(row + (c * 8 + j) * 16);
+            w[4 * j] = scaled_half2(x.x, f);
+            w[4 * j + 1] = scaled_half2(x.y, f);
+            w[4 * j + 2] = scaled_half2(x.z, f);
+            w[4 * j + 3] = scaled_half2(x.w, f);
           }
-          put(n8, c, w);
-          if (!ok) break;
-          give(c);
+        } else if (works) {
+          const int d = (c >> 1) * 128 + slot, kb = (c & 1) * 64;
+          const uint8_t* col = rows + kb * A::kRowB + d * 2;
+          const float2* fac = reinterpret_cast<const float2*>(s_vfac + kb);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            const uint32_t a = *reinterpret_cast<const uint16_t*>(col + 2 * q * A::kRowB);
+            const uint32_t b = *reinterpret_cast<const uint16_t*>(col + (2 * q + 1) * A::kRowB);
+            const float2 g = fac[q];
+            w[q] = pack_half2(__uint_as_float(a << 16) * g.x, __uint_as_float(b << 16) * g.y);
+          }
         }
+        if (c % kPer == 0) {
+          take(n8, c / kPer);
+          if (!ok) break;
+        }
+        if (works) tc::TmemIo<32>::store(t_op + c * 32, w);
+        if (c % kPer == kPer - 1) give(c / kPer);
       }
     }
+    };
+    if (warp >= SW + 4) convert(std::true_type{});
+    else convert(std::false_type{});
   } else {
     // ------------------------------------------------------ Q, tree, softmax
     const int cg = warp >> 2;                  // column group
@@ -622,51 +624,53 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
 #pragma unroll
     for (int c = 0; c < HC; ++c) l[c] = 0.0f;
     const uint32_t t_s = tmem + lanes + A::kTS + cg * HC;
-    const uint32_t t_o = tmem + lanes + A::kTO + cg * HC;
+    const uint32_t t_o = t_s + (A::kTO - A::kTS);
     const float4* m4 = reinterpret_cast<const float4*>(s_neg + cg * HC);
     const float4* zero4 = reinterpret_cast<const float4*>(s_zero + cg * HC);
 
-    // a chunk's scales, read one chunk ahead
-    float ks_next = 0.0f, vs_next = 0.0f;
-    const int kb0 = fb + 2 * c0 + (key >> 6);
-    const float* ks_at = p.c.k_scale + static_cast<int64_t>(h) * p.nblk + kb0;
-    const float* vs_at = p.c.v_scale + static_cast<int64_t>(h) * p.nblk + kb0;
-    auto fetch_scales = [&](int i) {
-      if (i < n8 && kb0 + 2 * i < open) {
-        ks_next = __ldg(ks_at + 2 * i);
-        vs_next = __ldg(vs_at + 2 * i);
-      }
-    };
-    fetch_scales(0);
+    // Chunks [m_lo, m_hi) need no mask: their blocks are complete and inside
+    // every node's window. The loop keeps little beside x and l: what a masked
+    // chunk needs is worked out in its branch.
+    int m_lo = p.window > 0 ? (lo_all + kBlk - 1) / kBlk - fb - 2 * c0 : 0;   // in blocks, from c0
+    m_lo = m_lo > 0 ? (m_lo + 1) / 2 : 0;
+    const int m_hi = n8 - (n8 > 0 && fb + 2 * (c0 + n8) > open ? 1 : 0);
+    // a chunk's scales, read one chunk ahead: this lane's block of chunk i is
+    // sc_at + 2 i of the scales, there for i < sc_n
+    const uint32_t sc_at = static_cast<uint32_t>(h) * p.nblk + fb + 2 * c0 + (key >> 6);
+    const int sc_n = min(n8, (open - (fb + 2 * c0 + (key >> 6)) + 1) / 2);
+    float ks = 0.0f, vs = 0.0f;
+    if (0 < sc_n) {
+      ks = __ldg(p.c.k_scale + sc_at);
+      vs = __ldg(p.c.v_scale + sc_at);
+    }
 
     for (int i = 0; i < n; ++i) {
-      // this lane's key
+      // this lane's key: its factors, and the columns that see it
       const bool bf = has_tree && i == n - 1;
-      const int b = fb + 2 * (c0 + i);
-      float a = 0.0f, lv = 0.0f, iv = 0.0f;
-      uint32_t vis = ~0u;   // columns that see it
+      const bool masked = i < m_lo || i >= m_hi;
+      const float sv = fmaxf(vs, 7.1054274e-15f);   // 2^-47
+      float a = ks * sc;
+      float lv = lg2_fast(sv);      // within 2^-20, in both
+      float iv = tc::ex2(-lv);
+      uint32_t vis = ~0u;
       bool bad = false;
-      const bool masked = bf || b + 2 > open || b * kBlk < lo_all;
-      {
-        const int kb = bf ? open + (key >= T) : b + (key >> 6);
-        const int pos = bf ? open * kBlk + key : kb * kBlk + (key & 63);
-        const bool live = bf ? key < live_rows : kb < open;
-        if (live && !bf) {
-          a = ks_next * sc;
-          const float sv = fmaxf(vs_next, 7.1054274e-15f);   // 2^-47
-          lv = lg2_fast(sv);      // within 2^-20, in both
-          iv = tc::ex2(-lv);
-        }
-        if (masked) {
-          if (!live) vis = 0;
-          else if (bf && key >= T) vis = s_see[key - T][cg];
-          else if (p.window > 0) {
-            const int dd = pos - C + p.window - 1;   // deepest node that sees it
-            vis = dd < 0 ? 0u : s_upto[min(dd, maxdepth)][cg];
-          }
+      if (masked) {
+        const int pos = bf ? open * kBlk + key : (fb + 2 * (c0 + i)) * kBlk + key;
+        const bool live = bf ? key < live_rows : pos < open * kBlk;
+        if (!live) {
+          vis = 0;
+          a = lv = iv = 0.0f;
+        } else if (bf && key >= T) {
+          vis = s_see[key - T][cg];
+        } else if (p.window > 0) {
+          const int dd = pos - C + p.window - 1;   // deepest node that sees it
+          vis = dd < 0 ? 0u : s_upto[min(dd, s_maxdepth)][cg];
         }
       }
-      fetch_scales(i + 1);
+      if (i + 1 < sc_n) {
+        ks = __ldg(p.c.k_scale + (sc_at + 2 * (i + 1)));
+        vs = __ldg(p.c.v_scale + (sc_at + 2 * (i + 1)));
+      }
       ok = ok && role_wait(&b_kfree[A::kKSub - 1], i & 1, &s_dead);
       if (bf) {   // the key's scales were written with the operands
         ok = ok && role_wait(&b_khat[A::kKSub - 1], i & 1, &s_dead) &&

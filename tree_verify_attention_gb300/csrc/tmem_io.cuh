@@ -37,6 +37,36 @@ template <> struct TmemIo<8> {
   }
 };
 
+template <> struct TmemIo<12> {
+  static __device__ __forceinline__ void load(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7}, [%12];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 "
+        "{%8,%9,%10,%11}, [%13];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        :
+        "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
+        "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11])
+        :
+        "r"(taddr + 0u), "r"(taddr + 8u)
+        : "memory");
+  }
+  // no wait: store_wait() before the columns are used
+  static __device__ __forceinline__ void store(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%12], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7};\n\t"
+        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%13], "
+        "{%8,%9,%10,%11};\n\t"
+        :
+        :
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(taddr + 0u), "r"(taddr + 8u)
+        : "memory");
+  }
+};
+
 template <> struct TmemIo<16> {
   static __device__ __forceinline__ void load(uint32_t taddr, uint32_t* r) {
     asm volatile(
