@@ -36,7 +36,7 @@
 // Roles of a CTA (one per SM): 8 or 16 softmax warps (lane quadrant w % 4,
 // column group w / 4), four warps that put K codes into TMEM, four for V, one
 // that issues MMAs, two that copy K and V. A unit is (KV head, tile of at
-// most 80 query rows, slice of the chunks). Bound by HBM while a tile has few
+// most 80 or 96 query rows, slice of the chunks). Bound by HBM while a tile has few
 // rows, by the softmax and the conversion of the codes for many.
 
 #include <atomic>
@@ -940,15 +940,17 @@ struct AttnPlan {
   int tiles, rows_tile, r, splits;
 };
 
-constexpr int kMaxRows = 80;   // query rows of a tile (TMEM columns at D = 256)
+// Query rows of a tile: TMEM columns bound it at D = 256, the softmax's
+// registers (a quarter of the columns a thread, twice) below.
+constexpr int max_rows(int d) { return d == 256 ? 80 : 96; }
 
-// Tiles of at most 80 rows, as even as they come. Slices: a unit costs its
+// The fewest tiles, as even as they come. Slices: a unit costs its
 // chunks plus about two for its start and end, and the SMs take units in
 // waves; the count with the least time, the fewest of equals.
-static AttnPlan attn_plan(int n_nodes, int hq, int hkv, int window, int capacity) {
+static AttnPlan attn_plan(int n_nodes, int hq, int hkv, int d, int window, int capacity) {
   AttnPlan pl;
   const int rows = n_nodes * (hq / hkv);
-  pl.tiles = (rows + kMaxRows - 1) / kMaxRows;
+  pl.tiles = (rows + max_rows(d) - 1) / max_rows(d);
   pl.rows_tile = (rows + pl.tiles - 1) / pl.tiles;
   pl.r = (pl.rows_tile + 15) / 16 * 16;
   const int span = window > 0 && window < capacity ? window : capacity;
@@ -1012,7 +1014,10 @@ static dfv_status attn_launch_r(const AttnParams& p, const MergeParams& m, cudaS
     case 32: return attn_launch<D, 32>(p, m, stream);
     case 48: return attn_launch<D, 48>(p, m, stream);
     case 64: return attn_launch<D, 64>(p, m, stream);
-    default: return attn_launch<D, 80>(p, m, stream);
+    case 80: return attn_launch<D, 80>(p, m, stream);
+    default:
+      if constexpr (D <= 128) return attn_launch<D, 96>(p, m, stream);
+      return DFV_ERR_UNSUPPORTED;
   }
 }
 
@@ -1022,7 +1027,7 @@ extern "C" size_t dfv_kv8_attn_workspace_bytes(int n_nodes, int n_q_heads, int n
                                                int head_dim, int window, int cache_capacity) {
   using namespace dfv;
   if (!attn_shape_ok(n_nodes, n_q_heads, n_kv_heads, head_dim, window, cache_capacity)) return 0;
-  return attn_ws_bytes(attn_plan(n_nodes, n_q_heads, n_kv_heads, window, cache_capacity),
+  return attn_ws_bytes(attn_plan(n_nodes, n_q_heads, n_kv_heads, head_dim, window, cache_capacity),
                        n_kv_heads, head_dim);
 }
 
@@ -1041,7 +1046,7 @@ extern "C" dfv_status dfv_kv8_attn(const dfv_kv8_cache* cache, int n_nodes, int 
   if (!q || !tree_k || !tree_v || !parent || !out || !aligned(q, 16) || !aligned(tree_k, 16) ||
       !aligned(tree_v, 16) || !aligned(out, 16))
     return DFV_ERR_INVALID;
-  const AttnPlan pl = attn_plan(n_nodes, n_q_heads, hkv, window, cache->capacity);
+  const AttnPlan pl = attn_plan(n_nodes, n_q_heads, hkv, d, window, cache->capacity);
   if (!workspace || !aligned(workspace, 256)) return DFV_ERR_INVALID;
   if (workspace_bytes < attn_ws_bytes(pl, hkv, d)) return DFV_ERR_WORKSPACE;
   AttnParams p = {};
