@@ -9,9 +9,10 @@
 // Everything comes from one pass over the row: each thread carries a running
 // (m, s, sum exp(z) z), rescaled when its maximum moves, and the partial
 // triples are merged in a fixed order. The kernel is bound by memory for many
-// rows and by latency for few, so a row belongs to a cluster of 1 to 8 CTAs
-// (the fewer the rows, the more) whose results meet through distributed
-// shared memory: one launch, no workspace, nothing to reset.
+// rows and by latency for few, so a row belongs to a cluster of 1 to 16 CTAs
+// that write their results into the first one's shared memory (one launch, no
+// workspace, nothing to reset). Few rows get CTAs of 1024 threads: a slice of
+// 152 K logits then is one round of loads.
 //
 // The alternatives cost next to nothing beside that pass. The first chunk of
 // a slice (its values stay in registers) is cut into 64 groups; the top-th
@@ -23,6 +24,7 @@
 // Candidates are ordered by a 64-bit key (value, then lower index), which is
 // unique, so the result does not depend on the order of collection.
 
+#include <atomic>
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -31,9 +33,9 @@ namespace dfv {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpThreads = 256;
 constexpr int kLpGroups = 64;       // >= DFV_MAX_TOP
 constexpr int kLpCap = 2048;        // candidates a CTA can hold
+constexpr int kLpMaxCluster = 16;
 constexpr int kLpVecs = 4;          // 16-byte loads per thread and chunk
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -55,11 +57,37 @@ __device__ __forceinline__ float lp_ex2(float x) {
   return y;
 }
 
-// max that keeps a NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
+// maximum that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
+}
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 lp_add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 lp_mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 lp_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
 
 // Orders like (value, lower index first); -0 equals +0.
@@ -126,15 +154,19 @@ struct LpSmem {
   uint64_t buf[kLpCap];
   uint64_t gkey[kLpGroups];
   uint64_t best[DFV_MAX_TOP];   // the slice's, in order
-  float gmax[kLpThreads];
-  LpStats wst[kLpThreads / 32];
+  float gmax[kLpGroups];
+  LpStats wst[32];
   LpStats st;
   uint64_t cut;
   float bound;
   int count, n_best;
+  // the cluster's slices, written by their CTAs (first CTA only)
+  LpStats cst[kLpMaxCluster];
+  int cn[kLpMaxCluster];
+  uint64_t cbest[kLpMaxCluster][DFV_MAX_TOP];
 };
 
-// Adds n values (all of one thread) to its statistics.
+// Adds kN values with maximum vm (all of one thread) to its statistics.
 template <int kN, typename F>
 __device__ __forceinline__ void lp_add(LpStats& st, float vm, F value) {
   if (!(vm <= st.m)) {
@@ -142,22 +174,21 @@ __device__ __forceinline__ void lp_add(LpStats& st, float vm, F value) {
     else st.m = st.s = st.t = NAN;   // NaN stays: comparisons with it fail
   }
   if (st.m == -INFINITY) return;     // nothing but -inf so far
-  float s0 = 0.0f, s1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+  float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
+  const float2 m2 = make_float2(-st.m, -st.m), c2 = make_float2(kLog2e, kLog2e);
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
+  for (int i = 0; i < kN; i += 2) {
+    float2 z = lp_add2(make_float2(value(i), kN > 1 ? value(i + 1) : -INFINITY), m2);
     // exp(-200) is zero; the limit keeps 0 * -inf out of the sum
-    const float z = fmaxf(value(i) - st.m, -200.0f);
-    const float e = lp_ex2(z * kLog2e);
-    if (i & 1) {
-      s1 += e;
-      t1 = fmaf(e, z, t1);
-    } else {
-      s0 += e;
-      t0 = fmaf(e, z, t0);
-    }
+    z.x = fmaxf(z.x, -200.0f);
+    z.y = fmaxf(z.y, -200.0f);
+    const float2 y = lp_mul2(z, c2);
+    const float2 e = make_float2(lp_ex2(y.x), lp_ex2(y.y));
+    s2 = lp_add2(s2, e);
+    t2 = lp_fma2(e, z, t2);
   }
-  st.s += s0 + s1;
-  st.t += t0 + t1;
+  st.s += s2.x + s2.y;
+  st.t += t2.x + t2.y;
 }
 
 __device__ __forceinline__ void lp_push(LpSmem& sm, float x, int idx) {
@@ -168,12 +199,12 @@ __device__ __forceinline__ void lp_push(LpSmem& sm, float x, int idx) {
 // The best `top` of buf[0, c), in order, into sm.best (n_best of them).
 // All threads; c <= kLpCap. Large sets are cut first: at least `top` keys
 // reach the top-th largest of the group maxima.
+template <int kLpThreads>
 __device__ void lp_select(LpSmem& sm, int c, int top) {
   const int tid = threadIdx.x;
-  while (c > kLpThreads) {
+  while (c > 256) {
     uint64_t mine = 0;
     for (int i = tid; i < c; i += kLpThreads) mine = max(mine, sm.buf[i]);
-    // threads tid, tid ^ 64, ... form a group
     uint64_t* all = sm.gkey;
     if (tid < kLpGroups) all[tid] = 0;
     __syncthreads();
@@ -187,10 +218,11 @@ __device__ void lp_select(LpSmem& sm, int c, int top) {
     }
     __syncthreads();
     const uint64_t cut = sm.cut;
-    uint64_t keep[kLpCap / kLpThreads];
+    constexpr int kKeep = kLpCap / kLpThreads;
+    uint64_t keep[kKeep];
     int n = 0;
 #pragma unroll
-    for (int j = 0; j < kLpCap / kLpThreads; ++j) {
+    for (int j = 0; j < kKeep; ++j) {
       const int i = tid + j * kLpThreads;
       keep[j] = i < c ? sm.buf[i] : 0;
       n += keep[j] >= cut && keep[j] != 0;
@@ -199,7 +231,7 @@ __device__ void lp_select(LpSmem& sm, int c, int top) {
     __syncthreads();
     int at = n ? atomicAdd(&sm.count, n) : 0;
 #pragma unroll
-    for (int j = 0; j < kLpCap / kLpThreads; ++j)
+    for (int j = 0; j < kKeep; ++j)
       if (keep[j] >= cut && keep[j] != 0) sm.buf[at++] = keep[j];
     __syncthreads();
     const int left = sm.count;
@@ -211,6 +243,7 @@ __device__ void lp_select(LpSmem& sm, int c, int top) {
   for (int i = tid; i < c; i += kLpThreads) {
     const uint64_t mine = sm.buf[i];
     int above = 0;
+#pragma unroll 8
     for (int k = 0; k < c; ++k) above += sm.buf[k] > mine;
     if (above < top) sm.best[above] = mine;
   }
@@ -218,8 +251,15 @@ __device__ void lp_select(LpSmem& sm, int c, int top) {
   __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_constant__ LogprobParams p) {
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <typename T, int kLpThreads>
+__global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) logprob_kernel(const __grid_constant__ LogprobParams p) {
   __shared__ LpSmem sm;
   constexpr int kV = LpVec<T>::kN;
   cg::cluster_group cl = cg::this_cluster();
@@ -242,6 +282,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
                       (rank == cs - 1 ? p.vocab - head - nv * kV : 0);
   const int top = p.top;
   if (tid == 0) sm.count = 0;
+  if (cs > 1) cluster_arrive();   // waited for before the first CTA's memory is written
 
   LpStats st;
   st.init();
@@ -257,15 +298,22 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
     }
   };
   auto value = [&](int i) { return LpVec<T>::at(v[i / kV], i % kV); };
+  float jm[kLpVecs];   // maximum of each vector
   auto chunk_max = [&]() {
-    float vm = value(0);
 #pragma unroll
-    for (int i = 1; i < kV * kLpVecs; ++i) vm = max_nan(vm, value(i));
-    return vm;
+    for (int j = 0; j < kLpVecs; ++j) {
+      jm[j] = max_nan(value(j * kV), value(j * kV + 1), value(j * kV + 2));
+#pragma unroll
+      for (int e = 3; e < kV; e += 2)
+        jm[j] = max_nan(jm[j], value(j * kV + e), value(j * kV + (e + 1 < kV ? e + 1 : e)));
+    }
+    static_assert(kLpVecs == 4, "maximum of four");
+    return max_nan(max_nan(jm[0], jm[1], jm[2]), jm[3], jm[3]);
   };
   auto push_from = [&](int base, float bound) {
 #pragma unroll
     for (int j = 0; j < kLpVecs; ++j) {
+      if (!(jm[j] >= bound)) continue;
       const int i = base + j * kLpThreads + tid;
 #pragma unroll
       for (int e = 0; e < kV; ++e) {
@@ -283,20 +331,16 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
   if (extra >= 0) lp_add<1>(st, xe, [&](int) { return xe; });
   float bound = INFINITY;
   if (top > 0) {
-    sm.gmax[tid] = fmaxf(vm, xe);
+    constexpr int kLanes = kLpThreads / kLpGroups;   // neighbouring lanes form a group
+    float g = fmaxf(vm, xe);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
+    if (tid % kLanes == 0) sm.gmax[tid / kLanes] = g;
     __syncthreads();
-    float g = 0.0f;
     if (tid < kLpGroups) {
       g = sm.gmax[tid];
-#pragma unroll
-      for (int k = 1; k < kLpThreads / kLpGroups; ++k) g = fmaxf(g, sm.gmax[tid + k * kLpGroups]);
-    }
-    __syncthreads();
-    if (tid < kLpGroups) sm.gmax[tid] = g;
-    __syncthreads();
-    if (tid < kLpGroups) {
       int above = 0, same = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int k = 0; k < kLpGroups; ++k) {
         above += sm.gmax[k] > g;
         same += sm.gmax[k] >= g;
@@ -327,10 +371,18 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
   }
   if (lane == 0) sm.wst[warp] = st;
   __syncthreads();
-  if (tid == 0) {
-    LpStats a = sm.wst[0];
-    for (int w = 1; w < kLpThreads / 32; ++w) a.merge(sm.wst[w]);
-    sm.st = a;
+  if (warp == 0) {   // then the warps, in a tree as well
+    st.init();
+    if (lane < kLpThreads / 32) st = sm.wst[lane];
+#pragma unroll
+    for (int o = kLpThreads / 64; o > 0; o >>= 1) {
+      LpStats b;
+      b.m = __shfl_down_sync(0xFFFFFFFFu, st.m, o);
+      b.s = __shfl_down_sync(0xFFFFFFFFu, st.s, o);
+      b.t = __shfl_down_sync(0xFFFFFFFFu, st.t, o);
+      st.merge(b);
+    }
+    if (lane == 0) sm.st = st;
   }
   // ---- alternatives of the slice
   if (top > 0) {
@@ -354,7 +406,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
         c = sm.count;
         __syncthreads();
         if (c > kLpCap - kRound) {
-          lp_select(sm, c, top);
+          lp_select<kLpThreads>(sm, c, top);
           c = sm.n_best;
           cut = c == top ? sm.best[top - 1] : 0;
           if (tid < c) sm.buf[tid] = sm.best[tid];
@@ -363,56 +415,69 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
         }
       }
     }
-    lp_select(sm, c, top);
+    lp_select<kLpThreads>(sm, c, top);
   } else {
     __syncthreads();
   }
-  // ---- the cluster's CTAs in order, by the first one
-  if (cs > 1) cl.sync();
-  if (rank == 0) {
-    LpStats a = sm.st;
-    for (int r = 1; r < cs; ++r) a.merge(*cl.map_shared_rank(&sm.st, r));
-    const float logs = logf(a.s);
+  // ---- the cluster's slices meet in the first CTA
+  if (cs > 1) {
+    __syncthreads();   // the slice's results are there
+    cluster_wait();
+    LpSmem* o = cl.map_shared_rank(&sm, 0);
     if (tid == 0) {
-      if (p.logprob) {
-        const int t = p.tokens[row];
-        const bool in = t >= 0 && t < p.vocab;
-        if (!in) report(p.status, DFV_DEV_BAD_TOKEN);
-        p.logprob[row] = in ? (lp_to_f32(x[t]) - a.m) - logs : NAN;
+      o->cst[rank] = sm.st;
+      o->cn[rank] = top > 0 ? sm.n_best : 0;
+    }
+    if (top > 0 && tid < sm.n_best) o->cbest[rank][tid] = sm.best[tid];
+    cluster_arrive();
+    cluster_wait();
+    if (rank != 0) return;
+    if (warp == 0) {
+      st.init();
+      if (lane < cs) st = sm.cst[lane];
+#pragma unroll
+      for (int k = kLpMaxCluster / 2; k > 0; k >>= 1) {
+        LpStats b;
+        b.m = __shfl_down_sync(0xFFFFFFFFu, st.m, k);
+        b.s = __shfl_down_sync(0xFFFFFFFFu, st.s, k);
+        b.t = __shfl_down_sync(0xFFFFFFFFu, st.t, k);
+        st.merge(b);
       }
-      if (p.entropy) p.entropy[row] = logs - a.t / a.s;
+      if (lane == 0) sm.st = st;
     }
     if (top > 0) {
-      int c = sm.n_best;
-      if (cs > 1) {
-        __syncthreads();
-        if (tid < c) sm.buf[tid] = sm.best[tid];
-        for (int r = 1; r < cs; ++r) {
-          const LpSmem* o = cl.map_shared_rank(&sm, r);
-          const int n = o->n_best;
-          if (tid < n) sm.buf[c + tid] = o->best[tid];
-          c += n;
-        }
-        __syncthreads();
-        lp_select(sm, c, top);
+      int c = 0;
+      for (int r = 0; r < cs; ++r) {
+        const int n = sm.cn[r];
+        if (tid < n) sm.buf[c + tid] = sm.cbest[r][tid];
+        c += n;
       }
-      if (tid < top) {
-        const uint64_t key = sm.best[tid];
-        const int64_t at = static_cast<int64_t>(row) * top + tid;
-        if (p.top_ids) p.top_ids[at] = lp_index(key);
-        if (p.top_logprobs) p.top_logprobs[at] = (lp_value(key) - a.m) - logs;
-      }
+      __syncthreads();
+      lp_select<kLpThreads>(sm, c, top);
     }
   }
-  if (cs > 1) cl.sync();   // the others' shared memory is read until here
+  __syncthreads();
+  const LpStats a = sm.st;
+  const float logs = logf(a.s);
+  if (tid == 0) {
+    if (p.logprob) {
+      const int t = p.tokens[row];
+      const bool in = t >= 0 && t < p.vocab;
+      if (!in) report(p.status, DFV_DEV_BAD_TOKEN);
+      p.logprob[row] = in ? (lp_to_f32(x[t]) - a.m) - logs : NAN;
+    }
+    if (p.entropy) p.entropy[row] = logs - a.t / a.s;
+  }
+  if (tid < top) {
+    const uint64_t key = sm.best[tid];
+    const int64_t at = static_cast<int64_t>(row) * top + tid;
+    if (p.top_ids) p.top_ids[at] = lp_index(key);
+    if (p.top_logprobs) p.top_logprobs[at] = (lp_value(key) - a.m) - logs;
+  }
 }
 
-template <typename T>
-dfv_status logprob_launch(const LogprobParams& p, int rows, cudaStream_t stream) {
-  // CTAs per row: about four per SM in all
-  const int slots = sm_count() * 4;
-  int cs = 8;
-  while (cs > 1 && static_cast<int64_t>(rows) * cs > slots) cs >>= 1;
+template <typename T, int kLpThreads>
+dfv_status logprob_launch_t(const LogprobParams& p, int rows, int cs, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows) * cs);
   cfg.blockDim = dim3(kLpThreads);
@@ -424,7 +489,47 @@ dfv_status logprob_launch(const LogprobParams& p, int rows, cudaStream_t stream)
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprob_kernel<T>, p) == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<T, kLpThreads>, p) == cudaSuccess ? DFV_OK
+                                                                                   : DFV_ERR_CUDA;
+}
+
+// Few rows: CTAs of 1024 threads, one to an SM, as many to a row as leave a
+// round of loads per slice (a cluster of more than eight lies in one GPC, so
+// only for a handful of rows). Many: CTAs of 128 threads, eight to an SM; a row
+// is split where that fills the last wave better (a CTA costs about as much
+// as a twentieth of a 152 K row beside its share).
+template <typename T>
+dfv_status logprob_launch(const LogprobParams& p, int rows, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (rows <= 64) {
+    const int round = 1024 * kLpVecs * LpVec<T>::kN;
+    const int most = rows <= 4 ? 16 : rows <= 16 ? 8 : rows <= 32 ? 4 : 2;
+    int cs = 1;
+    while (cs < most && p.vocab > cs * round) cs <<= 1;
+    if (cs == 16) {
+      static std::atomic<int> allowed[64];   // clusters above eight need leave, once per device
+      int dev = 0;
+      if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DFV_ERR_CUDA;
+      if (!allowed[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(logprob_kernel<T, 1024>,
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+          return DFV_ERR_CUDA;
+        allowed[dev].store(1, std::memory_order_release);
+      }
+    }
+    return logprob_launch_t<T, 1024>(p, rows, cs, stream);
+  }
+  const int64_t slots = static_cast<int64_t>(sms) * 8;
+  int cs = 1;
+  double best = 1e30;
+  for (int c = 1; c <= 8; c <<= 1) {
+    const double cost = ((rows * static_cast<int64_t>(c) + slots - 1) / slots) * (1.0 / c + 0.05);
+    if (cost < best) {
+      best = cost;
+      cs = c;
+    }
+  }
+  return logprob_launch_t<T, 128>(p, rows, cs, stream);
 }
 
 }  // namespace dfv
