@@ -57,10 +57,15 @@ __device__ __forceinline__ float lp_ex2(float x) {
   return y;
 }
 
-// maximum that keeps a NaN
-__device__ __forceinline__ float max_nan(float a, float b, float c) {
+__device__ __forceinline__ float lp_max3(float a, float b, float c) {
   float y;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// at least -200, and NaN if x is
+__device__ __forceinline__ float lp_floor(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0fC3480000;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -119,16 +124,18 @@ struct LpStats {
     s *= f;
     m = to;
   }
-  __device__ __forceinline__ void merge(const LpStats& o) {
-    if (o.m != o.m || m != m) {
-      m = s = t = NAN;
-      return;
+  // All 32 lanes' triples joined, in every lane: one common maximum, then sums
+  // by exchanges whose order is fixed.
+  __device__ __forceinline__ void warp_join() {
+    float to;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(to) : "f"(m));
+    if (to > m) raise(to);
+    else if (to != to) m = s = t = NAN;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     }
-    LpStats b = o;
-    if (b.m > m) raise(b.m);
-    else if (m > b.m) b.raise(m);
-    s += b.s;
-    t += b.t;
   }
 };
 
@@ -180,8 +187,8 @@ __device__ __forceinline__ void lp_add(LpStats& st, float vm, F value) {
   for (int i = 0; i < kN; i += 2) {
     float2 z = lp_add2(make_float2(value(i), kN > 1 ? value(i + 1) : -INFINITY), m2);
     // exp(-200) is zero; the limit keeps 0 * -inf out of the sum
-    z.x = fmaxf(z.x, -200.0f);
-    z.y = fmaxf(z.y, -200.0f);
+    z.x = lp_floor(z.x);
+    z.y = lp_floor(z.y);
     const float2 y = lp_mul2(z, c2);
     const float2 e = make_float2(lp_ex2(y.x), lp_ex2(y.y));
     s2 = lp_add2(s2, e);
@@ -284,6 +291,14 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) logprob_kernel(
   if (tid == 0) sm.count = 0;
   if (cs > 1) cluster_arrive();   // waited for before the first CTA's memory is written
 
+  // the given token and its logit, read meanwhile
+  int token = 0;
+  float x_token = NAN;
+  if (tid == 0 && rank == 0 && p.logprob) {
+    token = p.tokens[row];
+    if (token >= 0 && token < p.vocab) x_token = lp_to_f32(x[token]);
+    else report(p.status, DFV_DEV_BAD_TOKEN);
+  }
   LpStats st;
   st.init();
   constexpr int kStep = kLpThreads * kLpVecs;
@@ -297,18 +312,23 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) logprob_kernel(
       v[j] = i < v1 ? __ldg(xv + i) : none;
     }
   };
+  const uint4* mine = xv + tid;
+  auto load_full = [&](int base) {
+#pragma unroll
+    for (int j = 0; j < kLpVecs; ++j) v[j] = __ldg(mine + base + j * kLpThreads);
+  };
   auto value = [&](int i) { return LpVec<T>::at(v[i / kV], i % kV); };
   float jm[kLpVecs];   // maximum of each vector
   auto chunk_max = [&]() {
 #pragma unroll
     for (int j = 0; j < kLpVecs; ++j) {
-      jm[j] = max_nan(value(j * kV), value(j * kV + 1), value(j * kV + 2));
+      jm[j] = lp_max3(value(j * kV), value(j * kV + 1), value(j * kV + 2));
 #pragma unroll
       for (int e = 3; e < kV; e += 2)
-        jm[j] = max_nan(jm[j], value(j * kV + e), value(j * kV + (e + 1 < kV ? e + 1 : e)));
+        jm[j] = lp_max3(jm[j], value(j * kV + e), value(j * kV + (e + 1 < kV ? e + 1 : e)));
     }
     static_assert(kLpVecs == 4, "maximum of four");
-    return max_nan(max_nan(jm[0], jm[1], jm[2]), jm[3], jm[3]);
+    return fmaxf(lp_max3(jm[0], jm[1], jm[2]), jm[3]);
   };
   auto push_from = [&](int base, float bound) {
 #pragma unroll
@@ -353,35 +373,41 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) logprob_kernel(
     push_from(v0, bound);
     if (extra >= 0 && xe >= bound) lp_push(sm, xe, extra);
   }
-  // ---- the rest of the slice
+  // ---- the rest of the slice. The bound is renewed after one more chunk and
+  // after five, nine, ... times as many: the top-th best collected so far.
+  int renew = v0 + 2 * kStep;
   for (int base = v0 + kStep; base < v1; base += kStep) {
-    load(base);
+    if (base + kStep <= v1) load_full(base);
+    else load(base);
+    if (top > 0 && base >= renew) {
+      renew = base + 4 * (base - v0);
+      __syncthreads();
+      const int c = sm.count;
+      if (c >= top && c <= kLpThreads) {
+        const float mine_v = tid < c ? lp_value(sm.buf[tid]) : -INFINITY;
+        int above = 0, same = 0;
+        for (int k = 0; k < c; ++k) {
+          const float w = lp_value(sm.buf[k]);
+          above += w > mine_v;
+          same += w >= mine_v;
+        }
+        if (tid < c && above < top && same >= top) sm.bound = mine_v;
+      }
+      __syncthreads();
+      bound = fmaxf(sm.bound, -3.4028235e38f);
+    }
     vm = chunk_max();
     lp_add<kV * kLpVecs>(st, vm, value);
     if (vm >= bound) push_from(base, bound);
   }
   // ---- statistics of the CTA: lanes, then warps in order
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    LpStats b;
-    b.m = __shfl_down_sync(0xFFFFFFFFu, st.m, o);
-    b.s = __shfl_down_sync(0xFFFFFFFFu, st.s, o);
-    b.t = __shfl_down_sync(0xFFFFFFFFu, st.t, o);
-    st.merge(b);
-  }
+  st.warp_join();
   if (lane == 0) sm.wst[warp] = st;
   __syncthreads();
-  if (warp == 0) {   // then the warps, in a tree as well
+  if (warp == 0) {
     st.init();
     if (lane < kLpThreads / 32) st = sm.wst[lane];
-#pragma unroll
-    for (int o = kLpThreads / 64; o > 0; o >>= 1) {
-      LpStats b;
-      b.m = __shfl_down_sync(0xFFFFFFFFu, st.m, o);
-      b.s = __shfl_down_sync(0xFFFFFFFFu, st.s, o);
-      b.t = __shfl_down_sync(0xFFFFFFFFu, st.t, o);
-      st.merge(b);
-    }
+    st.warp_join();
     if (lane == 0) sm.st = st;
   }
   // ---- alternatives of the slice
@@ -435,14 +461,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) logprob_kernel(
     if (warp == 0) {
       st.init();
       if (lane < cs) st = sm.cst[lane];
-#pragma unroll
-      for (int k = kLpMaxCluster / 2; k > 0; k >>= 1) {
-        LpStats b;
-        b.m = __shfl_down_sync(0xFFFFFFFFu, st.m, k);
-        b.s = __shfl_down_sync(0xFFFFFFFFu, st.s, k);
-        b.t = __shfl_down_sync(0xFFFFFFFFu, st.t, k);
-        st.merge(b);
-      }
+      st.warp_join();
       if (lane == 0) sm.st = st;
     }
     if (top > 0) {
@@ -460,12 +479,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) logprob_kernel(
   const LpStats a = sm.st;
   const float logs = logf(a.s);
   if (tid == 0) {
-    if (p.logprob) {
-      const int t = p.tokens[row];
-      const bool in = t >= 0 && t < p.vocab;
-      if (!in) report(p.status, DFV_DEV_BAD_TOKEN);
-      p.logprob[row] = in ? (lp_to_f32(x[t]) - a.m) - logs : NAN;
-    }
+    if (p.logprob) p.logprob[row] = (x_token - a.m) - logs;   // NaN for no token
     if (p.entropy) p.entropy[row] = logs - a.t / a.s;
   }
   if (tid < top) {
