@@ -52,7 +52,22 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// kN values from global memory as packed bf16 (f32: rounded to nearest even).
+// 32 bytes in one access; the address is a multiple of 32.
+__device__ __forceinline__ void ld32b(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st32b(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// kN (4 or 16) values from global memory as packed bf16 (f32: rounded to
+// nearest even).
 template <typename T, int kN, bool kVec>
 __device__ __forceinline__ void load_bf16(const T* s, uint32_t* w) {
   if constexpr (!kVec) {
@@ -66,21 +81,20 @@ __device__ __forceinline__ void load_bf16(const T* s, uint32_t* w) {
       }
     }
   } else if constexpr (sizeof(T) == 4) {
+    if constexpr (kN == 16) {
+      uint32_t f[16];
+      ld32b(s, f);
+      ld32b(s + 8, f + 8);
 #pragma unroll
-    for (int k = 0; k < kN / 4; ++k) {
-      const float4 v = reinterpret_cast<const float4*>(s)[k];
-      w[2 * k] = bf16x2_bits(v.x, v.y);
-      w[2 * k + 1] = bf16x2_bits(v.z, v.w);
+      for (int k = 0; k < 8; ++k)
+        w[k] = bf16x2_bits(__uint_as_float(f[2 * k]), __uint_as_float(f[2 * k + 1]));
+    } else {
+      const float4 v = *reinterpret_cast<const float4*>(s);
+      w[0] = bf16x2_bits(v.x, v.y);
+      w[1] = bf16x2_bits(v.z, v.w);
     }
-  } else if constexpr (kN % 8 == 0) {
-#pragma unroll
-    for (int k = 0; k < kN / 8; ++k) {
-      const uint4 v = reinterpret_cast<const uint4*>(s)[k];
-      w[4 * k] = v.x;
-      w[4 * k + 1] = v.y;
-      w[4 * k + 2] = v.z;
-      w[4 * k + 3] = v.w;
-    }
+  } else if constexpr (kN == 16) {
+    ld32b(s, w);
   } else {
     const uint2 v = *reinterpret_cast<const uint2*>(s);
     w[0] = v.x;
@@ -88,20 +102,26 @@ __device__ __forceinline__ void load_bf16(const T* s, uint32_t* w) {
   }
 }
 
-// Four values as codes, lowest byte first.
+// Four values as codes, lowest byte first. Adding 1.5 * 2^23 rounds to the
+// nearest even integer and leaves it in the low bits.
 __device__ __forceinline__ uint32_t quantise4(float a, float b, float c, float d, float inv,
                                               float amax) {
+  constexpr float kMagic = 12582912.0f;
   const float x[4] = {a, b, c, d};
-  int q[4];
+  float r[4], off = 0.0f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float t = x[k] * inv;
-    float r = rintf(t);
-    if (fabsf(t - r) > 0.4998f) r = rintf(__fdiv_rn(x[k] * 127.0f, amax));
-    q[k] = static_cast<int>(r);
+    r[k] = t + kMagic;
+    off = fmaxf(off, fabsf(t - (r[k] - kMagic)));
   }
-  return (q[0] & 0xFF) | ((q[1] & 0xFF) << 8) | ((q[2] & 0xFF) << 16) |
-         (static_cast<uint32_t>(q[3] & 0xFF) << 24);
+  if (off > 0.4998f) {   // near a half-way point: by the exact quotient
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = __fdiv_rn(x[k] * 127.0f, amax) + kMagic;
+  }
+  const uint32_t lo = __byte_perm(__float_as_uint(r[0]), __float_as_uint(r[1]), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(r[2]), __float_as_uint(r[3]), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
 }
 
 // The 64 values of one thread: 32 packed words. K: piece j of 16 dims at w[8 j]; V: position i of
@@ -135,6 +155,22 @@ struct BlockIo {
   static __device__ __forceinline__ void load(const Kv8AppendParams& p, const Kv8Span& s,
                                               const int* path, int h, int b, uint32_t* w) {
     const int tid = threadIdx.x;
+    if (!path && b * kBlk >= s.at && (b + 1) * kBlk <= s.end) {
+      // a block of source rows: no choice per row, so every load is in
+      // flight before the first is used
+      const T* src = static_cast<const T*>(p.src[kV]) + h * p.s_head[kV];
+      const int64_t r0 = b * kBlk - s.at;
+      if constexpr (!kV) {
+        src += (r0 + tid / kTpt) * p.s_row[0] + tid % kTpt * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_bf16<T, 16, kVec>(src + j * kTpt * 16, w + 8 * j);
+      } else {
+        src += (r0 + tid / kVt * 16) * p.s_row[1] + tid % kVt * 4;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) load_bf16<T, 4, kVec>(src + i * p.s_row[1], w + 2 * i);
+      }
+      return;
+    }
     if constexpr (!kV) {
       const int pos = b * kBlk + tid / kTpt;
 #pragma unroll
@@ -185,45 +221,57 @@ struct BlockIo {
       (kV ? p.c.v_scale : p.c.k_scale)[static_cast<int64_t>(h) * p.nblk + b] =
           zero ? 0.0f : __fdiv_rn(amax, 127.0f);
     int8_t* base = (kV ? p.c.v_codes : p.c.k_codes) + static_cast<int64_t>(h) * p.nblk * kBlk * D;
+    if constexpr (!kV) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t q[4];
-      int64_t off;
-      if constexpr (!kV) {
+      for (int j = 0; j < 4; ++j) {
+        uint32_t q[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t a = w[8 * j + 2 * e], c = w[8 * j + 2 * e + 1];
           q[e] = quantise4(bf16_lo(a), bf16_hi(a), bf16_lo(c), bf16_hi(c), inv, amax);
         }
-        off = kv8_k_piece(b, tid / kTpt, tid % kTpt + j * kTpt, D);
-      } else {   // dim j of the thread's four, 16 positions
+        *reinterpret_cast<uint4*>(base + kv8_k_piece(b, tid / kTpt, tid % kTpt + j * kTpt, D)) =
+            make_uint4(q[0], q[1], q[2], q[3]);
+      }
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+      for (int j = 0; j < 4; j += 2) {   // two of the thread's dims: 32 bytes in a row
+        uint32_t q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
           float x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t a = w[2 * (4 * e + i) + j / 2];
-            x[i] = j & 1 ? bf16_hi(a) : bf16_lo(a);
+            const uint32_t a = w[2 * (4 * (e & 3) + i) + j / 2];
+            x[i] = e >= 4 ? bf16_hi(a) : bf16_lo(a);
           }
           q[e] = quantise4(x[0], x[1], x[2], x[3], inv, amax);
         }
-        off = kv8_v_piece(b, tid / kVt, tid % kVt * 4 + j, D);
+        st32b(base + kv8_v_piece(b, tid / kVt, tid % kVt * 4 + j, D), q);
       }
-      *reinterpret_cast<uint4*>(base + off) = make_uint4(q[0], q[1], q[2], q[3]);
     }
   }
 };
 
-// Values that are not stored become zeros; returns whether there were any.
-__device__ __forceinline__ bool drop_big(uint32_t* w) {
-  bool any = false;
+// Largest magnitude of a thread's values (bf16 bits).
+__device__ __forceinline__ uint32_t max_bits(const uint32_t* w) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// The same once values that are not stored have become zeros.
+__device__ __forceinline__ uint32_t keep_storable(uint32_t* w, uint32_t* status) {
+  const uint32_t m = max_bits(w);
+  if (m < kBigBits) return m;
+  report(status, DFV_DEV_NONFINITE);
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
-    const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
-    if (lo >= kBigBits) { w[k] &= 0xFFFF0000u; any = true; }
-    if (hi >= kBigBits) { w[k] &= 0x0000FFFFu; any = true; }
+    if ((w[k] & 0x7FFFu) >= kBigBits) w[k] &= 0xFFFF0000u;
+    if (((w[k] >> 16) & 0x7FFFu) >= kBigBits) w[k] &= 0x0000FFFFu;
   }
-  return any;
+  return max_bits(w);
 }
 
 template <typename T, int D, bool kVec, bool kV>
@@ -234,12 +282,7 @@ __device__ __forceinline__ void append_block(const Kv8AppendParams& p, const Kv8
   const int tid = threadIdx.x;
   uint32_t w[32];
   Io::template load<kV>(p, s, path, h, b, w);
-  if (drop_big(w)) report(p.status, DFV_DEV_NONFINITE);
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < 32; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
-  m = max(m & 0xFFFFu, m >> 16);
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  uint32_t m = __reduce_max_sync(0xFFFFFFFFu, keep_storable(w, p.status));
   if ((tid & 31) == 0) s_max[tid >> 5] = m;
   __syncthreads();   // also: the block's tail rows have been read
 #pragma unroll
@@ -255,7 +298,7 @@ __device__ __forceinline__ void append_block(const Kv8AppendParams& p, const Kv8
     const int other = ((s.open - s.b0) & 1) ? s.open - 1 : s.open;
     if (other > b) {
       Io::template load<kV>(p, s, path, h, other, w);
-      drop_big(w);
+      keep_storable(w, p.status);
       Io::template store_tail<kV>(p, s, h, other, w);
     }
   }
@@ -337,7 +380,7 @@ dfv_status kv8_append_launch(Kv8AppendParams& p, int rows, int dtype, cudaStream
   const int e = dtype == DFV_DTYPE_F32 ? 4 : 2;
   bool vec = true;
   for (int k = 0; k < 2; ++k)
-    vec = vec && aligned(p.src[k], 16) && (p.s_row[k] * e) % 16 == 0 && (p.s_head[k] * e) % 16 == 0;
+    vec = vec && aligned(p.src[k], 32) && (p.s_row[k] * e) % 32 == 0 && (p.s_head[k] * e) % 32 == 0;
   if (dtype == DFV_DTYPE_F32)
     return vec ? append_launch_t<float, true>(p, rows, stream)
                : append_launch_t<float, false>(p, rows, stream);
@@ -358,34 +401,36 @@ struct Kv8ReadParams {
 
 template <typename T, int kN, bool kVec>
 __device__ __forceinline__ void store_values(T* dst, const float* x) {
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (kVec) {
+  if constexpr (!kVec) {
 #pragma unroll
-      for (int k = 0; k < kN / 4; ++k)
-        reinterpret_cast<float4*>(dst)[k] =
-            make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kN; ++k) dst[k] = x[k];
+    for (int k = 0; k < kN; ++k) {
+      if constexpr (sizeof(T) == 4) dst[k] = x[k];
+      else dst[k] = __float2bfloat16_rn(x[k]);
     }
-  } else if constexpr (!kVec) {
+  } else if constexpr (sizeof(T) == 4) {
+    if constexpr (kN == 16) {
+      uint32_t w[16];
 #pragma unroll
-    for (int k = 0; k < kN; ++k) dst[k] = __float2bfloat16_rn(x[k]);
-  } else if constexpr (kN % 8 == 0) {
+      for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(x[k]);
+      st32b(dst, w);
+      st32b(dst + 8, w + 8);
+    } else {
+      *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+  } else if constexpr (kN == 16) {
+    uint32_t w[8];
 #pragma unroll
-    for (int k = 0; k < kN / 8; ++k)
-      reinterpret_cast<uint4*>(dst)[k] =
-          make_uint4(bf16x2_bits(x[8 * k], x[8 * k + 1]), bf16x2_bits(x[8 * k + 2], x[8 * k + 3]),
-                     bf16x2_bits(x[8 * k + 4], x[8 * k + 5]),
-                     bf16x2_bits(x[8 * k + 6], x[8 * k + 7]));
+    for (int k = 0; k < 8; ++k) w[k] = bf16x2_bits(x[2 * k], x[2 * k + 1]);
+    st32b(dst, w);
   } else {
     *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]));
   }
 }
 
-__device__ __forceinline__ float code_at(const uint4& v, int i) {
-  const uint32_t w = i < 4 ? v.x : i < 8 ? v.y : i < 12 ? v.z : v.w;
-  return static_cast<float>(static_cast<int8_t>((w >> (8 * (i & 3))) & 0xFF));
+// Code i of a row of codes, of which every byte has been flipped by 0x80:
+// 0x4B0000uu is 2^23 + u.
+__device__ __forceinline__ float code_at(const uint32_t* flipped, int i) {
+  return __uint_as_float(__byte_perm(flipped[i >> 2], 0x4B000000u, 0x7440 | (i & 3))) - 8388736.0f;
 }
 
 template <typename T, int D, bool kVec>
@@ -416,35 +461,39 @@ __global__ void __launch_bounds__(D) kv8_read_kernel(const __grid_constant__ Kv8
   const float scale = (kv ? p.c.v_scale : p.c.k_scale)[static_cast<int64_t>(h) * p.nblk + b];
   const int8_t* codes =
       (kv ? p.c.v_codes : p.c.k_codes) + static_cast<int64_t>(h) * p.nblk * kBlk * D;
+  uint32_t q[16];
   if (kv == 0) {
     const int pos = b * kBlk + tid / kTpt;
     if (pos < first || pos >= last) return;
-    uint4 q[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      q[j] = *reinterpret_cast<const uint4*>(
+      *reinterpret_cast<uint4*>(q + 4 * j) = *reinterpret_cast<const uint4*>(
           codes + kv8_k_piece(b, tid / kTpt, tid % kTpt + j * kTpt, D));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) q[j] ^= 0x80808080u;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float x[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = code_at(q[j], i) * scale;
+      for (int i = 0; i < 16; ++i) x[i] = code_at(q + 4 * j, i) * scale;
       store_values<T, 16, kVec>(dst + (pos - p.pos0) * p.s_row + (tid % kTpt + j * kTpt) * 16, x);
     }
   } else {
-    uint4 q[4];
+    const int8_t* at = codes + kv8_v_piece(b, tid / kVt, tid % kVt * 4, D);
+    ld32b(at, q);
+    ld32b(at + 32, q + 8);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      q[j] = *reinterpret_cast<const uint4*>(
-          codes + kv8_v_piece(b, tid / kVt, tid % kVt * 4 + j, D));
+    for (int j = 0; j < 16; ++j) q[j] ^= 0x80808080u;
+    const int pos0 = b * kBlk + tid / kVt * 16;
+    T* o = dst + (pos0 - p.pos0) * p.s_row + tid % kVt * 4;
+    const bool whole = pos0 >= first && pos0 + 16 <= last;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int pos = b * kBlk + tid / kVt * 16 + i;
-      if (pos < first || pos >= last) continue;
       float x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = code_at(q[j], i) * scale;
-      store_values<T, 4, kVec>(dst + (pos - p.pos0) * p.s_row + tid % kVt * 4, x);
+      for (int j = 0; j < 4; ++j) x[j] = code_at(q + 4 * j, i) * scale;
+      if (whole || (pos0 + i >= first && pos0 + i < last))
+        store_values<T, 4, kVec>(o + i * p.s_row, x);
     }
   }
 }
@@ -540,8 +589,8 @@ extern "C" dfv_status dfv_kv8_read(const dfv_kv8_cache* cache, int pos0, int n_r
   p.s_row = stride_row;
   p.s_head = stride_head;
   p.status = status;
-  const bool vec = aligned(k_dst, 16) && aligned(v_dst, 16) && (stride_row * e) % 16 == 0 &&
-                   (stride_head * e) % 16 == 0;
+  const bool vec = aligned(k_dst, 32) && aligned(v_dst, 32) && (stride_row * e) % 32 == 0 &&
+                   (stride_head * e) % 32 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dst_dtype == DFV_DTYPE_F32)
     return vec ? read_launch_t<float, true>(p, s) : read_launch_t<float, false>(p, s);
