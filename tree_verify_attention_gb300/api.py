@@ -169,9 +169,14 @@ class Int8Cache:
         self.v = torch.zeros(h, nblk, KV8_BLOCK // 16, d, 16, dtype=torch.int8, device=device)
         self.k_scale = torch.zeros(h, nblk, device=device)
         self.v_scale = torch.zeros(h, nblk, device=device)
-        self.k_tail = torch.zeros(h, 2, KV8_BLOCK, d, dtype=torch.bfloat16, device=device)
-        self.v_tail = torch.zeros_like(self.k_tail)
-        self.state = torch.zeros(4, dtype=torch.int32, device=device)
+        # the open end in one buffer: a copy of it (and copying it back) saves
+        # and restores a point to which the cache can return
+        tail = h * 2 * KV8_BLOCK * d
+        self.open_end = torch.zeros(128 + 4 * tail, dtype=torch.uint8, device=device)
+        self.state = self.open_end[:16].view(torch.int32)
+        self.k_tail, self.v_tail = (
+            self.open_end[128 + 2 * i * tail:128 + 2 * (i + 1) * tail].view(torch.bfloat16)
+            .view(h, 2, KV8_BLOCK, d) for i in range(2))
         self.ctx_len = self.state[:1]
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self._struct = _lib.Kv8CacheStruct(

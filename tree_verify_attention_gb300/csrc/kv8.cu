@@ -274,34 +274,45 @@ __device__ __forceinline__ uint32_t keep_storable(uint32_t* w, uint32_t* status)
   return max_bits(w);
 }
 
-template <typename T, int D, bool kVec, bool kV>
-__device__ __forceinline__ void append_block(const Kv8AppendParams& p, const Kv8Span& s,
-                                             const int* path, uint32_t* s_max) {
+// The block of this CTA. `refused` is asked once the block's loads are in
+// flight; nothing is written if it says so. True if the CTA is the last of
+// the grid to have read the cache's state.
+template <typename T, int D, bool kVec, bool kV, typename F>
+__device__ __forceinline__ bool append_block(const Kv8AppendParams& p, const Kv8Span& s,
+                                             const int* path, uint32_t* s_max, F refused) {
   using Io = BlockIo<T, D, kVec>;
   const int h = blockIdx.y, b = s.b0 + blockIdx.x;
   const int tid = threadIdx.x;
+  const bool mine = b * kBlk < s.end;
   uint32_t w[32];
-  Io::template load<kV>(p, s, path, h, b, w);
-  uint32_t m = __reduce_max_sync(0xFFFFFFFFu, keep_storable(w, p.status));
+  if (mine) Io::template load<kV>(p, s, path, h, b, w);
+  if (refused()) return false;
+  uint32_t m = 0;
+  if (mine) m = __reduce_max_sync(0xFFFFFFFFu, keep_storable(w, p.status));
   if ((tid & 31) == 0) s_max[tid >> 5] = m;
-  __syncthreads();   // also: the block's tail rows have been read
+  __syncthreads();   // also: the block's tail rows and the state have been read
+  unsigned ticket = 0;
+  if (tid == 0) ticket = atomicAdd(reinterpret_cast<unsigned*>(p.c.state) + 1, 1u);
+  if (mine) {
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) m = max(m, s_max[k]);
-  if (s.end >= (b + 1) * kBlk) Io::template store_codes<kV>(p, h, b, w, m);
-  // The blocks that the tail keeps afterwards are the open one and the one
-  // before. Their slots may hold rows that block b0 still needs (its own
-  // slot has the same parity every second block); b0's CTA then writes them.
-  const bool shared = s.at % kBlk != 0;   // b0 reads its slot
-  if (b >= s.open - 1 && (b == s.b0 || !shared || ((b - s.b0) & 1)))
-    Io::template store_tail<kV>(p, s, h, b, w);
-  if (b == s.b0 && shared) {
-    const int other = ((s.open - s.b0) & 1) ? s.open - 1 : s.open;
-    if (other > b) {
-      Io::template load<kV>(p, s, path, h, other, w);
-      keep_storable(w, p.status);
-      Io::template store_tail<kV>(p, s, h, other, w);
+    for (int k = 0; k < D / 32; ++k) m = max(m, s_max[k]);
+    if (s.end >= (b + 1) * kBlk) Io::template store_codes<kV>(p, h, b, w, m);
+    // The blocks that the tail keeps afterwards are the open one and the one
+    // before. Their slots may hold rows that block b0 still needs (its own
+    // slot has the same parity every second block); b0's CTA then writes them.
+    const bool shared = s.at % kBlk != 0;   // b0 reads its slot
+    if (b >= s.open - 1 && (b == s.b0 || !shared || ((b - s.b0) & 1)))
+      Io::template store_tail<kV>(p, s, h, b, w);
+    if (b == s.b0 && shared) {
+      const int other = ((s.open - s.b0) & 1) ? s.open - 1 : s.open;
+      if (other > b) {
+        Io::template load<kV>(p, s, path, h, other, w);
+        keep_storable(w, p.status);
+        Io::template store_tail<kV>(p, s, h, other, w);
+      }
     }
   }
+  return tid == 0 && ticket == gridDim.x * gridDim.y * gridDim.z - 1;
 }
 
 template <typename T, int D, bool kVec>
@@ -310,20 +321,19 @@ __global__ void __launch_bounds__(D) kv8_append_kernel(const __grid_constant__ K
   __shared__ int s_path[kMaxNodes];
   __shared__ int s_bad;
   const int tid = threadIdx.x;
-  const int C = *static_cast<volatile int32_t*>(p.c.state);
-  int n = p.n;
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const int C = static_cast<volatile int32_t*>(p.c.state)[0];
+  const int held = static_cast<volatile int32_t*>(p.c.state)[2];
+  int at = p.at, n = p.n;
   uint32_t bad = 0;
-  if (C < 0 || C > p.c.capacity) bad = DFV_DEV_CTX;
+  if (at < 0) {
+    if (C < 0 || C > p.c.capacity) bad = DFV_DEV_CTX;
+    at = C;
+  }
   if (p.accept_len) {
     n = *p.accept_len;
     if (n < 1 || n > p.n_nodes) bad |= DFV_DEV_BAD_PATH;
-  }
-  const int at = p.at < 0 ? C : p.at;
-  // the rows of at's block before it have to be in the tail
-  const int held = static_cast<volatile int32_t*>(p.c.state)[2];
-  if (!bad && (at > C || (at % kBlk != 0 && at / kBlk < held))) bad = DFV_DEV_CTX;
-  if (!bad && at + n > p.c.capacity) bad = DFV_DEV_CAPACITY;
-  if (p.accept_len) {
     if (tid == 0) s_bad = 0;
     __syncthreads();
     if (!bad)
@@ -335,8 +345,17 @@ __global__ void __launch_bounds__(D) kv8_append_kernel(const __grid_constant__ K
     __syncthreads();
     if (s_bad) bad |= DFV_DEV_BAD_PATH;
   }
-  if (bad) {   // the same for every CTA: nothing is written
-    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) report(p.status, bad);
+  if (!bad && at + n > p.c.capacity) bad = DFV_DEV_CAPACITY;
+  // the rows of at's block before it have to be in the tail
+  auto refused = [&]() {
+    if (C < 0 || C > p.c.capacity || at > C || (at % kBlk != 0 && at / kBlk < held))
+      bad |= DFV_DEV_CTX;
+    if (bad && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+      report(p.status, bad);
+    return bad != 0;   // the same for every CTA: nothing is written
+  };
+  if (bad) {
+    refused();
     return;
   }
   Kv8Span s;
@@ -344,35 +363,46 @@ __global__ void __launch_bounds__(D) kv8_append_kernel(const __grid_constant__ K
   s.end = at + n;
   s.b0 = at / kBlk;
   s.open = s.end / kBlk;
-  if ((s.b0 + static_cast<int>(blockIdx.x)) * kBlk < s.end) {
-    const int* path = p.accept_len ? s_path : nullptr;
-    if (blockIdx.z == 0) append_block<T, D, kVec, false>(p, s, path, s_max);
-    else append_block<T, D, kVec, true>(p, s, path, s_max);
+  const int* path = p.accept_len ? s_path : nullptr;
+  const bool last = blockIdx.z == 0
+                        ? append_block<T, D, kVec, false>(p, s, path, s_max, refused)
+                        : append_block<T, D, kVec, true>(p, s, path, s_max, refused);
+  // The last CTA to have read the state advances the committed length; the
+  // counter beside it is left at zero. (What the grid writes is read by later
+  // launches only.)
+  if (last) {
+    p.c.state[1] = 0;
+    p.c.state[0] = s.end;
+    // the first block whose bf16 rows the tail now has
+    p.c.state[2] = s.open > s.b0 ? s.open - 1 : s.b0 < held ? s.b0 : max(held, s.b0 - 1);
   }
-  // the last CTA to finish advances the committed length, which the others
-  // have read; the counter beside it is left at zero
-  __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    const unsigned total = gridDim.x * gridDim.y * gridDim.z;
-    if (atomicAdd(reinterpret_cast<unsigned*>(p.c.state) + 1, 1u) == total - 1) {
-      p.c.state[1] = 0;
-      p.c.state[0] = s.end;
-      // the first block whose bf16 rows the tail now has
-      p.c.state[2] = s.open > s.b0 ? s.open - 1 : s.b0 < held ? s.b0 : max(held, s.b0 - 1);
-    }
-  }
+}
+
+// Launch that may be set up while the kernel before it runs (its kernels wait
+// for that one before they touch anything).
+template <typename P>
+dfv_status launch_after(void (*kernel)(P), dim3 grid, int threads, const P& p,
+                        cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
 }
 
 template <typename T, bool kVec>
 dfv_status append_launch_t(const Kv8AppendParams& p, int rows, cudaStream_t stream) {
   const dim3 grid((rows + kBlk - 2) / kBlk + 1, p.c.n_kv_heads, 2);   // blocks that `rows` can touch
   switch (p.c.head_dim) {
-    case 64: kv8_append_kernel<T, 64, kVec><<<grid, 64, 0, stream>>>(p); break;
-    case 128: kv8_append_kernel<T, 128, kVec><<<grid, 128, 0, stream>>>(p); break;
-    default: kv8_append_kernel<T, 256, kVec><<<grid, 256, 0, stream>>>(p); break;
+    case 64: return launch_after(kv8_append_kernel<T, 64, kVec>, grid, 64, p, stream);
+    case 128: return launch_after(kv8_append_kernel<T, 128, kVec>, grid, 128, p, stream);
+    default: return launch_after(kv8_append_kernel<T, 256, kVec>, grid, 256, p, stream);
   }
-  return cudaGetLastError() == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
 }
 
 dfv_status kv8_append_launch(Kv8AppendParams& p, int rows, int dtype, cudaStream_t stream) {
@@ -436,6 +466,8 @@ __device__ __forceinline__ float code_at(const uint32_t* flipped, int i) {
 template <typename T, int D, bool kVec>
 __global__ void __launch_bounds__(D) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
   constexpr int kTpt = D / 64, kVt = D / 4;
+  grid_dep_launch_dependents();
+  grid_dep_wait();
   const int C = *p.c.state;
   const int tid = threadIdx.x, h = blockIdx.y, kv = blockIdx.z;
   int end = p.end;
@@ -502,11 +534,10 @@ template <typename T, bool kVec>
 dfv_status read_launch_t(const Kv8ReadParams& p, cudaStream_t stream) {
   const dim3 grid((p.end - 1) / kBlk - p.pos0 / kBlk + 1, p.c.n_kv_heads, 2);
   switch (p.c.head_dim) {
-    case 64: kv8_read_kernel<T, 64, kVec><<<grid, 64, 0, stream>>>(p); break;
-    case 128: kv8_read_kernel<T, 128, kVec><<<grid, 128, 0, stream>>>(p); break;
-    default: kv8_read_kernel<T, 256, kVec><<<grid, 256, 0, stream>>>(p); break;
+    case 64: return launch_after(kv8_read_kernel<T, 64, kVec>, grid, 64, p, stream);
+    case 128: return launch_after(kv8_read_kernel<T, 128, kVec>, grid, 128, p, stream);
+    default: return launch_after(kv8_read_kernel<T, 256, kVec>, grid, 256, p, stream);
   }
-  return cudaGetLastError() == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
 }
 
 }  // namespace dfv
