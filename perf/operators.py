@@ -233,7 +233,7 @@ def prepare(case, seed):
         if op == "write" and ctx % BLOCK and (ctx + extra) // BLOCK > ctx // BLOCK + 1:
             # the write closes blocks behind the one it starts in: a pass over
             # the same place again first puts that block's rows back
-            s["open"] = [cache.state.clone(), cache.k_tail.clone(), cache.v_tail.clone()]
+            s["open"] = cache.open_end.clone()
         if op == "attend":
             s["out"] = torch.empty(n, hq, d, dtype=torch.bfloat16, device=DEV)
             s["lse"] = torch.empty(n, hq, device=DEV)
@@ -359,9 +359,7 @@ def run(s):
     from tree_verify_attention_gb300 import api
     if op == "write":
         if "open" in s:
-            c = s["cache"]
-            c.state.copy_(s["open"][0])
-            torch._foreach_copy_([c.k_tail, c.v_tail], s["open"][1:])
+            s["cache"].open_end.copy_(s["open"])
         s["cache"].append(s["k_rows"], s["v_rows"], at=s["case"]["at"])
         k, v = s["out"]
         s["cache"].read(s["case"]["at"] // BLOCK * BLOCK, k.shape[0], k, v)
