@@ -49,8 +49,10 @@ def _check(st, name):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle without building a Stream object (2 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _p(t):
@@ -123,25 +125,29 @@ class Q4Cache(KVCache):
         super().__init__(n_kv_heads, head_dim, capacity, device=device, fmt="q4_0")
 
 
-def _same_device(device, **tensors):
-    """All of ``tensors`` (None allowed) on ``device``, which is the current
-    one: the library launches on the current device."""
-    if device.index != torch.cuda.current_device():
-        raise DfvError(f"tensors on {device}, but the current device is "
+def _same_device(index, *tensors):
+    """All of ``tensors`` (None allowed) on device ``index``, which is the
+    current one: the library launches on the current device."""
+    if index != torch.cuda.current_device():
+        raise DfvError(f"tensors on cuda:{index}, but the current device is "
                        f"cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise DfvError(f"{name} is on {t.device}, expected {device}")
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise DfvError(f"a tensor is on {t.device}, expected cuda:{index}")
 
 
-def _float_rows(t, name, shape, dtypes=(torch.float32, torch.bfloat16)):
+_ROWS = (torch.float32, torch.bfloat16)
+
+
+def _float_rows(t, name, shape, dtypes=_ROWS):
     if t is None or not t.is_cuda or t.dtype not in dtypes:
         raise DfvError(f"{name} must be a CUDA f32 or bf16 tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise DfvError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.numel() and t.stride(-1) != 1:
+    if t.shape != shape:
+        raise DfvError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    st = t.stride()
+    if st[-1] != 1 and t.numel():
         raise DfvError(f"{name} rows must be contiguous")
-    return t
+    return st
 
 
 class Int8Cache:
@@ -184,6 +190,8 @@ class Int8Cache:
             self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.k_tail.data_ptr(),
             self.v_tail.data_ptr())
         self.handle = ctypes.addressof(self._struct)
+        self._index = self.state.get_device()
+        self._status_ptr = self.status.data_ptr()
 
     def append(self, k_rows, v_rows, at=None, head_major=False, stream=None, status=None):
         """Write float rows [n, Hkv, D] (or [Hkv, n, D] with head_major=True;
@@ -192,18 +200,17 @@ class Int8Cache:
         length. An ``at`` behind that length, or inside a block whose bf16
         rows are no longer held, writes nothing and sets DEV_CTX."""
         h, d = self.n_kv_heads, self.head_dim
-        n = k_rows.shape[1 if head_major else 0]
-        shape = (h, n, d) if head_major else (n, h, d)
-        _float_rows(k_rows, "k_rows", shape)
-        _float_rows(v_rows, "v_rows", shape, (k_rows.dtype,))
-        status = self.status if status is None else status
-        _same_device(self.state.device, k_rows=k_rows, v_rows=v_rows, status=status)
         r, hd = (1, 0) if head_major else (0, 1)
+        n = k_rows.shape[r]
+        shape = (h, n, d) if head_major else (n, h, d)
+        ks = _float_rows(k_rows, "k_rows", shape)
+        vs = _float_rows(v_rows, "v_rows", shape, (k_rows.dtype,))
+        _same_device(self._index, k_rows, v_rows, status)
         _check(lib().dfv_kv8_append(
             self.handle, -1 if at is None else at, n, k_rows.data_ptr(), v_rows.data_ptr(),
-            DTYPE_F32 if k_rows.dtype == torch.float32 else DTYPE_BF16, k_rows.stride(r),
-            k_rows.stride(hd), v_rows.stride(r), v_rows.stride(hd), status.data_ptr(),
-            _stream(stream)), "dfv_kv8_append")
+            DTYPE_F32 if k_rows.dtype == torch.float32 else DTYPE_BF16, ks[r], ks[hd], vs[r],
+            vs[hd], self._status_ptr if status is None else status.data_ptr(), _stream(stream)),
+            "dfv_kv8_append")
 
     def fill(self, k_rows, v_rows, pos0=0, stream=None):
         """Rows [Hkv, n, D] at positions [pos0, pos0 + n), as KVCache.fill."""
@@ -220,18 +227,17 @@ class Int8Cache:
         D] (or [Hkv, n, D]) f32 or bf16 with equal strides. Rows behind the
         committed length are left as they were (DEV_CTX)."""
         h, d = self.n_kv_heads, self.head_dim
-        shape = (h, n, d) if head_major else (n, h, d)
-        _float_rows(k_out, "k_out", shape)
-        _float_rows(v_out, "v_out", shape, (k_out.dtype,))
-        if k_out.stride() != v_out.stride():
-            raise DfvError("k_out and v_out must have the same strides")
-        status = self.status if status is None else status
-        _same_device(self.state.device, k_out=k_out, v_out=v_out, status=status)
         r, hd = (1, 0) if head_major else (0, 1)
+        shape = (h, n, d) if head_major else (n, h, d)
+        st = _float_rows(k_out, "k_out", shape)
+        if _float_rows(v_out, "v_out", shape, (k_out.dtype,)) != st:
+            raise DfvError("k_out and v_out must have the same strides")
+        _same_device(self._index, k_out, v_out, status)
         _check(lib().dfv_kv8_read(
             self.handle, pos0, n, k_out.data_ptr(), v_out.data_ptr(),
-            DTYPE_F32 if k_out.dtype == torch.float32 else DTYPE_BF16, k_out.stride(r),
-            k_out.stride(hd), status.data_ptr(), _stream(stream)), "dfv_kv8_read")
+            DTYPE_F32 if k_out.dtype == torch.float32 else DTYPE_BF16, st[r], st[hd],
+            self._status_ptr if status is None else status.data_ptr(), _stream(stream)),
+            "dfv_kv8_read")
 
 
 def int8_attn_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity):
@@ -248,21 +254,20 @@ def _int8_attn(cache, q, tree_k, tree_v, parent, window, max_depth, out, lse, ws
     _dev(q, "q", _BF16)
     for t, name in ((tree_k, "tree_k"), (tree_v, "tree_v")):
         _dev(t, name, _BF16)
-        if tuple(t.shape) != (n, hkv, d):
+        if t.shape != (n, hkv, d):
             raise DfvError(f"{name} has shape {tuple(t.shape)}, expected {(n, hkv, d)}")
     _dev(parent, "parent", _I32, n)
-    _dev(out, "out", (torch.float32, torch.bfloat16), n * hq * d)
+    _dev(out, "out", _ROWS, n * hq * d)
     if lse is not None:
         _dev(lse, "lse", _F32, n * hq)
     _dev(ws, "workspace", (torch.uint8,))
-    status = cache.status if status is None else status
-    _same_device(cache.state.device, q=q, tree_k=tree_k, tree_v=tree_v, parent=parent, out=out,
-                 lse=lse, workspace=ws, status=status)
+    _same_device(cache._index, q, tree_k, tree_v, parent, out, lse, ws, status)
     _check(lib().dfv_kv8_attn(
         cache.handle, n, max_depth, hq, window, q.data_ptr(), tree_k.data_ptr(),
         tree_v.data_ptr(), parent.data_ptr(), float(scale), out.data_ptr(),
         DTYPE_F32 if out.dtype == torch.float32 else DTYPE_BF16, _p(lse), ws.data_ptr(),
-        ws.numel(), status.data_ptr(), _stream(stream)), "dfv_kv8_attn")
+        ws.numel(), cache._status_ptr if status is None else status.data_ptr(),
+        _stream(stream)), "dfv_kv8_attn")
 
 
 def kv_quantize_rows(cache, src, pos0, n_kv_heads, head_dim, capacity, head_major=False,
@@ -404,8 +409,7 @@ def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logp
         top = t.shape[1]
     if top > min(MAX_TOP, vocab):
         raise DfvError(f"{top} alternatives asked for, at most {min(MAX_TOP, vocab)}")
-    _same_device(logits.device, tokens=tokens, logprob=logprob, entropy=entropy, top_ids=top_ids,
-                 top_logprobs=top_logprobs, status=status)
+    _same_device(logits.get_device(), tokens, logprob, entropy, top_ids, top_logprobs, status)
     _check(lib().dfv_token_logprobs(
         n, vocab, DTYPE_F32 if logits.dtype == torch.float32 else DTYPE_BF16, logits.data_ptr(),
         logits.stride(0) if n > 1 else vocab, _p(tokens), top, _p(logprob), _p(entropy),
@@ -423,12 +427,11 @@ def kv_commit(cache, accept_len, path, tree_k, tree_v, status=None, stream=None)
                 tree_v.shape != tree_k.shape:
             raise DfvError("tree_k and tree_v must be [N, Hkv, D] of the cache")
         _dev(path, "path", _I32, n)
-        status = cache.status if status is None else status
-        _same_device(cache.state.device, accept_len=accept_len, path=path, tree_k=tree_k,
-                     tree_v=tree_v, status=status)
+        _same_device(cache._index, accept_len, path, tree_k, tree_v, status)
         _check(lib().dfv_kv8_commit(
             cache.handle, n, accept_len.data_ptr(), path.data_ptr(), tree_k.data_ptr(),
-            tree_v.data_ptr(), status.data_ptr(), _stream(stream)), "dfv_kv8_commit")
+            tree_v.data_ptr(), cache._status_ptr if status is None else status.data_ptr(),
+            _stream(stream)), "dfv_kv8_commit")
         return
     _check(lib().dfv_kv_commit(
         n, cache.n_kv_heads, cache.head_dim, cache.kv_format, cache.capacity, cache.ctx_len.data_ptr(),
