@@ -131,33 +131,50 @@ struct BlockIo {
   static constexpr int kTpt = D / 64;      // K: threads per position
   static constexpr int kVt = D / 4;        // V: threads per 16 positions
 
-  // Row of position p: its tail row, its source row, or none.
-  template <bool kV, int kN>
-  static __device__ __forceinline__ void load_row(const Kv8AppendParams& p, const Kv8Span& s,
-                                                  const int* path, int h, int pos, int dim,
-                                                  uint32_t* w) {
-    if (pos >= s.end) {
+  // Piece `dim` (kN values) of the rows pos + 0 .. kRows - 1, row i at
+  // w[i * kN / 2]: source rows, tail rows where the block is complete and
+  // begins before the write, zeros elsewhere. Every load is issued whatever
+  // the row (from a row that exists) and the choice made on its value: a
+  // branch per row would wait for each load in turn.
+  template <bool kV, int kN, int kRows>
+  static __device__ __forceinline__ void load_rows(const Kv8AppendParams& p, const Kv8Span& s,
+                                                   const int* path, int h, int b, int pos,
+                                                   int dim, uint32_t* w) {
+    const int n = s.end - s.at;
+    if (n > 0) {
+      const T* src = static_cast<const T*>(p.src[kV]) + h * p.s_head[kV] + dim;
 #pragma unroll
-      for (int k = 0; k < kN / 2; ++k) w[k] = 0u;
-    } else if (pos < s.at) {
-      const __nv_bfloat16* tail =
-          static_cast<const __nv_bfloat16*>(kV ? p.c.v_tail : p.c.k_tail) +
-          ((static_cast<int64_t>(h) * 2 + ((pos / kBlk) & 1)) * kBlk + pos % kBlk) * D + dim;
-      load_bf16<__nv_bfloat16, kN, true>(tail, w);
-    } else {
-      const int64_t r = path ? path[pos - s.at] : pos - s.at;
-      const T* src = static_cast<const T*>(p.src[kV]) + r * p.s_row[kV] + h * p.s_head[kV] + dim;
-      load_bf16<T, kN, kVec>(src, w);
+      for (int i = 0; i < kRows; ++i) {
+        const int k = min(max(pos + i - s.at, 0), n - 1);
+        load_bf16<T, kN, kVec>(src + (path ? path[k] : k) * p.s_row[kV], w + i * kN / 2);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (pos + i < s.at || pos + i >= s.end) {
+#pragma unroll
+        for (int e = 0; e < kN / 2; ++e) w[i * kN / 2 + e] = 0u;
+      }
+    if (s.at <= b * kBlk || s.end < (b + 1) * kBlk) return;
+    const __nv_bfloat16* tail = static_cast<const __nv_bfloat16*>(kV ? p.c.v_tail : p.c.k_tail) +
+                                (static_cast<int64_t>(h) * 2 + (b & 1)) * kBlk * D + dim;
+    uint32_t t[kN / 2 * kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      load_bf16<__nv_bfloat16, kN, true>(tail + min(pos + i, s.at - 1) % kBlk * D, t + i * kN / 2);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (pos + i < s.at) {
+#pragma unroll
+        for (int e = 0; e < kN / 2; ++e) w[i * kN / 2 + e] = t[i * kN / 2 + e];
+      }
   }
 
   template <bool kV>
   static __device__ __forceinline__ void load(const Kv8AppendParams& p, const Kv8Span& s,
                                               const int* path, int h, int b, uint32_t* w) {
     const int tid = threadIdx.x;
-    if (!path && b * kBlk >= s.at && (b + 1) * kBlk <= s.end) {
-      // a block of source rows: no choice per row, so every load is in
-      // flight before the first is used
+    if (!path && b * kBlk >= s.at && (b + 1) * kBlk <= s.end) {   // source rows throughout
       const T* src = static_cast<const T*>(p.src[kV]) + h * p.s_head[kV];
       const int64_t r0 = b * kBlk - s.at;
       if constexpr (!kV) {
@@ -169,17 +186,13 @@ struct BlockIo {
 #pragma unroll
         for (int i = 0; i < 16; ++i) load_bf16<T, 4, kVec>(src + i * p.s_row[1], w + 2 * i);
       }
-      return;
-    }
-    if constexpr (!kV) {
-      const int pos = b * kBlk + tid / kTpt;
+    } else if constexpr (!kV) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        load_row<false, 16>(p, s, path, h, pos, (tid % kTpt + j * kTpt) * 16, w + 8 * j);
+        load_rows<false, 16, 1>(p, s, path, h, b, b * kBlk + tid / kTpt,
+                                (tid % kTpt + j * kTpt) * 16, w + 8 * j);
     } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        load_row<true, 4>(p, s, path, h, b * kBlk + tid / kVt * 16 + i, tid % kVt * 4, w + 2 * i);
+      load_rows<true, 4, 16>(p, s, path, h, b, b * kBlk + tid / kVt * 16, tid % kVt * 4, w);
     }
   }
 
@@ -482,11 +495,28 @@ __global__ void __launch_bounds__(D) kv8_read_kernel(const __grid_constant__ Kv8
   if (b == C / kBlk) {   // the open block: bf16 rows
     const __nv_bfloat16* tail = static_cast<const __nv_bfloat16*>(kv ? p.c.v_tail : p.c.k_tail) +
                                 (static_cast<int64_t>(h) * 2 + (b & 1)) * kBlk * D;
-    for (int pos = first; pos < last; ++pos) {
-      const float x = __bfloat162float(tail[(pos % kBlk) * D + tid]);
-      T* o = dst + (pos - p.pos0) * p.s_row + tid;
-      if constexpr (sizeof(T) == 4) *o = x;
-      else *o = __float2bfloat16_rn(x);
+    // eight values a step and thread, all loads before the first store
+    constexpr int kPer = D / 8;
+    uint4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int row = (tid + k * D) / kPer;
+      v[k] = *reinterpret_cast<const uint4*>(tail + row * D + (tid + k * D) % kPer * 8);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int pos = b * kBlk + (tid + k * D) / kPer;
+      if (pos < first || pos >= last) continue;
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(w[e]);
+        x[2 * e + 1] = bf16_hi(w[e]);
+      }
+      T* o = dst + (pos - p.pos0) * p.s_row + (tid + k * D) % kPer * 8;
+      store_values<T, 4, kVec>(o, x);
+      store_values<T, 4, kVec>(o + 4, x + 4);
     }
     return;
   }
