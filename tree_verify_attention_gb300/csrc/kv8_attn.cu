@@ -221,8 +221,11 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   __shared__ int s_vexp[kAtKeys], s_bad[2][kAtKeys];
   __shared__ uint32_t s_qmax;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int C = *p.c.state;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // both the same in every lane, which the compiler knows of a reduction's
+  // result: what follows from them then lives in uniform registers
+  const int warp = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tid >> 5)));
+  int C = __reduce_max_sync(0xFFFFFFFFu, *p.c.state);
   grid_dep_launch_dependents();   // the merge may be set up meanwhile
   const int split = blockIdx.x, splits = gridDim.x, tile = blockIdx.y, h = blockIdx.z;
   const int row0 = tile * p.rows_tile, n_rows = min(p.rows_tile, p.rows - row0);
