@@ -225,10 +225,41 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   // both the same in every lane, which the compiler knows of a reduction's
   // result: what follows from them then lives in uniform registers
   const int warp = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tid >> 5)));
-  int C = __reduce_max_sync(0xFFFFFFFFu, *p.c.state);
+  // what touches no global memory may run under the kernel before
   grid_dep_launch_dependents();   // the merge may be set up meanwhile
+  if (warp == SW + 8) {
+    tc::tmem_alloc(&s_tmem, 512);
+  } else if (warp == SW + 9 && lane == 0) {
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&b_kraw[s], 1);
+      mbar_init(&b_vraw[s], 1);
+      mbar_init(&b_kdone[s], 4);
+      mbar_init(&b_vdone[s], 4);
+      mbar_init(&b_khat[s], 4);
+      mbar_init(&b_vhat[s], 4);
+      mbar_init(&b_kfree[s], 1);
+      mbar_init(&b_vfree[s], 1);
+    }
+    mbar_init(&b_sfree, SW);
+    mbar_init(&b_q, SW);
+    mbar_init(&b_end, 1);
+    mbar_init(&b_krow, 1);
+    mbar_init(&b_vrow, 1);
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&b_p[k], SW);
+      mbar_init(&b_pv[k], 1);
+    }
+    fence_mbar_init();
+  }
+  if (tid == 0) {
+    s_dead = 0;
+    s_qmax = 0;
+    s_maxdepth = 0;
+  }
   const int split = blockIdx.x, splits = gridDim.x, tile = blockIdx.y, h = blockIdx.z;
   const int row0 = tile * p.rows_tile, n_rows = min(p.rows_tile, p.rows - row0);
+  grid_dep_wait();
+  int C = __reduce_max_sync(0xFFFFFFFFu, *p.c.state);
   for (int i = tid; i < p.n_nodes; i += A::kThreads) {
     int pa = i == 0 ? -1 : p.parent[i];
     if (i > 0 && (pa < 0 || pa >= i)) {
@@ -283,39 +314,10 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   const int first_copies = min(n8, A::kStages);
   // the copying warps, one for K and one for V: the first copies wait for nothing
   if (warp >= SW + 9) {
-    if (warp == SW + 9 && lane == 0) {
-      for (int s = 0; s < 4; ++s) {
-        mbar_init(&b_kraw[s], 1);
-        mbar_init(&b_vraw[s], 1);
-        mbar_init(&b_kdone[s], 4);
-        mbar_init(&b_vdone[s], 4);
-        mbar_init(&b_khat[s], 4);
-        mbar_init(&b_vhat[s], 4);
-        mbar_init(&b_kfree[s], 1);
-        mbar_init(&b_vfree[s], 1);
-      }
-      mbar_init(&b_sfree, SW);
-      mbar_init(&b_q, SW);
-      mbar_init(&b_end, 1);
-      mbar_init(&b_krow, 1);
-      mbar_init(&b_vrow, 1);
-      for (int k = 0; k < 2; ++k) {
-        mbar_init(&b_p[k], SW);
-        mbar_init(&b_pv[k], 1);
-      }
-      fence_mbar_init();
-    }
-    named_sync(1, 64);
+    named_sync(1, 64);   // the barriers are there
     if (lane == 0)
       for (int i = 0; i < first_copies; ++i) copy_codes(i, warp == SW + 10);
     if (has_tree && n8 == 0) copy_rows(warp == SW + 10);
-  } else if (warp == SW + 8) {
-    tc::tmem_alloc(&s_tmem, 512);
-  }
-  if (tid == 0) {
-    s_dead = 0;
-    s_qmax = 0;
-    s_maxdepth = 0;
   }
   // Q rows of the tile, into registers meanwhile (softmax warps)
   constexpr int kQSteps = (R * D / 8 + SW * 32 - 1) / (SW * 32);
@@ -582,21 +584,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     }
     qm = __reduce_max_sync(0xFFFFFFFFu, qm);
     if (lane == 0) atomicMax(&s_qmax, qm);
-    // columns: what each row sees of the tree, and its depth
     if (tid < R) {
-      if (tid < n_rows) {
-        const int grp = tid / HC;
-        const uint32_t bit = 1u << (tid - grp * HC);
-        int depth = -1;
-        for (int x = p.group == 1 ? row0 + tid : static_cast<int>(__umulhi(row0 + tid, p.group_m));
-             x >= 0; x = s_parent[x]) {
-          atomicOr(&s_see[x][grp], bit);
-          ++depth;
-        }
-        if (depth > p.max_depth) report(p.status, DFV_DEV_DEPTH);
-        atomicOr(&s_dep[depth][grp], bit);
-        atomicMax(&s_maxdepth, depth);
-      }
       s_neg[tid] = kNoRef;
       s_zero[tid] = 0.0f;
     }
@@ -614,14 +602,33 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&b_q);
-    const int maxdepth = s_maxdepth;
-    for (int k = tid; k < NG * (maxdepth + 1); k += SW * 32) {
-      uint32_t m = 0;
-      for (int x = 0; x <= k / NG; ++x) m |= s_dep[x][k % NG];
-      s_upto[k / NG][k % NG] = m;
+    // Columns: what each row sees of the tree, and its depth. Only a unit with
+    // the tree, or one at the window's edge (whatever the depths), needs it.
+    int lo_all = INT32_MIN;   // (no window, or none that reaches this unit)
+    if (has_tree || (p.window > 0 && (fb + 2 * c0) * kBlk < C + p.n_nodes - p.window)) {
+      if (tid < n_rows) {
+        const int grp = tid / HC;
+        const uint32_t bit = 1u << (tid - grp * HC);
+        int depth = -1;
+        for (int x = p.group == 1 ? row0 + tid : static_cast<int>(__umulhi(row0 + tid, p.group_m));
+             x >= 0; x = s_parent[x]) {
+          atomicOr(&s_see[x][grp], bit);
+          ++depth;
+        }
+        if (depth > p.max_depth) report(p.status, DFV_DEV_DEPTH);
+        atomicOr(&s_dep[depth][grp], bit);
+        atomicMax(&s_maxdepth, depth);
+      }
+      named_sync(4, SW * 32);
+      const int maxdepth = s_maxdepth;
+      for (int k = tid; k < NG * (maxdepth + 1); k += SW * 32) {
+        uint32_t m = 0;
+        for (int x = 0; x <= k / NG; ++x) m |= s_dep[x][k % NG];
+        s_upto[k / NG][k % NG] = m;
+      }
+      named_sync(4, SW * 32);
+      if (p.window > 0) lo_all = C + maxdepth - p.window + 1;
     }
-    named_sync(4, SW * 32);
-    const int lo_all = p.window > 0 ? C + maxdepth - p.window + 1 : INT32_MIN;
     const float sc = p.scale * kLog2eF * pow2i(max(qe - 141, -126));
     float l[HC];
 #pragma unroll
@@ -634,7 +641,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     // Chunks [m_lo, m_hi) need no mask: their blocks are complete and inside
     // every node's window. The loop keeps little beside x and l: what a masked
     // chunk needs is worked out in its branch.
-    int m_lo = p.window > 0 ? (lo_all + kBlk - 1) / kBlk - fb - 2 * c0 : 0;   // in blocks, from c0
+    int m_lo = lo_all > 0 ? (lo_all + kBlk - 1) / kBlk - fb - 2 * c0 : 0;   // in blocks, from c0
     m_lo = m_lo > 0 ? (m_lo + 1) / 2 : 0;
     const int m_hi = n8 - (n8 > 0 && fb + 2 * (c0 + n8) > open ? 1 : 0);
     // a chunk's scales, read one chunk ahead: this lane's block of chunk i is
@@ -665,7 +672,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
           a = lv = iv = 0.0f;
         } else if (bf && key >= T) {
           vis = s_see[key - T][cg];
-        } else if (p.window > 0) {
+        } else if (lo_all != INT32_MIN) {
           const int dd = pos - C + p.window - 1;   // deepest node that sees it
           vis = dd < 0 ? 0u : s_upto[min(dd, s_maxdepth)][cg];
         }
@@ -834,6 +841,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
         if (D >= 128 || key < D) {
 #pragma unroll
           for (int c = 0; c < HC; c += 4) {
+            if (cg * HC + c >= n_rows) break;   // rows past the tile's
             const float4 f = f4[c / 4];
             dst[hh * 128 + c * D] = x[c] * f.x;
             dst[hh * 128 + (c + 1) * D] = x[c + 1] * f.y;
@@ -884,6 +892,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int64_t at = ((static_cast<int64_t>(h) * p.tiles + tile) * splits) * p.r + r - tile * p.rows_tile;
   const float* part_lse = p.part_lse + at;
   const float* part_o = p.part_o + at * D;
+  grid_dep_launch_dependents();
   grid_dep_wait();
   float m = -INFINITY;
   for (int s = lane; s < splits; s += 32) m = fmaxf(m, part_lse[s * p.r]);
@@ -947,9 +956,11 @@ struct AttnPlan {
 // registers (a quarter of the columns a thread, twice) below.
 constexpr int max_rows(int d) { return d == 256 ? 80 : 96; }
 
-// The fewest tiles, as even as they come. Slices: a unit costs its
-// chunks plus about two for its start and end, and the SMs take units in
-// waves; the count with the least time, the fewest of equals.
+// The fewest tiles, as even as they come. Slices: the SMs take units in waves,
+// a unit costs its chunks plus its start and end, and each slice adds its
+// partial rows, written and read once. Measured at ctx 61440, window 2048, 23
+// nodes (18 chunks, 8 units, 0.28 us of partial rows a slice): 6, 9, 12 and
+// 18 slices take 20.4, 16.2, 18.2 and 17.7 us; the model says 9.
 static AttnPlan attn_plan(int n_nodes, int hq, int hkv, int d, int window, int capacity) {
   AttnPlan pl;
   const int rows = n_nodes * (hq / hkv);
@@ -961,11 +972,13 @@ static AttnPlan attn_plan(int n_nodes, int hq, int hkv, int d, int window, int c
   const int64_t units = static_cast<int64_t>(hkv) * pl.tiles;
   const int sms = sm_count();
   const int most = chunks < kMaxSplits ? chunks : kMaxSplits;
-  int64_t best = INT64_MAX;
+  const double chunk_us = 0.4 + d / 256.0 * (1.0 + 0.6 * pl.r / 80.0);
+  const double merge_us = static_cast<double>(n_nodes) * hq * d * 8 / 4e6;   // of one slice
+  double best = 1e30;
   pl.splits = 1;
   for (int s = 1; s <= most && (s == 1 || units * s <= 4 * sms); ++s) {
-    const int64_t waves = (units * s + sms - 1) / sms;
-    const int64_t cost = waves * ((chunks + s - 1) / s + 2);
+    const double cost = ((units * s + sms - 1) / sms) * ((chunks + s - 1) / s * chunk_us + 6.0) +
+                        s * merge_us;
     if (cost < best) {
       best = cost;
       pl.splits = s;
@@ -995,18 +1008,21 @@ static dfv_status attn_launch(const AttnParams& p, const MergeParams& m, cudaStr
       return DFV_ERR_CUDA;
     configured[dev].store(1, std::memory_order_release);
   }
-  kv8_attn_kernel<D, R>
-      <<<dim3(m.splits, m.tiles, p.c.n_kv_heads), A::kThreads, A::kBytes, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return DFV_ERR_CUDA;
+  // both launches may be set up while the kernel before them runs
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.hq, p.n_nodes);
-  cfg.blockDim = dim3(kMergeThreads);
+  cfg.gridDim = dim3(m.splits, m.tiles, p.c.n_kv_heads);
+  cfg.blockDim = dim3(A::kThreads);
+  cfg.dynamicSmemBytes = A::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv8_attn_kernel<D, R>, p) != cudaSuccess) return DFV_ERR_CUDA;
+  cfg.gridDim = dim3(p.hq, p.n_nodes);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D>, m) == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
 }
 
