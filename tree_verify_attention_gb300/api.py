@@ -445,10 +445,19 @@ class VerifyStep:
 
     ``pipelined=True`` launches each step so that it overlaps the previous
     kernel of the stream (``DFV_STEP_PIPELINED``); the object then keeps two
-    workspaces and uses them in turn, as consecutive pipelined steps need."""
+    workspaces and uses them in turn, as consecutive pipelined steps need.
+
+    ``fmt="int8"`` plans for an :class:`Int8Cache`: the step is then the
+    attention, the argmax with the walk, and the commit, launched one after
+    the other (not pipelined, no ``tree_as_cache``).
+
+    ``top=K`` also gives, per node, the log probability of its argmax token
+    (``logprob``; the emitted tokens are the path's), the entropy of its
+    logits (``entropy``) and its K most probable tokens (``top_ids``,
+    ``top_logprobs``); ``top=0`` the first two alone."""
 
     def __init__(self, n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity, vocab,
-                 max_depth=16, device="cuda", pipelined=False):
+                 max_depth=16, device="cuda", pipelined=False, fmt="q4_0", top=None):
         self.shape = (n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity, vocab)
         self.max_depth = max_depth
         dev = torch.device(device)
@@ -459,10 +468,28 @@ class VerifyStep:
         self.path = torch.empty(n_nodes, dtype=torch.int32, device=dev)
         self.out_tokens = torch.empty(n_nodes, dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        nb = step_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity,
-                                  vocab)
+        self.int8 = fmt == "int8"
+        if not self.int8:
+            _fmt_code(fmt)
+        elif pipelined:
+            raise DfvError("pipelined is not available with an Int8Cache")
+        if self.int8:
+            nb = int8_attn_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window,
+                                           capacity)
+        else:
+            nb = step_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity,
+                                      vocab)
         if nb == 0:
             raise DfvError(f"unsupported step shape {self.shape}")
+        if self.int8:
+            self.accept_ws = workspace(accept_workspace_bytes(n_nodes, vocab), device=dev)
+        self.top = top
+        if top is not None:
+            self.logprob = torch.empty(n_nodes, dtype=torch.float32, device=dev)
+            self.entropy = torch.empty(n_nodes, dtype=torch.float32, device=dev)
+            self.top_ids = torch.empty(n_nodes, top, dtype=torch.int32, device=dev) if top else None
+            self.top_logprobs = torch.empty(n_nodes, top, dtype=torch.float32,
+                                            device=dev) if top else None
         self.pipelined = bool(pipelined)
         self.workspaces = [workspace(nb, device=dev) for _ in range(2 if self.pipelined else 1)]
         self.ws = self.workspaces[0]
@@ -473,6 +500,18 @@ class VerifyStep:
         n, hq, hkv, d, window, cap, vocab = self.shape
         if cache.capacity != cap:
             raise DfvError("cache capacity differs from the planned one")
+        if isinstance(cache, Int8Cache) != self.int8:
+            raise DfvError("the step is planned for another kind of cache")
+        if self.int8:
+            tree_verify_attn(cache, q, tree_k, tree_v, parent, window, self.max_depth, self.out,
+                             self.lse, self.ws, scale=scale, status=self.status, stream=stream,
+                             tree_as_cache=tree_as_cache)
+            greedy_accept(logits, parent, tokens, self.argmax, self.accept_len, self.path,
+                          self.out_tokens, self.accept_ws, status=self.status, stream=stream)
+            kv_commit(cache, self.accept_len, self.path, tree_k, tree_v, status=self.status,
+                      stream=stream)
+            self._logprobs(logits, stream)
+            return
         _dev(q, "q", _BF16, n * hq * d)
         _dev(tree_k, "tree_k", _BF16, n * hkv * d)
         _dev(tree_v, "tree_v", _BF16, n * hkv * d)
@@ -492,3 +531,11 @@ class VerifyStep:
             self.argmax.data_ptr(), self.accept_len.data_ptr(), self.path.data_ptr(),
             self.out_tokens.data_ptr(), ws.data_ptr(), ws.numel(),
             self.status.data_ptr(), _stream(stream)), "dfv_verify_step")
+        self._logprobs(logits, stream)
+
+    def _logprobs(self, logits, stream):
+        if self.top is None:
+            return
+        token_logprobs(logits if logits.dtype != torch.int16 else logits.view(torch.bfloat16),
+                       self.argmax, self.logprob, self.entropy, self.top_ids, self.top_logprobs,
+                       status=self.status, stream=stream)
