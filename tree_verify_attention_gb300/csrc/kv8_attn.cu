@@ -41,7 +41,6 @@
 
 #include <atomic>
 #include <math.h>
-#include <type_traits>
 
 #include "kv8.cuh"
 #include "tc.cuh"
@@ -436,29 +435,34 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     }
   } else if (warp >= SW) {
     // ------------------------------------------------------ operands to TMEM
-    // One body for both operands, unrolled: what differs are constants.
-    auto convert = [&](auto tag) {
-      constexpr bool kV = decltype(tag)::value;
-      const int slot = (warp & 3) * 32 + lane;   // key (K) or dim of a half (V)
-      uint64_t* raw_full = kV ? b_vraw : b_kraw;
-      uint64_t* raw_done = kV ? b_vdone : b_kdone;
-      uint64_t* hat = kV ? b_vhat : b_khat;
-      const uint32_t t_op = tmem + lanes + (kV ? A::kTV : A::kTK);
-      constexpr int kParts = kV ? A::kVSub : A::kKSub, kPer = A::kPart / 32;   // of 32-column pieces
-      constexpr int kPieces = kParts * kPer;
-      const bool works = !kV || D >= 128 || slot < D;   // D = 64: V^T has 64 lanes
-      // the bytes of a piece, for this thread: K 64 dims of its key (16-byte
-      // pieces 64 * 16 apart), V 64 keys of its dim (D * 16 apart)
-      const int base0 = kV ? A::kRaw + slot * 16 : (slot >> 6) * kBlk * D + (slot & 63) * 16;
-      bool ok = true;
-      // A part's columns are free once the products have read the last chunk's.
-      auto take = [&](int i, int part) {
-        if (i > 0)
-          ok = kV && part == kParts - 1
-                   ? role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead)
-                   : role_wait(kV ? &b_vfree[part] : &b_kfree[part], (i - 1) & 1, &s_dead);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        tc::fence_after_sync();
+    // One body for both operands: the loops of all roles together have to
+    // stay in the instruction cache (a body per operand: 110 instead of 107 us
+    // for 23 nodes at ctx 131072).
+    const bool is_v = warp >= SW + 4;
+    const int slot = (warp & 3) * 32 + lane;   // key (K) or dim of a half (V)
+    uint64_t* raw_full = is_v ? b_vraw : b_kraw;
+    uint64_t* raw_done = is_v ? b_vdone : b_kdone;
+    uint64_t* hat = is_v ? b_vhat : b_khat;
+    const uint32_t t_op = tmem + lanes + (is_v ? A::kTV : A::kTK);
+    constexpr int kPer = A::kPart / 32, kPieces = A::kVSub * kPer;   // pieces of 32 columns
+    static_assert(A::kKSub == A::kVSub || (D == 64 && A::kKSub == 1), "parts");
+    const int pieces = D == 64 && !is_v ? 1 : kPieces;
+    const bool works = !is_v || D >= 128 || slot < D;   // D = 64: V^T has 64 lanes
+    // the bytes of a piece, for this thread: K 64 dims of its key (16-byte
+    // pieces 64 * 16 apart), V 64 keys of its dim (D * 16 apart); pieces of V
+    // run over the chunk's blocks, then the halves of the dims
+    const int base0 = is_v ? A::kRaw + slot * 16 : (slot >> 6) * kBlk * D + (slot & 63) * 16;
+    const int step = is_v ? D * 16 : kBlk * 16;
+    const int step1 = is_v ? kBlk * D : 4 * kBlk * 16, step2 = is_v ? 128 * 16 : 8 * kBlk * 16;
+    bool ok = true;
+    // A part's columns are free once the products have read the last chunk's.
+    auto take = [&](int i, int part) {
+      if (i > 0)
+        ok = is_v && part == A::kVSub - 1
+                 ? role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead)
+                 : role_wait(is_v ? &b_vfree[part] : &b_kfree[part], (i - 1) & 1, &s_dead);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      tc::fence_after_sync();
     };
     auto give = [&](int part) {
       tc::store_wait();
@@ -473,22 +477,22 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
       if (!ok) break;
       const uint8_t* raw = smem + s * 2 * A::kRaw + base0;
       uint4 q[4];
-      auto fetch = [&](int c) {   // V piece (half, block): dims 128 on, keys of the second block
-        const int at = kV ? (c >> 1) * 128 * 16 + (c & 1) * kBlk * D : c * 4 * kBlk * 16;
+      auto fetch = [&](int c) {
+        const uint8_t* mine = raw + (c >> 1) * step2 + (c & 1) * step1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          q[j] = *reinterpret_cast<const uint4*>(raw + at + j * (kV ? D : kBlk) * 16);
+        for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const uint4*>(mine + j * step);
       };
       if (works) fetch(0);
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) {
+        if (c >= pieces) break;
         uint32_t w[32];
         if (works) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) codes_to_half(q[j], w + 8 * j);
-          if (c + 1 < kPieces) fetch(c + 1);   // lands while this piece is handed over
+          if (c + 1 < pieces) fetch(c + 1);   // lands while this piece is handed over
         }
-        if (c + 1 == kPieces) {   // every code is in registers
+        if (c + 1 == pieces) {   // every code is in registers
           __syncwarp();
           if (lane == 0) mbar_arrive(&raw_done[s]);
         }
@@ -501,25 +505,26 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
         if (works) tc::TmemIo<32>::store(t_op + c * 32, w);
       }
       if (!ok) break;
-      give(kParts - 1);
+      give((pieces - 1) / kPer);
     }
     if (has_tree) {
       // The bf16 chunk: key slots [0, T) are the open block's rows, then the
       // tree nodes. Each key is scaled to binary16 by a power of two (largest
       // magnitude in [64, 128)).
-      ok = ok && role_wait(kV ? &b_vrow : &b_krow, 0, &s_dead);
-      ok = named_sync_and(kV ? 3 : 2, 128, ok);
-      if (!ok) return;
-      uint8_t* rows = smem + (kV ? kAtKeys * A::kRowB : 0);
+      ok = ok && role_wait(is_v ? &b_vrow : &b_krow, 0, &s_dead);
+      ok = named_sync_and(is_v ? 3 : 2, 128, ok);
+    }
+    if (has_tree && ok) {
+      uint8_t* rows = smem + (is_v ? kAtKeys * A::kRowB : 0);
       uint8_t* row = rows + slot * A::kRowB;
       const bool live = slot < live_rows;
       const uint32_t m = live ? row_max<D>(row) : 0u;
       const bool bad = m >= kBigBits;   // infinite, NaN or out of range
       const int e = max(static_cast<int>(m >> 7), 86);
       const float f = bad || !live ? 0.0f : pow2i(133 - e);
-      s_bad[kV][slot] = bad;
+      s_bad[is_v][slot] = bad;
       if (bad) report(p.status, DFV_DEV_NONFINITE);
-      if (!kV) {
+      if (!is_v) {
         s_ksc[slot] = bad ? 0.0f : pow2i(e - 133);
       } else {
         s_vexp[slot] = bad ? 0 : e - 133;
@@ -530,11 +535,11 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
         for (int j = 0; j < D / 8; ++j)
           *reinterpret_cast<uint4*>(row + j * 16) = make_uint4(0, 0, 0, 0);
       }
-      if (kV) named_sync(3, 128);
+      if (is_v) named_sync(3, 128);   // V reads across rows
 #pragma unroll 1
-      for (int c = 0; c < kPieces; ++c) {
+      for (int c = 0; c < pieces; ++c) {
         uint32_t w[32];
-        if (!kV) {
+        if (!is_v) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint4 x = *reinterpret_cast<const uint4*>(row + (c * 8 + j) * 16);
@@ -555,17 +560,12 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
             w[q] = pack_half2(__uint_as_float(a << 16) * g.x, __uint_as_float(b << 16) * g.y);
           }
         }
-        if (c % kPer == 0) {
-          take(n8, c / kPer);
-          if (!ok) break;
-        }
+        if (c % kPer == 0) take(n8, c / kPer);
+        if (!ok) break;
         if (works) tc::TmemIo<32>::store(t_op + c * 32, w);
         if (c % kPer == kPer - 1) give(c / kPer);
       }
     }
-    };
-    if (warp >= SW + 4) convert(std::true_type{});
-    else convert(std::false_type{});
   } else {
     // ------------------------------------------------------ Q, tree, softmax
     const int cg = warp >> 2;                  // column group
