@@ -72,6 +72,32 @@ def test_append_in_pieces(d, dtype, pieces):
         assert torch.equal(bk, gk.to(torch.bfloat16)) and torch.equal(bv, gv.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("hkv,d,n,at", [(8, 256, 64 * 60, 0), (8, 256, 64 * 60 + 17, 45),
+                                        (16, 128, 64 * 90 + 63, 64), (32, 64, 64 * 85 + 1, 127),
+                                        (3, 256, 64 * 250 + 31, 5)])
+def test_long_writes(hkv, d, n, at):
+    """Long bf16 writes take their inner blocks through another kernel."""
+    k, v = rows(35, at + n, hkv, d), rows(36, at + n, hkv, d)
+    v[at + 300, hkv - 1, 3] = float("inf")
+    kd, vd = k.to(DEV, torch.bfloat16), v.to(DEV, torch.bfloat16)
+    v[at + 300, hkv - 1, 3] = 0.0
+    cache = api.Int8Cache(hkv, d, at + n + 10, device=DEV)
+    cache.append(kd[:at], vd[:at])
+    cache.append(kd[at:], vd[at:])
+    assert int(cache.status) == api.DEV_NONFINITE
+    check(cache, k, v, at + n)
+    if at:      # the same place again, refused: its block is no longer held
+        before = cache.k.clone()
+        cache.status.zero_()
+        cache.append(vd[at:], kd[at:], at=at if at % 64 else at + 1)
+        assert int(cache.status) == api.DEV_CTX and torch.equal(cache.k, before)
+    cache.append(vd, kd, at=0)
+    check(cache, v, k, at + n)
+    other = api.Int8Cache(hkv, d, at + n + 10, device=DEV)
+    other.append(k.to(DEV), v.to(DEV))        # float32 rows take the other path
+    check(other, k, v, at + n)
+
+
 def test_float_rows_are_rounded_to_bf16_first():
     g = torch.Generator().manual_seed(3)
     x = torch.randn(130, 2, 64, generator=g)

@@ -23,6 +23,8 @@
 // dims of one position, a V thread 4 dims of 16 positions: the piece of the
 // layout that it writes is then whole in its registers.
 
+#include <atomic>
+
 #include "kv8.cuh"
 
 namespace dfv {
@@ -36,6 +38,7 @@ struct Kv8AppendParams {
   const int32_t* path;        // with accept_len: row k of the write is src row path[k]
   const int32_t* accept_len;
   int n_nodes;
+  int bulk;      // blocks b0 + 1 .. b0 + bulk are written by kv8_append_bulk_kernel
   uint32_t* status;
 };
 
@@ -294,7 +297,8 @@ template <typename T, int D, bool kVec, bool kV, typename F>
 __device__ __forceinline__ bool append_block(const Kv8AppendParams& p, const Kv8Span& s,
                                              const int* path, uint32_t* s_max, F refused) {
   using Io = BlockIo<T, D, kVec>;
-  const int h = blockIdx.y, b = s.b0 + blockIdx.x;
+  const int h = blockIdx.y;
+  const int b = s.b0 + static_cast<int>(blockIdx.x) + (blockIdx.x > 0 ? p.bulk : 0);
   const int tid = threadIdx.x;
   const bool mine = b * kBlk < s.end;
   uint32_t w[32];
@@ -391,12 +395,98 @@ __global__ void __launch_bounds__(D) kv8_append_kernel(const __grid_constant__ K
   }
 }
 
+// The inner blocks of a long write of bf16 rows: source rows throughout, and
+// none that the tail keeps. One wave of CTAs walks over them while the copy
+// engine brings each CTA its next block: with loads to registers a CTA's loads
+// and its arithmetic took turns (61440 rows of 4 heads of 256, written and
+// read back: 151 us, here 140; three slots and two CTAs an SM: 165). The
+// launch before kv8_append_kernel, which takes the blocks at both ends and
+// advances the length.
+constexpr int kBulkSlots = 2;
+
+template <int D>
+__global__ void __launch_bounds__(D) kv8_append_bulk_kernel(const __grid_constant__ Kv8AppendParams p) {
+  using Io = BlockIo<__nv_bfloat16, D, true>;
+  constexpr int kSlot = kBlk * D * 2;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kBulkSlots];
+  __shared__ uint32_t s_max[2][D / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_launch_dependents();
+  if (tid == 0) {
+    for (int k = 0; k < kBulkSlots; ++k) mbar_init(&full[k], 1);
+    fence_mbar_init();
+  }
+  grid_dep_wait();
+  const int C = p.c.state[0], held = p.c.state[2];
+  const int at = p.at < 0 ? C : p.at;
+  // refused as by kv8_append_kernel, which reports it
+  if (C < 0 || C > p.c.capacity || at > C || at + p.n > p.c.capacity ||
+      (at % kBlk != 0 && at / kBlk < held))
+    return;
+  __syncthreads();
+  const int b0 = at / kBlk, per = p.bulk * p.c.n_kv_heads;   // blocks of K, as many of V
+  const int total = 2 * per;
+  // block `it` of the walk, a head's blocks in a row
+  auto copy = [&](int it, int slot) {
+    const int kv = it >= per, r = kv ? it - per : it;
+    const int h = r / p.bulk, b = b0 + 1 + r - h * p.bulk;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.src[kv]) + h * p.s_head[kv] +
+                               static_cast<int64_t>(b * kBlk - at) * p.s_row[kv];
+    if (lane == 0) mbar_arrive_expect_tx(&full[slot], kSlot);
+    __syncwarp();
+    for (int t = lane; t < kBlk; t += 32)
+      bulk_g2s(smem + slot * kSlot + t * D * 2, src + t * p.s_row[kv], D * 2, &full[slot]);
+  };
+  const int step = gridDim.x;
+  int it = blockIdx.x;
+  if (warp == 0)
+    for (int k = 0; k < kBulkSlots - 1; ++k)
+      if (it + k * step < total) copy(it + k * step, k);
+  for (int k = 0; it < total; it += step, ++k) {
+    const int slot = k % kBulkSlots;
+    // the slot freed by the last block's reads (a barrier ago) is filled again
+    if (warp == 0 && it + (kBulkSlots - 1) * step < total)
+      copy(it + (kBulkSlots - 1) * step, (k + kBulkSlots - 1) % kBulkSlots);
+    if (!mbar_wait_bounded(&full[slot], (k / kBulkSlots) & 1)) report(p.status, DFV_DEV_TIMEOUT);
+    const int kv = it >= per, r = kv ? it - per : it;
+    const int h = r / p.bulk, b = b0 + 1 + r - h * p.bulk;
+    const uint8_t* rows = smem + slot * kSlot;
+    uint32_t w[32];
+    if (kv == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4* s = reinterpret_cast<const uint4*>(
+            rows + tid / Io::kTpt * D * 2 + (tid % Io::kTpt + j * Io::kTpt) * 32);
+        *reinterpret_cast<uint4*>(w + 8 * j) = s[0];
+        *reinterpret_cast<uint4*>(w + 8 * j + 4) = s[1];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint2 v = *reinterpret_cast<const uint2*>(
+            rows + (tid / Io::kVt * 16 + i) * D * 2 + tid % Io::kVt * 8);
+        w[2 * i] = v.x;
+        w[2 * i + 1] = v.y;
+      }
+    }
+    uint32_t m = __reduce_max_sync(0xFFFFFFFFu, keep_storable(w, p.status));
+    if (lane == 0) s_max[k & 1][warp] = m;
+    __syncthreads();   // maxima are there, and the slot has been read
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) m = max(m, s_max[k & 1][e]);
+    if (kv == 0) Io::template store_codes<false>(p, h, b, w, m);
+    else Io::template store_codes<true>(p, h, b, w, m);
+  }
+}
+
 // Launch that may be set up while the kernel before it runs (its kernels wait
 // for that one before they touch anything).
 template <typename P>
 dfv_status launch_after(void (*kernel)(P), dim3 grid, int threads, const P& p,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, int smem = 0) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
@@ -408,9 +498,42 @@ dfv_status launch_after(void (*kernel)(P), dim3 grid, int threads, const P& p,
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
 }
 
+template <int D>
+dfv_status bulk_launch(const Kv8AppendParams& p, cudaStream_t stream) {
+  constexpr int kSmem = kBulkSlots * kBlk * D * 2;
+  static std::atomic<int> configured[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DFV_ERR_CUDA;
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kv8_append_bulk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmem) != cudaSuccess)
+      return DFV_ERR_CUDA;
+    configured[dev].store(1, std::memory_order_release);
+  }
+  const int most = sm_count() * (768 / D);   // 64 KB of slots and 256 threads, three times an SM
+  const int64_t blocks = 2ll * p.bulk * p.c.n_kv_heads;
+  return launch_after(kv8_append_bulk_kernel<D>, dim3(blocks < most ? blocks : most), D, p, stream,
+                      kSmem);
+}
+
 template <typename T, bool kVec>
-dfv_status append_launch_t(const Kv8AppendParams& p, int rows, cudaStream_t stream) {
-  const dim3 grid((rows + kBlk - 2) / kBlk + 1, p.c.n_kv_heads, 2);   // blocks that `rows` can touch
+dfv_status append_launch_t(Kv8AppendParams& p, int rows, cudaStream_t stream) {
+  int blocks = (rows + kBlk - 2) / kBlk + 1;   // that `rows` can touch
+  if constexpr (sizeof(T) == 2 && kVec) {
+    // Wherever the write starts, blocks b0 + 1 .. b0 + n / 64 - 2 are complete
+    // and not among the two that the tail keeps. Worth a launch of their own
+    // from about four waves of blocks on.
+    const int inner = p.accept_len ? 0 : rows / kBlk - 2;
+    if (static_cast<int64_t>(inner) * p.c.n_kv_heads * p.c.head_dim >= 512ll * 2 * sm_count()) {
+      p.bulk = inner;
+      blocks -= inner;
+      const dfv_status st = p.c.head_dim == 64    ? bulk_launch<64>(p, stream)
+                            : p.c.head_dim == 128 ? bulk_launch<128>(p, stream)
+                                                  : bulk_launch<256>(p, stream);
+      if (st != DFV_OK) return st;
+    }
+  }
+  const dim3 grid(blocks, p.c.n_kv_heads, 2);
   switch (p.c.head_dim) {
     case 64: return launch_after(kv8_append_kernel<T, 64, kVec>, grid, 64, p, stream);
     case 128: return launch_after(kv8_append_kernel<T, 128, kVec>, grid, 128, p, stream);
