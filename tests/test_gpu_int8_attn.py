@@ -273,7 +273,8 @@ def test_captured_step_follows_the_committed_length():
     n, hq, hkv, d = 4, 4, 2, 128
     c = Case(n, hq, hkv, d, 120, cap=400, parent=[-1, 0, 1, 2])
     ref, _ = c.check()
-    out, lse = torch.empty(n, hq, d, device=DEV, dtype=torch.bfloat16), torch.empty(n, hq, device=DEV)
+    out = torch.empty(n, hq, d, device=DEV, dtype=torch.bfloat16)
+    lse = torch.empty(n, hq, device=DEV)
     ws = api.workspace(api.int8_attn_workspace_bytes(n, hq, hkv, d, 0, 400), device=DEV)
     length = torch.tensor([3], dtype=torch.int32, device=DEV)
     path = torch.arange(n, dtype=torch.int32, device=DEV)
@@ -314,6 +315,18 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for c, out in outs:
         assert np.array_equal(out.double().cpu().numpy(), (ra if c is a else rb)[0])
+
+
+def test_many_lengths_twice():
+    """Every hand-over between the kernel's roles, at many chunk counts: two
+    runs of each are equal to the bit, and the float64 result is met."""
+    rng = np.random.default_rng(11)
+    for _ in range(40):
+        n, ctx = int(rng.integers(1, 66)), int(rng.integers(0, 6000))
+        c = Case(n, 4, 1, int(rng.choice([64, 128, 256])), ctx, int(rng.choice([0, 0, 300, 4000])),
+                 seed=int(rng.integers(1000)))
+        a, b = c.check(), c.run()
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
 
 
 def test_offsets_past_31_bits():

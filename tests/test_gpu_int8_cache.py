@@ -122,7 +122,8 @@ def test_ties_round_to_even():
     check(cache, x, y.to(torch.bfloat16).float(), 64)
 
 
-@pytest.mark.parametrize("layout", ["head_major", "padded", "odd_base", "odd_stride", "reversed_k_v"])
+@pytest.mark.parametrize("layout", ["head_major", "padded", "odd_base", "odd_stride",
+                                    "reversed_k_v"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_strides(layout, dtype):
     n, hkv, d = 150, 4, 128
@@ -311,11 +312,11 @@ def test_commit_the_same_node_twice_and_bad_paths():
     assert int(cache.status) == 0
     i = [0, 2, 2]
     check(cache, tk[i], tv[i], 3)
-    for L, path, bit in ((2, (0, 5, 0, 0, 0), api.DEV_BAD_PATH), (2, (0, -1, 0, 0, 0), api.DEV_BAD_PATH),
-                         (0, (0, 0, 0, 0, 0), api.DEV_BAD_PATH), (6, (0, 0, 0, 0, 0), api.DEV_BAD_PATH)):
+    for L, path in ((2, (0, 5, 0, 0, 0)), (2, (0, -1, 0, 0, 0)), (0, (0, 0, 0, 0, 0)),
+                    (6, (0, 0, 0, 0, 0))):
         cache.status.zero_()
         api.kv_commit(cache, dev(L), dev(*path), *args)
-        assert int(cache.status) == bit
+        assert int(cache.status) == api.DEV_BAD_PATH
         check(cache, tk[i], tv[i], 3)
     cache.status.zero_()
     api.kv_commit(cache, dev(5), dev(0, 1, 2, 3, 4), *args)

@@ -48,7 +48,8 @@ def check(logits, tokens, top):
     def near(got, ref, extra=0.0):
         fin = np.isfinite(ref)
         assert np.array_equal(got[~fin], ref[~fin])
-        assert np.all(np.abs(got[fin] - ref[fin]) <= base + extra + 2.0 ** -22 * np.abs(ref[fin]) + 1e-7)
+        tol = base + extra + 2.0 ** -22 * np.abs(ref[fin]) + 1e-7
+        assert np.all(np.abs(got[fin] - ref[fin]) <= tol)
 
     near(lp, want[0])
     near(tlp, want[3])

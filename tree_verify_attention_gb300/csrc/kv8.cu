@@ -405,7 +405,8 @@ __global__ void __launch_bounds__(D) kv8_append_kernel(const __grid_constant__ K
 constexpr int kBulkSlots = 2;
 
 template <int D>
-__global__ void __launch_bounds__(D) kv8_append_bulk_kernel(const __grid_constant__ Kv8AppendParams p) {
+__global__ void __launch_bounds__(D)
+    kv8_append_bulk_kernel(const __grid_constant__ Kv8AppendParams p) {
   using Io = BlockIo<__nv_bfloat16, D, true>;
   constexpr int kSlot = kBlk * D * 2;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -425,6 +426,7 @@ __global__ void __launch_bounds__(D) kv8_append_bulk_kernel(const __grid_constan
       (at % kBlk != 0 && at / kBlk < held))
     return;
   __syncthreads();
+  fence_proxy_async_global();   // what earlier kernels wrote, to the copy engine
   const int b0 = at / kBlk, per = p.bulk * p.c.n_kv_heads;   // blocks of K, as many of V
   const int total = 2 * per;
   // block `it` of the walk, a head's blocks in a row

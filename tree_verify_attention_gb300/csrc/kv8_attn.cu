@@ -35,9 +35,11 @@
 //
 // Roles of a CTA (one per SM): 8 or 16 softmax warps (lane quadrant w % 4,
 // column group w / 4), four warps that put K codes into TMEM, four for V, one
-// that issues MMAs, two that copy K and V. A unit is (KV head, tile of at
-// most 80 or 96 query rows, slice of the chunks). Bound by HBM while a tile has few
-// rows, by the softmax and the conversion of the codes for many.
+// that issues MMAs, two that copy K and V. A unit is (KV head, tile of at most
+// 80 query rows, or 96 below D = 256, slice of the chunks). Bound by HBM while
+// a tile has few rows, by the softmax and the conversion for many: 24 heads of
+// 256 over 131072 positions take 51.5 us for one node (5.2 TB/s) and 106 us for
+// 23 (700 TFLOP/s; 63 % of the issue slots busy).
 
 #include <atomic>
 #include <math.h>
@@ -58,7 +60,8 @@ template <int D, int R>
 struct AttnShape {
   // Softmax warps: four lane quadrants times the column groups. The softmax
   // of many columns is a long chain per warp; twice the warps, with half the
-  // columns each, shorten it (and leave 72 registers a thread).
+  // columns each, shorten it and leave 72 registers a thread (23 nodes, ctx
+  // 131072: 127 -> 120 us; 12 warps of 24 columns were no better than 16).
   static constexpr int kSoft = R >= 64 ? 16 : 8;
   static constexpr int kGroups = kSoft / 4;
   static constexpr int kCols = R / kGroups;             // columns of a softmax thread
@@ -204,10 +207,11 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   // products (K's last part read: the scores are there); scores read; P
   // written and O there (two each, used in turn: a phase's parity tells it
   // from its neighbours only, and the softmax may lag P V by two chunks);
-  // bf16 rows landed
+  // bf16 rows landed, and their scales written (once: the operands' own
+  // phases may be one behind or ahead of the softmax here)
   __shared__ uint64_t b_kraw[4], b_kdone[4], b_vraw[4], b_vdone[4];
   __shared__ uint64_t b_khat[4], b_kfree[4], b_vhat[4], b_vfree[4];
-  __shared__ uint64_t b_sfree, b_q, b_end, b_krow, b_vrow, b_p[2], b_pv[2];
+  __shared__ uint64_t b_sfree, b_q, b_end, b_krow, b_vrow, b_rowsc, b_p[2], b_pv[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_dead;
   __shared__ int s_parent[kMaxNodes], s_maxdepth;
@@ -223,7 +227,8 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   // both the same in every lane, which the compiler knows of a reduction's
   // result: what follows from them then lives in uniform registers
-  const int warp = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tid >> 5)));
+  const int warp =
+      static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tid >> 5)));
   // what touches no global memory may run under the kernel before
   grid_dep_launch_dependents();   // the merge may be set up meanwhile
   if (warp == SW + 8) {
@@ -244,6 +249,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     mbar_init(&b_end, 1);
     mbar_init(&b_krow, 1);
     mbar_init(&b_vrow, 1);
+    mbar_init(&b_rowsc, 8);
     for (int k = 0; k < 2; ++k) {
       mbar_init(&b_p[k], SW);
       mbar_init(&b_pv[k], 1);
@@ -314,6 +320,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   // the copying warps, one for K and one for V: the first copies wait for nothing
   if (warp >= SW + 9) {
     named_sync(1, 64);   // the barriers are there
+    fence_proxy_async_global();   // what earlier kernels wrote, to the copy engine
     if (lane == 0)
       for (int i = 0; i < first_copies; ++i) copy_codes(i, warp == SW + 10);
     if (has_tree && n8 == 0) copy_rows(warp == SW + 10);
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
-  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // first lane of the quadrant << 16
+  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // quadrant's first lane << 16
 
   if (warp >= SW + 9) {
     // ------------------------------------------------------ bulk copies
@@ -535,6 +542,8 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
         for (int j = 0; j < D / 8; ++j)
           *reinterpret_cast<uint4*>(row + j * 16) = make_uint4(0, 0, 0, 0);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_rowsc);
       if (is_v) named_sync(3, 128);   // V reads across rows
 #pragma unroll 1
       for (int c = 0; c < pieces; ++c) {
@@ -645,13 +654,14 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     m_lo = m_lo > 0 ? (m_lo + 1) / 2 : 0;
     const int m_hi = n8 - (n8 > 0 && fb + 2 * (c0 + n8) > open ? 1 : 0);
     // a chunk's scales, read one chunk ahead: this lane's block of chunk i is
-    // sc_at + 2 i of the scales, there for i < sc_n
+    // sc_at + 2 i of the scales, there for i < sc_n (plain loads, not the
+    // read-only path: this kernel may start before the one that wrote them ends)
     const uint32_t sc_at = static_cast<uint32_t>(h) * p.nblk + fb + 2 * c0 + (key >> 6);
     const int sc_n = min(n8, (open - (fb + 2 * c0 + (key >> 6)) + 1) / 2);
     float ks = 0.0f, vs = 0.0f;
     if (0 < sc_n) {
-      ks = __ldg(p.c.k_scale + sc_at);
-      vs = __ldg(p.c.v_scale + sc_at);
+      ks = p.c.k_scale[sc_at];
+      vs = p.c.v_scale[sc_at];
     }
 
     for (int i = 0; i < n; ++i) {
@@ -678,13 +688,12 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
         }
       }
       if (i + 1 < sc_n) {
-        ks = __ldg(p.c.k_scale + (sc_at + 2 * (i + 1)));
-        vs = __ldg(p.c.v_scale + (sc_at + 2 * (i + 1)));
+        ks = p.c.k_scale[sc_at + 2 * (i + 1)];
+        vs = p.c.v_scale[sc_at + 2 * (i + 1)];
       }
       ok = ok && role_wait(&b_kfree[A::kKSub - 1], i & 1, &s_dead);
-      if (bf) {   // the key's scales were written with the operands
-        ok = ok && role_wait(&b_khat[A::kKSub - 1], i & 1, &s_dead) &&
-             role_wait(&b_vhat[0], i & 1, &s_dead);
+      if (bf) {
+        ok = ok && role_wait(&b_rowsc, 0, &s_dead);
         if (ok && key < live_rows) {
           a = s_ksc[key] * sc;
           lv = static_cast<float>(s_vexp[key]);
@@ -889,7 +898,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int tile = r / p.rows_tile;
   const int64_t row = static_cast<int64_t>(node) * p.hq + head;
   // this row of slice 0, and what lies between slices
-  const int64_t at = ((static_cast<int64_t>(h) * p.tiles + tile) * splits) * p.r + r - tile * p.rows_tile;
+  const int64_t at = ((static_cast<int64_t>(h) * p.tiles + tile) * splits) * p.r + r -
+                     tile * p.rows_tile;
   const float* part_lse = p.part_lse + at;
   const float* part_o = p.part_o + at * D;
   grid_dep_launch_dependents();
@@ -913,7 +923,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   for (int s = tid / kV; s < splits; s += kG) {
     const float w = s_w[s];
     if (w == 0.0f) continue;   // an empty slice has no row
-    const float4 v = reinterpret_cast<const float4*>(part_o + static_cast<int64_t>(s) * p.r * D)[tid % kV];
+    const float4 v =
+        reinterpret_cast<const float4*>(part_o + static_cast<int64_t>(s) * p.r * D)[tid % kV];
     a.x = fmaf(w, v.x, a.x);
     a.y = fmaf(w, v.y, a.y);
     a.z = fmaf(w, v.z, a.z);
@@ -935,9 +946,11 @@ __global__ void __launch_bounds__(kMergeThreads)
     a.z *= inv;
     a.w *= inv;
     if (p.out_bf16) {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(a.z, a.w);
       reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D)[tid] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                     *reinterpret_cast<const uint32_t*>(&hi));
     } else {
       reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D)[tid] = a;
     }

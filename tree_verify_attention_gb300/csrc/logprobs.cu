@@ -266,7 +266,8 @@ __device__ __forceinline__ void cluster_wait() {
 }
 
 template <typename T, int kLpThreads>
-__global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) logprob_kernel(const __grid_constant__ LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
+    logprob_kernel(const __grid_constant__ LogprobParams p) {
   __shared__ LpSmem sm;
   constexpr int kV = LpVec<T>::kN;
   cg::cluster_group cl = cg::this_cluster();
@@ -276,7 +277,8 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) logprob_kernel(
   // The row: a head before the first 16-byte boundary, whole vectors, a
   // tail. The vectors are dealt in equal runs; the first CTA of the cluster
   // has the head too, the last one the tail.
-  const int head = min(p.vocab, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
+  const int over = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15);   // bytes past one
+  const int head = min(p.vocab, (16 - over) % 16 / static_cast<int>(sizeof(T)));
   const int nv = (p.vocab - head) / kV;
   const int v0 = static_cast<int>(static_cast<int64_t>(nv) * rank / cs);
   const int v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / cs);
