@@ -51,6 +51,7 @@
 namespace dfv {
 
 constexpr int kAtKeys = 128;         // keys of a chunk
+constexpr int kTreeCost = 6;         // chunks that the bf16 chunk counts as
 constexpr float kRaise = 10.0f;      // a larger exponent moves the reference
 constexpr float kNoRef = 1e30f;      // -reference of a column that has seen no key
 constexpr float kLog2eF = 1.4426950408889634f;
@@ -279,17 +280,18 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     if (tid == 0) report(p.status, DFV_DEV_CTX);
     C = max(0, min(C, p.c.capacity));
   }
-  // chunks: complete blocks [fb, open) two at a time, then the bf16 chunk
+  // Chunks: complete blocks [fb, open) two at a time, then the bf16 chunk,
+  // which belongs to the last slice and counts as several: it waits for its
+  // rows when the others already land.
   const int open = C / kBlk, T = C % kBlk;
   const int lo_min = p.window > 0 ? max(0, C - p.window + 1) : 0;
   const int fb = min(lo_min / kBlk, open);
-  const int nq = (open - fb + 1) / 2, nch = nq + 1;
-  const int per = nch / splits, rem = nch - per * splits;
-  const int c0 = split * per + split * rem / splits;
-  const int c1 = (split + 1) * per + (split + 1) * rem / splits;
-  const int n = c1 - c0;
-  const bool has_tree = c1 == nch && n > 0;     // its last chunk is the bf16 one
-  const int n8 = n - (has_tree ? 1 : 0);
+  const int nq = (open - fb + 1) / 2;
+  const int per = (nq + kTreeCost) / splits, rem = nq + kTreeCost - per * splits;
+  const bool has_tree = split == splits - 1;    // its last chunk is the bf16 one
+  const int c0 = min(nq, split * per + split * rem / splits);
+  const int n8 = (has_tree ? nq : min(nq, (split + 1) * per + (split + 1) * rem / splits)) - c0;
+  const int n = n8 + (has_tree ? 1 : 0);
   const int live_rows = T + p.n_nodes;          // keys of the bf16 chunk
 
   // raw K (V) codes of chunk i into its stage (one thread)
