@@ -292,6 +292,8 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
   const int top = p.top;
   if (tid == 0) sm.count = 0;
   if (cs > 1) cluster_arrive();   // waited for before the first CTA's memory is written
+  grid_dep_launch_dependents();
+  grid_dep_wait();   // set up under the kernel before; nothing has been read yet
 
   // the given token and its logit, read meanwhile
   int token = 0;
@@ -311,13 +313,13 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
 #pragma unroll
     for (int j = 0; j < kLpVecs; ++j) {
       const int i = base + j * kLpThreads + tid;
-      v[j] = i < v1 ? __ldg(xv + i) : none;
+      v[j] = i < v1 ? xv[i] : none;
     }
   };
   const uint4* mine = xv + tid;
   auto load_full = [&](int base) {
 #pragma unroll
-    for (int j = 0; j < kLpVecs; ++j) v[j] = __ldg(mine + base + j * kLpThreads);
+    for (int j = 0; j < kLpVecs; ++j) v[j] = mine[base + j * kLpThreads];
   };
   auto value = [&](int i) { return LpVec<T>::at(v[i / kV], i % kV); };
   float jm[kLpVecs];   // maximum of each vector
@@ -498,13 +500,15 @@ dfv_status logprob_launch_t(const LogprobParams& p, int rows, int cs, cudaStream
   cfg.gridDim = dim3(static_cast<unsigned>(rows) * cs);
   cfg.blockDim = dim3(kLpThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cs;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, logprob_kernel<T, kLpThreads>, p) == cudaSuccess ? DFV_OK
                                                                                    : DFV_ERR_CUDA;
 }
