@@ -48,11 +48,12 @@ def _check(st, name):
         raise DfvError(f"{name}: {msg} (status {st})")
 
 
-def _stream(stream):
+def _stream(stream, index=None):
     if stream is not None:
         return stream.cuda_stream
     # the current stream's handle without building a Stream object (2 us a call)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if index is None else index)
 
 
 def _p(t):
@@ -60,6 +61,9 @@ def _p(t):
 
 
 def _dev(t, name, dtypes, numel=None):
+    if (t is not None and t.dtype in dtypes and t.is_cuda and t.is_contiguous()
+            and (numel is None or t.numel() >= numel)):
+        return t
     if t is None:
         raise DfvError(f"{name} is required")
     if not t.is_cuda or not t.is_contiguous():
@@ -209,8 +213,8 @@ class Int8Cache:
         _check(lib().dfv_kv8_append(
             self.handle, -1 if at is None else at, n, k_rows.data_ptr(), v_rows.data_ptr(),
             DTYPE_F32 if k_rows.dtype == torch.float32 else DTYPE_BF16, ks[r], ks[hd], vs[r],
-            vs[hd], self._status_ptr if status is None else status.data_ptr(), _stream(stream)),
-            "dfv_kv8_append")
+            vs[hd], self._status_ptr if status is None else status.data_ptr(),
+            _stream(stream, self._index)), "dfv_kv8_append")
 
     def fill(self, k_rows, v_rows, pos0=0, stream=None):
         """Rows [Hkv, n, D] at positions [pos0, pos0 + n), as KVCache.fill."""
@@ -236,8 +240,8 @@ class Int8Cache:
         _check(lib().dfv_kv8_read(
             self.handle, pos0, n, k_out.data_ptr(), v_out.data_ptr(),
             DTYPE_F32 if k_out.dtype == torch.float32 else DTYPE_BF16, st[r], st[hd],
-            self._status_ptr if status is None else status.data_ptr(), _stream(stream)),
-            "dfv_kv8_read")
+            self._status_ptr if status is None else status.data_ptr(),
+            _stream(stream, self._index)), "dfv_kv8_read")
 
 
 def int8_attn_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity):
@@ -267,7 +271,7 @@ def _int8_attn(cache, q, tree_k, tree_v, parent, window, max_depth, out, lse, ws
         tree_v.data_ptr(), parent.data_ptr(), float(scale), out.data_ptr(),
         DTYPE_F32 if out.dtype == torch.float32 else DTYPE_BF16, _p(lse), ws.data_ptr(),
         ws.numel(), cache._status_ptr if status is None else status.data_ptr(),
-        _stream(stream)), "dfv_kv8_attn")
+        _stream(stream, cache._index)), "dfv_kv8_attn")
 
 
 def kv_quantize_rows(cache, src, pos0, n_kv_heads, head_dim, capacity, head_major=False,
