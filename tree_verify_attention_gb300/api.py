@@ -175,10 +175,11 @@ class Int8Cache:
         self.n_kv_heads, self.head_dim, self.capacity = n_kv_heads, head_dim, capacity
         nblk = -(-capacity // KV8_BLOCK)
         h, d = n_kv_heads, head_dim
-        self.k = torch.zeros(h, nblk, d // 16, KV8_BLOCK, 16, dtype=torch.int8, device=device)
-        self.v = torch.zeros(h, nblk, KV8_BLOCK // 16, d, 16, dtype=torch.int8, device=device)
-        self.k_scale = torch.zeros(h, nblk, device=device)
-        self.v_scale = torch.zeros(h, nblk, device=device)
+        # nothing is read of a block before it is complete: no need to clear
+        self.k = torch.empty(h, nblk, d // 16, KV8_BLOCK, 16, dtype=torch.int8, device=device)
+        self.v = torch.empty(h, nblk, KV8_BLOCK // 16, d, 16, dtype=torch.int8, device=device)
+        self.k_scale = torch.empty(h, nblk, device=device)
+        self.v_scale = torch.empty(h, nblk, device=device)
         # the open end in one buffer: a copy of it (and copying it back) saves
         # and restores a point to which the cache can return
         tail = h * 2 * KV8_BLOCK * d
