@@ -383,7 +383,7 @@ dfv_status dfv_build_tree_mask(int n_nodes, const int32_t* parent, int32_t* dept
  *   v_codes  int8 [n_kv_heads][nblk][4][D][16]: byte (t, c) at
  *            (((h * nblk + b) * 4 + t / 16) * D + c) * 16 + t % 16
  *   k_scale, v_scale  f32 [n_kv_heads][nblk]
- *   k_tail, v_tail    bf16 [n_kv_heads][2][64][D], 16-byte aligned: block b in
+ *   k_tail, v_tail    bf16 [n_kv_heads][2][64][D], 32-byte aligned: block b in
  *            slot b % 2. With a copy of state and tails a caller can return to
  *            the point at which it was taken (codes of blocks that were
  *            complete then must not have been written over)

@@ -37,7 +37,8 @@ BAD_CACHES = [dict(n_kv_heads=0), dict(n_kv_heads=70000), dict(capacity=0),
               dict(capacity=(1 << 30) + 1), dict(state=None), dict(k_codes=None),
               dict(v_codes=None), dict(k_scale=None), dict(v_scale=None), dict(k_tail=None),
               dict(v_tail=None), dict(k_codes=A + 64), dict(v_codes=A + 16), dict(k_tail=A + 8),
-              dict(v_scale=A + 2)]
+              dict(v_scale=A + 2),
+              dict(k_tail=A + 16), dict(v_tail=A + 16)]
 
 
 def append(lib, c, at=0, n=5, k=A, v=A, dt=1):

@@ -40,7 +40,7 @@ inline bool kv8_cache_ok(const dfv_kv8_cache* c) {
          c->capacity <= (1 << 30) && c->state && c->k_codes && c->v_codes && c->k_scale &&
          c->v_scale && c->k_tail && c->v_tail && aligned(c->state, 4) && aligned(c->k_codes, 128) &&
          aligned(c->v_codes, 128) && aligned(c->k_scale, 4) && aligned(c->v_scale, 4) &&
-         aligned(c->k_tail, 16) && aligned(c->v_tail, 16);
+         aligned(c->k_tail, 32) && aligned(c->v_tail, 32);   // read 32 bytes at a time
 }
 
 inline bool kv8_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
