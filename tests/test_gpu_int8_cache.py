@@ -2,13 +2,15 @@
 back, bit for bit against the definition in ``oracle/int8.py`` (codes and
 scales have one right value, so nothing here has a tolerance)."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import oracle.int8 as I8
 from _helpers import DEV, need_gpu
-from tree_verify_attention_gb300 import api
+from tree_verify_attention_gb300 import _lib, api
 
 pytestmark = pytest.mark.gpu
 
@@ -229,6 +231,24 @@ def test_capacity_and_length_errors_write_nothing():
     cache.status.zero_()
     cache.append(k[:1].to(DEV), v[:1].to(DEV))
     assert int(cache.status) == api.DEV_CTX
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_a_write_whose_end_passes_31_bits(dtype):
+    # The largest capacity, full, and as many rows again: refused on the
+    # device before anything but the state is read, so small buffers do.
+    cap = 1 << 30
+    buf = torch.zeros(4096, dtype=torch.uint8, device=DEV)
+    state = torch.tensor([cap, 0, cap // 64 - 1, 0], dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    a = buf.data_ptr()
+    c = _lib.Kv8CacheStruct(1, 64, cap, 0, state.data_ptr(), a, a, a, a, a, a)
+    st = torch.cuda.current_stream().cuda_stream
+    assert _lib.load().dfv_kv8_append(ctypes.addressof(c), -1, cap, a, a, dtype, 0, 0, 0, 0,
+                                      status.data_ptr(), st) == 0
+    torch.cuda.synchronize()
+    assert int(status) == api.DEV_CAPACITY
+    assert state.tolist() == [cap, 0, cap // 64 - 1, 0] and not buf.any()
 
 
 def test_untouched_blocks_stay_as_they_are():

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(D) kv8_append_kernel(const __grid_constant__ K
     __syncthreads();
     if (s_bad) bad |= DFV_DEV_BAD_PATH;
   }
-  if (!bad && at + n > p.c.capacity) bad = DFV_DEV_CAPACITY;
+  if (!bad && n > p.c.capacity - at) bad = DFV_DEV_CAPACITY;   // (no sum: both reach 2^30)
   // the rows of at's block before it have to be in the tail
   auto refused = [&]() {
     if (C < 0 || C > p.c.capacity || at > C || (at % kBlk != 0 && at / kBlk < held))
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(D)
   const int C = p.c.state[0], held = p.c.state[2];
   const int at = p.at < 0 ? C : p.at;
   // refused as by kv8_append_kernel, which reports it
-  if (C < 0 || C > p.c.capacity || at > C || at + p.n > p.c.capacity ||
+  if (C < 0 || C > p.c.capacity || at > C || p.n > p.c.capacity - at ||
       (at % kBlk != 0 && at / kBlk < held))
     return;
   __syncthreads();
