@@ -178,3 +178,17 @@ def test_repeats_are_bit_equal_and_capture():
         torch.cuda.synchronize()
         for o, f in zip(outs, first):
             assert torch.equal(o, f)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("order", ["random", "ascending", "descending", "ties"])
+@pytest.mark.parametrize("n,v,top", [(66, 100003, 32), (80, 60000, 20), (30, 200001, 32)])
+def test_long_rows_of_many(n, v, top, order, dtype):
+    # slices of many chunks: the bound of the alternatives is renewed several
+    # times, and (ascending, ties) the candidates outgrow their buffer
+    x, t = make(n + v, n, v, torch.float32)
+    if order != "random":
+        x = x.sort(dim=1, descending=order == "descending").values
+    if order == "ties":
+        x = x[:, torch.randperm(v, generator=torch.Generator().manual_seed(n))].clamp(max=2.0)
+    check(x.to(dtype).to(DEV), t, top)

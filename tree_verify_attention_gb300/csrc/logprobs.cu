@@ -25,6 +25,7 @@
 // unique, so the result does not depend on the order of collection.
 
 #include <atomic>
+#include <climits>
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -34,7 +35,7 @@ namespace dfv {
 namespace cg = cooperative_groups;
 
 constexpr int kLpGroups = 64;       // >= DFV_MAX_TOP
-constexpr int kLpCap = 2048;        // candidates a CTA can hold
+constexpr int kLpCap = 1024;        // candidates a CTA can hold
 constexpr int kLpMaxCluster = 16;
 constexpr int kLpVecs = 4;          // 16-byte loads per thread and chunk
 constexpr float kLog2e = 1.4426950408889634f;
@@ -161,7 +162,7 @@ struct LpSmem {
   uint64_t buf[kLpCap];
   uint64_t gkey[kLpGroups];
   uint64_t best[DFV_MAX_TOP];   // the slice's, in order
-  float gmax[kLpGroups];
+  alignas(16) float gmax[kLpGroups];
   LpStats wst[32];
   LpStats st;
   uint64_t cut;
@@ -258,6 +259,14 @@ __device__ void lp_select(LpSmem& sm, int c, int top) {
   __syncthreads();
 }
 
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -306,6 +315,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
   LpStats st;
   st.init();
   constexpr int kStep = kLpThreads * kLpVecs;
+  constexpr bool kAhead = kLpThreads == 128 && sizeof(T) == 2;
   uint4 v[kLpVecs];
   const uint32_t lowest = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;   // -inf
   const uint4 none = make_uint4(lowest, lowest, lowest, lowest);
@@ -315,6 +325,22 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
       const int i = base + j * kLpThreads + tid;
       v[j] = i < v1 ? xv[i] : none;
     }
+  };
+  // 16-bit rows in CTAs of 128 threads: whole chunks come by way of shared
+  // memory, each thread copying its own vectors of the next chunk before it
+  // works on this one, so that loads are in flight throughout (1024 x 151936,
+  // top 5: 64 us, by loads to registers 70; f32 rows, which are bound by
+  // memory already: 112 to 117 for 99). A slot is overwritten only after the
+  // values read from it have been used.
+  __shared__ uint4 ring[kAhead ? 2 * kStep : 1];
+  auto fetch = [&](int base, int slot) {
+    if (base + kStep <= v1) {
+#pragma unroll
+      for (int j = 0; j < kLpVecs; ++j)
+        cp_async16(&ring[(slot * kLpVecs + j) * kLpThreads + tid],
+                   xv + base + j * kLpThreads + tid);
+    }
+    cp_async_commit();
   };
   const uint4* mine = xv + tid;
   auto load_full = [&](int base) {
@@ -347,8 +373,22 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
     }
   };
 
+  // The top-th largest of 4 * quads group maxima, which as many values reach.
+  auto raise_bound = [&](float g, int quads) {
+    const float4* all = reinterpret_cast<const float4*>(sm.gmax);
+    int above = 0, same = 0;
+#pragma unroll 4
+    for (int k = 0; k < quads; ++k) {
+      const float4 o = all[k];
+      above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
+      same += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
+    }
+    if (above < top && same >= top) sm.bound = g;   // the same value from each such thread
+  };
+
   // ---- first chunk: statistics, and the bound for the alternatives
   load(v0);
+  if constexpr (kAhead) fetch(v0 + kStep, 0);
   const float xe = extra >= 0 ? lp_to_f32(x[extra]) : -INFINITY;
   float vm = chunk_max();
   lp_add<kV * kLpVecs>(st, vm, value);
@@ -361,44 +401,48 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
     for (int o = kLanes / 2; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
     if (tid % kLanes == 0) sm.gmax[tid / kLanes] = g;
     __syncthreads();
-    if (tid < kLpGroups) {
-      g = sm.gmax[tid];
-      int above = 0, same = 0;
-#pragma unroll 16
-      for (int k = 0; k < kLpGroups; ++k) {
-        above += sm.gmax[k] > g;
-        same += sm.gmax[k] >= g;
-      }
-      if (above < top && same >= top) sm.bound = g;   // the same value from each such thread
-    }
+    if (tid < kLpGroups) raise_bound(sm.gmax[tid], kLpGroups / 4);
     __syncthreads();
     // -inf is no bound: what is above it is collected, the rest if that is too little
     bound = fmaxf(sm.bound, -3.4028235e38f);
     push_from(v0, bound);
     if (extra >= 0 && xe >= bound) lp_push(sm, xe, extra);
   }
-  // ---- the rest of the slice. The bound is renewed after one more chunk and
-  // after five, nine, ... times as many: the top-th best collected so far.
-  int renew = v0 + 2 * kStep;
-  for (int base = v0 + kStep; base < v1; base += kStep) {
-    if (base + kStep <= v1) load_full(base);
-    else load(base);
-    if (top > 0 && base >= renew) {
-      renew = base + 4 * (base - v0);
+  // ---- the rest of the slice. The bound is renewed before the fourth chunk
+  // and then whenever three times as many have been read, from the candidates
+  // so far: 64 groups of them give one that about `top` reach, however many
+  // there are. (1024 x 151936 bf16, top 5 / 20 / 32: 66 / 80 / 85 us; with
+  // renewals five times as far apart and only while the candidates were 128
+  // at most 72 / 104 / 544, the last by the path for full buffers.)
+  int renew = v0 + 3 * kStep;
+  if (top == 0 || renew + kStep > v1) renew = INT_MAX;
+  for (int base = v0 + kStep, slot = 0; base < v1; base += kStep, slot ^= 1) {
+    if constexpr (kAhead) fetch(base + kStep, slot ^ 1);
+    if (base + kStep > v1) {
+      load(base);
+    } else if constexpr (kAhead) {
+      cp_async_wait<1>();
+#pragma unroll
+      for (int j = 0; j < kLpVecs; ++j) v[j] = ring[(slot * kLpVecs + j) * kLpThreads + tid];
+    } else {
+      load_full(base);
+    }
+    if (base >= renew) {
+      renew = base + 2 * (base - v0);
+      if (renew + kStep > v1) renew = INT_MAX;
       __syncthreads();
       const int c = sm.count;
-      if (c >= top && c <= kLpThreads) {
-        const float mine_v = tid < c ? lp_value(sm.buf[tid]) : -INFINITY;
-        int above = 0, same = 0;
-        for (int k = 0; k < c; ++k) {
-          const float w = lp_value(sm.buf[k]);
-          above += w > mine_v;
-          same += w >= mine_v;
+      if (c >= top && c <= kLpCap) {
+        if (tid < kLpGroups) {
+          float g = -INFINITY;
+          for (int k = tid; k < c; k += kLpGroups) g = fmaxf(g, lp_value(sm.buf[k]));
+          sm.gmax[tid] = g;
         }
-        if (tid < c && above < top && same >= top) sm.bound = mine_v;
+        __syncthreads();
+        if (tid < min(c, kLpGroups)) raise_bound(sm.gmax[tid], (min(c, kLpGroups) + 3) / 4);
       }
       __syncthreads();
-      bound = fmaxf(sm.bound, -3.4028235e38f);
+      bound = fmaxf(bound, sm.bound);
     }
     vm = chunk_max();
     lp_add<kV * kLpVecs>(st, vm, value);
@@ -515,9 +559,10 @@ dfv_status logprob_launch_t(const LogprobParams& p, int rows, int cs, cudaStream
 
 // Few rows: CTAs of 1024 threads, one to an SM, as many to a row as leave a
 // round of loads per slice (a cluster of more than eight lies in one GPC, so
-// only for a handful of rows). Many: CTAs of 128 threads, eight to an SM; a row
-// is split where that fills the last wave better (a CTA costs about as much
-// as a twentieth of a 152 K row beside its share).
+// only for a handful of rows). Many: CTAs of 128 threads, eight to an SM
+// (seven with 16-bit rows, for their shared memory); a row is split where that
+// fills the last wave better (a CTA costs about as much as a twentieth of a
+// 152 K row beside its share).
 template <typename T>
 dfv_status logprob_launch(const LogprobParams& p, int rows, cudaStream_t stream) {
   const int sms = sm_count();
@@ -539,7 +584,7 @@ dfv_status logprob_launch(const LogprobParams& p, int rows, cudaStream_t stream)
     }
     return logprob_launch_t<T, 1024>(p, rows, cs, stream);
   }
-  const int64_t slots = static_cast<int64_t>(sms) * 8;
+  const int64_t slots = static_cast<int64_t>(sms) * (sizeof(T) == 2 ? 7 : 8);
   int cs = 1;
   double best = 1e30;
   for (int c = 1; c <= 8; c <<= 1) {
