@@ -182,7 +182,8 @@ def test_repeats_are_bit_equal_and_capture():
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("order", ["random", "ascending", "descending", "ties"])
-@pytest.mark.parametrize("n,v,top", [(66, 100003, 32), (80, 60000, 20), (30, 200001, 32)])
+@pytest.mark.parametrize("n,v,top", [(66, 100003, 32), (80, 60000, 20), (30, 200001, 32),
+                                     (320, 50021, 32), (310, 90001, 7)])
 def test_long_rows_of_many(n, v, top, order, dtype):
     # slices of many chunks: the bound of the alternatives is renewed several
     # times, and (ascending, ties) the candidates outgrow their buffer

@@ -210,7 +210,7 @@ __device__ __forceinline__ void lp_push(LpSmem& sm, float x, int idx) {
 template <int kLpThreads>
 __device__ void lp_select(LpSmem& sm, int c, int top) {
   const int tid = threadIdx.x;
-  while (c > 256) {
+  while (c > 128) {
     uint64_t mine = 0;
     for (int i = tid; i < c; i += kLpThreads) mine = max(mine, sm.buf[i]);
     uint64_t* all = sm.gkey;
@@ -557,18 +557,21 @@ dfv_status logprob_launch_t(const LogprobParams& p, int rows, int cs, cudaStream
                                                                                    : DFV_ERR_CUDA;
 }
 
-// Few rows: CTAs of 1024 threads, one to an SM, as many to a row as leave a
-// round of loads per slice (a cluster of more than eight lies in one GPC, so
-// only for a handful of rows). Many: CTAs of 128 threads, eight to an SM
-// (seven with 16-bit rows, for their shared memory); a row is split where that
-// fills the last wave better (a CTA costs about as much as a twentieth of a
-// 152 K row beside its share).
+// Up to two rows an SM (64 if they are short): CTAs of 1024 threads, one to an
+// SM, for few rows as many to a row as leave a round of loads per slice (a
+// cluster of more than eight lies in one GPC, so only for a handful of rows).
+// More: CTAs of 128 threads, eight to an SM (seven with 16-bit rows, for their
+// shared memory); a row is split where that fills the last wave better. A
+// CTA's start and end cost about as much as a twentieth of a 152 K row beside
+// its share, with alternatives more the more there are. (bf16, 151936 logits,
+// top 8, us, by 1024 / 128 threads: 100 rows 13 / 18, 300 rows 26 / 39, 1024
+// rows 93 / 67; 100 rows of 5000 4.5 / 7.0, 300 rows of 1000 9.3 / 6.4.)
 template <typename T>
 dfv_status logprob_launch(const LogprobParams& p, int rows, cudaStream_t stream) {
   const int sms = sm_count();
-  if (rows <= 64) {
+  if (rows <= 64 || (rows <= 2 * sms && p.vocab >= 4096)) {
     const int round = 1024 * kLpVecs * LpVec<T>::kN;
-    const int most = rows <= 4 ? 16 : rows <= 16 ? 8 : rows <= 32 ? 4 : 2;
+    const int most = rows <= 4 ? 16 : rows <= 16 ? 8 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
     int cs = 1;
     while (cs < most && p.vocab > cs * round) cs <<= 1;
     if (cs == 16) {
@@ -585,10 +588,11 @@ dfv_status logprob_launch(const LogprobParams& p, int rows, cudaStream_t stream)
     return logprob_launch_t<T, 1024>(p, rows, cs, stream);
   }
   const int64_t slots = static_cast<int64_t>(sms) * (sizeof(T) == 2 ? 7 : 8);
+  const double start = p.top > 0 ? 0.12 + 0.006 * p.top : 0.05;
   int cs = 1;
   double best = 1e30;
   for (int c = 1; c <= 8; c <<= 1) {
-    const double cost = ((rows * static_cast<int64_t>(c) + slots - 1) / slots) * (1.0 / c + 0.05);
+    const double cost = ((rows * static_cast<int64_t>(c) + slots - 1) / slots) * (1.0 / c + start);
     if (cost < best) {
       best = cost;
       cs = c;
