@@ -14,11 +14,12 @@
 // workspace, nothing to reset). Few rows get CTAs of 1024 threads: a slice of
 // 152 K logits then is one round of loads.
 //
-// The alternatives cost next to nothing beside that pass. The first chunk of
+// The alternatives cost little beside that pass. The first chunk of
 // a slice (its values stay in registers) is cut into 64 groups; the top-th
 // largest of the group maxima is a lower bound of the slice's top-th value,
-// and whatever reaches that bound is collected in shared memory: for a row
-// in random order some top * slice / chunk candidates. Rows that collect more
+// and whatever reaches that bound is collected in shared memory. The bound is
+// renewed from the candidates as the slice goes on, so that a row in random
+// order collects a few times `top` of them per renewal. Rows that collect more
 // than the buffer holds (many equal values, ascending values) are read once
 // more by a path that cuts the buffer back to the best `top` as it fills.
 // Candidates are ordered by a 64-bit key (value, then lower index), which is
