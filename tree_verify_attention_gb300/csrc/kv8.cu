@@ -413,7 +413,6 @@ __global__ void __launch_bounds__(D)
   __shared__ uint64_t full[kBulkSlots];
   __shared__ uint32_t s_max[2][D / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_dep_launch_dependents();
   if (tid == 0) {
     for (int k = 0; k < kBulkSlots; ++k) mbar_init(&full[k], 1);
     fence_mbar_init();
@@ -480,6 +479,10 @@ __global__ void __launch_bounds__(D)
     if (kv == 0) Io::template store_codes<false>(p, h, b, w, m);
     else Io::template store_codes<true>(p, h, b, w, m);
   }
+  // Not earlier: CTAs of the launches behind, waiting in an SM's room, would
+  // keep some of the next write's wave out (six caches in turn, 61440 rows of
+  // 4 heads of 256 each: 132 us a write, so 92).
+  grid_dep_launch_dependents();
 }
 
 // Launch that may be set up while the kernel before it runs (its kernels wait
