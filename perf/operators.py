@@ -230,10 +230,6 @@ def prepare(case, seed):
                 getattr(cache, name).copy_(s.pop(name))
         cache.ctx_len.fill_(ctx)
         s["cache"] = cache
-        if op == "write" and ctx % BLOCK and (ctx + extra) // BLOCK > ctx // BLOCK + 1:
-            # the write closes blocks behind the one it starts in: a pass over
-            # the same place again first puts that block's rows back
-            s["open"] = cache.open_end.clone()
         if op == "attend":
             s["out"] = torch.empty(n, hq, d, dtype=torch.bfloat16, device=DEV)
             s["lse"] = torch.empty(n, hq, device=DEV)
@@ -358,8 +354,6 @@ def run(s):
                 "score": _plain_score}[op](s)
     from tree_verify_attention_gb300 import api
     if op == "write":
-        if "open" in s:
-            s["cache"].open_end.copy_(s["open"])
         s["cache"].append(s["k_rows"], s["v_rows"], at=s["case"]["at"])
         k, v = s["out"]
         s["cache"].read(s["case"]["at"] // BLOCK * BLOCK, k.shape[0], k, v)
