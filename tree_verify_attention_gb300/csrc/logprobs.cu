@@ -59,9 +59,16 @@ __device__ __forceinline__ float lp_ex2(float x) {
   return y;
 }
 
+// Maxima that are NaN if an operand is: a thread that has seen nothing but -inf
+// learns of a NaN only by them.
 __device__ __forceinline__ float lp_max3(float a, float b, float c) {
   float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float lp_max(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
 // at least -200, and NaN if x is
@@ -300,7 +307,10 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
   const int slice_n = (v1 - v0) * kV + (rank == 0 ? head : 0) +
                       (rank == cs - 1 ? p.vocab - head - nv * kV : 0);
   const int top = p.top;
-  if (tid == 0) sm.count = 0;
+  if (tid == 0) {
+    sm.count = 0;
+    sm.bound = -INFINITY;   // stays where too many groups hold a NaN
+  }
   if (cs > 1) cluster_arrive();   // waited for before the first CTA's memory is written
   grid_dep_launch_dependents();
   grid_dep_wait();   // set up under the kernel before; nothing has been read yet
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
         jm[j] = lp_max3(jm[j], value(j * kV + e), value(j * kV + (e + 1 < kV ? e + 1 : e)));
     }
     static_assert(kLpVecs == 4, "maximum of four");
-    return fmaxf(lp_max3(jm[0], jm[1], jm[2]), jm[3]);
+    return lp_max(lp_max3(jm[0], jm[1], jm[2]), jm[3]);
   };
   auto push_from = [&](int base, float bound) {
 #pragma unroll
