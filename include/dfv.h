@@ -113,6 +113,11 @@ typedef enum dfv_status {
  * workspace, and may OR bits into *status. ctx_len, the cache and every
  * output are read and written only after it has completed, so a chain of
  * steps over one cache gives the same results as plain launches.
+ * Where that kernel belongs to another entry point of this library, the
+ * inputs may be written by anything before that call (not by the call):
+ * its kernels let the one behind them start only once what ran before the
+ * call has completed. Another library's kernel that lets its successor start
+ * early has to do the same to stand between the inputs' writer and the step.
  * Consecutive pipelined calls in a stream must use different workspaces
  * (two, used in turn, suffice). Needs one CTA on every SM: returns
  * DFV_ERR_UNSUPPORTED on a device with more than 256 SMs. */

@@ -93,6 +93,14 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // it or exited. wait: blocks until the grids this one depends on have
 // completed and their memory operations are visible. Both are no-ops for a
 // plain launch.
+//
+// A pipelined step reads its inputs before it waits, and its caller is asked
+// only that the kernel right before it does not write them. So a kernel that
+// can stand there triggers after its own wait: the step then starts when what
+// ran before that kernel has completed. (A trigger before the wait would start
+// it beside the kernel that writes its inputs, if that one triggers early too.)
+// The step itself triggers at once: each of its CTAs holds a whole SM until it
+// has waited, so no other step starts beside it.
 __device__ __forceinline__ void grid_dep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(D) kv8_append_kernel(const __grid_constant__ K
   __shared__ int s_path[kMaxNodes];
   __shared__ int s_bad;
   const int tid = threadIdx.x;
-  grid_dep_launch_dependents();
   grid_dep_wait();
+  grid_dep_launch_dependents();   // (after the wait: see common.cuh)
   const int C = static_cast<volatile int32_t*>(p.c.state)[0];
   const int held = static_cast<volatile int32_t*>(p.c.state)[2];
   int at = p.at, n = p.n;
@@ -607,8 +607,8 @@ __device__ __forceinline__ float code_at(const uint32_t* flipped, int i) {
 template <typename T, int D, bool kVec>
 __global__ void __launch_bounds__(D) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
   constexpr int kTpt = D / 64, kVt = D / 4;
-  grid_dep_launch_dependents();
   grid_dep_wait();
+  grid_dep_launch_dependents();   // (after the wait: see common.cuh)
   const int C = *p.c.state;
   const int tid = threadIdx.x, h = blockIdx.y, kv = blockIdx.z;
   int end = p.end;

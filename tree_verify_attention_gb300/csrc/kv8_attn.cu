@@ -234,7 +234,6 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   const int warp =
       static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tid >> 5)));
   // what touches no global memory may run under the kernel before
-  grid_dep_launch_dependents();   // the merge may be set up meanwhile
   if (warp == SW + 8) {
     tc::tmem_alloc(&s_tmem, 512);
   } else if (warp == SW + 9 && lane == 0) {
@@ -269,6 +268,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   const int split = blockIdx.x, splits = gridDim.x, tile = blockIdx.y, h = blockIdx.z;
   const int row0 = tile * p.rows_tile, n_rows = min(p.rows_tile, p.rows - row0);
   grid_dep_wait();
+  grid_dep_launch_dependents();   // the merge may be set up (after the wait: see common.cuh)
   int C = __reduce_max_sync(0xFFFFFFFFu, *p.c.state);
   for (int i = tid; i < p.n_nodes; i += A::kThreads) {
     int pa = i == 0 ? -1 : p.parent[i];
@@ -930,6 +930,8 @@ __global__ void __launch_bounds__(kMergeThreads)
                      tile * p.rows_tile;
   const float* part_lse = p.part_lse + at;
   const float* part_o = p.part_o + at * D;
+  // The attention has triggered behind its wait, so what ran before the call
+  // has completed; what follows may be set up under the attention itself.
   grid_dep_launch_dependents();
   grid_dep_wait();
   float m = -INFINITY;

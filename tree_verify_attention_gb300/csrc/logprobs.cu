@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads)
     sm.bound = -INFINITY;   // stays where too many groups hold a NaN
   }
   if (cs > 1) cluster_arrive();   // waited for before the first CTA's memory is written
-  grid_dep_launch_dependents();
   grid_dep_wait();   // set up under the kernel before; nothing has been read yet
+  grid_dep_launch_dependents();   // (after the wait: see common.cuh)
 
   // the given token and its logit, read meanwhile
   int token = 0;
