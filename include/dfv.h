@@ -95,7 +95,7 @@ typedef enum dfv_status {
  * gives up after 100 ms of the GPU's global timer and sets DFV_DEV_TIMEOUT;
  * the kernel then skips what depended on the wait (a walker that timed out
  * commits nothing) and returns. Clear the workspace (dfv_workspace_clear)
- * before using it again after a timeout. */
+ * before using it again after a timeout (an 8-bit cache: see its state). */
 
 #define DFV_KV_F16 1  /* binary16 values, 2 * D bytes per row                */
 #define DFV_KV_Q4_0 2 /* Q4_0 blocks, D / 32 * 18 bytes per row               */
@@ -381,7 +381,11 @@ dfv_status dfv_build_tree_mask(int n_nodes, const int32_t* parent, int32_t* dept
  * memory; the struct itself is read by the host during the call.
  *   state    int32[4]: [0] the committed length; [1] a counter the library
  *            keeps at zero between calls; [2] the first block whose bf16 rows
- *            the tail still holds; [3] unused. Zero it for an empty cache.
+ *            the tail still holds; [3] set if a bounded wait of a long write
+ *            gave up (DFV_DEV_TIMEOUT): the length is not advanced, rows from
+ *            the write's start on are undefined, and every later write is
+ *            refused with the same bit until the caller zeroes this word.
+ *            Zero all four for an empty cache.
  *   k_codes  int8 [n_kv_heads][nblk][D / 16][64][16]: byte (position t of
  *            block b, dim c) at (((h * nblk + b) * (D / 16) + c / 16) * 64 + t)
  *            * 16 + c % 16. 128-byte aligned.

@@ -163,7 +163,9 @@ class Int8Cache:
 
     Every method is asynchronous on ``stream`` (the current one by default);
     problems that only the device can see are OR-ed into ``status`` (int32[1],
-    DEV_* bits; :attr:`status` of the cache by default)."""
+    DEV_* bits; :attr:`status` of the cache by default). After DEV_TIMEOUT from
+    a write, later writes are refused until ``state[3]`` is zeroed; rows from
+    the start of the write that gave up have to be written again."""
 
     fmt = "int8"
 

@@ -342,10 +342,11 @@ __global__ void __launch_bounds__(D) kv8_append_kernel(const __grid_constant__ K
   grid_dep_launch_dependents();   // (after the wait: see common.cuh)
   const int C = static_cast<volatile int32_t*>(p.c.state)[0];
   const int held = static_cast<volatile int32_t*>(p.c.state)[2];
+  const int stopped = static_cast<volatile int32_t*>(p.c.state)[3];
   int at = p.at, n = p.n;
-  uint32_t bad = 0;
+  uint32_t bad = stopped ? DFV_DEV_TIMEOUT : 0;   // a wait of a long write gave up
   if (at < 0) {
-    if (C < 0 || C > p.c.capacity) bad = DFV_DEV_CTX;
+    if (C < 0 || C > p.c.capacity) bad |= DFV_DEV_CTX;
     at = C;
   }
   if (p.accept_len) {
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(D)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kBulkSlots];
   __shared__ uint32_t s_max[2][D / 32];
+  constexpr uint32_t kNoRows = ~0u;   // in a maximum's place: a thread's wait gave up
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int k = 0; k < kBulkSlots; ++k) mbar_init(&full[k], 1);
@@ -421,8 +423,8 @@ __global__ void __launch_bounds__(D)
   const int C = p.c.state[0], held = p.c.state[2];
   const int at = p.at < 0 ? C : p.at;
   // refused as by kv8_append_kernel, which reports it
-  if (C < 0 || C > p.c.capacity || at > C || p.n > p.c.capacity - at ||
-      (at % kBlk != 0 && at / kBlk < held))
+  if (static_cast<volatile int32_t*>(p.c.state)[3] != 0 || C < 0 || C > p.c.capacity || at > C ||
+      p.n > p.c.capacity - at || (at % kBlk != 0 && at / kBlk < held))
     return;
   __syncthreads();
   fence_proxy_async_global();   // what earlier kernels wrote, to the copy engine
@@ -444,12 +446,13 @@ __global__ void __launch_bounds__(D)
   if (warp == 0)
     for (int k = 0; k < kBulkSlots - 1; ++k)
       if (it + k * step < total) copy(it + k * step, k);
-  for (int k = 0; it < total; it += step, ++k) {
+  int k = 0;
+  for (; it < total; it += step, ++k) {
     const int slot = k % kBulkSlots;
     // the slot freed by the last block's reads (a barrier ago) is filled again
     if (warp == 0 && it + (kBulkSlots - 1) * step < total)
       copy(it + (kBulkSlots - 1) * step, (k + kBulkSlots - 1) % kBulkSlots);
-    if (!mbar_wait_bounded(&full[slot], (k / kBulkSlots) & 1)) report(p.status, DFV_DEV_TIMEOUT);
+    const bool there = mbar_wait_bounded(&full[slot], (k / kBulkSlots) & 1);
     const int kv = it >= per, r = kv ? it - per : it;
     const int h = r / p.bulk, b = b0 + 1 + r - h * p.bulk;
     const uint8_t* rows = smem + slot * kSlot;
@@ -471,13 +474,23 @@ __global__ void __launch_bounds__(D)
         w[2 * i + 1] = v.y;
       }
     }
-    uint32_t m = __reduce_max_sync(0xFFFFFFFFu, keep_storable(w, p.status));
+    uint32_t m = __reduce_max_sync(0xFFFFFFFFu, there ? keep_storable(w, p.status) : kNoRows);
     if (lane == 0) s_max[k & 1][warp] = m;
     __syncthreads();   // maxima are there, and the slot has been read
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) m = max(m, s_max[k & 1][e]);
+    if (m == kNoRows) break;   // nothing is stored of rows that did not come
     if (kv == 0) Io::template store_codes<false>(p, h, b, w, m);
     else Io::template store_codes<true>(p, h, b, w, m);
+  }
+  if (it < total && tid == 0) {
+    // No later write advances the length over what is missing: kv8_append_kernel
+    // asks for this word. Copies in flight land before the CTA ends.
+    *static_cast<volatile int32_t*>(p.c.state + 3) = 1;
+    report(p.status, DFV_DEV_TIMEOUT);
+    for (int j = 0; j < kBulkSlots; ++j)
+      if (it + j * step < total)
+        mbar_wait_bounded(&full[(k + j) % kBulkSlots], ((k + j) / kBulkSlots) & 1);
   }
   // Not earlier: CTAs of the launches behind, waiting in an SM's room, would
   // keep some of the next write's wave out (six caches in turn, 61440 rows of
