@@ -25,13 +25,18 @@
 //   l_c  += P'_jc / v_scale_j                      (f32, per thread)
 //
 // with m_c a reference of the column, not its exact maximum: a chunk only has
-// to show that no exponent passes 2^10 (binary16 P' holds 2^15), which one
-// vote decides; columns' maxima are reduced across lanes only when one does.
+// to show that no P' passes 2^15 (what binary16 holds), which one vote decides;
+// columns' maxima are reduced across lanes only when one does. A new reference
+// puts the largest P' so far at 2^8, not at 1: binary16 then keeps its full
+// 2^-11 for contributions down to 2^-22 of it (a key that takes nearly all of
+// the weight and adds nothing leaves the output to such ones), and smaller
+// ones are within 2^-33 of it.
 // The tail and tree rows (bf16) are one last chunk of at most 63 + 65 = 128
 // keys, scaled by a power of two per key to binary16 range, so that it runs
 // through the same products with its own a_j and v_scale_j. Q is scaled by one
 // power of two per tile. Every operand is then exact in binary16 except P',
-// whose rounding (2^-12) is below that of the bf16 output.
+// whose rounding (2^-11 of each weight, the normaliser has none) is below that
+// of the bf16 output; a float32 output is as exact as its weights.
 //
 // Roles of a CTA (one per SM): 8 or 16 softmax warps (lane quadrant w % 4,
 // column group w / 4), four warps that put K codes into TMEM, four for V, one
@@ -52,7 +57,8 @@ namespace dfv {
 
 constexpr int kAtKeys = 128;         // keys of a chunk
 constexpr int kTreeCost = 6;         // chunks that the bf16 chunk counts as
-constexpr float kRaise = 10.0f;      // a larger exponent moves the reference
+constexpr float kTop = 8.0f;         // exponent of the largest P' under a new reference
+constexpr float kRaise = 15.0f;      // a larger exponent moves the reference
 constexpr float kNoRef = 1e30f;      // -reference of a column that has seen no key
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kLn2F = 0.6931471805599453f;
@@ -777,7 +783,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
             for (int c = cg * HC + lane; c < (cg + 1) * HC; c += 32) {
               const float was = -s_neg[c];
               const float m = fmaxf(fmaxf(fmaxf(s_red[0][c], s_red[1][c]),
-                                          fmaxf(s_red[2][c], s_red[3][c])), was);
+                                          fmaxf(s_red[2][c], s_red[3][c])) - kTop, was);
               s_neg[c] = -m;
               s_f[c] = tc::ex2(was - m);
             }
