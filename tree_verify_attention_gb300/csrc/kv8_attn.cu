@@ -34,9 +34,13 @@
 // The tail and tree rows (bf16) are one last chunk of at most 63 + 65 = 128
 // keys, scaled by a power of two per key to binary16 range, so that it runs
 // through the same products with its own a_j and v_scale_j. Q is scaled by one
-// power of two per tile. Every operand is then exact in binary16 except P',
-// whose rounding (2^-11 of each weight, the normaliser has none) is below that
-// of the bf16 output; a float32 output is as exact as its weights.
+// power of two per tile while the tile's rows lie within 2^10 of each other;
+// else each row has its own and the difference becomes a factor of the column
+// ("wide" units, which a row of garbage beside ordinary ones leads to). Every
+// operand is then exact in binary16 but P', whose rounding (2^-11 of each
+// weight, the normaliser has none) is below that of the bf16 output; a float32
+// output is as exact as its weights. (Elements below 2^-21 of their row's
+// largest are not exact either: they are within 2^-29 of that one.)
 //
 // Roles of a CTA (one per SM): 8 or 16 softmax warps (lane quadrant w % 4,
 // column group w / 4), four warps that put K codes into TMEM, four for V, one
@@ -48,6 +52,7 @@
 
 #include <atomic>
 #include <math.h>
+#include <type_traits>
 
 #include "kv8.cuh"
 #include "tc.cuh"
@@ -59,7 +64,10 @@ constexpr int kAtKeys = 128;         // keys of a chunk
 constexpr int kTreeCost = 6;         // chunks that the bf16 chunk counts as
 constexpr float kTop = 8.0f;         // exponent of the largest P' under a new reference
 constexpr float kRaise = 15.0f;      // a larger exponent moves the reference
-constexpr float kNoRef = 1e30f;      // -reference of a column that has seen no key
+constexpr float kNoRef = 3e38f;      // -reference of a column that has seen no key
+constexpr float kFar = 262144.0f;    // a larger reference is kept in two parts
+constexpr int kSpread = 10;          // log2 of the ratio of rows that share a scale
+constexpr uint32_t kNotFinite = 0x10000u;   // in a row's magnitude: it holds inf or NaN
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kLn2F = 0.6931471805599453f;
 
@@ -225,14 +233,17 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   __shared__ int s_parent[kMaxNodes], s_maxdepth;
   // columns (of each group) that see a tree node; columns by depth, and up to a depth
   __shared__ uint32_t s_see[kMaxNodes][NG], s_dep[kMaxNodes][NG], s_upto[kMaxNodes][NG];
-  __shared__ __align__(16) float s_neg[R], s_f[R], s_zero[R];   // s_neg: -reference
+  // -(reference), and in a wide unit its second part and the column's factor
+  __shared__ __align__(16) float s_neg[R], s_f[R], s_lo[R], s_cf[R];
   __shared__ float s_red[4][R];
   // (K scale, log2 and inverse of the V scale) of the blocks of two times 16 chunks
   __shared__ __align__(16) float4 s_sc[64];
   __shared__ float s_ksc[kAtKeys];
   __shared__ __align__(8) float s_vfac[kAtKeys];
-  __shared__ int s_vexp[kAtKeys], s_bad[2][kAtKeys];
-  __shared__ uint32_t s_qmax;
+  __shared__ int s_vexp[kAtKeys];
+  __shared__ uint8_t s_bad[2][kAtKeys];
+  __shared__ uint32_t s_qmax, s_qmin;   // largest and smallest of the rows' magnitudes
+  __shared__ int s_far[NG];    // a reference of the group is so large that it takes two parts
 
   const int tid = threadIdx.x, lane = tid & 31;
   // both the same in every lane, which the compiler knows of a reduction's
@@ -269,6 +280,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   if (tid == 0) {
     s_dead = 0;
     s_qmax = 0;
+    s_qmin = kNotFinite;
     s_maxdepth = 0;
   }
   const int split = blockIdx.x, splits = gridDim.x, tile = blockIdx.y, h = blockIdx.z;
@@ -340,7 +352,6 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   // Q rows of the tile, into registers meanwhile (softmax warps)
   constexpr int kQSteps = (R * D / 8 + SW * 32 - 1) / (SW * 32);
   uint4 qv[kQSteps];
-  uint32_t qm = 0;
   if (warp < SW) {
 #pragma unroll
     for (int k = 0; k < kQSteps; ++k) {
@@ -629,33 +640,62 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     const int cg = warp >> 2;                  // column group
     const int key = (warp & 3) * 32 + lane;
     bool ok = true;
-    // Q scaled so that the tile's largest magnitude is in [2^14, 2^15)
+    // Q scaled so that the tile's largest magnitude is in [2^14, 2^15), or each
+    // row's own. D / 8 lanes hold a row. A row that is not finite counts for
+    // nothing.
+    // (The rows' magnitudes lie where the columns' maxima will: those are
+    // written once the first product is there, which waits for all of Q.)
+    uint32_t* s_qrow = reinterpret_cast<uint32_t*>(s_red[0]);
+    uint32_t qmax = 0, qmin = kNotFinite;
 #pragma unroll
     for (int k = 0; k < kQSteps; ++k) {
       const uint32_t in[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+      uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = in[e] & 0x7FFFu, hi = (in[e] >> 16) & 0x7FFFu;
-        if (lo < 0x7F80u) qm = max(qm, lo);   // infinities and NaN stay in their row
-        if (hi < 0x7F80u) qm = max(qm, hi);
+      for (int e = 0; e < 4; ++e) m = __vmaxu2(m, in[e] & 0x7FFF7FFFu);
+      m = max(m & 0xFFFFu, m >> 16);
+      if (m >= 0x7F80u) m = kNotFinite;
+#pragma unroll
+      for (int o = D / 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const int r = (tid + k * (SW * 32)) / (D / 8);
+      if (lane % (D / 8) == 0 && r < R) s_qrow[r] = m;
+      if (m < kNotFinite) {
+        qmax = max(qmax, m);
+        if (m > 0) qmin = min(qmin, m);
       }
     }
-    qm = __reduce_max_sync(0xFFFFFFFFu, qm);
-    if (lane == 0) atomicMax(&s_qmax, qm);
+    qmax = __reduce_max_sync(0xFFFFFFFFu, qmax);
+    qmin = __reduce_min_sync(0xFFFFFFFFu, qmin);
+    if (lane == 0) {
+      atomicMax(&s_qmax, qmax);
+      atomicMin(&s_qmin, qmin);
+    }
     if (tid < R) {
       s_neg[tid] = kNoRef;
-      s_zero[tid] = 0.0f;
+      s_lo[tid] = 0.0f;
     }
+    if (tid < NG) s_far[tid] = 0;
     named_sync(4, SW * 32);
-    const int qe = max(static_cast<int>(s_qmax >> 7), 20);
-    const float qf = pow2i(min(141 - qe, 126));
+    auto exponent = [](uint32_t m) { return max(static_cast<int>(m >> 7), 20); };
+    const int qe = exponent(s_qmax);
+    // Beyond 2^73 a zero score would meet an infinite factor of its key's.
+    const bool rows_apart = exponent(s_qmin) + kSpread < qe || qe > 200;
+    // wide: row r's scores carry 2^(its exponent - qe + lift), keys 2^(qe - lift)
+    const int lift = rows_apart ? min(max(qe - 141, 0), 60) : 0;
+    if (key < HC) {
+      const int e = exponent(s_qrow[cg * HC + key] & 0x7FFFu);
+      s_cf[cg * HC + key] = rows_apart ? pow2i(max(e - qe + lift, -126)) : 1.0f;
+    }
 #pragma unroll
     for (int k = 0; k < kQSteps; ++k) {
       const int it = tid + k * (SW * 32), r = it / (D / 8), j = it % (D / 8);
-      if (r < R)
+      if (r < R) {
+        const uint32_t m = s_qrow[r];
+        const float qf = pow2i(141 - (rows_apart && m < kNotFinite ? exponent(m) : qe));
         *reinterpret_cast<uint4*>(sQ + tc::sw128_offset(r, j, R)) =
             make_uint4(scaled_half2(qv[k].x, qf), scaled_half2(qv[k].y, qf),
                        scaled_half2(qv[k].z, qf), scaled_half2(qv[k].w, qf));
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -687,14 +727,14 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
       named_sync(4, SW * 32);
       if (p.window > 0) lo_all = C + maxdepth - p.window + 1;
     }
-    const float sc = p.scale * kLog2eF * pow2i(max(qe - 141, -126));
+    const float sc = p.scale * kLog2eF * pow2i(qe - 141 - lift);
     float l[HC];
 #pragma unroll
     for (int c = 0; c < HC; ++c) l[c] = 0.0f;
     const uint32_t t_s = tmem + lanes + A::kTS + cg * HC;
     const uint32_t t_o = t_s + (A::kTO - A::kTS);
     const float4* m4 = reinterpret_cast<const float4*>(s_neg + cg * HC);
-    const float4* zero4 = reinterpret_cast<const float4*>(s_zero + cg * HC);
+    const float4* lo4 = reinterpret_cast<const float4*>(s_lo + cg * HC);
 
     // Chunks [m_lo, m_hi) need no mask: their blocks are complete and inside
     // every node's window. The loop keeps little beside x and l: what a masked
@@ -704,147 +744,201 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     const int m_hi = n8 - (n8 > 0 && fb + 2 * (c0 + n8) > open ? 1 : 0);
     if (n8 > 0) ok = role_wait(&b_sc, 0, &s_dead);
 
-    for (int i = 0; i < n; ++i) {
-      // this lane's key: its factors, and the columns that see it
-      const bool bf = has_tree && i == n - 1;
-      const bool masked = i < m_lo || i >= m_hi;
-      uint32_t vis = ~0u;
-      bool bad = false, live = true;
-      if (masked) {
-        const int pos = bf ? open * kBlk + key : (fb + 2 * (c0 + i)) * kBlk + key;
-        live = bf ? key < live_rows : pos < open * kBlk;
-        if (!live) {
-          vis = 0;
-        } else if (bf && key >= T) {
-          vis = s_see[key - T][cg];
-        } else if (lo_all != INT32_MIN) {
-          const int dd = pos - C + p.window - 1;   // deepest node that sees it
-          vis = dd < 0 ? 0u : s_upto[min(dd, s_maxdepth)][cg];
-        }
-      }
-      ok = ok && role_wait(&b_kfree[A::kKSub - 1], i & 1, &s_dead);
-      const float4 scales = s_sc[(i & 31) * 2 + (key >> 6)];
-      float a = live ? scales.x * sc : 0.0f, lv = live ? scales.y : 0.0f;
-      float iv = live ? scales.z : 0.0f;
-      if (bf) {
-        ok = ok && role_wait(&b_rowsc, 0, &s_dead);
-        if (ok && key < live_rows) {
-          a = s_ksc[key] * sc;
-          lv = static_cast<float>(s_vexp[key]);
-          iv = pow2i(-s_vexp[key]);
-          bad = s_bad[0][key] || s_bad[1][key];
-        }
-      }
-      ok = __all_sync(0xFFFFFFFFu, ok);   // the TMEM loads are warp-wide
-      tc::fence_after_sync();
-      float x[HC];
-      // Exponents against the references (pass 0). Where one is too large, and
-      // in the first chunk: scores alone, columns' maxima, new references
-      // (pass 1), and the exponents again (pass 2).
-      bool alive = true;
-#pragma unroll 1
-      for (int pass = i == 0 ? 1 : 0; pass < 3; ++pass) {
-        if (pass == 1) {   // a wait gave up somewhere in the group?
-          ok = named_sync_and(5 + cg, 128, ok);
-          if (!ok) {
-            alive = false;
-            break;
+    // Chunks [i0, n), of which the first gets new references; returns the first
+    // one not done: n, but for the narrow form where a reference is far out.
+    // Wide units have a form of their own: one for both, with the difference
+    // behind a branch, took 105 to 108 us for 23 nodes at ctx 131072, and 73 to
+    // 94 for 65 nodes, instead of 104.4 and 71.9 (narrow alone: 101.8, 71.9).
+    auto chunks = [&](auto form, const int i0) {
+      constexpr bool kWide = decltype(form)::value;
+      for (int i = i0; i < n; ++i) {
+        // this lane's key: its factors, and the columns that see it
+        const bool bf = has_tree && i == n - 1;
+        const bool masked = i < m_lo || i >= m_hi;
+        uint32_t vis = ~0u;
+        bool bad = false, live = true;
+        if (masked) {
+          const int pos = bf ? open * kBlk + key : (fb + 2 * (c0 + i)) * kBlk + key;
+          live = bf ? key < live_rows : pos < open * kBlk;
+          if (!live) {
+            vis = 0;
+          } else if (bf && key >= T) {
+            vis = s_see[key - T][cg];
+          } else if (lo_all != INT32_MIN) {
+            const int dd = pos - C + p.window - 1;   // deepest node that sees it
+            vis = dd < 0 ? 0u : s_upto[min(dd, s_maxdepth)][cg];
           }
         }
-        if (ok) tc::TmemIo<HC>::load(t_s, reinterpret_cast<uint32_t*>(x));
-        const float4* ref = pass == 1 ? zero4 : m4;
-#pragma unroll
-        for (int c = 0; c < HC; c += 4) {
-          float4 m = ref[c / 4];
-          add2(m.x, m.y, m.x, m.y, lv, lv);
-          add2(m.z, m.w, m.z, m.w, lv, lv);
-          fma2(x[c], x[c + 1], x[c], x[c + 1], a, a, m.x, m.y);
-          fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], a, a, m.z, m.w);
+        ok = ok && role_wait(&b_kfree[A::kKSub - 1], i & 1, &s_dead);
+        const float4 scales = s_sc[(i & 31) * 2 + (key >> 6)];
+        float a = live ? scales.x * sc : 0.0f, lv = live ? scales.y : 0.0f;
+        float iv = live ? scales.z : 0.0f;
+        if (bf) {
+          ok = ok && role_wait(&b_rowsc, 0, &s_dead);
+          if (ok && key < live_rows) {
+            a = s_ksc[key] * sc;
+            lv = static_cast<float>(s_vexp[key]);
+            iv = pow2i(-s_vexp[key]);
+            bad = s_bad[0][key] || s_bad[1][key];
+          }
         }
-        if (masked) {
+        ok = __all_sync(0xFFFFFFFFu, ok);   // the TMEM loads are warp-wide
+        tc::fence_after_sync();
+        float x[HC];
+        // Exponents against the references (pass 0). Where one is too large, and
+        // in the first chunk: scores alone, columns' maxima, new references
+        // (pass 1), and the exponents again (pass 3). In a wide unit the scores
+        // have their column's factor, the key's V scale is added behind the fma,
+        // which is exact near the reference, and a second part of the reference
+        // takes what rounding has left of the first (pass 2).
+        bool alive = true;
+#pragma unroll 1
+        for (int pass = i == i0 ? 1 : 0; pass < 4; ++pass) {
+          if (pass == 1) {   // a wait gave up somewhere in the group?
+            ok = named_sync_and(5 + cg, 128, ok);
+            if (!ok) {
+              alive = false;
+              break;
+            }
+          }
+          if (ok) tc::TmemIo<HC>::load(t_s, reinterpret_cast<uint32_t*>(x));
+          if constexpr (!kWide) {
+            const float4* ref = pass == 1 ? lo4 : m4;   // (lo4: zeros)
 #pragma unroll
-          for (int c = 0; c < HC; ++c)
-            if (!(vis & (1u << c))) x[c] = -INFINITY;
+            for (int c = 0; c < HC; c += 4) {
+              float4 m = ref[c / 4];
+              add2(m.x, m.y, m.x, m.y, lv, lv);
+              add2(m.z, m.w, m.z, m.w, lv, lv);
+              fma2(x[c], x[c + 1], x[c], x[c + 1], a, a, m.x, m.y);
+              fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], a, a, m.z, m.w);
+            }
+          } else {
+            float xw[HC];   // rolled, by way of local memory: the registers are the narrow form's
+#pragma unroll
+            for (int c = 0; c < HC; ++c) xw[c] = x[c];
+#pragma unroll 1
+            for (int c = 0; c < HC; ++c) {
+              const int col = cg * HC + c;
+              xw[c] = fmaf(xw[c] * s_cf[col], a, pass == 1 ? 0.0f : s_neg[col]) +
+                     (pass == 1 || pass == 2 ? lv : lv + s_lo[col]);
+            }
+#pragma unroll
+            for (int c = 0; c < HC; ++c) x[c] = xw[c];
+          }
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < HC; ++c)
+              if (!(vis & (1u << c))) x[c] = -INFINITY;
+          }
+          if (pass == 0) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < HC; c += 2) top = max3(top, x[c], x[c + 1]);
+            if (named_sync_and(5 + cg, 128, ok && !(top > kRaise))) break;
+          } else if (pass < 3) {
+#pragma unroll
+            for (int c = 0; c < HC; ++c) {
+              float m;
+              asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x[c]));
+              if (lane == 0) s_red[warp & 3][cg * HC + c] = m;
+            }
+            named_sync(5 + cg, 128);
+            if ((warp & 3) == 0) {
+              static_assert(HC <= 32, "a lane has one column of the group");
+              const int c = cg * HC + min(lane, HC - 1);
+              const float top = fmaxf(fmaxf(s_red[0][c], s_red[1][c]),
+                                      fmaxf(s_red[2][c], s_red[3][c]));
+              const float was = -s_neg[c], lo = s_lo[c], old = s_f[c];
+              __syncwarp();
+              if constexpr (!kWide) {
+                const float size = fabsf(top);
+                const bool far = __any_sync(0xFFFFFFFFu, size > kFar && size < INFINITY);
+                const float m = fmaxf(top - kTop, was);
+                if (far) {
+                  s_far[cg] = 1;   // nothing changes before the wide form
+                } else if (lane < HC) {
+                  s_neg[c] = -m;
+                  s_f[c] = tc::ex2(was - m);
+                }
+              } else if (lane < HC) {
+                if (pass == 1) {
+                  // s_f: the reference that it was, where there is a new one
+                  // (not with NaN, where the comparison fails)
+                  const bool up = top - kTop > was - lo;
+                  s_f[c] = up ? was : INFINITY;
+                  if (up) s_neg[c] = kTop - top;
+                } else {
+                  const bool up = old < INFINITY && top > -INFINITY;
+                  if (up) s_lo[c] = kTop - top;
+                  s_f[c] = up ? tc::ex2((old - was) + (kTop - top - lo)) : 1.0f;
+                }
+              }
+            }
+            if (pass == 1 && i > 0)
+              ok = role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead);
+            ok = named_sync_and(5 + cg, 128, ok);
+            if (!ok) {
+              alive = false;
+              break;
+            }
+            if (kWide && pass == 1) continue;
+            if (!kWide && s_far[cg]) return i;
+            if (i > 0) {
+              tc::fence_after_sync();
+#pragma unroll
+              for (int c = 0; c < HC; ++c) l[c] *= s_f[cg * HC + c];
+#pragma unroll 1
+              for (int hh = 0; hh < A::kHalves; ++hh) {
+                tc::TmemIo<HC>::load(t_o + hh * R, reinterpret_cast<uint32_t*>(x));
+#pragma unroll
+                for (int c = 0; c < HC; ++c) x[c] *= s_f[cg * HC + c];
+                tc::TmemIo<HC>::store(t_o + hh * R, reinterpret_cast<const uint32_t*>(x));
+                tc::store_wait();
+              }
+            }
+            pass = 2;
+          }
         }
-        if (pass == 0) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < HC; c += 2) top = max3(top, x[c], x[c + 1]);
-          if (named_sync_and(5 + cg, 128, ok && !(top > kRaise))) break;
-        } else if (pass == 1) {
+        if (!alive) break;
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_sfree);
+        if (bad) {   // whoever sees the key has no result
 #pragma unroll
           for (int c = 0; c < HC; ++c) {
-            float m;
-            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x[c]));
-            if (lane == 0) s_red[warp & 3][cg * HC + c] = m;
+            if (x[c] > -INFINITY) l[c] = NAN;
+            x[c] = -INFINITY;
           }
-          named_sync(5 + cg, 128);
-          if ((warp & 3) == 0) {
-            for (int c = cg * HC + lane; c < (cg + 1) * HC; c += 32) {
-              const float was = -s_neg[c];
-              const float m = fmaxf(fmaxf(fmaxf(s_red[0][c], s_red[1][c]),
-                                          fmaxf(s_red[2][c], s_red[3][c])) - kTop, was);
-              s_neg[c] = -m;
-              s_f[c] = tc::ex2(was - m);
+        }
+        // P' as the B operand: 16-byte pieces of 8 columns of this key's row
+        const int pb = i & 1;
+        if (A::kPBufs == 1 && i >= 1) ok = role_wait(&b_pv[pb ^ 1], ((i - 1) >> 1) & 1, &s_dead);
+        if (ok) {
+          uint8_t* dst = sP + (A::kPBufs == 2 ? pb : 0) * A::kPBytes;
+          const uint32_t krow = static_cast<uint32_t>((key >> 3) * 1024 + (key & 7) * 128);
+#pragma unroll
+          for (int j = 0; j < HC / 4; ++j) {   // half a 16-byte piece
+            uint32_t o[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = 4 * j + 2 * e;
+              const float p0 = tc::ex2(x[c]), p1 = tc::ex2(x[c + 1]);
+              fma2(l[c], l[c + 1], p0, p1, iv, iv, l[c], l[c + 1]);
+              o[e] = pack_half2(p0, p1);
             }
-          }
-          if (i > 0) ok = role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead);
-          ok = named_sync_and(5 + cg, 128, ok);
-          if (!ok) {
-            alive = false;
-            break;
-          }
-          if (i > 0) {
-            tc::fence_after_sync();
-#pragma unroll
-            for (int c = 0; c < HC; ++c) l[c] *= s_f[cg * HC + c];
-#pragma unroll 1
-            for (int hh = 0; hh < A::kHalves; ++hh) {
-              tc::TmemIo<HC>::load(t_o + hh * R, reinterpret_cast<uint32_t*>(x));
-#pragma unroll
-              for (int c = 0; c < HC; ++c) x[c] *= s_f[cg * HC + c];
-              tc::TmemIo<HC>::store(t_o + hh * R, reinterpret_cast<const uint32_t*>(x));
-              tc::store_wait();
-            }
+            const int col = cg * HC + 4 * j, piece = col >> 3;
+            *reinterpret_cast<uint2*>(dst + (piece >> 3) * (kAtKeys * 128) + krow +
+                                      (((piece & 7) ^ (key & 7)) << 4) + (col & 4) * 2) =
+                make_uint2(o[0], o[1]);
           }
         }
+        fence_proxy_async_smem();
+        if (__all_sync(0xFFFFFFFFu, ok) && lane == 0) mbar_arrive(&b_p[pb]);
       }
-      if (!alive) break;
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b_sfree);
-      if (bad) {   // whoever sees the key has no result
-#pragma unroll
-        for (int c = 0; c < HC; ++c) {
-          if (x[c] > -INFINITY) l[c] = NAN;
-          x[c] = -INFINITY;
-        }
-      }
-      // P' as the B operand: 16-byte pieces of 8 columns of this key's row
-      const int pb = i & 1;
-      if (A::kPBufs == 1 && i >= 1) ok = role_wait(&b_pv[pb ^ 1], ((i - 1) >> 1) & 1, &s_dead);
-      if (ok) {
-        uint8_t* dst = sP + (A::kPBufs == 2 ? pb : 0) * A::kPBytes;
-        const uint32_t krow = static_cast<uint32_t>((key >> 3) * 1024 + (key & 7) * 128);
-#pragma unroll
-        for (int j = 0; j < HC / 4; ++j) {   // half a 16-byte piece
-          uint32_t o[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = 4 * j + 2 * e;
-            const float p0 = tc::ex2(x[c]), p1 = tc::ex2(x[c + 1]);
-            fma2(l[c], l[c + 1], p0, p1, iv, iv, l[c], l[c + 1]);
-            o[e] = pack_half2(p0, p1);
-          }
-          const int col = cg * HC + 4 * j, piece = col >> 3;
-          *reinterpret_cast<uint2*>(dst + (piece >> 3) * (kAtKeys * 128) + krow +
-                                    (((piece & 7) ^ (key & 7)) << 4) + (col & 4) * 2) =
-              make_uint2(o[0], o[1]);
-        }
-      }
-      fence_proxy_async_smem();
-      if (__all_sync(0xFFFFFFFFu, ok) && lane == 0) mbar_arrive(&b_p[pb]);
-    }
+      return n;
+    };
+    const int done = rows_apart ? 0 : chunks(std::false_type{}, 0);
+    if (ok && done < n) chunks(std::true_type{}, done);
     // ---- the unit's result
     // sums over the lanes, four columns at a time: two exchanges that halve
     // the columns a lane holds, then three plain ones
@@ -868,7 +962,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
       for (int c = cg * HC + lane; c < (cg + 1) * HC; c += 32) {
         const float s = (s_red[0][c] + s_red[1][c]) + (s_red[2][c] + s_red[3][c]);
         s_f[c] = s == 0.0f ? 0.0f : 1.0f / s;
-        p.part_lse[slice * R + c] = s == 0.0f ? -INFINITY : log2f(s) - s_neg[c];
+        p.part_lse[slice * R + c] = s == 0.0f ? -INFINITY : (log2f(s) - s_lo[c]) - s_neg[c];
       }
     }
     if (ok && n > 0) ok = role_wait(&b_pv[(n - 1) & 1], ((n - 1) >> 1) & 1, &s_dead);
