@@ -448,10 +448,11 @@ dfv_status dfv_kv8_read(const dfv_kv8_cache* cache, int pos0, int n_rows, void* 
  * Softmax weights enter the product with V as binary16, also where out is f32:
  * each is off by at most 2^-11 of itself (or, below 2^-22 of the largest
  * contribution beside it, by 2^-33 of that one); their sum is not rounded.
- * n_nodes = 1 is plain decode. q may have any finite bf16 magnitude,
- * and another in each row; a non-finite q row gives a non-finite result for that row alone. A node that
- * sees a tree row holding a value of 2^40 or more, an infinity or a NaN gets
- * NaN for that head (DFV_DEV_NONFINITE); the others are not affected. */
+ * n_nodes = 1 is plain decode. q may have any finite bf16 magnitude, and
+ * another in each row; a row that holds an infinity or a NaN has NaN results,
+ * and the others are not affected. A node that sees a tree row holding a value
+ * of 2^40 or more, an infinity or a NaN gets NaN for that head
+ * (DFV_DEV_NONFINITE); the others are not affected. */
 size_t dfv_kv8_attn_workspace_bytes(int n_nodes, int n_q_heads, int n_kv_heads, int head_dim,
                                     int window, int cache_capacity);
 

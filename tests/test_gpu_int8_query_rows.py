@@ -96,6 +96,31 @@ def test_zero_and_small_rows_beside_a_large_one(power):
     assert_rows(out, lse, ref, rows)
 
 
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("n,hq,hkv,d,ctx,window", [(1, 1, 1, 64, 0, 0), (1, 2, 1, 128, 300, 0),
+                                                   (9, 6, 2, 256, 500, 100),
+                                                   (65, 12, 2, 64, 900, 0)])
+def test_a_row_that_is_not_finite_has_no_result(value, n, hq, hkv, d, ctx, window):
+    """Also where every key has the same sign in that place, so that all of
+    the row's scores are -inf."""
+    def positive(x):
+        return torch.cat([x[..., :9], x[..., 9:10].abs() + 1.0, x[..., 10:]], -1)
+
+    def make():
+        c = Case(n, hq, hkv, d, ctx, window, k_fun=positive)
+        c.tk[..., 9] = c.tk[..., 9].abs() + 1.0
+        return c
+
+    good, c = make(), make()
+    ref, rlse = good.check(torch.float32)
+    c.q[n - 1, hq - 1, 9] = value
+    out, lse = c.run(torch.float32)
+    rows = np.ones((n, hq), bool)
+    rows[n - 1, hq - 1] = False
+    assert np.isnan(out[n - 1, hq - 1]).all() and not np.isfinite(lse[n - 1, hq - 1])
+    assert np.array_equal(out[rows], ref[rows]) and np.array_equal(lse[rows], rlse[rows])
+
+
 def test_rows_of_many_sizes_against_the_definition():
     """Every node's rows on a scale of their own, 2^-24 to 2^4."""
     c = Case(30, 4, 1, 128, 400)

@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     bool ok = true;
     // Q scaled so that the tile's largest magnitude is in [2^14, 2^15), or each
     // row's own. D / 8 lanes hold a row. A row that is not finite counts for
-    // nothing.
+    // nothing and becomes NaN throughout: all of its scores are NaN then, also
+    // where each would be -inf.
     // (The rows' magnitudes lie where the columns' maxima will: those are
     // written once the first product is there, which waits for all of Q.)
     uint32_t* s_qrow = reinterpret_cast<uint32_t*>(s_red[0]);
@@ -691,7 +692,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
       const int it = tid + k * (SW * 32), r = it / (D / 8), j = it % (D / 8);
       if (r < R) {
         const uint32_t m = s_qrow[r];
-        const float qf = pow2i(141 - (rows_apart && m < kNotFinite ? exponent(m) : qe));
+        const float qf = m >= kNotFinite ? NAN : pow2i(141 - (rows_apart ? exponent(m) : qe));
         *reinterpret_cast<uint4*>(sQ + tc::sw128_offset(r, j, R)) =
             make_uint4(scaled_half2(qv[k].x, qf), scaled_half2(qv[k].y, qf),
                        scaled_half2(qv[k].z, qf), scaled_half2(qv[k].w, qf));
