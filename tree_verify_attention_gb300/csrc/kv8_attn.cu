@@ -251,9 +251,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   const int warp =
       static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tid >> 5)));
   // what touches no global memory may run under the kernel before
-  if (warp == SW + 8) {
-    tc::tmem_alloc(&s_tmem, 512);
-  } else if (warp == SW + 9 && lane == 0) {
+  if (warp == SW + 9 && lane == 0) {
     for (int s = 0; s < 4; ++s) {
       mbar_init(&b_kraw[s], 1);
       mbar_init(&b_vraw[s], 1);
@@ -287,6 +285,9 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   const int row0 = tile * p.rows_tile, n_rows = min(p.rows_tile, p.rows - row0);
   grid_dep_wait();
   grid_dep_launch_dependents();   // the merge may be set up (after the wait: see common.cuh)
+  // Not before the wait: a kernel that has let this one start may allocate its
+  // own columns only after that, and would wait for these for ever.
+  if (warp == SW + 8) tc::tmem_alloc(&s_tmem, 512);
   int C = __reduce_max_sync(0xFFFFFFFFu, *p.c.state);
   for (int i = tid; i < p.n_nodes; i += A::kThreads) {
     int pa = i == 0 ? -1 : p.parent[i];
