@@ -210,6 +210,8 @@ class Int8Cache:
         r, hd = (1, 0) if head_major else (0, 1)
         n = k_rows.shape[r]
         shape = (h, n, d) if head_major else (n, h, d)
+        if at is not None and not 0 <= at <= self.capacity:
+            raise DfvError(f"at {at} is outside [0, {self.capacity}]")
         ks = _float_rows(k_rows, "k_rows", shape)
         vs = _float_rows(v_rows, "v_rows", shape, (k_rows.dtype,))
         _same_device(self._index, k_rows, v_rows, status)
@@ -236,6 +238,8 @@ class Int8Cache:
         h, d = self.n_kv_heads, self.head_dim
         r, hd = (1, 0) if head_major else (0, 1)
         shape = (h, n, d) if head_major else (n, h, d)
+        if not 0 <= pos0 <= pos0 + n <= self.capacity:
+            raise DfvError(f"rows [{pos0}, {pos0 + n}) are outside [0, {self.capacity})")
         st = _float_rows(k_out, "k_out", shape)
         if _float_rows(v_out, "v_out", shape, (k_out.dtype,)) != st:
             raise DfvError("k_out and v_out must have the same strides")
