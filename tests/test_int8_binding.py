@@ -28,3 +28,26 @@ def test_reads_past_the_capacity():
     for pos, n in ((198, 3), (0, 201), (0, -1), (5, 1 << 32)):
         with pytest.raises(api.DfvError, match="outside"):
             c.read(pos, n, rows, rows)
+
+
+class OnDevice:
+    """A host tensor that says it is on the GPU (nothing may be launched)."""
+
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("ids,tlp", [(0, 5), (5, 0), (3, 5), (5, 3)])
+def test_alternatives_of_two_widths(ids, tlp):
+    """Also where one has no columns: a view of none still has an address."""
+    n, v = 3, 40
+    store = torch.zeros(n, 8, dtype=torch.int32)
+    ids = OnDevice(store[:, :ids].contiguous() if ids else store[:, :0])
+    tlp = OnDevice(torch.zeros(n, tlp))
+    with pytest.raises(api.DfvError, match="the same K"):
+        api.token_logprobs(OnDevice(torch.zeros(n, v)), None, None, None, ids, tlp)

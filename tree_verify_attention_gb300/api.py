@@ -410,14 +410,15 @@ def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logp
         _dev(logprob, "logprob", _F32, n)
     if entropy is not None:
         _dev(entropy, "entropy", _F32, n)
-    top = 0
+    top = None
     for t, name, dt in ((top_ids, "top_ids", _I32), (top_logprobs, "top_logprobs", _F32)):
         if t is None:
             continue
         _dev(t, name, dt)
-        if t.dim() != 2 or t.shape[0] != n or (top and t.shape[1] != top):
+        if t.dim() != 2 or t.shape[0] != n or t.shape[1] != (t.shape[1] if top is None else top):
             raise DfvError(f"{name} must be [{n}, K], the same K for ids and log probabilities")
         top = t.shape[1]
+    top = top or 0
     if top > min(MAX_TOP, vocab):
         raise DfvError(f"{top} alternatives asked for, at most {min(MAX_TOP, vocab)}")
     _same_device(logits.get_device(), tokens, logprob, entropy, top_ids, top_logprobs, status)
