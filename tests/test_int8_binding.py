@@ -51,3 +51,37 @@ def test_alternatives_of_two_widths(ids, tlp):
     tlp = OnDevice(torch.zeros(n, tlp))
     with pytest.raises(api.DfvError, match="the same K"):
         api.token_logprobs(OnDevice(torch.zeros(n, v)), None, None, None, ids, tlp)
+
+
+def planned_step(top=None):
+    step = object.__new__(api.VerifyStep)      # (a step's buffers need a GPU)
+    step.shape, step.int8, step.max_depth, step.top = (4, 6, 2, 64, 0, 200, 50), True, 8, top
+    return step
+
+
+@pytest.mark.parametrize("name,shape", [
+    ("q", (3, 6, 64)), ("q", (5, 6, 64)), ("q", (4, 4, 64)), ("q", (4, 6, 128)),
+    ("tree_k", (3, 2, 64)), ("tree_k", (4, 1, 64)), ("tree_v", (5, 2, 64)),
+    ("tree_v", (4, 2, 128)), ("logits", (3, 50)), ("logits", (5, 50)), ("logits", (4, 49)),
+    ("logits", (200,))])
+def test_a_step_over_an_int8_cache_takes_what_it_is_planned_for(name, shape):
+    """Fewer rows of logits than nodes would leave argmax and path of an
+    earlier step in place, for the commit to follow."""
+    shapes = {"q": (4, 6, 64), "tree_k": (4, 2, 64), "tree_v": (4, 2, 64), "logits": (4, 50)}
+    shapes[name] = shape
+    a = {k: OnDevice(torch.zeros(s, dtype=torch.bfloat16)) for k, s in shapes.items()}
+    i32 = OnDevice(torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(api.DfvError, match=f"{name} .*planned"):
+        planned_step().run(cpu_cache(), a["q"], a["tree_k"], a["tree_v"], i32, i32, a["logits"])
+
+
+@pytest.mark.parametrize("name", ["parent", "tokens"])
+def test_a_step_over_an_int8_cache_checks_before_it_launches(name):
+    a = {"parent": OnDevice(torch.zeros(4, dtype=torch.int32)),
+         "tokens": OnDevice(torch.zeros(4, dtype=torch.int32))}
+    rows = OnDevice(torch.zeros(4, 2, 64, dtype=torch.bfloat16))
+    for bad in (torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int64)):
+        with pytest.raises(api.DfvError, match=name):
+            planned_step().run(cpu_cache(), OnDevice(torch.zeros(4, 6, 64, dtype=torch.bfloat16)),
+                               rows, rows, *{**a, name: OnDevice(bad)}.values(),
+                               OnDevice(torch.zeros(4, 50)))

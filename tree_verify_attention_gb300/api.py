@@ -515,6 +515,14 @@ class VerifyStep:
         if isinstance(cache, Int8Cache) != self.int8:
             raise DfvError("the step is planned for another kind of cache")
         if self.int8:
+            for t, name, shape in ((q, "q", (n, hq, d)), (tree_k, "tree_k", (n, hkv, d)),
+                                   (tree_v, "tree_v", (n, hkv, d)), (logits, "logits", (n, vocab))):
+                if tuple(t.shape) != shape:
+                    raise DfvError(f"{name} has shape {tuple(t.shape)}, the step is planned for "
+                                   f"{shape}")
+            _dev(parent, "parent", _I32, n)
+            _dev(tokens, "tokens", _I32, n)
+            _dev(logits, "logits", (torch.float32,) + _BF16)
             tree_verify_attn(cache, q, tree_k, tree_v, parent, window, self.max_depth, self.out,
                              self.lse, self.ws, scale=scale, status=self.status, stream=stream,
                              tree_as_cache=tree_as_cache)
