@@ -85,3 +85,11 @@ def test_a_step_over_an_int8_cache_checks_before_it_launches(name):
             planned_step().run(cpu_cache(), OnDevice(torch.zeros(4, 6, 64, dtype=torch.bfloat16)),
                                rows, rows, *{**a, name: OnDevice(bad)}.values(),
                                OnDevice(torch.zeros(4, 50)))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "q4_0", "f16"])
+@pytest.mark.parametrize("top,vocab", [(33, 1000), (6, 5), (-1, 1000)])
+def test_a_step_with_too_many_alternatives(top, vocab, fmt):
+    """Refused when it is planned, not when a step has been committed."""
+    with pytest.raises(api.DfvError, match="alternatives"):
+        api.VerifyStep(4, 6, 2, 64, 0, 200, vocab, fmt=fmt, top=top, device="cpu")

@@ -470,6 +470,8 @@ class VerifyStep:
 
     def __init__(self, n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity, vocab,
                  max_depth=16, device="cuda", pipelined=False, fmt="q4_0", top=None):
+        if top is not None and not 0 <= top <= min(MAX_TOP, vocab):
+            raise DfvError(f"top={top} alternatives, at most {min(MAX_TOP, vocab)}")
         self.shape = (n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity, vocab)
         self.max_depth = max_depth
         dev = torch.device(device)
