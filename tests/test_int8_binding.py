@@ -93,3 +93,20 @@ def test_a_step_with_too_many_alternatives(top, vocab, fmt):
     """Refused when it is planned, not when a step has been committed."""
     with pytest.raises(api.DfvError, match="alternatives"):
         api.VerifyStep(4, 6, 2, 64, 0, 200, vocab, fmt=fmt, top=top, device="cpu")
+
+
+@pytest.mark.parametrize("shape,dtype", [((4 * 50,), torch.float32), ((1, 4, 50), torch.bfloat16),
+                                         ((5, 50), torch.float32), ((4, 50), torch.int16)])
+def test_log_probabilities_of_whatever_logits_a_step_takes(shape, dtype, monkeypatch):
+    """The other formats take n * vocab logits in any shape; the log
+    probabilities come after the commit and must not refuse them then."""
+    seen = []
+    monkeypatch.setattr(api, "token_logprobs", lambda x, *a, **k: seen.append(x))
+    step = planned_step(top=2)
+    for name in ("argmax", "logprob", "entropy", "top_ids", "top_logprobs", "status"):
+        setattr(step, name, None)
+    x = torch.arange(torch.Size(shape).numel()).view(shape).to(dtype)
+    step._logprobs(x, None)
+    got = seen[0] if dtype != torch.int16 else seen[0].view(torch.int16)
+    assert got.shape == (4, 50) and torch.equal(got, x.reshape(-1)[:200].view(4, 50))
+    assert seen[0].dtype == (torch.bfloat16 if dtype == torch.int16 else dtype)

@@ -558,6 +558,9 @@ class VerifyStep:
     def _logprobs(self, logits, stream):
         if self.top is None:
             return
+        # a step takes any shape of n * vocab logits
+        n, vocab = self.shape[0], self.shape[-1]
+        logits = logits.view(-1)[:n * vocab].view(n, vocab)
         token_logprobs(logits if logits.dtype != torch.int16 else logits.view(torch.bfloat16),
                        self.argmax, self.logprob, self.entropy, self.top_ids, self.top_logprobs,
                        status=self.status, stream=stream)
