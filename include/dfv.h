@@ -372,7 +372,9 @@ dfv_status dfv_build_tree_mask(int n_nodes, const int32_t* parent, int32_t* dept
  *   scale = amax / 127,  code = round-half-even(127 x / amax)
  *
  * The open block, and the one before it, are kept as bf16 rows in the tail,
- * so a write can start up to one whole block back (rollback). The content
+ * so a write can start up to one whole block back (rollback): after a write
+ * that ended at C, from 64 (C / 64 - 1) on, 64 rows at least; after a rollback
+ * only as far as the rows that were held then. The content
  * does not depend on how the rows were split into calls. Values of 2^40 or
  * more (also infinities and NaN) enter as zeros and set DFV_DEV_NONFINITE; a
  * block whose largest magnitude is below 2^-40 is stored as zeros.

@@ -227,7 +227,8 @@ class Int8Cache:
 
     def truncate(self, length, stream=None, status=None):
         """Set the committed length back to ``length`` (the same rule as
-        :meth:`append`'s ``at``)."""
+        :meth:`append`'s ``at``: 64 rows can always be taken back after a
+        write, more if the open block has rows, and any multiple of 64)."""
         none = self.k_tail.new_empty(0, self.n_kv_heads, self.head_dim)
         self.append(none, none, at=length, stream=stream, status=status)
 
