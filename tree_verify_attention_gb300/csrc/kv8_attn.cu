@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
         ok = is_v && part == A::kVSub - 1
                  ? role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead)
                  : role_wait(is_v ? &b_vfree[part] : &b_kfree[part], (i - 1) & 1, &s_dead);
-      __syncwarp();
+      ok = __all_sync(0xFFFFFFFFu, ok);   // the TMEM stores are warp-wide
       tc::fence_after_sync();
     };
     auto give = [&](int part) {
@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
       return n;
     };
     const int done = rows_apart ? 0 : chunks(std::false_type{}, 0);
-    if (ok && done < n) chunks(std::true_type{}, done);
+    if (done < n) chunks(std::true_type{}, done);
     // ---- the unit's result
     // sums over the lanes, four columns at a time: two exchanges that halve
     // the columns a lane holds, then three plain ones
