@@ -243,7 +243,6 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   __shared__ int s_vexp[kAtKeys];
   __shared__ uint8_t s_bad[2][kAtKeys];
   __shared__ uint32_t s_qmax, s_qmin;   // largest and smallest of the rows' magnitudes
-  __shared__ int s_far[NG];    // a reference of the group is so large that it takes two parts
 
   const int tid = threadIdx.x, lane = tid & 31;
   // both the same in every lane, which the compiler knows of a reduction's
@@ -676,7 +675,6 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
       s_neg[tid] = kNoRef;
       s_lo[tid] = 0.0f;
     }
-    if (tid < NG) s_far[tid] = 0;
     named_sync(4, SW * 32);
     auto exponent = [](uint32_t m) { return max(static_cast<int>(m >> 7), 20); };
     const int qe = exponent(s_qmax);
@@ -737,6 +735,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     const uint32_t t_o = t_s + (A::kTO - A::kTS);
     const float4* m4 = reinterpret_cast<const float4*>(s_neg + cg * HC);
     const float4* lo4 = reinterpret_cast<const float4*>(s_lo + cg * HC);
+    const float4* cf4 = reinterpret_cast<const float4*>(s_cf + cg * HC);
 
     // Chunks [m_lo, m_hi) need no mask: their blocks are complete and inside
     // every node's window. The loop keeps little beside x and l: what a masked
@@ -748,9 +747,11 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
 
     // Chunks [i0, n), of which the first gets new references; returns the first
     // one not done: n, but for the narrow form where a reference is far out.
-    // Wide units have a form of their own: one for both, with the difference
-    // behind a branch, took 105 to 108 us for 23 nodes at ctx 131072, and 73 to
-    // 94 for 65 nodes, instead of 104.4 and 71.9 (narrow alone: 101.8, 71.9).
+    // Wide units have a form of their own, and new references are made beside
+    // the loop's common path, not by further turns through it: one form with
+    // the difference behind a branch took 105 to 108 us for 23 nodes at ctx
+    // 131072, two with three turns a chunk 104.4, this 100.2 (narrow alone, in
+    // turns: 101.5). A wide tile of 69 rows takes 120 us.
     auto chunks = [&](auto form, const int i0) {
       constexpr bool kWide = decltype(form)::value;
       for (int i = i0; i < n; ++i) {
@@ -787,121 +788,117 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, ok);   // the TMEM loads are warp-wide
         tc::fence_after_sync();
         float x[HC];
-        // Exponents against the references (pass 0). Where one is too large, and
-        // in the first chunk: scores alone, columns' maxima, new references
-        // (pass 1), and the exponents again (pass 3). In a wide unit the scores
-        // have their column's factor, the key's V scale is added behind the fma,
-        // which is exact near the reference, and a second part of the reference
-        // takes what rounding has left of the first (pass 2).
-        bool alive = true;
-#pragma unroll 1
-        for (int pass = i == i0 ? 1 : 0; pass < 4; ++pass) {
-          if (pass == 1) {   // a wait gave up somewhere in the group?
-            ok = named_sync_and(5 + cg, 128, ok);
-            if (!ok) {
-              alive = false;
-              break;
-            }
-          }
+        // Exponents against the references. Where one is too large, and in the
+        // first chunk: scores alone, columns' maxima, new references, and the
+        // exponents again. In a wide unit the scores have their column's factor,
+        // the key's V scale is added behind the fma, which is exact near the
+        // reference, and a second part of the reference takes what rounding has
+        // left of the first.
+        // kRef 0: no references, 1: both parts, 2: the first part alone
+        auto exponents = [&](auto with_ref) {
+          constexpr int kRef = decltype(with_ref)::value;
           if (ok) tc::TmemIo<HC>::load(t_s, reinterpret_cast<uint32_t*>(x));
-          if constexpr (!kWide) {
-            const float4* ref = pass == 1 ? lo4 : m4;   // (lo4: zeros)
+          if constexpr (kWide) {
 #pragma unroll
             for (int c = 0; c < HC; c += 4) {
-              float4 m = ref[c / 4];
-              add2(m.x, m.y, m.x, m.y, lv, lv);
-              add2(m.z, m.w, m.z, m.w, lv, lv);
+              const float4 f = cf4[c / 4];
+              fma2(x[c], x[c + 1], x[c], x[c + 1], f.x, f.y, 0.0f, 0.0f);
+              fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], f.z, f.w, 0.0f, 0.0f);
+            }
+          }
+          if constexpr (kRef == 0) {
+#pragma unroll
+            for (int c = 0; c < HC; c += 2) fma2(x[c], x[c + 1], x[c], x[c + 1], a, a, lv, lv);
+          } else {
+#pragma unroll
+            for (int c = 0; c < HC; c += 4) {
+              float4 m = m4[c / 4];
+              if constexpr (!kWide) {
+                add2(m.x, m.y, m.x, m.y, lv, lv);
+                add2(m.z, m.w, m.z, m.w, lv, lv);
+              }
               fma2(x[c], x[c + 1], x[c], x[c + 1], a, a, m.x, m.y);
               fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], a, a, m.z, m.w);
             }
-          } else {
-            float xw[HC];   // rolled, by way of local memory: the registers are the narrow form's
+            if constexpr (kWide) {
 #pragma unroll
-            for (int c = 0; c < HC; ++c) xw[c] = x[c];
-#pragma unroll 1
-            for (int c = 0; c < HC; ++c) {
-              const int col = cg * HC + c;
-              xw[c] = fmaf(xw[c] * s_cf[col], a, pass == 1 ? 0.0f : s_neg[col]) +
-                     (pass == 1 || pass == 2 ? lv : lv + s_lo[col]);
+              for (int c = 0; c < HC; c += 4) {
+                const float4 m = kRef == 2 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : lo4[c / 4];
+                add2(x[c], x[c + 1], x[c], x[c + 1], lv + m.x, lv + m.y);
+                add2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], lv + m.z, lv + m.w);
+              }
             }
-#pragma unroll
-            for (int c = 0; c < HC; ++c) x[c] = xw[c];
           }
           if (masked) {
 #pragma unroll
             for (int c = 0; c < HC; ++c)
               if (!(vis & (1u << c))) x[c] = -INFINITY;
           }
-          if (pass == 0) {
-            float top = -INFINITY;
+        };
+        auto maxima = [&]() {   // of the columns, by lane; for the group's first warp
 #pragma unroll
-            for (int c = 0; c < HC; c += 2) top = max3(top, x[c], x[c + 1]);
-            if (named_sync_and(5 + cg, 128, ok && !(top > kRaise))) break;
-          } else if (pass < 3) {
-#pragma unroll
-            for (int c = 0; c < HC; ++c) {
-              float m;
-              asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x[c]));
-              if (lane == 0) s_red[warp & 3][cg * HC + c] = m;
-            }
-            named_sync(5 + cg, 128);
-            if ((warp & 3) == 0) {
-              static_assert(HC <= 32, "a lane has one column of the group");
-              const int c = cg * HC + min(lane, HC - 1);
-              const float top = fmaxf(fmaxf(s_red[0][c], s_red[1][c]),
-                                      fmaxf(s_red[2][c], s_red[3][c]));
-              const float was = -s_neg[c], lo = s_lo[c], old = s_f[c];
-              __syncwarp();
-              if constexpr (!kWide) {
-                const float size = fabsf(top);
-                const bool far = __any_sync(0xFFFFFFFFu, size > kFar && size < INFINITY);
-                const float m = fmaxf(top - kTop, was);
-                if (far) {
-                  s_far[cg] = 1;   // nothing changes before the wide form
-                } else if (lane < HC) {
-                  s_neg[c] = -m;
-                  s_f[c] = tc::ex2(was - m);
-                }
-              } else if (lane < HC) {
-                if (pass == 1) {
-                  // s_f: the reference that it was, where there is a new one
-                  // (not with NaN, where the comparison fails)
-                  const bool up = top - kTop > was - lo;
-                  s_f[c] = up ? was : INFINITY;
-                  if (up) s_neg[c] = kTop - top;
-                } else {
-                  const bool up = old < INFINITY && top > -INFINITY;
-                  if (up) s_lo[c] = kTop - top;
-                  s_f[c] = up ? tc::ex2((old - was) + (kTop - top - lo)) : 1.0f;
-                }
-              }
-            }
-            if (pass == 1 && i > 0)
-              ok = role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead);
-            ok = named_sync_and(5 + cg, 128, ok);
-            if (!ok) {
-              alive = false;
-              break;
-            }
-            if (kWide && pass == 1) continue;
-            if (!kWide && s_far[cg]) return i;
-            if (i > 0) {
-              tc::fence_after_sync();
-#pragma unroll
-              for (int c = 0; c < HC; ++c) l[c] *= s_f[cg * HC + c];
-#pragma unroll 1
-              for (int hh = 0; hh < A::kHalves; ++hh) {
-                tc::TmemIo<HC>::load(t_o + hh * R, reinterpret_cast<uint32_t*>(x));
-#pragma unroll
-                for (int c = 0; c < HC; ++c) x[c] *= s_f[cg * HC + c];
-                tc::TmemIo<HC>::store(t_o + hh * R, reinterpret_cast<const uint32_t*>(x));
-                tc::store_wait();
-              }
-            }
-            pass = 2;
+          for (int c = 0; c < HC; ++c) {
+            float m;
+            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x[c]));
+            if (lane == 0) s_red[warp & 3][cg * HC + c] = m;
           }
+          named_sync(5 + cg, 128);
+          static_assert(HC <= 32, "a lane has one column of the group");
+          const int c = cg * HC + min(lane, HC - 1);
+          return fmaxf(fmaxf(s_red[0][c], s_red[1][c]), fmaxf(s_red[2][c], s_red[3][c]));
+        };
+        bool renew = i == i0;
+        float top = -INFINITY;
+        if (!renew) {
+          exponents(std::integral_constant<int, 1>{});
+#pragma unroll
+          for (int c = 0; c < HC; c += 2) top = max3(top, x[c], x[c + 1]);
+          renew = !named_sync_and(5 + cg, 128, ok && !(top > kRaise));
         }
-        if (!alive) break;
+        if (renew) {
+          ok = named_sync_and(5 + cg, 128, ok);   // or has a wait given up?
+          if (!ok) break;
+          const int c = cg * HC + min(lane, HC - 1);
+          const bool mine = (warp & 3) == 0 && lane < HC;
+          exponents(std::integral_constant<int, 0>{});
+          top = maxima();
+          float was = -s_neg[c], lo = s_lo[c];
+          bool up = top - kTop > was - lo;   // (not with NaN, where the comparison fails)
+          if constexpr (!kWide) {
+            const bool far = __any_sync(0xFFFFFFFFu, fabsf(top) > kFar && fabsf(top) < INFINITY);
+            if (far) return i;   // nothing changes before the wide form
+          }
+          __syncwarp();
+          if (mine && up) s_neg[c] = kTop - top;
+          float f = up ? tc::ex2(was - (top - kTop)) : 1.0f;
+          if constexpr (kWide) {
+            named_sync(5 + cg, 128);
+            exponents(std::integral_constant<int, 2>{});
+            const float first = top - kTop;
+            top = maxima();
+            up = up && top > -INFINITY;
+            if (mine && up) s_lo[c] = kTop - top;
+            f = up ? tc::ex2((was - first) + (kTop - top - lo)) : 1.0f;
+          }
+          if (mine) s_f[c] = f;
+          if (i > 0) ok = role_wait(&b_pv[(i - 1) & 1], ((i - 1) >> 1) & 1, &s_dead);
+          ok = named_sync_and(5 + cg, 128, ok);
+          if (!ok) break;
+          if (i > 0) {
+            tc::fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < HC; ++c) l[c] *= s_f[cg * HC + c];
+#pragma unroll 1
+            for (int hh = 0; hh < A::kHalves; ++hh) {
+              tc::TmemIo<HC>::load(t_o + hh * R, reinterpret_cast<uint32_t*>(x));
+#pragma unroll
+              for (int c = 0; c < HC; ++c) x[c] *= s_f[cg * HC + c];
+              tc::TmemIo<HC>::store(t_o + hh * R, reinterpret_cast<const uint32_t*>(x));
+              tc::store_wait();
+            }
+          }
+          exponents(std::integral_constant<int, 1>{});
+        }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_sfree);
