@@ -381,7 +381,10 @@ dfv_status dfv_build_tree_mask(int n_nodes, const int32_t* parent, int32_t* dept
  *
  * nblk = (capacity + 63) / 64 blocks per head. All pointers are device
  * memory; the struct itself is read by the host during the call.
- *   state    int32[4]: [0] the committed length; [1] a counter the library
+ *   state    int32[4]: [0] the committed length (set back by dfv_kv8_append
+ *            with n_rows = 0; written directly to a place inside a block that
+ *            the tail no longer holds, the rows of that block are left out of
+ *            reads and attention, with DFV_DEV_CTX); [1] a counter the library
  *            keeps at zero between calls; [2] the first block whose bf16 rows
  *            the tail still holds; [3] set if a bounded wait of a long write
  *            gave up (DFV_DEV_TIMEOUT): the length is not advanced, rows from

@@ -622,13 +622,15 @@ __global__ void __launch_bounds__(D) kv8_read_kernel(const __grid_constant__ Kv8
   constexpr int kTpt = D / 64, kVt = D / 4;
   grid_dep_wait();
   grid_dep_launch_dependents();   // (after the wait: see common.cuh)
-  const int C = *p.c.state;
+  const int C = p.c.state[0], held = p.c.state[2];
   const int tid = threadIdx.x, h = blockIdx.y, kv = blockIdx.z;
-  int end = p.end;
-  if (C < 0 || C > p.c.capacity || end > C) {   // rows behind the committed ones stay as they are
-    if (tid == 0 && blockIdx.x == 0 && h == 0 && kv == 0) report(p.status, DFV_DEV_CTX);
-    end = C < 0 || C > p.c.capacity ? 0 : min(end, C);
-  }
+  // Rows behind the committed ones stay as they are, and rows of an open block
+  // where the tail has others.
+  int rows = C < 0 || C > p.c.capacity ? 0 : C;
+  if (C / kBlk < held) rows = rows / kBlk * kBlk;
+  const int end = min(p.end, rows);
+  if (end < p.end && tid == 0 && blockIdx.x == 0 && h == 0 && kv == 0)
+    report(p.status, DFV_DEV_CTX);
   const int b = p.pos0 / kBlk + blockIdx.x;
   const int first = max(p.pos0, b * kBlk), last = min(end, (b + 1) * kBlk);
   if (first >= last) return;

@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
   // Not before the wait: a kernel that has let this one start may allocate its
   // own columns only after that, and would wait for these for ever.
   if (warp == SW + 8) tc::tmem_alloc(&s_tmem, 512);
-  int C = __reduce_max_sync(0xFFFFFFFFu, *p.c.state);
+  int C = __reduce_max_sync(0xFFFFFFFFu, p.c.state[0]);
+  const int held = p.c.state[2];
   for (int i = tid; i < p.n_nodes; i += A::kThreads) {
     int pa = i == 0 ? -1 : p.parent[i];
     if (i > 0 && (pa < 0 || pa >= i)) {
@@ -298,9 +299,10 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
 #pragma unroll
     for (int g = 0; g < NG; ++g) s_see[i][g] = s_dep[i][g] = 0;
   }
-  if (C < 0 || C > p.c.capacity) {
+  if (C < 0 || C > p.c.capacity || (C % kBlk != 0 && C / kBlk < held)) {
     if (tid == 0) report(p.status, DFV_DEV_CTX);
     C = max(0, min(C, p.c.capacity));
+    if (C / kBlk < held) C = C / kBlk * kBlk;   // the tail has other rows there
   }
   // Chunks: complete blocks [fb, open) two at a time, then the bf16 chunk,
   // which belongs to the last slice and counts as several: it waits for its
