@@ -47,8 +47,8 @@
 // that issues MMAs, two that copy K and V. A unit is (KV head, tile of at most
 // 80 query rows, or 96 below D = 256, slice of the chunks). Bound by HBM while
 // a tile has few rows, by the softmax and the conversion for many: 24 heads of
-// 256 over 131072 positions take 51.5 us for one node (5.2 TB/s) and 106 us for
-// 23 (700 TFLOP/s; 63 % of the issue slots busy).
+// 256 over 131072 positions take 48.9 us for one node (5.5 TB/s) and 99 us for
+// 23 (750 TFLOP/s; 71 % of the issue slots busy).
 
 #include <atomic>
 #include <math.h>
@@ -750,10 +750,11 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
     // Chunks [i0, n), of which the first gets new references; returns the first
     // one not done: n, but for the narrow form where a reference is far out.
     // Wide units have a form of their own, and new references are made beside
-    // the loop's common path, not by further turns through it: one form with
-    // the difference behind a branch took 105 to 108 us for 23 nodes at ctx
-    // 131072, two with three turns a chunk 104.4, this 100.2 (narrow alone, in
-    // turns: 101.5). A wide tile of 69 rows takes 120 us.
+    // the loop's common path, not by further turns through it (23 nodes at ctx
+    // 131072: 98.2 us; one form with the difference behind a branch 105 to 108,
+    // two with three turns a chunk 104.5; narrow alone, in turns, 101.5). A wide
+    // tile of 69 rows takes 221 us; unrolled like the narrow form 120, but the
+    // narrow one then 100.3, and up to 8 % more at other shapes.
     auto chunks = [&](auto form, const int i0) {
       constexpr bool kWide = decltype(form)::value;
       for (int i = i0; i < n; ++i) {
@@ -801,34 +802,42 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
           constexpr int kRef = decltype(with_ref)::value;
           if (ok) tc::TmemIo<HC>::load(t_s, reinterpret_cast<uint32_t*>(x));
           if constexpr (kWide) {
+            // by way of local memory, four columns a turn: the registers are the
+            // narrow form's
+            float4 xw[HC / 4];
 #pragma unroll
-            for (int c = 0; c < HC; c += 4) {
-              const float4 f = cf4[c / 4];
-              fma2(x[c], x[c + 1], x[c], x[c + 1], f.x, f.y, 0.0f, 0.0f);
-              fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], f.z, f.w, 0.0f, 0.0f);
+            for (int j = 0; j < HC / 4; ++j)
+              xw[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+#pragma unroll 1
+            for (int j = 0; j < HC / 4; ++j) {
+              const float4 f = cf4[j];
+              float4 y = xw[j], m = make_float4(0.0f, 0.0f, 0.0f, 0.0f), m2 = m;
+              if constexpr (kRef != 0) m = m4[j];
+              if constexpr (kRef == 1) m2 = lo4[j];
+              y.x = fmaf(y.x * f.x, a, m.x) + (lv + m2.x);
+              y.y = fmaf(y.y * f.y, a, m.y) + (lv + m2.y);
+              y.z = fmaf(y.z * f.z, a, m.z) + (lv + m2.z);
+              y.w = fmaf(y.w * f.w, a, m.w) + (lv + m2.w);
+              xw[j] = y;
             }
-          }
-          if constexpr (kRef == 0) {
+#pragma unroll
+            for (int j = 0; j < HC / 4; ++j) {
+              x[4 * j] = xw[j].x;
+              x[4 * j + 1] = xw[j].y;
+              x[4 * j + 2] = xw[j].z;
+              x[4 * j + 3] = xw[j].w;
+            }
+          } else if constexpr (kRef == 0) {
 #pragma unroll
             for (int c = 0; c < HC; c += 2) fma2(x[c], x[c + 1], x[c], x[c + 1], a, a, lv, lv);
           } else {
 #pragma unroll
             for (int c = 0; c < HC; c += 4) {
               float4 m = m4[c / 4];
-              if constexpr (!kWide) {
-                add2(m.x, m.y, m.x, m.y, lv, lv);
-                add2(m.z, m.w, m.z, m.w, lv, lv);
-              }
+              add2(m.x, m.y, m.x, m.y, lv, lv);
+              add2(m.z, m.w, m.z, m.w, lv, lv);
               fma2(x[c], x[c + 1], x[c], x[c + 1], a, a, m.x, m.y);
               fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], a, a, m.z, m.w);
-            }
-            if constexpr (kWide) {
-#pragma unroll
-              for (int c = 0; c < HC; c += 4) {
-                const float4 m = kRef == 2 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : lo4[c / 4];
-                add2(x[c], x[c + 1], x[c], x[c + 1], lv + m.x, lv + m.y);
-                add2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], lv + m.z, lv + m.w);
-              }
             }
           }
           if (masked) {
