@@ -413,6 +413,7 @@ __global__ void __launch_bounds__(D)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kBulkSlots];
   __shared__ uint32_t s_max[2][D / 32];
+  __shared__ int s_stopped;
   constexpr uint32_t kNoRows = ~0u;   // in a maximum's place: a thread's wait gave up
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -422,11 +423,13 @@ __global__ void __launch_bounds__(D)
   grid_dep_wait();
   const int C = p.c.state[0], held = p.c.state[2];
   const int at = p.at < 0 ? C : p.at;
-  // refused as by kv8_append_kernel, which reports it
-  if (static_cast<volatile int32_t*>(p.c.state)[3] != 0 || C < 0 || C > p.c.capacity || at > C ||
-      p.n > p.c.capacity - at || (at % kBlk != 0 && at / kBlk < held))
-    return;
+  // (asked by one thread: another CTA of this launch may set it meanwhile)
+  if (tid == 0) s_stopped = static_cast<volatile int32_t*>(p.c.state)[3];
   __syncthreads();
+  // refused as by kv8_append_kernel, which reports it
+  if (s_stopped != 0 || C < 0 || C > p.c.capacity || at > C || p.n > p.c.capacity - at ||
+      (at % kBlk != 0 && at / kBlk < held))
+    return;
   fence_proxy_async_global();   // what earlier kernels wrote, to the copy engine
   const int b0 = at / kBlk, per = p.bulk * p.c.n_kv_heads;   // blocks of K, as many of V
   const int total = 2 * per;
