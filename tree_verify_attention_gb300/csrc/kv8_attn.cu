@@ -66,6 +66,10 @@ constexpr float kTop = 8.0f;         // exponent of the largest P' under a new r
 constexpr float kRaise = 15.0f;      // a larger exponent moves the reference
 constexpr float kNoRef = 3e38f;      // -reference of a column that has seen no key
 constexpr float kFar = 262144.0f;    // a larger reference is kept in two parts
+// V scale that a key without any value counts with: it adds nothing to the
+// output, so its weight must not make the others' small (its sum of up to 2^17
+// keys of 2^15 / kNoValue stays in float32).
+constexpr float kNoValue = 8.0779357e-28f;   // 2^-90
 constexpr int kSpread = 10;          // log2 of the ratio of rows that share a scale
 constexpr uint32_t kNotFinite = 0x10000u;   // in a row's magnitude: it holds inf or NaN
 constexpr float kLog2eF = 1.4426950408889634f;
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
       }
     };
     auto put_scales = [&](int batch) {
-      const float sv = fmaxf(vs, 7.1054274e-15f);   // 2^-47
+      const float sv = fmaxf(vs, kNoValue);         // (others are 2^-47 at least)
       const float lv = lg2_fast(sv);                // within 2^-20, in both
       s_sc[(batch & 1) * 32 + lane] = make_float4(ks, lv, tc::ex2(-lv), 0.0f);
       __syncwarp();
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(AttnShape<D, R>::kThreads, 1)
       if (!is_v) {
         s_ksc[slot] = bad ? 0.0f : pow2i(e - 133);
       } else {
-        s_vexp[slot] = bad ? 0 : e - 133;
+        s_vexp[slot] = bad ? 0 : m == 0 ? -90 : e - 133;
         s_vfac[slot] = f;
       }
       if (bad || !live) {   // no 0 * inf below
