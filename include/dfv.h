@@ -21,7 +21,9 @@
  *
  * Beside them, for the same loop: a cache held in 8 bits with one scale per
  * 64 positions and head (dfv_kv8_append, dfv_kv8_commit, dfv_kv8_read,
- * dfv_kv8_attn), and dfv_token_logprobs, log probabilities of given tokens.
+ * dfv_kv8_attn), dfv_token_logprobs, log probabilities of given tokens, and
+ * what comes before a step: dfv_qk_norm_rope, a projection's queries and keys
+ * normed and rotated to the tree's positions.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -495,6 +497,50 @@ dfv_status dfv_token_logprobs(int n_rows, int vocab, int logits_dtype, const voi
                               int64_t stride_row, const int32_t* tokens, int top, float* logprob,
                               float* entropy, int32_t* top_ids, float* top_logprobs,
                               uint32_t* status, dfv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dfv_qk_norm_rope -- a projection's output as the attention takes it: each
+ * query and key head normed and rotated, the value rows carried along.
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * w              (w: q_weight or k_weight)
+ *   the first rot_dim dims of y in pairs (a, b):
+ *   (a cos t - b sin t, b cos t + a sin t), t = position * frequency of the pair
+ *
+ * computed in f32 (angles exact to 2^-26 of a turn at any position), rounded
+ * once.
+ *
+ *   q, k, v    device f32 or bf16 (src_dtype), element (row r, head h, dim c)
+ *              at x[r * stride_row + h * stride_head + c]; v may be NULL, q or
+ *              k too where there are no such heads. Rows that start on 16-byte
+ *              boundaries are read by 16-byte loads
+ *   head_dim   64, 128 or 256
+ *   q_weight, k_weight  device f32 [D], 16-byte aligned, or NULL (ones)
+ *   eps        added to the mean of squares; negative: no norm (no weights)
+ *   turns      device uint64 [rot_dim / 2]: turns of pair i per position,
+ *              frequency / (2 pi), as a binary fraction: times 2^64, modulo 2^64
+ *   rot_dim    0 (no rotation) to D, a multiple of 16
+ *   interleaved  pairs are dims (2i, 2i + 1); else (i, i + rot_dim / 2)
+ *   positions  device int32 [n_rows], the rows' positions; or NULL:
+ *              *ctx_len + *dropped (NULL: 0) + depth of the node in the tree
+ *              `parent` (as in dfv_build_tree_mask, n_rows <= DFV_MAX_NODES) or,
+ *              with parent NULL, + the row's number. `dropped` is the number of
+ *              positions by which cache rows lie below their place in the
+ *              sequence (dfv_kv_evict).
+ *   q_out, k_out, v_out  device f32 or bf16 (dst_dtype), [n_rows][heads][D],
+ *              16-byte aligned; each may be its source itself if that has the
+ *              same type and layout, and overlaps nothing else
+ * One launch, no workspace.
+ * ---------------------------------------------------------------------- */
+dfv_status dfv_qk_norm_rope(int n_rows, int n_q_heads, int n_kv_heads, int head_dim,
+                            const void* q, const void* k, const void* v, int src_dtype,
+                            int64_t q_stride_row, int64_t q_stride_head, int64_t k_stride_row,
+                            int64_t k_stride_head, int64_t v_stride_row, int64_t v_stride_head,
+                            const float* q_weight, const float* k_weight, float eps,
+                            const uint64_t* turns, int rot_dim, int interleaved,
+                            const int32_t* positions, const int32_t* parent,
+                            const int32_t* ctx_len, const int32_t* dropped, void* q_out,
+                            void* k_out, void* v_out, int dst_dtype, uint32_t* status,
+                            dfv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -34,6 +34,7 @@ Module map:
 * ``step``      -- the whole verify step composed from the above.
 * ``int8``      -- the 8-bit cache with a scale per 64 positions and head.
 * ``logprobs``  -- log probabilities of given tokens, entropy, alternatives.
+* ``encode``    -- norm and rotation of queries and keys.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against brute force, closed forms, invariants or library routines. Parity
@@ -41,4 +42,5 @@ with the pages' own implementation is unpinned: the pages print no worked
 example and no kernel output.
 """
 
-from . import q4_0, f16, tree, attention, accept, commit, step, int8, logprobs  # noqa: F401
+from . import (q4_0, f16, tree, attention, accept, commit, step, int8, logprobs,  # noqa: F401
+               encode)

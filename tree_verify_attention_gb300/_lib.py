@@ -45,6 +45,8 @@ SIGNATURES = {
     "dfv_kv8_attn": (_i32, [_vp] + [_i32] * 4 + [_vp] * 4 + [_f32, _vp, _i32, _vp, _vp, _sz, _vp,
                                                             _vp]),
     "dfv_token_logprobs": (_i32, [_i32, _i32, _i32, _vp, _i64, _vp, _i32] + [_vp] * 6),
+    "dfv_qk_norm_rope": (_i32, [_i32] * 4 + [_vp] * 3 + [_i32] + [_i64] * 6 + [_vp, _vp, _f32, _vp,
+                                _i32, _i32] + [_vp] * 7 + [_i32, _vp, _vp]),
 }
 
 _lib = None

@@ -6,6 +6,7 @@ non-OK status. No compute happens here.
 """
 
 import ctypes
+import math
 
 import torch
 
@@ -427,6 +428,101 @@ def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logp
         n, vocab, DTYPE_F32 if logits.dtype == torch.float32 else DTYPE_BF16, logits.data_ptr(),
         logits.stride(0) if n > 1 else vocab, _p(tokens), top, _p(logprob), _p(entropy),
         _p(top_ids), _p(top_logprobs), _p(status), _stream(stream)), "dfv_token_logprobs")
+
+
+class Rope:
+    """Frequencies of the position rotation of :func:`qk_norm_rope`: the first
+    ``rot_dim`` dims of a head (all by default) turn in pairs, pair i by
+    ``base ** (-2 i / rot_dim)`` rad per position, or by ``inv_freq[i]``
+    (rot_dim / 2 numbers). Pairs are dims (i, i + rot_dim / 2), or (2 i, 2 i + 1)
+    with ``interleaved``. Kept as turns per position in 64-bit fractions."""
+
+    def __init__(self, head_dim, rot_dim=None, base=10000.0, inv_freq=None, interleaved=False,
+                 device="cuda"):
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        if head_dim not in (64, 128, 256):
+            raise DfvError(f"head_dim {head_dim} is not one of 64, 128, 256")
+        if not 0 <= rot_dim <= head_dim or rot_dim % 16:
+            raise DfvError(f"rot_dim {rot_dim} is not a multiple of 16 in [0, {head_dim}]")
+        if inv_freq is None:
+            inv_freq = [float(base) ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+        inv_freq = [float(f) for f in inv_freq]
+        if len(inv_freq) != rot_dim // 2 or not all(math.isfinite(f) for f in inv_freq):
+            raise DfvError(f"inv_freq must be {rot_dim // 2} finite numbers")
+        turns = [int(math.fmod(f / (2.0 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in inv_freq]
+        self.head_dim, self.rot_dim, self.interleaved = head_dim, rot_dim, bool(interleaved)
+        self.turns = torch.tensor([t - (t >> 63 << 64) for t in turns], dtype=torch.int64,
+                                  device=device)
+
+
+def qk_norm_rope(q, k, v, rope, q_out, k_out, v_out=None, q_weight=None, k_weight=None, eps=1e-6,
+                 positions=None, ctx_len=None, dropped=None, parent=None, status=None,
+                 stream=None):
+    """RMS norm of each head of ``q`` [N, Hq, D] and ``k`` [N, Hkv, D], times
+    ``q_weight`` / ``k_weight`` (f32 [D]), then ``rope``'s rotation; ``v``
+    [N, Hkv, D] (or None) is carried along. Sources are f32 or bf16 of any
+    strides over contiguous heads (slices of one projection, say), outputs
+    contiguous f32 or bf16, and may be the sources themselves. ``q`` or ``k``
+    may be None. ``eps=None``: no norm.
+
+    Row i stands at ``positions[i]`` (int32), or at ``ctx_len + dropped`` (both
+    int32[1], ``dropped`` optional) plus its depth in the tree ``parent`` (int32
+    [N], N <= MAX_NODES) or, without one, plus i."""
+    first = q if q is not None else k
+    if first is None:
+        raise DfvError("q or k is required")
+    if first.dim() != 3:
+        raise DfvError("q and k must be [N, heads, D]")
+    n, _, d = first.shape
+    if rope.head_dim != d:
+        raise DfvError(f"rope is for head_dim {rope.head_dim}, the rows have {d}")
+    if (k is None) and v is not None:
+        raise DfvError("v without k")
+    src, dst, heads, strides = _ROWS, _ROWS, [], []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
+        if x is None:
+            heads.append(0)
+            strides += [0, 0]
+            continue
+        h = (k if name == "v" else x).shape[1] if x.dim() == 3 else -1
+        st = _float_rows(x, name, (n, h, d), src)
+        _dev(out, name + "_out", dst)
+        if tuple(out.shape) != (n, h, d):
+            raise DfvError(f"{name}_out has shape {tuple(out.shape)}, expected {(n, h, d)}")
+        src, dst = (x.dtype,), (out.dtype,)    # one type for all sources, one for all outputs
+        heads.append(h)
+        strides += [st[0], st[1]]
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            if eps is None:
+                raise DfvError(f"{name} without a norm")
+            _dev(w, name, _F32, d)
+    if eps is not None and not eps >= 0:
+        raise DfvError(f"eps {eps} must be 0 or more")
+    if positions is not None:
+        if ctx_len is not None or dropped is not None or parent is not None:
+            raise DfvError("positions are given: no ctx_len, dropped or parent beside them")
+        _dev(positions, "positions", _I32, n)
+    else:
+        _dev(ctx_len, "ctx_len", _I32, 1)
+        if dropped is not None:
+            _dev(dropped, "dropped", _I32, 1)
+        if parent is not None:
+            _dev(parent, "parent", _I32, n)
+            if n > MAX_NODES:
+                raise DfvError(f"{n} tree nodes, at most {MAX_NODES}")
+    index = first.get_device()
+    q_out, k_out, v_out = (o if x is not None else None
+                           for x, o in ((q, q_out), (k, k_out), (v, v_out)))
+    _same_device(index, q, k, v, q_out, k_out, v_out, rope.turns, q_weight, k_weight, positions,
+                 ctx_len, dropped, parent, status)
+    _check(lib().dfv_qk_norm_rope(
+        n, heads[0], heads[1], d, _p(q), _p(k), _p(v),
+        DTYPE_F32 if first.dtype == torch.float32 else DTYPE_BF16, *strides,
+        _p(q_weight), _p(k_weight), -1.0 if eps is None else float(eps), rope.turns.data_ptr(),
+        rope.rot_dim, rope.interleaved, _p(positions), _p(parent), _p(ctx_len), _p(dropped),
+        _p(q_out), _p(k_out), _p(v_out), DTYPE_F32 if dst[0] == torch.float32 else DTYPE_BF16,
+        _p(status), _stream(stream, index)), "dfv_qk_norm_rope")
 
 
 def kv_commit(cache, accept_len, path, tree_k, tree_v, status=None, stream=None):

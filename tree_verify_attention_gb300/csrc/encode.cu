@@ -1,0 +1,349 @@
+// Queries, keys and values of a projection as the attention takes them: RMS
+// norm of each query and key head, the position rotation, the values carried
+// along, in one pass.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w
+//   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = pos * freq_i
+//
+// The kernel is bound by memory (each element is read once and written once)
+// and by latency for a few rows. A head is D / 16 lanes of a warp, each with
+// two chunks of eight elements, picked so that both elements of a rotated pair
+// are in one lane; the same lane then has the same eight pairs in every head
+// of the row, so their sines and cosines are computed once per row and stay in
+// registers. A warp works through the heads of a row; few rows are split over
+// more warps.
+//
+// Angles: pos * freq in 32 bits would be off by 2^-8 rad at position 131072.
+// The table holds turns per position as a 64-bit binary fraction, so the
+// integer product pos * turns, modulo 2^64, is the angle's fraction of a turn,
+// off by at most pos * 2^-65 of one; its upper 32 bits go to sincospi.
+
+#include "common.cuh"
+
+namespace dfv {
+
+constexpr int kEncWarps = 4;
+
+struct EncodeParams {
+  int n_rows, hq, hkv, rot, iters, splits, per_split;
+  const void *q, *k, *v;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+  const float *q_weight, *k_weight;
+  float eps;
+  const uint64_t* turns;
+  const int32_t *positions, *parent, *ctx_len, *dropped;
+  void *q_out, *k_out, *v_out;
+  uint32_t* status;
+};
+
+// Eight consecutive elements as float32.
+template <typename T, bool kVec> struct EncLoad;
+template <> struct EncLoad<__nv_bfloat16, true> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
+template <> struct EncLoad<float, true> {
+  float4 r[2];
+  __device__ __forceinline__ void load(const float* p) {
+    r[0] = reinterpret_cast<const float4*>(p)[0];
+    r[1] = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const float4& v = r[i >> 2];
+    return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+  }
+};
+// rows of any alignment, an element at a time
+template <typename T> struct EncLoad<T, false> {
+  float r[8];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = static_cast<float>(p[i]);
+  }
+  __device__ __forceinline__ float at(int i) const { return r[i]; }
+};
+
+__device__ __forceinline__ void enc_store(__nv_bfloat16* p, const float* y) {
+  uint4 o;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = o;
+}
+__device__ __forceinline__ void enc_store(float* p, const float* y) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+}
+
+// Depth of node `row`, by steps to the root (all lanes, same row).
+__device__ __forceinline__ int enc_depth(const EncodeParams& p, int row, int lane) {
+  int par[3];
+  bool bad = false;
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    const int i = lane + 32 * s;
+    par[s] = 0;
+    if (i >= 1 && i < p.n_rows) {
+      const int v = p.parent[i];
+      if (v < 0 || v >= i) bad = true;
+      else par[s] = v;
+    }
+  }
+  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) report(p.status, DFV_DEV_BAD_TREE);
+  int depth = 0;
+  for (int cur = row; cur > 0; ++depth) {   // par[i] < i: ends
+    const int a = __shfl_sync(0xFFFFFFFFu, par[0], cur & 31);
+    const int b = __shfl_sync(0xFFFFFFFFu, par[1], cur & 31);
+    const int c = __shfl_sync(0xFFFFFFFFu, par[2], cur & 31);
+    cur = cur < 32 ? a : cur < 64 ? b : c;
+  }
+  return depth;
+}
+
+template <typename TS, typename TD, int D, bool kVec>
+__global__ void __launch_bounds__(kEncWarps * 32)
+    encode_kernel(const __grid_constant__ EncodeParams p, int near) {
+  constexpr int kLanes = D / 16;         // lanes of a head
+  constexpr int kHeads = 32 / kLanes;    // heads of a warp at a time
+  constexpr int kAhead = sizeof(TS) == 2 ? 4 : 2;   // whose loads are in flight together
+  const int lane = threadIdx.x & 31;
+  const uint32_t task = blockIdx.x * kEncWarps + (threadIdx.x >> 5);   // below 2^27
+  const int row = static_cast<int>(task / static_cast<uint32_t>(p.splits));
+  grid_dep_wait();
+  grid_dep_launch_dependents();   // (after the wait: see common.cuh)
+  if (row >= p.n_rows) return;
+  const int64_t row64 = row;
+  const int it0 = (static_cast<int>(task) - row * p.splits) * p.per_split;
+  const int it1 = min(p.iters, it0 + p.per_split);
+  const int j = lane % kLanes;
+  const int rl = p.rot >> 4;             // lanes with rotated pairs
+  const bool turned = j < rl;
+  const int ca = turned && !near ? 8 * j : 16 * j;
+  const int cb = turned && !near ? 8 * (j + rl) : 16 * j + 8;
+
+  // element (head, dim 0) of the lane's head in iteration `it`, null behind the last
+  auto source = [&](int it) -> const TS* {
+    const int h = it * kHeads + lane / kLanes;
+    if (h < p.hq) return static_cast<const TS*>(p.q) + row * p.q_row + h * p.q_head;
+    if (h < p.hq + p.hkv)
+      return static_cast<const TS*>(p.k) + row * p.k_row + (h - p.hq) * p.k_head;
+    if (h < p.hq + 2 * p.hkv && p.v)
+      return static_cast<const TS*>(p.v) + row * p.v_row + (h - p.hq - p.hkv) * p.v_head;
+    return nullptr;
+  };
+  EncLoad<TS, kVec> xa[kAhead], xb[kAhead];
+  auto fetch = [&](int it) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const TS* src = it + u < it1 ? source(it + u) : nullptr;
+      if (src) {
+        xa[u].load(src + ca);
+        xb[u].load(src + cb);
+      }
+    }
+  };
+  fetch(it0);
+
+  int64_t pos;
+  if (p.positions) {
+    pos = p.positions[row];
+  } else {
+    pos = static_cast<int64_t>(*p.ctx_len) + (p.dropped ? *p.dropped : 0);
+    pos += p.parent ? enc_depth(p, row, lane) : row;
+  }
+  float cs[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    cs[e] = 1.0f;
+    sn[e] = 0.0f;
+    if (turned) {
+      const uint64_t t = static_cast<uint64_t>(pos) * p.turns[8 * j + e];
+      // the upper half as a signed fraction of a turn, in units of half a turn
+      sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &sn[e], &cs[e]);
+    }
+  }
+  const bool norm = p.eps >= 0.0f;
+
+  for (int it = it0; it < it1; it += kAhead) {
+    if (it != it0) fetch(it);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (it + u >= it1) break;
+      const int h = (it + u) * kHeads + lane / kLanes;
+      const bool on = source(it + u) != nullptr;
+      float a[8], b[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        a[e] = on ? xa[u].at(e) : 0.0f;
+        b[e] = on ? xb[u].at(e) : 0.0f;
+      }
+      const bool is_v = h >= p.hq + p.hkv;
+      if (norm) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(b[e], b[e], fmaf(a[e], a[e], ss));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        const float* w = h < p.hq ? p.q_weight : p.k_weight;
+        float wa[8], wb[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.0f;
+        if (w && on && !is_v) {
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(w + ca + e);
+            const float4 g = *reinterpret_cast<const float4*>(w + cb + e);
+            wa[e] = f.x, wa[e + 1] = f.y, wa[e + 2] = f.z, wa[e + 3] = f.w;
+            wb[e] = g.x, wb[e + 1] = g.y, wb[e + 2] = g.z, wb[e + 3] = g.w;
+          }
+        }
+        const float r = is_v ? 1.0f : 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+        // squares that leave float32 (or vanish in it where eps does not hide
+        // them): the head once more in 64 bits
+        const bool wide = !is_v && on && (!(ss <= 1e37f) || (ss < 1e-25f && p.eps < 1e-15f));
+        if (__any_sync(0xFFFFFFFFu, wide)) {
+          double s2 = 0.0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            s2 += static_cast<double>(a[e]) * a[e] + static_cast<double>(b[e]) * b[e];
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+          const double rd = 1.0 / sqrt(s2 / D + static_cast<double>(p.eps));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            a[e] = wide ? static_cast<float>(a[e] * rd) * wa[e] : a[e] * r * wa[e];
+            b[e] = wide ? static_cast<float>(b[e] * rd) * wb[e] : b[e] * r * wb[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            a[e] = a[e] * r * wa[e];
+            b[e] = b[e] * r * wb[e];
+          }
+        }
+      }
+      if (turned && !is_v) {
+        if (near) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a0 = a[2 * e], a1 = a[2 * e + 1], b0 = b[2 * e], b1 = b[2 * e + 1];
+            a[2 * e] = fmaf(a0, cs[e], -a1 * sn[e]);
+            a[2 * e + 1] = fmaf(a1, cs[e], a0 * sn[e]);
+            b[2 * e] = fmaf(b0, cs[4 + e], -b1 * sn[4 + e]);
+            b[2 * e + 1] = fmaf(b1, cs[4 + e], b0 * sn[4 + e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a0 = a[e], b0 = b[e];
+            a[e] = fmaf(a0, cs[e], -b0 * sn[e]);
+            b[e] = fmaf(b0, cs[e], a0 * sn[e]);
+          }
+        }
+      }
+      if (on) {
+        TD* dst = h < p.hq ? static_cast<TD*>(p.q_out) + (row64 * p.hq + h) * D
+                  : !is_v ? static_cast<TD*>(p.k_out) + (row64 * p.hkv + (h - p.hq)) * D
+                          : static_cast<TD*>(p.v_out) + (row64 * p.hkv + (h - p.hq - p.hkv)) * D;
+        enc_store(dst + ca, a);
+        enc_store(dst + cb, b);
+      }
+    }
+  }
+}
+
+template <typename TS, typename TD, int D>
+dfv_status encode_launch(EncodeParams p, bool near, cudaStream_t stream) {
+  const int heads = p.hq + (p.v ? 2 : 1) * p.hkv;
+  constexpr int kHeads = 32 / (D / 16);
+  p.iters = (heads + kHeads - 1) / kHeads;
+  // One warp a row where that fills the GPU (the sines are computed once for
+  // all of its heads); else rows are split until there are about 32 warps an SM.
+  const int64_t want = (static_cast<int64_t>(sm_count()) * 32 + p.n_rows - 1) / p.n_rows;
+  const int splits = static_cast<int>(want < p.iters ? want : p.iters);
+  p.per_split = (p.iters + splits - 1) / splits;
+  p.splits = (p.iters + p.per_split - 1) / p.per_split;
+  // 16-byte loads where every row starts on such a boundary
+  constexpr int64_t kE = 16 / sizeof(TS);
+  auto fits = [&](const void* x, int64_t sr, int64_t sh) {
+    return !x || (aligned(x, 16) && sr % kE == 0 && sh % kE == 0);
+  };
+  const bool vec = fits(p.q, p.q_row, p.q_head) && fits(p.k, p.k_row, p.k_head) &&
+                   fits(p.v, p.v_row, p.v_head);
+  cudaLaunchConfig_t cfg = {};
+  const int64_t tasks = static_cast<int64_t>(p.n_rows) * p.splits;
+  cfg.gridDim = dim3(static_cast<unsigned>((tasks + kEncWarps - 1) / kEncWarps));
+  cfg.blockDim = dim3(kEncWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e =
+      vec ? cudaLaunchKernelEx(&cfg, encode_kernel<TS, TD, D, true>, p, near ? 1 : 0)
+          : cudaLaunchKernelEx(&cfg, encode_kernel<TS, TD, D, false>, p, near ? 1 : 0);
+  return e == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
+}
+
+template <typename TS, typename TD>
+dfv_status encode_launch_d(const EncodeParams& p, int D, bool near, cudaStream_t stream) {
+  return D == 64    ? encode_launch<TS, TD, 64>(p, near, stream)
+         : D == 128 ? encode_launch<TS, TD, 128>(p, near, stream)
+                    : encode_launch<TS, TD, 256>(p, near, stream);
+}
+
+}  // namespace dfv
+
+extern "C" dfv_status dfv_qk_norm_rope(
+    int n_rows, int n_q_heads, int n_kv_heads, int head_dim, const void* q, const void* k,
+    const void* v, int src_dtype, int64_t q_stride_row, int64_t q_stride_head,
+    int64_t k_stride_row, int64_t k_stride_head, int64_t v_stride_row, int64_t v_stride_head,
+    const float* q_weight, const float* k_weight, float eps, const uint64_t* turns, int rot_dim,
+    int interleaved, const int32_t* positions, const int32_t* parent, const int32_t* ctx_len,
+    const int32_t* dropped, void* q_out, void* k_out, void* v_out, int dst_dtype,
+    uint32_t* status, dfv_stream_t stream) {
+  using namespace dfv;
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+      (src_dtype != DFV_DTYPE_F32 && src_dtype != DFV_DTYPE_BF16) ||
+      (dst_dtype != DFV_DTYPE_F32 && dst_dtype != DFV_DTYPE_BF16))
+    return DFV_ERR_UNSUPPORTED;
+  if (n_rows < 0 || n_rows > (1 << 26) || n_q_heads < 0 || n_kv_heads < 0 || n_q_heads > 1024 ||
+      n_kv_heads > 1024 || n_q_heads + n_kv_heads == 0 || rot_dim < 0 || rot_dim > head_dim ||
+      rot_dim % 16 != 0 || eps != eps || (parent && n_rows > kMaxNodes))
+    return DFV_ERR_INVALID;
+  if (n_rows == 0) return DFV_OK;
+  const size_t size = src_dtype == DFV_DTYPE_F32 ? 4 : 2;
+  if ((n_q_heads > 0 && (!q || !q_out)) || (n_kv_heads > 0 && (!k || !k_out)) ||
+      (v && (!v_out || n_kv_heads == 0)) || (rot_dim > 0 && !turns) ||
+      (!positions && !ctx_len) || (positions && (parent || ctx_len || dropped)) ||
+      (eps < 0.0f && (q_weight || k_weight)))
+    return DFV_ERR_INVALID;
+  if (!aligned(q, size) || !aligned(k, size) || !aligned(v, size) || !aligned(q_out, 16) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(q_weight, 16) ||
+      !aligned(k_weight, 16) || !aligned(turns, 8) || !aligned(positions, 4) ||
+      !aligned(parent, 4) || !aligned(ctx_len, 4) || !aligned(dropped, 4))
+    return DFV_ERR_INVALID;
+  const EncodeParams p = {n_rows, n_q_heads, n_kv_heads, rot_dim, 0, 0, 0,
+                          n_q_heads > 0 ? q : nullptr, n_kv_heads > 0 ? k : nullptr, v,
+                          q_stride_row, q_stride_head, k_stride_row, k_stride_head, v_stride_row,
+                          v_stride_head, q_weight, k_weight, eps, turns, positions, parent,
+                          ctx_len, dropped, q_out, k_out, v_out, status};
+  const bool near = interleaved != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (src_dtype == DFV_DTYPE_F32)
+    return dst_dtype == DFV_DTYPE_F32 ? encode_launch_d<float, float>(p, head_dim, near, s)
+                                      : encode_launch_d<float, __nv_bfloat16>(p, head_dim, near, s);
+  return dst_dtype == DFV_DTYPE_F32
+             ? encode_launch_d<__nv_bfloat16, float>(p, head_dim, near, s)
+             : encode_launch_d<__nv_bfloat16, __nv_bfloat16>(p, head_dim, near, s);
+}
