@@ -22,8 +22,9 @@
  * Beside them, for the same loop: a cache held in 8 bits with one scale per
  * 64 positions and head (dfv_kv8_append, dfv_kv8_commit, dfv_kv8_read,
  * dfv_kv8_attn), dfv_token_logprobs, log probabilities of given tokens, and
- * what comes before a step: dfv_qk_norm_rope, a projection's queries and keys
- * normed and rotated to the tree's positions.
+ * what comes before and after a step: dfv_qk_norm_rope, a projection's queries
+ * and keys normed and rotated to the tree's positions; dfv_sample and
+ * dfv_sample_accept, tokens drawn from logits and the walk along them.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -93,6 +94,8 @@ typedef enum dfv_status {
 #define DFV_DEV_TIMEOUT 0x20u  /* a bounded wait gave up; outputs undefined   */
 #define DFV_DEV_NONFINITE 0x40u /* a K/V value was infinite, NaN or >= 2^40  */
 #define DFV_DEV_BAD_TOKEN 0x80u /* a token outside the vocabulary            */
+#define DFV_DEV_BAD_SAMPLING 0x100u /* a row's sampling parameters or random  */
+                               /* number are NaN or out of range: token -1   */
 /* Every wait of a kernel (on a copy, an MMA, or another CTA of the step)
  * gives up after 100 ms of the GPU's global timer and sets DFV_DEV_TIMEOUT;
  * the kernel then skips what depended on the wait (a walker that timed out
@@ -541,6 +544,68 @@ dfv_status dfv_qk_norm_rope(int n_rows, int n_q_heads, int n_kv_heads, int head_
                             const int32_t* ctx_len, const int32_t* dropped, void* q_out,
                             void* k_out, void* v_out, int dst_dtype, uint32_t* status,
                             dfv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dfv_sample -- a token drawn from each row of logits x, from a given random
+ * number u in [0, 1):
+ *
+ *   w_i = exp((x_i - max x) / temperature)
+ *   top-k  the top_k largest x (ties to the lowest index); Z = sum of their w
+ *   top-p  of these, from the largest on, the fewest whose w reach top_p * Z
+ *   min-p  of these, the ones with w_i >= max(min_p, 2^-40)
+ *   token[i]  the first index, in index order, at which the running sum of the
+ *          kept w exceeds u times their total M;  logprob[i] = ln(w / M)
+ *
+ * Weights are exact to about 2^-31 and summed as integers, so a result does
+ * not depend on how the work is split, and a border between two tokens is off
+ * by about 2^-31 of the total. logprob is ln(w / M) to f32.
+ *
+ * temperature 0 (below 2^-100): the lowest index of the maximum, logprob 0.
+ * top_k <= 0 or >= vocab, top_p >= 1, min_p <= 0: off; top_p <= 0 keeps the
+ * most likely token. A temperature that is negative, infinite or NaN, a NaN in
+ * top_p or min_p, a u outside [0, 1): token -1, logprob NaN and
+ * DFV_DEV_BAD_SAMPLING. A row that holds a NaN or +inf, or nothing but -inf:
+ * token -1, logprob NaN and DFV_DEV_NONFINITE.
+ *
+ *   vocab      up to 2^19
+ *   logits     device f32 or bf16 (logits_dtype), row i at logits + i *
+ *              stride_row elements, any alignment of the type
+ *   uniform    device f32 [n_rows]
+ *   sampling   read by the host during the call: device arrays [n_rows] of
+ *              each row's own parameters, or NULL and one for all rows
+ *   token      device int32 [n_rows];  logprob device f32 [n_rows] or NULL
+ * One launch, no workspace.
+ * ---------------------------------------------------------------------- */
+typedef struct dfv_sampling {
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p;
+  float temperature_all;
+  int32_t top_k_all;
+  float top_p_all, min_p_all;
+} dfv_sampling;
+
+dfv_status dfv_sample(int n_rows, int vocab, int logits_dtype, const void* logits,
+                      int64_t stride_row, const float* uniform, const dfv_sampling* sampling,
+                      int32_t* token, float* logprob, uint32_t* status, dfv_stream_t stream);
+
+/* dfv_sample_accept -- dfv_greedy_accept with drawn tokens: target[i] is drawn
+ * from node i's logits, and the walk follows the lowest-index child whose
+ * token is its parent's target. With u independent of the draft the emitted
+ * tokens are distributed as if the target model had drawn them one by one.
+ * Other arguments and results as there; the workspace
+ * (dfv_sample_accept_workspace_bytes, 256-byte aligned) must be zeroed once
+ * before its first use, every call leaves it zeroed again, and calls sharing
+ * one must not overlap. A node whose row has no token (-1) ends the walk. */
+size_t dfv_sample_accept_workspace_bytes(int n_nodes, int vocab);
+
+dfv_status dfv_sample_accept(int n_nodes, int vocab, int logits_dtype, const void* logits,
+                             int64_t stride_row, const float* uniform,
+                             const dfv_sampling* sampling, const int32_t* parent,
+                             const int32_t* tokens, int32_t* target, float* logprob,
+                             int32_t* accept_len, int32_t* path, int32_t* out_tokens,
+                             void* workspace, size_t workspace_bytes, uint32_t* status,
+                             dfv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -35,6 +35,7 @@ Module map:
 * ``int8``      -- the 8-bit cache with a scale per 64 positions and head.
 * ``logprobs``  -- log probabilities of given tokens, entropy, alternatives.
 * ``encode``    -- norm and rotation of queries and keys.
+* ``sampling``  -- a token drawn from a row of logits, and the walk along drawn tokens.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against brute force, closed forms, invariants or library routines. Parity
@@ -43,4 +44,4 @@ example and no kernel output.
 """
 
 from . import (q4_0, f16, tree, attention, accept, commit, step, int8, logprobs,  # noqa: F401
-               encode)
+               encode, sampling)

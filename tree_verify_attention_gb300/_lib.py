@@ -22,6 +22,14 @@ class Kv8CacheStruct(C.Structure):
                 ("k_scale", _vp), ("v_scale", _vp), ("k_tail", _vp), ("v_tail", _vp)]
 
 
+class SamplingStruct(C.Structure):
+    """dfv_sampling of include/dfv.h."""
+
+    _fields_ = [("temperature", _vp), ("top_k", _vp), ("top_p", _vp), ("min_p", _vp),
+                ("temperature_all", _f32), ("top_k_all", C.c_int32), ("top_p_all", _f32),
+                ("min_p_all", _f32)]
+
+
 # name -> (restype, argtypes), in the order of include/dfv.h
 SIGNATURES = {
     "dfv_status_string": (C.c_char_p, [_i32]),
@@ -47,6 +55,9 @@ SIGNATURES = {
     "dfv_token_logprobs": (_i32, [_i32, _i32, _i32, _vp, _i64, _vp, _i32] + [_vp] * 6),
     "dfv_qk_norm_rope": (_i32, [_i32] * 4 + [_vp] * 3 + [_i32] + [_i64] * 6 + [_vp, _vp, _f32, _vp,
                                 _i32, _i32] + [_vp] * 7 + [_i32, _vp, _vp]),
+    "dfv_sample": (_i32, [_i32, _i32, _i32, _vp, _i64] + [_vp] * 6),
+    "dfv_sample_accept_workspace_bytes": (_sz, [_i32, _i32]),
+    "dfv_sample_accept": (_i32, [_i32, _i32, _i32, _vp, _i64] + [_vp] * 10 + [_sz, _vp, _vp]),
 }
 
 _lib = None

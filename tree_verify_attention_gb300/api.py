@@ -30,6 +30,7 @@ DEV_BAD_PATH = 0x10
 DEV_TIMEOUT = 0x20
 DEV_NONFINITE = 0x40
 DEV_BAD_TOKEN = 0x80
+DEV_BAD_SAMPLING = 0x100
 
 KV8_BLOCK = 64       # positions that share a scale in an Int8Cache
 MAX_TOP = 32         # alternatives token_logprobs can return
@@ -430,6 +431,93 @@ def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logp
         _p(top_ids), _p(top_logprobs), _p(status), _stream(stream)), "dfv_token_logprobs")
 
 
+class Sampling:
+    """How tokens are drawn: ``temperature``, ``top_k`` (0: off), ``top_p`` (1:
+    off) and ``min_p`` (0: off), in this order; each a number for all rows, or a
+    device tensor [N] (f32, ``top_k`` int32) with each row's own. Tensors are
+    read when a call runs, so their values may change between calls."""
+
+    def __init__(self, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+        self.tensors = []
+        values = []
+        for x, name, dt in ((temperature, "temperature", _F32), (top_k, "top_k", _I32),
+                            (top_p, "top_p", _F32), (min_p, "min_p", _F32)):
+            if isinstance(x, torch.Tensor):
+                self.tensors.append((_dev(x, name, dt), name))
+                values.append((x.data_ptr(), 0))
+                continue
+            if x != x or (name == "temperature" and not 0 <= x < math.inf):
+                raise DfvError(f"{name} {x} is out of range")
+            values.append((None, max(0, min(int(x), 2 ** 31 - 1)) if name == "top_k"
+                           else float(x)))
+        self._struct = _lib.SamplingStruct(*(v[0] for v in values), *(v[1] for v in values))
+        self.handle = ctypes.addressof(self._struct)
+
+    def check(self, n, index):
+        """That the tensors serve ``n`` rows on device ``index``."""
+        for t, name in self.tensors:
+            if t.numel() < n:
+                raise DfvError(f"{name} holds {t.numel()} elements, needs {n}")
+            if t.get_device() != index:
+                raise DfvError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _sample_args(logits, uniform, sampling, token, logprob, status):
+    if logits is None or not logits.is_cuda or logits.dim() != 2 or logits.dtype not in _ROWS:
+        raise DfvError("logits must be a CUDA f32 or bf16 tensor [N, V]")
+    n, vocab = logits.shape
+    if n and vocab > 1 and logits.stride(1) != 1:
+        raise DfvError("logits rows must be contiguous")
+    _dev(uniform, "uniform", _F32, n)
+    _dev(token, "token", _I32, n)
+    if logprob is not None:
+        _dev(logprob, "logprob", _F32, n)
+    if not isinstance(sampling, Sampling):
+        raise DfvError("sampling must be a Sampling")
+    index = logits.get_device()
+    sampling.check(n, index)
+    _same_device(index, uniform, token, logprob, status)
+    return (n, vocab, DTYPE_F32 if logits.dtype == torch.float32 else DTYPE_BF16,
+            logits.data_ptr(), logits.stride(0) if n > 1 else vocab, uniform.data_ptr(),
+            sampling.handle), index
+
+
+def sample_tokens(logits, uniform, sampling, token, logprob=None, status=None, stream=None):
+    """Draw a token from each row of ``logits`` [N, V] (f32 or bf16, rows may
+    be strided) by ``sampling`` (:class:`Sampling`) and the random numbers
+    ``uniform`` [N] in [0, 1) into ``token`` [N] (int32), and its log probability
+    among the tokens that could have been drawn into ``logprob`` [N]. The first
+    token in index order is taken at which the running sum of the kept
+    probabilities exceeds the random number. A row without a distribution gets
+    -1 and NaN (DEV_NONFINITE, DEV_BAD_SAMPLING)."""
+    args, index = _sample_args(logits, uniform, sampling, token, logprob, status)
+    _check(lib().dfv_sample(*args, token.data_ptr(), _p(logprob), _p(status),
+                            _stream(stream, index)), "dfv_sample")
+
+
+def sample_accept_workspace_bytes(n_nodes, vocab):
+    return lib().dfv_sample_accept_workspace_bytes(n_nodes, vocab)
+
+
+def sample_accept(logits, uniform, sampling, parent, tokens, target, accept_len, path, out_tokens,
+                  ws, logprob=None, status=None, stream=None):
+    """:func:`greedy_accept` with drawn tokens: ``target`` [N] is drawn from
+    each node's logits as by :func:`sample_tokens`, and the walk follows the
+    children whose ``tokens`` are their parents' targets."""
+    args, index = _sample_args(logits, uniform, sampling, target, logprob, status)
+    n = args[0]
+    for t, nm in ((parent, "parent"), (tokens, "tokens"), (path, "path"),
+                  (out_tokens, "out_tokens")):
+        _dev(t, nm, _I32, n)
+    _dev(accept_len, "accept_len", _I32, 1)
+    _dev(ws, "workspace", (torch.uint8,))
+    _same_device(index, parent, tokens, accept_len, path, out_tokens, ws)
+    _check(lib().dfv_sample_accept(
+        *args, parent.data_ptr(), tokens.data_ptr(), target.data_ptr(), _p(logprob),
+        accept_len.data_ptr(), path.data_ptr(), out_tokens.data_ptr(), ws.data_ptr(), ws.numel(),
+        _p(status), _stream(stream, index)), "dfv_sample_accept")
+
+
 class Rope:
     """Frequencies of the position rotation of :func:`qk_norm_rope`: the first
     ``rot_dim`` dims of a head (all by default) turn in pairs, pair i by
@@ -548,6 +636,11 @@ def kv_commit(cache, accept_len, path, tree_k, tree_v, status=None, stream=None)
         cache.k.data_ptr(), cache.v.data_ptr(), _p(status), _stream(stream)), "dfv_kv_commit")
 
 
+def _as_bf16(logits):
+    """Logits given as bf16 bit patterns in int16, as bf16."""
+    return logits if logits.dtype != torch.int16 else logits.view(torch.bfloat16)
+
+
 class VerifyStep:
     """Outputs and workspace of the verify step for one problem shape; call
     :meth:`run` once per step. All buffers live on the device.
@@ -563,10 +656,17 @@ class VerifyStep:
     ``top=K`` also gives, per node, the log probability of its argmax token
     (``logprob``; the emitted tokens are the path's), the entropy of its
     logits (``entropy``) and its K most probable tokens (``top_ids``,
-    ``top_logprobs``); ``top=0`` the first two alone."""
+    ``top_logprobs``); ``top=0`` the first two alone.
+
+    ``sampling`` (a :class:`Sampling`) draws each node's token instead of taking
+    the argmax (:func:`sample_accept`; ``run`` then takes ``uniform``, N random
+    numbers): ``argmax`` holds the drawn tokens, ``draw_logprob`` their log
+    probabilities. The step is then attention, draw with walk, and commit,
+    launched one after the other, over any cache (not pipelined)."""
 
     def __init__(self, n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity, vocab,
-                 max_depth=16, device="cuda", pipelined=False, fmt="q4_0", top=None):
+                 max_depth=16, device="cuda", pipelined=False, fmt="q4_0", top=None,
+                 sampling=None):
         if top is not None and not 0 <= top <= min(MAX_TOP, vocab):
             raise DfvError(f"top={top} alternatives, at most {min(MAX_TOP, vocab)}")
         self.shape = (n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity, vocab)
@@ -584,15 +684,29 @@ class VerifyStep:
             _fmt_code(fmt)
         elif pipelined:
             raise DfvError("pipelined is not available with an Int8Cache")
+        self.sampling = sampling
+        if sampling is not None:
+            if pipelined:
+                raise DfvError("pipelined is not available with sampling")
+            if not isinstance(sampling, Sampling):
+                raise DfvError("sampling must be a Sampling")
+            self.draw_logprob = torch.empty(n_nodes, dtype=torch.float32, device=dev)
         if self.int8:
             nb = int8_attn_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window,
                                            capacity)
+        elif sampling is not None:
+            nb = attn_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity)
         else:
             nb = step_workspace_bytes(n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity,
                                       vocab)
         if nb == 0:
             raise DfvError(f"unsupported step shape {self.shape}")
-        if self.int8:
+        if sampling is not None:
+            accept = sample_accept_workspace_bytes(n_nodes, vocab)
+            if accept == 0:
+                raise DfvError(f"unsupported step shape {self.shape}")
+            self.accept_ws = workspace(accept, device=dev)
+        elif self.int8:
             self.accept_ws = workspace(accept_workspace_bytes(n_nodes, vocab), device=dev)
         self.top = top
         if top is not None:
@@ -607,13 +721,15 @@ class VerifyStep:
         self._turn = 0
 
     def run(self, cache, q, tree_k, tree_v, parent, tokens, logits, scale=0.0, stream=None,
-            tree_as_cache=False):
+            tree_as_cache=False, uniform=None):
         n, hq, hkv, d, window, cap, vocab = self.shape
         if cache.capacity != cap:
             raise DfvError("cache capacity differs from the planned one")
         if isinstance(cache, Int8Cache) != self.int8:
             raise DfvError("the step is planned for another kind of cache")
-        if self.int8:
+        if (uniform is None) != (self.sampling is None):
+            raise DfvError("uniform goes with a step planned with sampling, and only with one")
+        if self.int8 or self.sampling is not None:
             for t, name, shape in ((q, "q", (n, hq, d)), (tree_k, "tree_k", (n, hkv, d)),
                                    (tree_v, "tree_v", (n, hkv, d)), (logits, "logits", (n, vocab))):
                 if tuple(t.shape) != shape:
@@ -622,11 +738,22 @@ class VerifyStep:
             _dev(parent, "parent", _I32, n)
             _dev(tokens, "tokens", _I32, n)
             _dev(logits, "logits", (torch.float32,) + _BF16)
+            if self.sampling is not None:
+                # before the first launch: what the draw would refuse
+                _dev(uniform, "uniform", _F32, n)
+                _same_device(logits.get_device(), uniform)
+                self.sampling.check(n, logits.get_device())
             tree_verify_attn(cache, q, tree_k, tree_v, parent, window, self.max_depth, self.out,
                              self.lse, self.ws, scale=scale, status=self.status, stream=stream,
                              tree_as_cache=tree_as_cache)
-            greedy_accept(logits, parent, tokens, self.argmax, self.accept_len, self.path,
-                          self.out_tokens, self.accept_ws, status=self.status, stream=stream)
+            if self.sampling is not None:
+                sample_accept(_as_bf16(logits), uniform, self.sampling, parent, tokens,
+                              self.argmax, self.accept_len, self.path, self.out_tokens,
+                              self.accept_ws, logprob=self.draw_logprob, status=self.status,
+                              stream=stream)
+            else:
+                greedy_accept(logits, parent, tokens, self.argmax, self.accept_len, self.path,
+                              self.out_tokens, self.accept_ws, status=self.status, stream=stream)
             kv_commit(cache, self.accept_len, self.path, tree_k, tree_v, status=self.status,
                       stream=stream)
             self._logprobs(logits, stream)
@@ -658,6 +785,5 @@ class VerifyStep:
         # a step takes any shape of n * vocab logits
         n, vocab = self.shape[0], self.shape[-1]
         logits = logits.view(-1)[:n * vocab].view(n, vocab)
-        token_logprobs(logits if logits.dtype != torch.int16 else logits.view(torch.bfloat16),
-                       self.argmax, self.logprob, self.entropy, self.top_ids, self.top_logprobs,
+        token_logprobs(_as_bf16(logits), self.argmax, self.logprob, self.entropy, self.top_ids, self.top_logprobs,
                        status=self.status, stream=stream)
