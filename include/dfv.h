@@ -24,7 +24,10 @@
  * dfv_kv8_attn), dfv_token_logprobs, log probabilities of given tokens, and
  * what comes before and after a step: dfv_qk_norm_rope, a projection's queries
  * and keys normed and rotated to the tree's positions; dfv_sample and
- * dfv_sample_accept, tokens drawn from logits and the walk along them.
+ * dfv_sample_accept, tokens drawn from logits and the walk along them; and for
+ * a bounded cache dfv_kv_weights, the attention weight its keys receive,
+ * dfv_kv_evict, the rows that received the most moved to another cache, and
+ * dfv_kv_read_rows, its rows as values.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -606,6 +609,85 @@ dfv_status dfv_sample_accept(int n_nodes, int vocab, int logits_dtype, const voi
                              int32_t* accept_len, int32_t* path, int32_t* out_tokens,
                              void* workspace, size_t workspace_bytes, uint32_t* status,
                              dfv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dfv_kv_weights -- the attention weight that each cached key receives from
+ * the last n committed rows, added to what it had:
+ *
+ *   weights[h][j] = decay * prev[h][j]
+ *                   + sum over rows s that see j and query heads hq of group h
+ *                     of exp(scale * q[s][hq] . k[h][j] - lse[s][hq])
+ *
+ * for every j < C = *ctx_len; the n rows stand at the last n positions, row s at
+ * C - n + s, and see j iff j <= C - n + s and (window == 0 or C - n + s - j <
+ * window). Keys at or behind C - n are new: they have no `prev`. So after a step
+ * has committed the accepted nodes, their queries and lse give every key its
+ * weight, the new ones included. Query head hq belongs to KV head hq / (Hq / Hkv).
+ *
+ *   n_rows       rows of q and lse, 1..65536
+ *   kv_format    DFV_KV_Q4_0 or DFV_KV_F16
+ *   q            device bf16 [n_rows][Hq][D], 16-byte aligned, of any finite
+ *                magnitude;  lse device f32 [n_rows][Hq] (natural log, what
+ *                the attention gave for these rows). A row of a head whose q or
+ *                lse is not finite counts for nothing (DFV_DEV_NONFINITE)
+ *   path, accept_len  device int32 as dfv_verify_step leaves them: n = *accept_len
+ *                and row s is node path[s]; each may be NULL (row s itself, n =
+ *                n_rows). An entry outside [0, n_rows) counts for nothing, an
+ *                accept_len outside is clamped (DFV_DEV_BAD_PATH)
+ *   scale        <= 0 means 1/sqrt(D)
+ *   prev         device f32 [Hkv][cache_capacity], or NULL (zeros); may be
+ *                `weights` itself
+ *   weights      device f32 [Hkv][cache_capacity]; entries from C on are left
+ *                as they were
+ * Products are exact, sums f32 in a fixed order: a weight is off by about 2^-19
+ * of itself at |lse| of 30. Cached K values must stay within the binary16 range.
+ * One launch, no workspace.
+ * ---------------------------------------------------------------------- */
+dfv_status dfv_kv_weights(int n_rows, int n_q_heads, int n_kv_heads, int head_dim, int window,
+                          int kv_format, int cache_capacity, const int32_t* ctx_len,
+                          const void* k_cache, const void* q, const float* lse,
+                          const int32_t* path, const int32_t* accept_len, float scale,
+                          float decay, const float* prev, float* weights, uint32_t* status,
+                          dfv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dfv_kv_evict -- keep the rows of a cache whose keys received the most weight.
+ *
+ * Of C = *ctx_len rows each KV head keeps min(C, keep): the first `sinks`, the
+ * last `recent`, and of the others the ones with the largest weights (ties to
+ * the lowest position, -0.0 equals +0.0, a NaN is below everything). They move,
+ * bit for bit and in their order, to rows 0.. of another cache of the same
+ * format; rows of it behind them are left as they were. Each head keeps its
+ * own rows, so cache rows no longer stand at their positions: *dst_dropped =
+ * *dropped + C - n is how far they lag, which dfv_qk_norm_rope adds for the
+ * next nodes. (A sliding window counts cache rows, not positions, then.)
+ *
+ *   dropped      device int32[1] of the source or NULL (0)
+ *   weights      device f32 [Hkv][cache_capacity]
+ *   keep         1..dst_capacity;  sinks, recent >= 0, together at most keep
+ *   k_dst, v_dst the other cache; must not overlap the source
+ *   dst_ctx_len  device int32[1], written: n = min(C, keep)
+ *   dst_dropped  device int32[1] or NULL
+ *   weights_out  device f32 [Hkv][dst_capacity] or NULL: the kept rows' weights
+ *   kept         device int32 [Hkv][keep]: the kept positions, ascending (the
+ *                first n of each head are written)
+ * Two launches, no workspace (`kept` passes from one to the other).
+ * ---------------------------------------------------------------------- */
+dfv_status dfv_kv_evict(int n_kv_heads, int head_dim, int kv_format, int cache_capacity,
+                        const int32_t* ctx_len, const int32_t* dropped, const void* k_cache,
+                        const void* v_cache, const float* weights, int keep, int sinks,
+                        int recent, int dst_capacity, void* k_dst, void* v_dst,
+                        int32_t* dst_ctx_len, int32_t* dst_dropped, float* weights_out,
+                        int32_t* kept, uint32_t* status, dfv_stream_t stream);
+
+/* dfv_kv_read_rows -- cache rows [pos0, pos0 + n_rows) of every KV head as
+ * values (the counterpart of dfv_kv_quantize_rows; ctx_len plays no part).
+ *   k_dst, v_dst  device f32 or bf16 (dst_dtype, nearest even); element (row r,
+ *                 head h, dim c) at dst[r * stride_row + h * stride_head + c] */
+dfv_status dfv_kv_read_rows(int n_kv_heads, int head_dim, int kv_format, int cache_capacity,
+                            int pos0, int n_rows, const void* k_cache, const void* v_cache,
+                            void* k_dst, void* v_dst, int dst_dtype, int64_t stride_row,
+                            int64_t stride_head, dfv_stream_t stream);
 
 #ifdef __cplusplus
 }

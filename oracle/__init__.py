@@ -36,6 +36,7 @@ Module map:
 * ``logprobs``  -- log probabilities of given tokens, entropy, alternatives.
 * ``encode``    -- norm and rotation of queries and keys.
 * ``sampling``  -- a token drawn from a row of logits, and the walk along drawn tokens.
+* ``eviction``  -- weights that cached keys receive, and the rows kept by them.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against brute force, closed forms, invariants or library routines. Parity
@@ -44,4 +45,4 @@ example and no kernel output.
 """
 
 from . import (q4_0, f16, tree, attention, accept, commit, step, int8, logprobs,  # noqa: F401
-               encode, sampling)
+               encode, sampling, eviction)

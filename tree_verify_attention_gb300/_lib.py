@@ -57,6 +57,9 @@ SIGNATURES = {
                                 _i32, _i32] + [_vp] * 7 + [_i32, _vp, _vp]),
     "dfv_sample": (_i32, [_i32, _i32, _i32, _vp, _i64] + [_vp] * 6),
     "dfv_sample_accept_workspace_bytes": (_sz, [_i32, _i32]),
+    "dfv_kv_weights": (_i32, [_i32] * 7 + [_vp] * 6 + [_f32, _f32] + [_vp] * 4),
+    "dfv_kv_evict": (_i32, [_i32] * 4 + [_vp] * 5 + [_i32] * 4 + [_vp] * 8),
+    "dfv_kv_read_rows": (_i32, [_i32] * 6 + [_vp] * 4 + [_i32, _i64, _i64, _vp]),
     "dfv_sample_accept": (_i32, [_i32, _i32, _i32, _vp, _i64] + [_vp] * 10 + [_sz, _vp, _vp]),
 }
 

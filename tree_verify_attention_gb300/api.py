@@ -101,8 +101,10 @@ def _fmt_code(fmt):
 
 class KVCache:
     """Device KV cache of one sequence in format ``fmt`` ("q4_0" or "f16"):
-    K and V byte tensors [Hkv, capacity, row bytes] and the committed length
-    (device int32)."""
+    K and V byte tensors [Hkv, capacity, row bytes], the committed length
+    (device int32), and ``dropped``, the number of positions by which its rows
+    lie below their place in the sequence (device int32; 0 until
+    :func:`kv_evict` has moved rows into it)."""
 
     def __init__(self, n_kv_heads, head_dim, capacity, device="cuda", fmt="q4_0"):
         self.n_kv_heads, self.head_dim, self.capacity = n_kv_heads, head_dim, capacity
@@ -112,6 +114,7 @@ class KVCache:
         self.k = torch.zeros(shape, dtype=torch.uint8, device=device)
         self.v = torch.zeros(shape, dtype=torch.uint8, device=device)
         self.ctx_len = torch.zeros(1, dtype=torch.int32, device=device)
+        self.dropped = torch.zeros(1, dtype=torch.int32, device=device)
 
     def fill(self, k_rows, v_rows, pos0=0, stream=None):
         """Encode float rows [Hkv, n, D] (f32 or bf16) into positions
@@ -121,6 +124,25 @@ class KVCache:
             kv_quantize_rows(dst, src, pos0, self.n_kv_heads, self.head_dim, self.capacity,
                              head_major=True, stream=stream, fmt=self.fmt)
         self.ctx_len.fill_(pos0 + n)
+
+    def read(self, pos0, n, k_out, v_out, head_major=False, stream=None):
+        """The values of rows [pos0, pos0 + n) into k_out and v_out, [n, Hkv,
+        D] (or [Hkv, n, D]) f32 or bf16 with equal strides."""
+        h, d = self.n_kv_heads, self.head_dim
+        r, hd = (1, 0) if head_major else (0, 1)
+        shape = (h, n, d) if head_major else (n, h, d)
+        if not 0 <= pos0 <= pos0 + n <= self.capacity:
+            raise DfvError(f"rows [{pos0}, {pos0 + n}) are outside [0, {self.capacity})")
+        st = _float_rows(k_out, "k_out", shape)
+        if _float_rows(v_out, "v_out", shape, (k_out.dtype,)) != st:
+            raise DfvError("k_out and v_out must have the same strides")
+        index = self.k.get_device()
+        _same_device(index, k_out, v_out)
+        _check(lib().dfv_kv_read_rows(
+            h, d, self.kv_format, self.capacity, pos0, n, self.k.data_ptr(), self.v.data_ptr(),
+            k_out.data_ptr(), v_out.data_ptr(),
+            DTYPE_F32 if k_out.dtype == torch.float32 else DTYPE_BF16, st[r], st[hd],
+            _stream(stream, index)), "dfv_kv_read_rows")
 
 
 class Q4Cache(KVCache):
@@ -429,6 +451,93 @@ def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logp
         n, vocab, DTYPE_F32 if logits.dtype == torch.float32 else DTYPE_BF16, logits.data_ptr(),
         logits.stride(0) if n > 1 else vocab, _p(tokens), top, _p(logprob), _p(entropy),
         _p(top_ids), _p(top_logprobs), _p(status), _stream(stream)), "dfv_token_logprobs")
+
+
+def _kv_cache(cache, name):
+    if not isinstance(cache, KVCache):
+        raise DfvError(f"{name} must be a KVCache (Q4_0 or F16)")
+
+
+def kv_weights(cache, q, lse, weights, prev=None, decay=1.0, path=None, accept_len=None, window=0,
+               scale=0.0, status=None, stream=None):
+    """The attention weight that each key of ``cache`` (a KVCache) receives
+    from its last committed rows, into ``weights`` [Hkv, capacity] (f32):
+    ``decay * prev`` (zero without, and for the new rows) plus, over the rows
+    that see the key and the query heads of its group, exp(scale q . k - lse).
+    ``prev`` may be ``weights`` itself.
+
+    ``q`` [N, Hq, D] (bf16) and ``lse`` [N, Hq] are the rows' queries and what
+    the attention gave for them; they stand at the last N positions, or, with a
+    step's ``path`` and ``accept_len``, its accepted nodes at the last
+    ``accept_len`` ones: call it after the commit."""
+    _kv_cache(cache, "cache")
+    _dev(q, "q", _BF16)
+    if q.dim() != 3:
+        raise DfvError("q must be [N, Hq, D]")
+    n, hq, d = q.shape
+    h, cap = cache.n_kv_heads, cache.capacity
+    if d != cache.head_dim:
+        raise DfvError(f"q has head_dim {d}, the cache {cache.head_dim}")
+    _dev(lse, "lse", _F32, n * hq)
+    for t, name in ((weights, "weights"), (prev, "prev")):
+        if t is None and name == "prev":
+            continue
+        _dev(t, name, _F32)
+        if tuple(t.shape) != (h, cap):
+            raise DfvError(f"{name} has shape {tuple(t.shape)}, expected {(h, cap)}")
+    if path is not None:
+        _dev(path, "path", _I32, n)
+    if accept_len is not None:
+        _dev(accept_len, "accept_len", _I32, 1)
+    index = q.get_device()
+    _same_device(index, cache.k, lse, weights, prev, path, accept_len, status)
+    _check(lib().dfv_kv_weights(
+        n, hq, h, d, window, cache.kv_format, cap, cache.ctx_len.data_ptr(), cache.k.data_ptr(),
+        q.data_ptr(), lse.data_ptr(), _p(path), _p(accept_len), float(scale), float(decay),
+        _p(prev), weights.data_ptr(), _p(status), _stream(stream, index)), "dfv_kv_weights")
+
+
+def kv_evict(cache, weights, into, kept, sinks=0, recent=0, weights_out=None, status=None,
+             stream=None):
+    """Move the rows of ``cache`` whose keys have the largest ``weights`` [Hkv,
+    capacity] into ``into``, another KVCache of the same heads and format: of
+    each head at most K rows, K the width of ``kept`` [Hkv, K] (int32), which
+    receives their positions: the first ``sinks``, the last ``recent``, the best
+    of the others (ties to the lowest position), in their order. ``into``'s length
+    and ``dropped`` follow, and ``weights_out`` [Hkv, into.capacity] receives
+    the kept rows' weights."""
+    _kv_cache(cache, "cache")
+    _kv_cache(into, "into")
+    h, d = cache.n_kv_heads, cache.head_dim
+    if (into.n_kv_heads, into.head_dim, into.fmt) != (h, d, cache.fmt):
+        raise DfvError("into must be a cache of the same heads and format")
+    if into is cache or into.k.data_ptr() == cache.k.data_ptr():
+        raise DfvError("into must be another cache")
+    _dev(weights, "weights", _F32)
+    if tuple(weights.shape) != (h, cache.capacity):
+        raise DfvError(f"weights has shape {tuple(weights.shape)}, expected "
+                       f"{(h, cache.capacity)}")
+    _dev(kept, "kept", _I32)
+    if kept.dim() != 2 or kept.shape[0] != h or not 1 <= kept.shape[1] <= into.capacity:
+        raise DfvError(f"kept must be [{h}, K], K in [1, {into.capacity}]")
+    keep = kept.shape[1]
+    if sinks < 0 or recent < 0 or sinks + recent > keep:
+        raise DfvError(f"{sinks} first and {recent} last rows of {keep}")
+    if weights_out is not None:
+        _dev(weights_out, "weights_out", _F32)
+        if tuple(weights_out.shape) != (h, into.capacity):
+            raise DfvError(f"weights_out has shape {tuple(weights_out.shape)}, expected "
+                           f"{(h, into.capacity)}")
+        if weights_out.data_ptr() == weights.data_ptr():
+            raise DfvError("weights_out must not be weights")
+    index = cache.k.get_device()
+    _same_device(index, into.k, weights, kept, weights_out, status)
+    _check(lib().dfv_kv_evict(
+        h, d, cache.kv_format, cache.capacity, cache.ctx_len.data_ptr(), cache.dropped.data_ptr(),
+        cache.k.data_ptr(), cache.v.data_ptr(), weights.data_ptr(), keep, sinks, recent,
+        into.capacity, into.k.data_ptr(), into.v.data_ptr(), into.ctx_len.data_ptr(),
+        into.dropped.data_ptr(), _p(weights_out), kept.data_ptr(), _p(status),
+        _stream(stream, index)), "dfv_kv_evict")
 
 
 class Sampling:

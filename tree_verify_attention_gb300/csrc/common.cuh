@@ -133,6 +133,24 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   return wait_bounded([&]() { return mbar_try_wait(bar, parity); });
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Bounded wait that also gives up when another role has.
+static __device__ __noinline__ bool role_wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  bool there = false;
+  const bool ended = wait_bounded([&]() {
+    there = mbar_try_wait(bar, parity);
+    return there || *dead;
+  });
+  if (!ended) *dead = 1;
+  return there;
+}
+__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  return mbar_try_wait(bar, parity) || role_wait_slow(bar, parity, dead);
+}
+
 // 1-D bulk copy global -> shared through the TMA engine, completing
 // `bytes` of transaction count on `bar`. dst, src 16-byte aligned; bytes a
 // multiple of 16.
@@ -195,6 +213,30 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// ---------------------------------------------------------------- float32
+
+__device__ __forceinline__ float pow2i(int e) {   // e in [-126, 127]
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
+                                     float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 // ---------------------------------------------------------------- Q4_0
 
 // Dequantise the 16 code bytes + fp16 scale of one Q4_0 block into 32 fp16

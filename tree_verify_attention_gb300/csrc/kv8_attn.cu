@@ -128,24 +128,6 @@ struct AttnParams {
   uint32_t* status;
 };
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// Bounded wait that also gives up when another role has.
-__device__ __noinline__ bool role_wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  bool there = false;
-  const bool ended = wait_bounded([&]() {
-    there = mbar_try_wait(bar, parity);
-    return there || *dead;
-  });
-  if (!ended) *dead = 1;
-  return there;
-}
-__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  return mbar_try_wait(bar, parity) || role_wait_slow(bar, parity, dead);
-}
-
 // 16 codes as 8 words of binary16 pairs: 0x6400 | u is 1024 + u, and u = code + 128.
 __device__ __forceinline__ void codes_to_half(const uint4& v, uint32_t* w) {
   const uint32_t in[4] = {v.x, v.y, v.z, v.w};
@@ -162,28 +144,6 @@ __device__ __forceinline__ void codes_to_half(const uint4& v, uint32_t* w) {
   }
 }
 
-__device__ __forceinline__ float pow2i(int e) {   // e in [-126, 127]
-  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
-
-// Two float32 operations in one instruction.
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
-                                     float c0, float c1) {
-  asm("{\n\t.reg .b64 a, b, c;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 c, a, b, c;\n\t"
-      "mov.b64 {%0, %1}, c;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
-}
-__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 a, a, b;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

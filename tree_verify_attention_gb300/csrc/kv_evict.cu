@@ -1,0 +1,413 @@
+// Eviction from a Q4_0 or F16 cache by the weight its keys have received, and
+// rows of such a cache read back as values.
+//
+// Each KV head keeps, of its C rows, the first `sinks`, the last `recent`, and
+// of the others the ones with the largest weight (ties to the lowest position);
+// the rows keep their order and move bit for bit to another cache.
+//
+// The selection is an exact radix select: three histograms of 11, 11 and 10
+// bits of the weights' ordered bits find the smallest kept weight and how many
+// equal ones are kept; a last pass counts in position order and writes the list.
+// A head belongs to a cluster of up to 8 CTAs, each with its own run of
+// positions; they read each other's histograms, so nothing goes through memory
+// and no counter has to be reset. It is bound by latency: four passes over half a
+// megabyte a head at most. The copy is a gather of whole rows and bound by
+// memory.
+
+#include "common.cuh"
+
+namespace dfv {
+
+constexpr int kEvThreads = 1024;
+constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvBins = 2048;
+constexpr int kEvMaxCluster = 8;
+
+struct EvictParams {
+  int capacity, keep, sinks, recent, dst_capacity;
+  const int32_t *ctx_len, *dropped;
+  const float* weights;      // [head][capacity]
+  int32_t* kept;             // [head][keep]
+  float* weights_out;        // [head][dst_capacity], may be null
+  int32_t *dst_ctx_len, *dst_dropped;
+  uint32_t* status;
+};
+
+// Larger for larger weights; -0 equals +0, a NaN is below everything.
+__device__ __forceinline__ uint32_t ev_order(float w) {
+  const uint32_t u = __float_as_uint(w + 0.0f);
+  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return w == w ? o : 0u;
+}
+
+__device__ __forceinline__ int ev_ctx(const EvictParams& p, bool tell) {
+  const int C = *p.ctx_len;
+  if (C >= 0 && C <= p.capacity) return C;
+  if (tell) report(p.status, DFV_DEV_CTX);
+  return max(0, min(C, p.capacity));
+}
+
+__device__ __forceinline__ uint32_t ev_remote(const uint32_t* p, int rank) {
+  uint64_t a;
+  uint32_t v;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(p), "r"(rank));
+  asm volatile("ld.u32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void ev_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kEvThreads, 1)
+    evict_select_kernel(const __grid_constant__ EvictParams p) {
+  // two in turn: one is read by the others while the next is filled
+  __shared__ uint32_t s_hist[2][kEvBins];
+  __shared__ uint32_t s_warp[2][kEvWarps], s_total[2];
+  __shared__ uint32_t s_bin, s_above;
+  int cs, rank;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int h = blockIdx.x / cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_wait();
+  grid_dep_launch_dependents();   // (after the wait: see common.cuh)
+  const int C = ev_ctx(p, blockIdx.x == 0 && tid == 0);
+  const int n = min(C, p.keep);
+  if (blockIdx.x == 0 && tid == 0) {
+    *p.dst_ctx_len = n;
+    if (p.dst_dropped) *p.dst_dropped = (p.dropped ? *p.dropped : 0) + (C - n);
+  }
+  const float* w = p.weights + static_cast<int64_t>(h) * p.capacity;
+  int32_t* kept = p.kept + static_cast<int64_t>(h) * p.keep;
+  // positions [s0, s1) compete for `need` places
+  const bool all = C <= p.keep;
+  const int s0 = all ? C : p.sinks, s1 = all ? C : C - p.recent;
+  uint32_t need = all ? 0 : static_cast<uint32_t>(p.keep - p.sinks - p.recent);
+  const int lo = static_cast<int>(static_cast<int64_t>(C) * rank / cs);
+  const int hi = static_cast<int>(static_cast<int64_t>(C) * (rank + 1) / cs);
+
+  // ---- the smallest kept weight, 11, 11 and 10 bits at a time
+  uint32_t prefix = 0xFFFFFFFFu;   // no place: nothing reaches it
+  if (need > 0) {
+    prefix = 0;
+    int known = 0;   // leading bits of `prefix` that are found
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass < 2 ? 11 : 10, shift = 32 - known - bits;
+      uint32_t* hist = s_hist[pass & 1];
+      for (int b = tid; b < kEvBins; b += kEvThreads) hist[b] = 0;
+      __syncthreads();
+      const int a = max(lo, s0), e = min(hi, s1);
+#pragma unroll 4
+      for (int j = a + tid; j < e; j += kEvThreads) {
+        const uint32_t o = ev_order(w[j]);
+        if (known == 0 || (o >> (32 - known)) == (prefix >> (32 - known)))
+          atomicAdd(&hist[(o >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+      ev_cluster_sync();
+      // bins from the largest down, two a thread: where the count reaches `need`
+      uint32_t c[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        c[k] = 0;
+        for (int r = 0; r < cs; ++r) c[k] += ev_remote(&hist[kEvBins - 1 - (2 * tid + k)], r);
+      }
+      uint32_t sum = c[0] + c[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (lane == 31) s_warp[0][warp] = sum;
+      __syncthreads();
+      for (int i = 0; i < warp; ++i) sum += s_warp[0][i];
+      uint32_t above = sum - c[0] - c[1];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (above < need && need <= above + c[k]) {   // one thread's
+          s_bin = kEvBins - 1 - (2 * tid + k);
+          s_above = above;
+        }
+        above += c[k];
+      }
+      __syncthreads();
+      need -= s_above;
+      prefix |= s_bin << shift;
+      known += bits;
+      __syncthreads();
+    }
+  }
+  // Now `need` of the weights that equal the smallest kept one stay.
+
+  // ---- the list, in position order: each warp has a run of positions
+  const int per = ((hi - lo + kEvWarps - 1) / kEvWarps + 31) / 32 * 32;
+  const int j0 = min(hi, lo + warp * per), j1 = min(hi, j0 + per);
+  auto classify = [&](int j, bool& over, bool& same) {
+    over = same = false;
+    if (j >= j1) return;
+    if (j < s0 || j >= s1) {
+      over = true;
+      return;
+    }
+    const uint32_t o = ev_order(w[j]);
+    over = need > 0 && o > prefix;
+    same = need > 0 && o == prefix;
+  };
+  uint32_t n_over = 0, n_same = 0;
+#pragma unroll 4
+  for (int j = j0; j < j1; j += 32) {
+    bool over, same;
+    classify(j + lane, over, same);
+    n_over += __popc(__ballot_sync(0xFFFFFFFFu, over));
+    n_same += __popc(__ballot_sync(0xFFFFFFFFu, same));
+  }
+  if (lane == 0) {
+    s_warp[0][warp] = n_over;
+    s_warp[1][warp] = n_same;
+  }
+  __syncthreads();
+  if (tid < 2) {
+    uint32_t t = 0;
+    for (int i = 0; i < kEvWarps; ++i) t += s_warp[tid][i];
+    s_total[tid] = t;
+  }
+  ev_cluster_sync();
+  uint32_t at_over = 0, at_same = 0;
+  for (int r = 0; r < rank; ++r) {
+    at_over += ev_remote(&s_total[0], r);
+    at_same += ev_remote(&s_total[1], r);
+  }
+  for (int i = 0; i < warp; ++i) {
+    at_over += s_warp[0][i];
+    at_same += s_warp[1][i];
+  }
+#pragma unroll 4
+  for (int j = j0; j < j1; j += 32) {
+    bool over, same;
+    classify(j + lane, over, same);
+    const unsigned bo = __ballot_sync(0xFFFFFFFFu, over), bs = __ballot_sync(0xFFFFFFFFu, same);
+    const unsigned below = (1u << lane) - 1u;
+    const uint32_t eo = at_over + __popc(bo & below), es = at_same + __popc(bs & below);
+    if (over || (same && es < need)) {
+      const uint32_t at = eo + min(es, need);
+      kept[at] = j + lane;
+      if (p.weights_out)
+        p.weights_out[static_cast<int64_t>(h) * p.dst_capacity + at] = w[j + lane];
+    }
+    at_over += __popc(bo);
+    at_same += __popc(bs);
+  }
+  ev_cluster_sync();   // the totals have been read
+}
+
+struct MoveParams {
+  int heads, capacity, dst_capacity, keep;
+  const int32_t* ctx_len;
+  const int32_t* kept;
+  const uint8_t *k, *v;
+  uint8_t *k_out, *v_out;
+};
+
+// One piece (4, 8 or 16 bytes) of a kept row per thread and step: writes are
+// contiguous, reads whole rows. kPieces is known for Q4_0 (9 pieces of D / 16
+// bytes), a power of two else.
+template <typename V, int kPieces>
+__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ MoveParams p) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();   // (after the wait: see common.cuh)
+  const int C = max(0, min(*p.ctx_len, p.capacity));
+  const int n = min(C, p.keep);
+  const int64_t per_head = static_cast<int64_t>(n) * kPieces;
+  const int h = blockIdx.y;
+  const uint8_t* src = (blockIdx.z ? p.v : p.k);
+  uint8_t* dst = (blockIdx.z ? p.v_out : p.k_out);
+  const V* s = reinterpret_cast<const V*>(src) + static_cast<int64_t>(h) * p.capacity * kPieces;
+  V* d = reinterpret_cast<V*>(dst) + static_cast<int64_t>(h) * p.dst_capacity * kPieces;
+  const int32_t* kept = p.kept + static_cast<int64_t>(h) * p.keep;
+  constexpr int kAhead = 4;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < per_head;
+       i += kAhead * stride) {
+    V x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t k = i + u * stride;
+      if (k >= per_head) break;
+      const int64_t row = k / kPieces;
+      x[u] = s[static_cast<int64_t>(kept[row]) * kPieces + (k - row * kPieces)];
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t k = i + u * stride;
+      if (k < per_head) d[k] = x[u];
+    }
+  }
+}
+
+struct ReadRowsParams {
+  int heads, head_dim, capacity, pos0, n_rows;
+  const uint8_t *k, *v;
+  void *k_dst, *v_dst;
+  int64_t stride_row, stride_head;
+};
+
+__device__ __forceinline__ void put8(float* d, const float* x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) d[i] = x[i];
+}
+__device__ __forceinline__ void put8(__nv_bfloat16* d, const float* x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) d[i] = __float2bfloat16_rn(x[i]);
+}
+
+// Eight values of a row per thread and step.
+template <typename T, bool kF16>
+__global__ void __launch_bounds__(256) read_rows_kernel(const __grid_constant__ ReadRowsParams p) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();   // (after the wait: see common.cuh)
+  const int groups = p.head_dim / 8, h = blockIdx.y;
+  const int64_t row_bytes = kv_row_bytes(kF16 ? DFV_KV_F16 : DFV_KV_Q4_0, p.head_dim);
+  const uint8_t* src = (blockIdx.z ? p.v : p.k) + static_cast<int64_t>(h) * p.capacity * row_bytes;
+  T* dst = static_cast<T*>(blockIdx.z ? p.v_dst : p.k_dst) + h * p.stride_head;
+  const int64_t total = static_cast<int64_t>(p.n_rows) * groups;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / groups;
+    const int g = static_cast<int>(i - r * groups);
+    const uint8_t* row = src + (p.pos0 + r) * row_bytes;
+    float x[8];
+    if constexpr (kF16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + g * 16);
+      const __half2* q = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(q[e]);
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+      }
+    } else {
+      // dims [8 (g % 4), + 8) of a block: low nibbles of its first 16, high of its last
+      const uint16_t* blk = reinterpret_cast<const uint16_t*>(row + (g >> 2) * 18);
+      const float d = __half2float(__ushort_as_half(blk[0]));
+      const int nib = (g & 2) ? 4 : 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t c = static_cast<uint32_t>(blk[1 + (g & 1) * 4 + e]) >> nib;
+        x[2 * e] = (static_cast<float>(c & 15u) - 8.0f) * d;
+        x[2 * e + 1] = (static_cast<float>((c >> 8) & 15u) - 8.0f) * d;
+      }
+    }
+    put8(dst + r * p.stride_row + g * 8, x);
+  }
+}
+
+template <typename F, typename P>
+dfv_status launch_after(F* kernel, const P& p, dim3 grid, int threads, cudaStream_t stream,
+                        int cluster = 1) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DFV_OK : DFV_ERR_CUDA;
+}
+
+template <typename V, int kPieces>
+dfv_status move_launch(const MoveParams& p, cudaStream_t stream) {
+  // about eight CTAs an SM over heads, K and V; four pieces a thread at a time
+  const int64_t want = (static_cast<int64_t>(p.keep) * kPieces + 1023) / 1024;
+  const int64_t most = (static_cast<int64_t>(sm_count()) * 8 + 2 * p.heads - 1) / (2 * p.heads);
+  const int64_t x = want < most ? want : most;
+  return launch_after(evict_move_kernel<V, kPieces>, p,
+                      dim3(static_cast<unsigned>(x < 1 ? 1 : x), p.heads, 2), 256, stream);
+}
+
+}  // namespace dfv
+
+extern "C" dfv_status dfv_kv_evict(int n_kv_heads, int head_dim, int kv_format,
+                                   int cache_capacity, const int32_t* ctx_len,
+                                   const int32_t* dropped, const void* k_cache,
+                                   const void* v_cache, const float* weights, int keep, int sinks,
+                                   int recent, int dst_capacity, void* k_dst, void* v_dst,
+                                   int32_t* dst_ctx_len, int32_t* dst_dropped,
+                                   float* weights_out, int32_t* kept, uint32_t* status,
+                                   dfv_stream_t stream) {
+  using namespace dfv;
+  if ((kv_format != DFV_KV_Q4_0 && kv_format != DFV_KV_F16) ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return DFV_ERR_UNSUPPORTED;
+  if (n_kv_heads < 1 || n_kv_heads > 65535 || cache_capacity < 1 ||
+      cache_capacity > (1 << 30) || keep < 1 || keep > dst_capacity || sinks < 0 || recent < 0 ||
+      static_cast<int64_t>(sinks) + recent > keep || dst_capacity > (1 << 30))
+    return DFV_ERR_INVALID;
+  if (!ctx_len || !k_cache || !v_cache || !weights || !k_dst || !v_dst || !dst_ctx_len || !kept ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_dst, 16) ||
+      !aligned(v_dst, 16) || !aligned(weights, 4) || !aligned(weights_out, 4) ||
+      !aligned(kept, 4) || !aligned(ctx_len, 4) || !aligned(dst_ctx_len, 4) ||
+      !aligned(dropped, 4) || !aligned(dst_dropped, 4))
+    return DFV_ERR_INVALID;
+  if (k_dst == k_cache || v_dst == v_cache || k_dst == v_cache || v_dst == k_cache ||
+      k_dst == v_dst || dst_ctx_len == ctx_len || weights_out == weights)
+    return DFV_ERR_INVALID;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const EvictParams e = {cache_capacity, keep, sinks, recent, dst_capacity, ctx_len, dropped,
+                         weights, kept, weights_out, dst_ctx_len, dst_dropped, status};
+  // a CTA for about 8192 positions of a head, eight at most
+  int cs = 1;
+  while (cs < kEvMaxCluster && cache_capacity > cs * 8192) cs <<= 1;
+  dfv_status st = launch_after(evict_select_kernel, e, dim3(n_kv_heads * cs), kEvThreads, s, cs);
+  if (st != DFV_OK) return st;
+  const MoveParams m = {n_kv_heads, cache_capacity, dst_capacity, keep, ctx_len, kept,
+                        static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
+                        static_cast<uint8_t*>(k_dst), static_cast<uint8_t*>(v_dst)};
+  if (kv_format == DFV_KV_F16)
+    return head_dim == 64    ? move_launch<uint4, 8>(m, s)
+           : head_dim == 128 ? move_launch<uint4, 16>(m, s)
+                             : move_launch<uint4, 32>(m, s);
+  return head_dim == 64    ? move_launch<uint32_t, 9>(m, s)
+         : head_dim == 128 ? move_launch<uint2, 9>(m, s)
+                           : move_launch<uint4, 9>(m, s);
+}
+
+extern "C" dfv_status dfv_kv_read_rows(int n_kv_heads, int head_dim, int kv_format,
+                                       int cache_capacity, int pos0, int n_rows,
+                                       const void* k_cache, const void* v_cache, void* k_dst,
+                                       void* v_dst, int dst_dtype, int64_t stride_row,
+                                       int64_t stride_head, dfv_stream_t stream) {
+  using namespace dfv;
+  if ((kv_format != DFV_KV_Q4_0 && kv_format != DFV_KV_F16) ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+      (dst_dtype != DFV_DTYPE_F32 && dst_dtype != DFV_DTYPE_BF16))
+    return DFV_ERR_UNSUPPORTED;
+  if (n_kv_heads < 1 || n_kv_heads > 65535 || cache_capacity < 1 || pos0 < 0 || n_rows < 0 ||
+      static_cast<int64_t>(pos0) + n_rows > cache_capacity)
+    return DFV_ERR_INVALID;
+  if (n_rows == 0) return DFV_OK;
+  const size_t size = dst_dtype == DFV_DTYPE_F32 ? 4 : 2;
+  if (!k_cache || !v_cache || !k_dst || !v_dst || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_dst, size) || !aligned(v_dst, size))
+    return DFV_ERR_INVALID;
+  const ReadRowsParams p = {n_kv_heads, head_dim, cache_capacity, pos0, n_rows,
+                            static_cast<const uint8_t*>(k_cache),
+                            static_cast<const uint8_t*>(v_cache), k_dst, v_dst, stride_row,
+                            stride_head};
+  const int64_t want = (static_cast<int64_t>(n_rows) * (head_dim / 8) + 255) / 256;
+  const int64_t most = (static_cast<int64_t>(sm_count()) * 16 + 2 * n_kv_heads - 1) /
+                       (2 * n_kv_heads);
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most), n_kv_heads, 2);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (kv_format == DFV_KV_F16)
+    return dst_dtype == DFV_DTYPE_F32
+               ? launch_after(read_rows_kernel<float, true>, p, grid, 256, s)
+               : launch_after(read_rows_kernel<__nv_bfloat16, true>, p, grid, 256, s);
+  return dst_dtype == DFV_DTYPE_F32
+             ? launch_after(read_rows_kernel<float, false>, p, grid, 256, s)
+             : launch_after(read_rows_kernel<__nv_bfloat16, false>, p, grid, 256, s);
+}

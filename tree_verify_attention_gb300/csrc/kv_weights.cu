@@ -1,0 +1,576 @@
+// The attention weight that each cached key receives from the last committed
+// rows, summed over the rows and the query heads of the key's group:
+//
+//   weights[h][j] = decay * prev[h][j] + sum_{s, g} exp(scale q_{s,hg} . k_j - lse_{s,hg})
+//
+// over the rows s that see key j. Keys are the M dimension of the product (S^T
+// = K^ Q^T, 128 keys x up to 128 query rows), so a key is a lane of TMEM: the
+// sum over query rows is a sum over a thread's own columns, without any exchange
+// between lanes.
+//
+// The weights are f32 results, so K^ has to be exact: a Q4_0 value (code - 8) d
+// has 14 bits and binary16 holds 11. It is split into hi = rn16((code - 8) d)
+// and lo = (code - 8) d - hi, which fits binary16 exactly, and both are
+// multiplied (weights off by 1.4e-4 with hi alone, by 1e-6 so). F16 rows are
+// exact. Query rows are scaled by a power of two each, which the exponent's
+// factor takes back.
+//
+// A CTA works through a run of 128-key chunks of (at most a few) heads: one warp
+// copies raw rows into a ring, four convert them into TMEM in parts of 64 dims,
+// one issues the products, two groups of four take turns at the chunks' sums.
+
+#include <atomic>
+
+#include "common.cuh"
+#include "tc.cuh"
+#include "tmem_io.cuh"
+
+namespace dfv {
+
+constexpr int kWtKeys = 128;
+constexpr int kWtRows = 128;     // query rows of a tile, at most
+constexpr int kWtThreads = 14 * 32;
+
+template <int D, bool kQ4>
+struct WeightShape {
+  static constexpr int kRowBytes = kQ4 ? D / 32 * 18 : D * 2;
+  static constexpr int kPitch = kQ4 ? kRowBytes : kRowBytes + 16;   // of a row in shared memory
+  static constexpr int kStage = (kWtKeys * kPitch + 16 + 127) / 128 * 128;
+  static constexpr int kStages = kQ4 ? 4 : D == 256 ? 2 : 3;
+  static constexpr int kQBytes = kWtRows * D * 2;
+  static constexpr int kOffRaw = kQBytes;
+  static constexpr int kBytes = kOffRaw + kStages * kStage + 1024;
+  static constexpr int kParts = D / 64;               // of a chunk
+  static constexpr int kPartCols = kQ4 ? 64 : 32;     // TMEM columns of a part: hi, lo
+  static constexpr int kRing = 256 / kPartCols;       // parts in TMEM
+  static constexpr uint32_t kTS = 256;                // two buffers of scores
+  static_assert(kBytes <= 220 * 1024, "shared memory");
+};
+
+struct WeightParams {
+  int n_rows, hq, hkv, group, window, capacity;
+  const int32_t* ctx_len;
+  const uint8_t* k;
+  const __nv_bfloat16* q;
+  const float* lse;
+  const int32_t *path, *accept_len;
+  float scale, decay;
+  const float* prev;
+  float* weights;
+  uint32_t* status;
+};
+
+// Place of dim c of a block of 32 in the operands' K order: a word of four code
+// bytes gives pairs (bytes 0, 2 low), (0, 2 high), (1, 3 low), (1, 3 high).
+// Eight consecutive places are word w's dims 4w + {0, 2, 16, 18, 1, 3, 17, 19}.
+
+template <int D, bool kQ4>
+__global__ void __launch_bounds__(kWtThreads, 1)
+    kv_weights_kernel(const __grid_constant__ WeightParams p) {
+  using W = WeightShape<D, kQ4>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem;
+  uint8_t* sRaw = smem + W::kOffRaw;
+  __shared__ uint64_t b_raw[4], b_read[4];            // raw rows landed, read
+  __shared__ uint64_t b_part[8], b_free[8];           // operand part written, multiplied
+  __shared__ uint64_t b_s[2], b_sfree[2];             // scores there, read
+  __shared__ uint64_t b_q, b_qfree, b_end;            // query rows there, multiplied
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_dead;
+  // of a tile's columns, two tiles in turn: the exponent's slope and offset,
+  // and the first and last position that is seen
+  __shared__ __align__(16) float s_slope[2][kWtRows], s_off[2][kWtRows];
+  __shared__ __align__(16) int s_first[2][kWtRows], s_last[2][kWtRows];
+
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp =
+      static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(tid >> 5)));
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&b_raw[i], 1);
+      mbar_init(&b_read[i], 4);
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&b_part[i], 4);
+      mbar_init(&b_free[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b_s[i], 1);
+      mbar_init(&b_sfree[i], 4);
+    }
+    mbar_init(&b_q, 8);
+    mbar_init(&b_qfree, 1);
+    mbar_init(&b_end, 1);
+    s_dead = 0;
+    fence_mbar_init();
+  }
+  grid_dep_wait();
+  grid_dep_launch_dependents();   // (after the wait: see common.cuh)
+  if (warp == 12) tc::tmem_alloc(&s_tmem, 512);
+
+  // ---- the problem, the same in every thread
+  int C = __reduce_max_sync(0xFFFFFFFFu, *p.ctx_len);
+  if (C < 0 || C > p.capacity) {
+    if (tid == 0) report(p.status, DFV_DEV_CTX);
+    C = max(0, min(C, p.capacity));
+  }
+  int n = p.n_rows;
+  if (p.accept_len) {
+    const int L = __reduce_max_sync(0xFFFFFFFFu, *p.accept_len);
+    if ((L < 0 || L > n) && tid == 0) report(p.status, DFV_DEV_BAD_PATH);
+    n = max(0, min(L, n));
+  }
+  const int rows = n * p.group;                       // query rows of a KV head
+  const int tiles = (rows + kWtRows - 1) / kWtRows;
+  // columns of a tile, balanced, in steps of 16
+  const int R = tiles == 0 ? 16 : ((rows + tiles - 1) / tiles + 15) / 16 * 16;
+  // positions: row s stands at C - n + s; chunks [fc, lc) are seen by some row
+  const int at0 = C - n;
+  const int lc = tiles == 0 ? 0 : (C + kWtKeys - 1) / kWtKeys;
+  const int fc = p.window > 0 ? min(lc, max(0, at0 - p.window + 1) / kWtKeys) : 0;
+  const int64_t all = static_cast<int64_t>(p.hkv) * (lc - fc);
+  const int64_t u0 = all * blockIdx.x / gridDim.x, u1 = all * (blockIdx.x + 1) / gridDim.x;
+  const int per_head = max(1, lc - fc);
+
+  // Runs of chunks of one head, each for every tile: f(head, first chunk, last
+  // chunk + 1, tile) in the same order in every role; false ends.
+  auto runs = [&](auto f) {
+    for (int64_t u = u0; u < u1;) {
+      const int h = static_cast<int>(u / per_head), c = static_cast<int>(u % per_head);
+      const int m = static_cast<int>(min(u1 - u, static_cast<int64_t>(per_head - c)));
+      for (int t = 0; t < tiles; ++t)
+        if (!f(h, fc + c, fc + c + m, t)) return;
+      u += m;
+    }
+  };
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // quadrant's first lane << 16
+
+  if (warp == 13) {
+    // ------------------------------------------------------ raw rows
+    bool ok = true;
+    int k = 0;   // chunks so far
+    fence_proxy_async_global();   // what earlier kernels wrote, to the copy engine
+    runs([&](int h, int c0, int c1, int) {
+      for (int c = c0; c < c1; ++c, ++k) {
+        const int st = k % W::kStages;
+        if (k >= W::kStages) {
+          ok = role_wait(&b_read[st], (k / W::kStages - 1) & 1, &s_dead);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) return false;
+        }
+        const int live = min(kWtKeys, C - c * kWtKeys);
+        const int64_t from = (static_cast<int64_t>(h) * p.capacity + c * kWtKeys) * W::kRowBytes;
+        uint8_t* dst = sRaw + st * W::kStage;
+        if (kQ4) {
+          // one piece, from the 16-byte boundary before its start; what is
+          // behind the last boundary by words
+          const int64_t a = from & ~static_cast<int64_t>(15);
+          const int64_t e = from + static_cast<int64_t>(live) * W::kRowBytes;
+          const int64_t b = e & ~static_cast<int64_t>(15);
+          if (lane < static_cast<int>(e - b) / 4)
+            *reinterpret_cast<uint32_t*>(dst + (b - a) + lane * 4) =
+                *reinterpret_cast<const uint32_t*>(p.k + b + lane * 4);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&b_raw[st], static_cast<uint32_t>(b - a));
+            if (b > a) bulk_g2s(dst, p.k + a, static_cast<uint32_t>(b - a), &b_raw[st]);
+          }
+        } else {
+          if (lane == 0)
+            mbar_arrive_expect_tx(&b_raw[st], static_cast<uint32_t>(live * W::kRowBytes));
+          __syncwarp();
+          for (int r = lane; r < live; r += 32)
+            bulk_g2s(dst + r * W::kPitch, p.k + from + static_cast<int64_t>(r) * W::kRowBytes,
+                     W::kRowBytes, &b_raw[st]);
+        }
+      }
+      return true;
+    });
+    // copies that nobody waits for any more must still land
+    if (s_dead)
+      for (int i = max(0, k - W::kStages); i < k; ++i)
+        mbar_wait_bounded(&b_raw[i % W::kStages], (i / W::kStages) & 1);
+  } else if (warp == 12) {
+    // ------------------------------------------------------ products
+    bool ok = true;
+    int k = 0, part = 0, run = 0;
+    const uint32_t idesc = tc::idesc_f16(128, 0) | (static_cast<uint32_t>(R >> 3) << 17);
+    const uint64_t qd = tc::smem_desc_sw128(smem_u32(sQ), 1024);
+    const uint64_t q_block = static_cast<uint64_t>(R * 128) >> 4;   // 64 dims of all rows
+    auto all_wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = __all_sync(0xFFFFFFFFu, role_wait(bar, parity, &s_dead));
+      tc::fence_after_sync();
+      return got;
+    };
+    runs([&](int, int c0, int c1, int) {
+      ok = all_wait(&b_q, run & 1);
+      for (int c = c0; ok && c < c1; ++c, ++k) {
+        const int buf = k & 1;
+        if (k >= 2) ok = all_wait(&b_sfree[buf], ((k >> 1) - 1) & 1);
+        for (int i = 0; ok && i < W::kParts; ++i, ++part) {
+          const int slot = part % W::kRing;
+          ok = all_wait(&b_part[slot], (part / W::kRing) & 1);
+          if (!ok) break;
+          if (tc::elect_one()) {
+            const uint32_t a = tmem + slot * W::kPartCols;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_f16_ts(tmem + W::kTS + buf * kWtRows, a + kk * 8,
+                             qd + i * q_block + kk * 2, idesc, i > 0 || kk > 0 ? 1u : 0u);
+            if (kQ4) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_f16_ts(tmem + W::kTS + buf * kWtRows, a + 32 + kk * 8,
+                               qd + i * q_block + kk * 2, idesc, 1u);
+            }
+            tc::commit(&b_free[slot]);
+            if (i == W::kParts - 1) tc::commit(&b_s[buf]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) return false;
+      if (tc::elect_one()) tc::commit(&b_qfree);
+      __syncwarp();
+      ++run;
+      return true;
+    });
+    // products in flight must end before TMEM is freed
+    if (!ok) s_dead = 1;
+    if (tc::elect_one()) tc::commit(&b_end);
+    __syncwarp();
+    mbar_wait_bounded(&b_end, 0);
+  } else if (warp >= 8) {
+    // ------------------------------------------------------ rows to operands
+    const int slot = (warp & 3) * 32 + lane;   // key of the chunk
+    bool ok = true;
+    int k = 0, part = 0;
+    auto take = [&]() {
+      if (part >= W::kRing)
+        ok = role_wait(&b_free[part % W::kRing], (part / W::kRing - 1) & 1, &s_dead);
+      ok = __all_sync(0xFFFFFFFFu, ok);   // the TMEM stores are warp-wide
+      tc::fence_after_sync();
+    };
+    auto give = [&]() {
+      tc::store_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_part[part % W::kRing]);
+      ++part;
+    };
+    runs([&](int h, int c0, int c1, int) {
+      for (int c = c0; ok && c < c1; ++c, ++k) {
+        const int st = k % W::kStages;
+        ok = __all_sync(0xFFFFFFFFu, role_wait(&b_raw[st], (k / W::kStages) & 1, &s_dead));
+        if (!ok) break;
+        const uint8_t* row = sRaw + st * W::kStage + slot * W::kPitch;
+        auto done = [&]() {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b_read[st]);
+        };
+        if constexpr (kQ4) {
+          if (D < 256)   // rows of 36 or 72 bytes: the piece began at a 16-byte boundary
+            row += ((static_cast<int64_t>(h) * p.capacity + c * kWtKeys) * W::kRowBytes) & 15;
+          // a row is nine pieces of D / 16 bytes, two blocks of 18 nine words
+          constexpr int kWords = W::kRowBytes / 4;
+          uint32_t in[kWords];
+          if constexpr (D == 256) {
+#pragma unroll
+            for (int i = 0; i < 9; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(row + i * 16);
+              in[4 * i] = v.x, in[4 * i + 1] = v.y, in[4 * i + 2] = v.z, in[4 * i + 3] = v.w;
+            }
+          } else if constexpr (D == 128) {
+#pragma unroll
+            for (int i = 0; i < 9; ++i) {
+              const uint2 v = *reinterpret_cast<const uint2*>(row + i * 8);
+              in[2 * i] = v.x, in[2 * i + 1] = v.y;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 9; ++i) in[i] = *reinterpret_cast<const uint32_t*>(row + i * 4);
+          }
+          done();   // every code is in registers
+#pragma unroll
+          for (int i = 0; i < W::kParts; ++i) {
+            uint32_t hi[32], lo[32];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              // words of the block: scale and codes are 2 bytes apart from words in
+              // the first of the two
+              const uint32_t* w = in + 9 * i + 4 * b;
+              const uint32_t sc = b == 0 ? w[0] & 0xFFFFu : w[0] >> 16;
+              const uint32_t d2 = sc | (sc << 16);
+              const __half2 d = *reinterpret_cast<const __half2*>(&d2);
+              const __half2 bias = __float2half2_rn(1032.0f);   // 1024 + 8
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t x = b == 0 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j + 1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  // 0x6400 | code is 1024 + code
+                  const uint32_t y = ((x >> (e == 0 ? 0 : e == 1 ? 4 : e == 2 ? 8 : 12)) &
+                                      0x000F000Fu) | 0x64006400u;
+                  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
+                  const __half2 a = __hmul2(v, d);
+                  const __half2 r = __hfma2(v, d, __hneg2(a));
+                  hi[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&a);
+                  lo[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&r);
+                }
+              }
+            }
+            take();
+            if (!ok) break;
+            const uint32_t t = tmem + lanes + (part % W::kRing) * W::kPartCols;
+            tc::TmemIo<32>::store(t, hi);
+            tc::TmemIo<32>::store(t + 32, lo);
+            give();
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < W::kParts; ++i) {
+            uint32_t v[32];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint4 x = *reinterpret_cast<const uint4*>(row + i * 128 + j * 16);
+              v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
+            }
+            if (i == W::kParts - 1) done();
+            take();
+            if (!ok) break;
+            tc::TmemIo<32>::store(tmem + lanes + (part % W::kRing) * W::kPartCols, v);
+            give();
+          }
+        }
+      }
+      return ok;
+    });
+  } else {
+    // ------------------------------------------------------ query rows, sums
+    const int grp = warp >> 2;
+    bool ok = true;
+    int k = 0, run = 0;
+    runs([&](int h, int c0, int c1, int t) {
+      const int r0 = t * R, live = min(R, rows - r0), tb = run & 1;
+      if (ok && run > 0)
+        ok = __all_sync(0xFFFFFFFFu, role_wait(&b_qfree, (run - 1) & 1, &s_dead));
+      // A warp takes a query row at a time: its largest magnitude becomes a
+      // power of two, the lanes' 16-byte pieces go to the operand.
+      for (int r = warp; ok && r < R; r += 8) {
+        float slope = 0.0f, off = -INFINITY;
+        int first = 0, last = -1;
+        uint2 a = make_uint2(0, 0), b = a;
+        uint32_t m = 0;
+        if (r < live) {
+          const int s = (r0 + r) / p.group, g = (r0 + r) - s * p.group;
+          int node = p.path ? p.path[s] : s;
+          if (node < 0 || node >= p.n_rows) {
+            if (lane == 0) report(p.status, DFV_DEV_BAD_PATH);
+            node = -1;
+          }
+          if (node >= 0) {
+            const int64_t row = static_cast<int64_t>(node) * p.hq + h * p.group + g;
+            // places 8 lane .. of the K order (Q4_0), or as they are
+            const __nv_bfloat16* src = p.q + row * D;
+            if (lane < D / 8) {
+              if (kQ4) {
+                const __nv_bfloat16* w = src + (lane >> 2) * 32 + (lane & 3) * 4;
+                a = *reinterpret_cast<const uint2*>(w);
+                b = *reinterpret_cast<const uint2*>(w + 16);
+              } else {
+                const uint4 v = *reinterpret_cast<const uint4*>(src + lane * 8);
+                a = make_uint2(v.x, v.y);
+                b = make_uint2(v.z, v.w);
+              }
+              m = __vmaxu2(__vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu),
+                           __vmaxu2(b.x & 0x7FFF7FFFu, b.y & 0x7FFF7FFFu));
+              m = max(m & 0xFFFFu, m >> 16);
+            }
+            m = __reduce_max_sync(0xFFFFFFFFu, m);
+            const float l = p.lse[row];
+            if (m >= 0x7F80u || !(fabsf(l) < INFINITY)) {
+              // a row that is not finite counts for nothing
+              if (lane == 0) report(p.status, DFV_DEV_NONFINITE);
+              a = b = make_uint2(0, 0);
+              m = 0;
+            } else {
+              off = -l * 1.44269504f;
+              last = at0 + s;
+              first = p.window > 0 ? at0 + s - p.window + 1 : 0;
+            }
+          }
+        }
+        const int e = max(static_cast<int>(m >> 7), 40);   // largest magnitude below 2^(e - 126)
+        const float f = pow2i(141 - e);                    // to below 2^15
+        if (off > -INFINITY) slope = p.scale * 1.44269504f * pow2i(e - 141);
+        if (lane < D / 8) {
+          auto half2_of = [&](uint32_t lo16, uint32_t hi16) {
+            return pack_half2(__uint_as_float(lo16 << 16) * f, __uint_as_float(hi16 << 16) * f);
+          };
+          uint4 o;
+          if (kQ4)   // dims {0, 2, 16, 18, 1, 3, 17, 19} of the word
+            o = make_uint4(half2_of(a.x & 0xFFFFu, a.y & 0xFFFFu),
+                           half2_of(b.x & 0xFFFFu, b.y & 0xFFFFu), half2_of(a.x >> 16, a.y >> 16),
+                           half2_of(b.x >> 16, b.y >> 16));
+          else
+            o = make_uint4(half2_of(a.x & 0xFFFFu, a.x >> 16), half2_of(a.y & 0xFFFFu, a.y >> 16),
+                           half2_of(b.x & 0xFFFFu, b.x >> 16), half2_of(b.y & 0xFFFFu, b.y >> 16));
+          *reinterpret_cast<uint4*>(sQ + tc::sw128_offset(r, lane, R)) = o;
+        }
+        if (lane == 0) {
+          s_slope[tb][r] = slope;
+          s_off[tb][r] = off;
+          s_first[tb][r] = first;
+          s_last[tb][r] = last;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&b_q);
+      // The columns' factors are everyone's. All eight warps come here in every
+      // run, whatever their waits gave, and end together.
+      ok = named_sync_and(1, 256, ok);
+      if (!ok) return false;
+      const float* slope = s_slope[tb];
+      const float* off = s_off[tb];
+      for (int c = c0; ok && c < c1; ++c, ++k) {
+        if ((k & 1) != grp) continue;
+        const int j = c * kWtKeys + (warp & 3) * 32 + lane;
+        float* dst = p.weights + static_cast<int64_t>(h) * p.capacity + j;
+        float had = 0.0f;
+        if (j < C) {
+          if (t > 0) had = *dst;
+          else if (p.prev && j < at0)
+            had = p.decay * p.prev[static_cast<int64_t>(h) * p.capacity + j];
+        }
+        ok = __all_sync(0xFFFFFFFFu, role_wait(&b_s[grp], (k >> 1) & 1, &s_dead));
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t ts = tmem + lanes + W::kTS + grp * kWtRows;
+        // every row sees the whole chunk: up to row 0's own place, from the last row's window on
+        const bool whole = (c + 1) * kWtKeys <= at0 + 1 &&
+                           (p.window == 0 || c * kWtKeys >= C - p.window);
+        float s0 = 0.0f, s1 = 0.0f;
+        for (int r = 0; r < R; r += 16) {
+          uint32_t x[16];
+          tc::TmemIo<16>::load(ts + r, x);
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(slope + r + i);
+            const float4 o = *reinterpret_cast<const float4*>(off + r + i);
+            float y0, y1, y2, y3;
+            fma2(y0, y1, __uint_as_float(x[i]), __uint_as_float(x[i + 1]), f.x, f.y, o.x, o.y);
+            fma2(y2, y3, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]), f.z, f.w, o.z, o.w);
+            y0 = tc::ex2(y0), y1 = tc::ex2(y1), y2 = tc::ex2(y2), y3 = tc::ex2(y3);
+            if (!whole) {
+              const int4 a = *reinterpret_cast<const int4*>(s_first[tb] + r + i);
+              const int4 b = *reinterpret_cast<const int4*>(s_last[tb] + r + i);
+              y0 = j >= a.x && j <= b.x ? y0 : 0.0f;
+              y1 = j >= a.y && j <= b.y ? y1 : 0.0f;
+              y2 = j >= a.z && j <= b.z ? y2 : 0.0f;
+              y3 = j >= a.w && j <= b.w ? y3 : 0.0f;
+            }
+            add2(s0, s1, s0, s1, y0, y1);
+            add2(s0, s1, s0, s1, y2, y3);
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_sfree[grp]);
+        if (j < C) *dst = had + (s0 + s1);
+      }
+      ++run;
+      return true;
+    });
+    // keys that no row sees keep what they had
+    if (ok) {
+      const int seen = min(C, fc * kWtKeys), rest = tiles == 0 ? C : seen;
+      const int64_t total = static_cast<int64_t>(p.hkv) * rest;
+      for (int64_t i = blockIdx.x * 256 + tid; i < total;
+           i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t h = i / rest, j = i - h * rest;
+        const int64_t at = h * p.capacity + j;
+        p.weights[at] = p.prev && j < at0 ? p.decay * p.prev[at] : 0.0f;
+      }
+    }
+    tc::fence_before_sync();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 12) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0 && s_dead) report(p.status, DFV_DEV_TIMEOUT);
+}
+
+template <int D, bool kQ4>
+dfv_status weights_launch(const WeightParams& p, cudaStream_t stream) {
+  using W = WeightShape<D, kQ4>;
+  static std::atomic<int> allowed[64];   // per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DFV_ERR_CUDA;
+  if (!allowed[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kv_weights_kernel<D, kQ4>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             W::kBytes) != cudaSuccess)
+      return DFV_ERR_CUDA;
+    allowed[dev].store(1, std::memory_order_release);
+  }
+  const int64_t most =
+      static_cast<int64_t>(p.hkv) * ((static_cast<int64_t>(p.capacity) + kWtKeys - 1) / kWtKeys);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(most < sm_count() ? most : sm_count()));
+  cfg.blockDim = dim3(kWtThreads);
+  cfg.dynamicSmemBytes = W::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_weights_kernel<D, kQ4>, p) == cudaSuccess ? DFV_OK
+                                                                               : DFV_ERR_CUDA;
+}
+
+template <int D>
+dfv_status weights_launch_f(const WeightParams& p, bool q4, cudaStream_t stream) {
+  return q4 ? weights_launch<D, true>(p, stream) : weights_launch<D, false>(p, stream);
+}
+
+}  // namespace dfv
+
+extern "C" dfv_status dfv_kv_weights(int n_rows, int n_q_heads, int n_kv_heads, int head_dim,
+                                     int window, int kv_format, int cache_capacity,
+                                     const int32_t* ctx_len, const void* k_cache, const void* q,
+                                     const float* lse, const int32_t* path,
+                                     const int32_t* accept_len, float scale, float decay,
+                                     const float* prev, float* weights, uint32_t* status,
+                                     dfv_stream_t stream) {
+  using namespace dfv;
+  if ((kv_format != DFV_KV_Q4_0 && kv_format != DFV_KV_F16) ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return DFV_ERR_UNSUPPORTED;
+  if (n_rows < 1 || n_rows > 65536 || n_kv_heads < 1 || n_q_heads < n_kv_heads ||
+      n_q_heads > 1024 || n_q_heads % n_kv_heads != 0 || window < 0 || cache_capacity < 1 ||
+      cache_capacity > (1 << 30) || scale != scale || decay != decay)
+    return DFV_ERR_INVALID;
+  if (!ctx_len || !k_cache || !q || !lse || !weights || !aligned(k_cache, 16) ||
+      !aligned(q, 16) || !aligned(lse, 4) || !aligned(prev, 4) || !aligned(weights, 4) ||
+      !aligned(ctx_len, 4) || !aligned(path, 4) || !aligned(accept_len, 4))
+    return DFV_ERR_INVALID;
+  if (scale <= 0.0f) scale = head_dim == 64 ? 0.125f : head_dim == 256 ? 0.0625f : 0.08838834765f;
+  const WeightParams p = {n_rows, n_q_heads, n_kv_heads, n_q_heads / n_kv_heads, window,
+                          cache_capacity, ctx_len, static_cast<const uint8_t*>(k_cache),
+                          static_cast<const __nv_bfloat16*>(q), lse, path, accept_len, scale,
+                          decay, prev, weights, status};
+  const bool q4 = kv_format == DFV_KV_Q4_0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return head_dim == 64    ? weights_launch_f<64>(p, q4, s)
+         : head_dim == 128 ? weights_launch_f<128>(p, q4, s)
+                           : weights_launch_f<256>(p, q4, s);
+}
