@@ -110,11 +110,11 @@ __device__ __forceinline__ int enc_depth(const EncodeParams& p, int row, int lan
 }
 
 template <typename TS, typename TD, int D, bool kVec>
-__global__ void __launch_bounds__(kEncWarps * 32)
+__global__ void __launch_bounds__(kEncWarps * 32, 4)
     encode_kernel(const __grid_constant__ EncodeParams p, int near) {
   constexpr int kLanes = D / 16;         // lanes of a head
   constexpr int kHeads = 32 / kLanes;    // heads of a warp at a time
-  constexpr int kAhead = sizeof(TS) == 2 ? 4 : 2;   // whose loads are in flight together
+  constexpr int kAhead = sizeof(TS) == 2 ? 2 : 1;   // iterations worked on together
   const int lane = threadIdx.x & 31;
   const uint32_t task = blockIdx.x * kEncWarps + (threadIdx.x >> 5);   // below 2^27
   const int row = static_cast<int>(task / static_cast<uint32_t>(p.splits));
@@ -140,18 +140,19 @@ __global__ void __launch_bounds__(kEncWarps * 32)
       return static_cast<const TS*>(p.v) + row * p.v_row + (h - p.hq - p.hkv) * p.v_head;
     return nullptr;
   };
-  EncLoad<TS, kVec> xa[kAhead], xb[kAhead];
-  auto fetch = [&](int it) {
+  // loads of the next iterations are in flight while these are worked on
+  EncLoad<TS, kVec> xa[2][kAhead], xb[2][kAhead];
+  auto fetch = [&](int it, int s) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const TS* src = it + u < it1 ? source(it + u) : nullptr;
       if (src) {
-        xa[u].load(src + ca);
-        xb[u].load(src + cb);
+        xa[s][u].load(src + ca);
+        xb[s][u].load(src + cb);
       }
     }
   };
-  fetch(it0);
+  fetch(it0, 0);
 
   int64_t pos;
   if (p.positions) {
@@ -173,8 +174,7 @@ __global__ void __launch_bounds__(kEncWarps * 32)
   }
   const bool norm = p.eps >= 0.0f;
 
-  for (int it = it0; it < it1; it += kAhead) {
-    if (it != it0) fetch(it);
+  auto work = [&](int it, int s) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (it + u >= it1) break;
@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(kEncWarps * 32)
       float a[8], b[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        a[e] = on ? xa[u].at(e) : 0.0f;
-        b[e] = on ? xb[u].at(e) : 0.0f;
+        a[e] = on ? xa[s][u].at(e) : 0.0f;
+        b[e] = on ? xb[s][u].at(e) : 0.0f;
       }
       const bool is_v = h >= p.hq + p.hkv;
       if (norm) {
@@ -206,29 +206,38 @@ __global__ void __launch_bounds__(kEncWarps * 32)
             wb[e] = g.x, wb[e + 1] = g.y, wb[e + 2] = g.z, wb[e + 3] = g.w;
           }
         }
-        const float r = is_v ? 1.0f : 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-        // squares that leave float32 (or vanish in it where eps does not hide
-        // them): the head once more in 64 bits
-        const bool wide = !is_v && on && (!(ss <= 1e37f) || (ss < 1e-25f && p.eps < 1e-15f));
+        // Squares that leave float32, or vanish in it where eps does not hide
+        // them: the head is brought to [1, 2) by a power of two first, and eps
+        // with it (where that leaves float32, eps is all there is).
+        float eps = p.eps;
+        const bool wide = !is_v && on && (ss > 1e37f || (ss < 1e-25f && eps < 1e-15f));
         if (__any_sync(0xFFFFFFFFu, wide)) {
-          double s2 = 0.0;
+          float m = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            s2 += static_cast<double>(a[e]) * a[e] + static_cast<double>(b[e]) * b[e];
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(a[e]), fabsf(b[e])));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          const int e2 = static_cast<int>(__float_as_uint(m) >> 23);
+          float sc = wide && m > 0.0f && m < INFINITY ? pow2i(max(127 - e2, -126)) : 1.0f;
+          if (!(eps * sc * sc < INFINITY)) sc = 1.0f;
+          eps = eps * sc * sc;
+          float s2 = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            a[e] *= sc;
+            b[e] *= sc;
+            s2 = fmaf(b[e], b[e], fmaf(a[e], a[e], s2));
+          }
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
-          const double rd = 1.0 / sqrt(s2 / D + static_cast<double>(p.eps));
+          ss = s2;
+        }
+        const float r = is_v ? 1.0f : 1.0f / sqrtf(ss * (1.0f / D) + eps);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[e] = wide ? static_cast<float>(a[e] * rd) * wa[e] : a[e] * r * wa[e];
-            b[e] = wide ? static_cast<float>(b[e] * rd) * wb[e] : b[e] * r * wb[e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[e] = a[e] * r * wa[e];
-            b[e] = b[e] * r * wb[e];
-          }
+        for (int e = 0; e < 8; ++e) {
+          a[e] = a[e] * r * wa[e];
+          b[e] = b[e] * r * wb[e];
         }
       }
       if (turned && !is_v) {
@@ -258,6 +267,12 @@ __global__ void __launch_bounds__(kEncWarps * 32)
         enc_store(dst + cb, b);
       }
     }
+  };
+  for (int it = it0; it < it1; it += 2 * kAhead) {
+    fetch(it + kAhead, 1);
+    work(it, 0);
+    fetch(it + 2 * kAhead, 0);
+    work(it + kAhead, 1);
   }
 }
 

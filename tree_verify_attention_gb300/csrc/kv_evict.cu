@@ -9,10 +9,10 @@
 // bits of the weights' ordered bits find the smallest kept weight and how many
 // equal ones are kept; a last pass counts in position order and writes the list.
 // A head belongs to a cluster of up to 8 CTAs, each with its own run of
-// positions; they read each other's histograms, so nothing goes through memory
-// and no counter has to be reset. It is bound by latency: four passes over half a
-// megabyte a head at most. The copy is a gather of whole rows and bound by
-// memory.
+// positions, held in registers up to 131072 of them; they add their histograms
+// up in each other's shared memory, so nothing goes through memory and no counter
+// has to be reset. It is bound by latency: four rounds of a few us. The copy is a
+// gather of whole rows and bound by memory.
 
 #include "common.cuh"
 
@@ -47,27 +47,32 @@ __device__ __forceinline__ int ev_ctx(const EvictParams& p, bool tell) {
   return max(0, min(C, p.capacity));
 }
 
-__device__ __forceinline__ uint32_t ev_remote(const uint32_t* p, int rank) {
-  uint64_t a;
-  uint32_t v;
-  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(p), "r"(rank));
-  asm volatile("ld.u32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
-  return v;
+__device__ __forceinline__ void ev_remote_add(uint32_t* p, uint32_t v, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ void ev_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// A thread's weights stay in registers where its run is that short.
+constexpr int kEvHeld = 16;
+
+template <bool kHeld>
 __global__ void __launch_bounds__(kEvThreads, 1)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
-  // two in turn: one is read by the others while the next is filled
-  __shared__ uint32_t s_hist[2][kEvBins];
-  __shared__ uint32_t s_warp[2][kEvWarps], s_total[2];
+  __shared__ uint32_t s_hist[kEvBins];        // this CTA's
+  __shared__ __align__(8) uint32_t s_all[3][kEvBins];      // the cluster's, one for each pass
+  __shared__ uint32_t s_warp[2][kEvWarps], s_before[2];
   __shared__ uint32_t s_bin, s_above;
   int cs, rank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int h = blockIdx.x / cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int b = tid; b < 3 * kEvBins; b += kEvThreads) s_all[0][b] = 0;
+  if (tid < 2) s_before[tid] = 0;
+  ev_cluster_sync();   // everyone's sums are zero
   grid_dep_wait();
   grid_dep_launch_dependents();   // (after the wait: see common.cuh)
   const int C = ev_ctx(p, blockIdx.x == 0 && tid == 0);
@@ -82,8 +87,44 @@ __global__ void __launch_bounds__(kEvThreads, 1)
   const bool all = C <= p.keep;
   const int s0 = all ? C : p.sinks, s1 = all ? C : C - p.recent;
   uint32_t need = all ? 0 : static_cast<uint32_t>(p.keep - p.sinks - p.recent);
+  // each CTA has a run of positions, each of its warps a run of that
   const int lo = static_cast<int>(static_cast<int64_t>(C) * rank / cs);
   const int hi = static_cast<int>(static_cast<int64_t>(C) * (rank + 1) / cs);
+  const int steps = ((hi - lo + kEvWarps - 1) / kEvWarps + 31) / 32;
+  const int j0 = min(hi, lo + warp * steps * 32), j1 = min(hi, j0 + steps * 32);
+  float held[kHeld ? kEvHeld : 1];
+  if constexpr (kHeld) {
+#pragma unroll
+    for (int i = 0; i < kEvHeld; ++i) {
+      const int j = j0 + i * 32 + lane;
+      held[i] = j < j1 ? w[j] : 0.0f;
+    }
+  }
+  auto each = [&](auto f) {   // f(position, weight): every lane of the warp, j >= j1 too
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int i = 0; i < kEvHeld; ++i)
+        if (i < steps) f(j0 + i * 32 + lane, held[i]);
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < steps; ++i) {
+        const int j = j0 + i * 32 + lane;
+        f(j, j < j1 ? w[j] : 0.0f);
+      }
+    }
+  };
+  // Sum over the warps before this one, and over all; s_warp[k] holds each warp's.
+  auto warps_before = [&](int k, uint32_t& total) {
+    uint32_t v = s_warp[k][lane];
+    const uint32_t mine = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    total = __shfl_sync(0xFFFFFFFFu, v, 31);
+    return __shfl_sync(0xFFFFFFFFu, v - mine, warp);
+  };
 
   // ---- the smallest kept weight, 11, 11 and 10 bits at a time
   uint32_t prefix = 0xFFFFFFFFu;   // no place: nothing reaches it
@@ -93,24 +134,25 @@ __global__ void __launch_bounds__(kEvThreads, 1)
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass < 2 ? 11 : 10, shift = 32 - known - bits;
-      uint32_t* hist = s_hist[pass & 1];
-      for (int b = tid; b < kEvBins; b += kEvThreads) hist[b] = 0;
+      for (int b = tid; b < kEvBins; b += kEvThreads) s_hist[b] = 0;
       __syncthreads();
-      const int a = max(lo, s0), e = min(hi, s1);
-#pragma unroll 4
-      for (int j = a + tid; j < e; j += kEvThreads) {
-        const uint32_t o = ev_order(w[j]);
-        if (known == 0 || (o >> (32 - known)) == (prefix >> (32 - known)))
-          atomicAdd(&hist[(o >> shift) & ((1u << bits) - 1u)], 1u);
+      each([&](int j, float x) {
+        const uint32_t o = ev_order(x);
+        if (j < j1 && j >= s0 && j < s1 &&
+            (known == 0 || (o >> (32 - known)) == (prefix >> (32 - known))))
+          atomicAdd(&s_hist[(o >> shift) & ((1u << bits) - 1u)], 1u);
+      });
+      __syncthreads();
+      // few bins are not empty: they are added up in every CTA
+      for (int b = tid; b < kEvBins; b += kEvThreads) {
+        const uint32_t v = s_hist[b];
+        if (v)
+          for (int r = 0; r < cs; ++r) ev_remote_add(&s_all[pass][b], v, r);
       }
       ev_cluster_sync();
       // bins from the largest down, two a thread: where the count reaches `need`
-      uint32_t c[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        c[k] = 0;
-        for (int r = 0; r < cs; ++r) c[k] += ev_remote(&hist[kEvBins - 1 - (2 * tid + k)], r);
-      }
+      const uint2 two = *reinterpret_cast<const uint2*>(&s_all[pass][kEvBins - 2 - 2 * tid]);
+      const uint32_t c[2] = {two.y, two.x};
       uint32_t sum = c[0] + c[1];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -119,8 +161,8 @@ __global__ void __launch_bounds__(kEvThreads, 1)
       }
       if (lane == 31) s_warp[0][warp] = sum;
       __syncthreads();
-      for (int i = 0; i < warp; ++i) sum += s_warp[0][i];
-      uint32_t above = sum - c[0] - c[1];
+      uint32_t total;
+      uint32_t above = warps_before(0, total) + sum - c[0] - c[1];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (above < need && need <= above + c[k]) {   // one thread's
@@ -133,70 +175,55 @@ __global__ void __launch_bounds__(kEvThreads, 1)
       need -= s_above;
       prefix |= s_bin << shift;
       known += bits;
-      __syncthreads();
     }
   }
   // Now `need` of the weights that equal the smallest kept one stay.
 
-  // ---- the list, in position order: each warp has a run of positions
-  const int per = ((hi - lo + kEvWarps - 1) / kEvWarps + 31) / 32 * 32;
-  const int j0 = min(hi, lo + warp * per), j1 = min(hi, j0 + per);
-  auto classify = [&](int j, bool& over, bool& same) {
-    over = same = false;
-    if (j >= j1) return;
-    if (j < s0 || j >= s1) {
-      over = true;
-      return;
-    }
-    const uint32_t o = ev_order(w[j]);
-    over = need > 0 && o > prefix;
-    same = need > 0 && o == prefix;
+  // ---- the list, in position order
+  auto classify = [&](int j, float x, bool& over, bool& same) {
+    const bool in = j < j1, pinned = in && (j < s0 || j >= s1);
+    const uint32_t o = ev_order(x);
+    over = pinned || (in && need > 0 && o > prefix);
+    same = !pinned && in && need > 0 && o == prefix;
   };
   uint32_t n_over = 0, n_same = 0;
-#pragma unroll 4
-  for (int j = j0; j < j1; j += 32) {
+  each([&](int j, float x) {
     bool over, same;
-    classify(j + lane, over, same);
+    classify(j, x, over, same);
     n_over += __popc(__ballot_sync(0xFFFFFFFFu, over));
     n_same += __popc(__ballot_sync(0xFFFFFFFFu, same));
-  }
+  });
+  __syncthreads();   // s_warp has been read
   if (lane == 0) {
     s_warp[0][warp] = n_over;
     s_warp[1][warp] = n_same;
   }
   __syncthreads();
-  if (tid < 2) {
-    uint32_t t = 0;
-    for (int i = 0; i < kEvWarps; ++i) t += s_warp[tid][i];
-    s_total[tid] = t;
+  uint32_t t_over, t_same;
+  uint32_t at_over = warps_before(0, t_over), at_same = warps_before(1, t_same);
+  // a CTA adds its counts for those behind it
+  if (tid > rank && tid < cs) {
+    ev_remote_add(&s_before[0], t_over, tid);
+    ev_remote_add(&s_before[1], t_same, tid);
   }
   ev_cluster_sync();
-  uint32_t at_over = 0, at_same = 0;
-  for (int r = 0; r < rank; ++r) {
-    at_over += ev_remote(&s_total[0], r);
-    at_same += ev_remote(&s_total[1], r);
-  }
-  for (int i = 0; i < warp; ++i) {
-    at_over += s_warp[0][i];
-    at_same += s_warp[1][i];
-  }
-#pragma unroll 4
-  for (int j = j0; j < j1; j += 32) {
+  at_over += s_before[0];
+  at_same += s_before[1];
+  float* out = p.weights_out ? p.weights_out + static_cast<int64_t>(h) * p.dst_capacity : nullptr;
+  each([&](int j, float x) {
     bool over, same;
-    classify(j + lane, over, same);
+    classify(j, x, over, same);
     const unsigned bo = __ballot_sync(0xFFFFFFFFu, over), bs = __ballot_sync(0xFFFFFFFFu, same);
     const unsigned below = (1u << lane) - 1u;
     const uint32_t eo = at_over + __popc(bo & below), es = at_same + __popc(bs & below);
     if (over || (same && es < need)) {
       const uint32_t at = eo + min(es, need);
-      kept[at] = j + lane;
-      if (p.weights_out)
-        p.weights_out[static_cast<int64_t>(h) * p.dst_capacity + at] = w[j + lane];
+      kept[at] = j;
+      if (out) out[at] = x;
     }
     at_over += __popc(bo);
     at_same += __popc(bs);
-  }
-  ev_cluster_sync();   // the totals have been read
+  });
 }
 
 struct MoveParams {
@@ -250,53 +277,90 @@ struct ReadRowsParams {
   int64_t stride_row, stride_head;
 };
 
+template <bool kVec>
 __device__ __forceinline__ void put8(float* d, const float* x) {
+  if constexpr (kVec) {
+    reinterpret_cast<float4*>(d)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(d)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) d[i] = x[i];
+    for (int i = 0; i < 8; ++i) d[i] = x[i];
+  }
 }
+template <bool kVec>
 __device__ __forceinline__ void put8(__nv_bfloat16* d, const float* x) {
+  if constexpr (kVec) {
+    uint4 o;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) d[i] = __float2bfloat16_rn(x[i]);
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(d) = o;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = __float2bfloat16_rn(x[i]);
+  }
 }
 
-// Eight values of a row per thread and step.
-template <typename T, bool kF16>
+// Eight values of a row per thread, several rows in flight; a row's threads are
+// neighbours, so writes are contiguous (kVec: 16 bytes each).
+template <typename T, bool kF16, bool kVec>
 __global__ void __launch_bounds__(256) read_rows_kernel(const __grid_constant__ ReadRowsParams p) {
+  constexpr int kAhead = 4;
   grid_dep_wait();
   grid_dep_launch_dependents();   // (after the wait: see common.cuh)
-  const int groups = p.head_dim / 8, h = blockIdx.y;
+  const int shift = p.head_dim == 256 ? 5 : p.head_dim == 128 ? 4 : 3;   // threads of a row
+  const int g = threadIdx.x & ((1 << shift) - 1), h = blockIdx.y;
+  const int rows = 256 >> shift, step = gridDim.x * rows;
   const int64_t row_bytes = kv_row_bytes(kF16 ? DFV_KV_F16 : DFV_KV_Q4_0, p.head_dim);
-  const uint8_t* src = (blockIdx.z ? p.v : p.k) + static_cast<int64_t>(h) * p.capacity * row_bytes;
-  T* dst = static_cast<T*>(blockIdx.z ? p.v_dst : p.k_dst) + h * p.stride_head;
-  const int64_t total = static_cast<int64_t>(p.n_rows) * groups;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = i / groups;
-    const int g = static_cast<int>(i - r * groups);
-    const uint8_t* row = src + (p.pos0 + r) * row_bytes;
-    float x[8];
-    if constexpr (kF16) {
-      const uint4 v = *reinterpret_cast<const uint4*>(row + g * 16);
-      const __half2* q = reinterpret_cast<const __half2*>(&v);
+  const uint8_t* src = (blockIdx.z ? p.v : p.k) +
+                       (static_cast<int64_t>(h) * p.capacity + p.pos0) * row_bytes;
+  T* dst = static_cast<T*>(blockIdx.z ? p.v_dst : p.k_dst) + h * p.stride_head + g * 8;
+  // dims [8 g, + 8) of a Q4_0 block: low nibbles of its first 16 values, high of its last
+  const int off = kF16 ? g * 16 : (g >> 2) * 18, nib = (g & 2) ? 4 : 0, word = 1 + (g & 1) * 4;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows + (threadIdx.x >> shift);
+       r0 < p.n_rows; r0 += static_cast<int64_t>(kAhead) * step) {
+    uint32_t in[kAhead][5];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(q[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
-      }
-    } else {
-      // dims [8 (g % 4), + 8) of a block: low nibbles of its first 16, high of its last
-      const uint16_t* blk = reinterpret_cast<const uint16_t*>(row + (g >> 2) * 18);
-      const float d = __half2float(__ushort_as_half(blk[0]));
-      const int nib = (g & 2) ? 4 : 0;
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t r = r0 + static_cast<int64_t>(u) * step;
+      if (r >= p.n_rows) break;
+      const uint8_t* a = src + r * row_bytes + off;
+      if constexpr (kF16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(a);
+        in[u][0] = v.x, in[u][1] = v.y, in[u][2] = v.z, in[u][3] = v.w;
+      } else {
+        const uint16_t* b = reinterpret_cast<const uint16_t*>(a);
+        in[u][4] = b[0];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t c = static_cast<uint32_t>(blk[1 + (g & 1) * 4 + e]) >> nib;
-        x[2 * e] = (static_cast<float>(c & 15u) - 8.0f) * d;
-        x[2 * e + 1] = (static_cast<float>((c >> 8) & 15u) - 8.0f) * d;
+        for (int e = 0; e < 4; ++e) in[u][e] = b[word + e];
       }
     }
-    put8(dst + r * p.stride_row + g * 8, x);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t r = r0 + static_cast<int64_t>(u) * step;
+      if (r >= p.n_rows) break;
+      float x[8];
+      if constexpr (kF16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[u][e]));
+          x[2 * e] = f.x;
+          x[2 * e + 1] = f.y;
+        }
+      } else {
+        const float d = __half2float(__ushort_as_half(static_cast<uint16_t>(in[u][4])));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t c = in[u][e] >> nib;
+          x[2 * e] = (static_cast<float>(c & 15u) - 8.0f) * d;
+          x[2 * e + 1] = (static_cast<float>((c >> 8) & 15u) - 8.0f) * d;
+        }
+      }
+      put8<kVec>(dst + r * p.stride_row, x);
+    }
   }
 }
 
@@ -327,6 +391,12 @@ dfv_status move_launch(const MoveParams& p, cudaStream_t stream) {
   const int64_t x = want < most ? want : most;
   return launch_after(evict_move_kernel<V, kPieces>, p,
                       dim3(static_cast<unsigned>(x < 1 ? 1 : x), p.heads, 2), 256, stream);
+}
+
+template <typename T, bool kF16>
+dfv_status read_launch(const ReadRowsParams& p, dim3 grid, bool vec, cudaStream_t stream) {
+  return vec ? launch_after(read_rows_kernel<T, kF16, true>, p, grid, 256, stream)
+             : launch_after(read_rows_kernel<T, kF16, false>, p, grid, 256, stream);
 }
 
 }  // namespace dfv
@@ -362,7 +432,11 @@ extern "C" dfv_status dfv_kv_evict(int n_kv_heads, int head_dim, int kv_format,
   // a CTA for about 8192 positions of a head, eight at most
   int cs = 1;
   while (cs < kEvMaxCluster && cache_capacity > cs * 8192) cs <<= 1;
-  dfv_status st = launch_after(evict_select_kernel, e, dim3(n_kv_heads * cs), kEvThreads, s, cs);
+  // (a warp's run is rounded up to whole steps of 32)
+  const bool held = cache_capacity <= cs * kEvThreads * kEvHeld;
+  dfv_status st =
+      held ? launch_after(evict_select_kernel<true>, e, dim3(n_kv_heads * cs), kEvThreads, s, cs)
+           : launch_after(evict_select_kernel<false>, e, dim3(n_kv_heads * cs), kEvThreads, s, cs);
   if (st != DFV_OK) return st;
   const MoveParams m = {n_kv_heads, cache_capacity, dst_capacity, keep, ctx_len, kept,
                         static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
@@ -398,16 +472,17 @@ extern "C" dfv_status dfv_kv_read_rows(int n_kv_heads, int head_dim, int kv_form
                             static_cast<const uint8_t*>(k_cache),
                             static_cast<const uint8_t*>(v_cache), k_dst, v_dst, stride_row,
                             stride_head};
-  const int64_t want = (static_cast<int64_t>(n_rows) * (head_dim / 8) + 255) / 256;
-  const int64_t most = (static_cast<int64_t>(sm_count()) * 16 + 2 * n_kv_heads - 1) /
+  const int64_t want = (static_cast<int64_t>(n_rows) * (head_dim / 8) + 1023) / 1024;
+  const int64_t most = (static_cast<int64_t>(sm_count()) * 8 + 2 * n_kv_heads - 1) /
                        (2 * n_kv_heads);
   const dim3 grid(static_cast<unsigned>(want < most ? want : most), n_kv_heads, 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t e16 = static_cast<int64_t>(16 / size);
+  const bool vec = aligned(k_dst, 16) && aligned(v_dst, 16) && stride_row % e16 == 0 &&
+                   stride_head % e16 == 0;
   if (kv_format == DFV_KV_F16)
-    return dst_dtype == DFV_DTYPE_F32
-               ? launch_after(read_rows_kernel<float, true>, p, grid, 256, s)
-               : launch_after(read_rows_kernel<__nv_bfloat16, true>, p, grid, 256, s);
-  return dst_dtype == DFV_DTYPE_F32
-             ? launch_after(read_rows_kernel<float, false>, p, grid, 256, s)
-             : launch_after(read_rows_kernel<__nv_bfloat16, false>, p, grid, 256, s);
+    return dst_dtype == DFV_DTYPE_F32 ? read_launch<float, true>(p, grid, vec, s)
+                                      : read_launch<__nv_bfloat16, true>(p, grid, vec, s);
+  return dst_dtype == DFV_DTYPE_F32 ? read_launch<float, false>(p, grid, vec, s)
+                                    : read_launch<__nv_bfloat16, false>(p, grid, vec, s);
 }

@@ -15,9 +15,11 @@
 // exact. Query rows are scaled by a power of two each, which the exponent's
 // factor takes back.
 //
-// A CTA works through a run of 128-key chunks of (at most a few) heads: one warp
-// copies raw rows into a ring, four convert them into TMEM in parts of 64 dims,
-// one issues the products, two groups of four take turns at the chunks' sums.
+// A CTA works through a run of 128-key chunks of (at most a few) heads, in parts
+// of 64 dims. Q4_0: one warp copies raw rows into a ring, two groups of four
+// convert parts in turn into TMEM, the product's A operand. F16: the two groups
+// copy parts straight into swizzled tiles, A from shared memory. One warp
+// issues the products; two groups of four warps take turns at the chunks' sums.
 
 #include <atomic>
 
@@ -28,23 +30,28 @@
 namespace dfv {
 
 constexpr int kWtKeys = 128;
-constexpr int kWtRows = 128;     // query rows of a tile, at most
-constexpr int kWtThreads = 14 * 32;
+constexpr int kWtMma = 16, kWtRaw = 17;      // warps 0-7: sums, 8-15: operands
+constexpr int kWtThreads = 18 * 32;
 
 template <int D, bool kQ4>
 struct WeightShape {
+  static constexpr int kRows = kQ4 || D == 256 ? 128 : 256;   // query rows of a tile, at most
   static constexpr int kRowBytes = kQ4 ? D / 32 * 18 : D * 2;
-  static constexpr int kPitch = kQ4 ? kRowBytes : kRowBytes + 16;   // of a row in shared memory
-  static constexpr int kStage = (kWtKeys * kPitch + 16 + 127) / 128 * 128;
-  static constexpr int kStages = kQ4 ? 4 : D == 256 ? 2 : 3;
-  static constexpr int kQBytes = kWtRows * D * 2;
-  static constexpr int kOffRaw = kQBytes;
-  static constexpr int kBytes = kOffRaw + kStages * kStage + 1024;
-  static constexpr int kParts = D / 64;               // of a chunk
-  static constexpr int kPartCols = kQ4 ? 64 : 32;     // TMEM columns of a part: hi, lo
-  static constexpr int kRing = 256 / kPartCols;       // parts in TMEM
-  static constexpr uint32_t kTS = 256;                // two buffers of scores
+  static constexpr int kParts = D / 64;                       // of a chunk
+  static constexpr int kPartCols = 64;                        // Q4_0: TMEM columns, hi and lo
+  static constexpr int kPartBytes = kWtKeys * 128;            // F16: a tile of 64 dims
+  static constexpr int kRing = kQ4 ? 256 / kPartCols : 8;     // parts
+  static constexpr int kStages = 4;                           // Q4_0: raw chunks
+  static constexpr int kStage = (kWtKeys * kRowBytes + 16 + 127) / 128 * 128;
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kBytes = kQBytes + (kQ4 ? kStages * kStage : kRing * kPartBytes) + 1024;
+  static constexpr uint32_t kTS = kQ4 ? 256 : 0;              // two buffers of kRows scores
+  static_assert(kTS + 2 * kRows <= 512, "TMEM columns");
   static_assert(kBytes <= 220 * 1024, "shared memory");
+};
+
+template <int kN> struct Columns {
+  static constexpr int value = kN;
 };
 
 struct WeightParams {
@@ -60,7 +67,7 @@ struct WeightParams {
   uint32_t* status;
 };
 
-// Place of dim c of a block of 32 in the operands' K order: a word of four code
+// Place of dim c of a block of 32 in the operands' K order (Q4_0): a word of four code
 // bytes gives pairs (bytes 0, 2 low), (0, 2 high), (1, 3 low), (1, 3 high).
 // Eight consecutive places are word w's dims 4w + {0, 2, 16, 18, 1, 3, 17, 19}.
 
@@ -71,7 +78,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
-  uint8_t* sRaw = smem + W::kOffRaw;
+  uint8_t* sK = smem + W::kQBytes;                    // raw rows, or tiles
   __shared__ uint64_t b_raw[4], b_read[4];            // raw rows landed, read
   __shared__ uint64_t b_part[8], b_free[8];           // operand part written, multiplied
   __shared__ uint64_t b_s[2], b_sfree[2];             // scores there, read
@@ -80,8 +87,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   __shared__ volatile int s_dead;
   // of a tile's columns, two tiles in turn: the exponent's slope and offset,
   // and the first and last position that is seen
-  __shared__ __align__(16) float s_slope[2][kWtRows], s_off[2][kWtRows];
-  __shared__ __align__(16) int s_first[2][kWtRows], s_last[2][kWtRows];
+  __shared__ __align__(16) float s_slope[2][W::kRows], s_off[2][W::kRows];
+  __shared__ __align__(16) int s_first[2][W::kRows], s_last[2][W::kRows];
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp =
@@ -89,7 +96,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b_raw[i], 1);
-      mbar_init(&b_read[i], 4);
+      mbar_init(&b_read[i], W::kParts == 1 ? 4 : 8);   // the groups that read it
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(&b_part[i], 4);
@@ -107,7 +114,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   }
   grid_dep_wait();
   grid_dep_launch_dependents();   // (after the wait: see common.cuh)
-  if (warp == 12) tc::tmem_alloc(&s_tmem, 512);
+  if (warp == kWtMma) tc::tmem_alloc(&s_tmem, 512);
 
   // ---- the problem, the same in every thread
   int C = __reduce_max_sync(0xFFFFFFFFu, *p.ctx_len);
@@ -122,7 +129,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     n = max(0, min(L, n));
   }
   const int rows = n * p.group;                       // query rows of a KV head
-  const int tiles = (rows + kWtRows - 1) / kWtRows;
+  const int tiles = (rows + W::kRows - 1) / W::kRows;
   // columns of a tile, balanced, in steps of 16
   const int R = tiles == 0 ? 16 : ((rows + tiles - 1) / tiles + 15) / 16 * 16;
   // positions: row s stands at C - n + s; chunks [fc, lc) are seen by some row
@@ -149,13 +156,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   const uint32_t tmem = s_tmem;
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // quadrant's first lane << 16
 
-  if (warp == 13) {
-    // ------------------------------------------------------ raw rows
+  if (warp == kWtRaw) {
+    // ------------------------------------------------------ raw rows (Q4_0)
     bool ok = true;
     int k = 0;   // chunks so far
     fence_proxy_async_global();   // what earlier kernels wrote, to the copy engine
     runs([&](int h, int c0, int c1, int) {
-      for (int c = c0; c < c1; ++c, ++k) {
+      for (int c = c0; kQ4 && c < c1; ++c, ++k) {
         const int st = k % W::kStages;
         if (k >= W::kStages) {
           ok = role_wait(&b_read[st], (k / W::kStages - 1) & 1, &s_dead);
@@ -164,28 +171,19 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         const int live = min(kWtKeys, C - c * kWtKeys);
         const int64_t from = (static_cast<int64_t>(h) * p.capacity + c * kWtKeys) * W::kRowBytes;
-        uint8_t* dst = sRaw + st * W::kStage;
-        if (kQ4) {
-          // one piece, from the 16-byte boundary before its start; what is
-          // behind the last boundary by words
-          const int64_t a = from & ~static_cast<int64_t>(15);
-          const int64_t e = from + static_cast<int64_t>(live) * W::kRowBytes;
-          const int64_t b = e & ~static_cast<int64_t>(15);
-          if (lane < static_cast<int>(e - b) / 4)
-            *reinterpret_cast<uint32_t*>(dst + (b - a) + lane * 4) =
-                *reinterpret_cast<const uint32_t*>(p.k + b + lane * 4);
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&b_raw[st], static_cast<uint32_t>(b - a));
-            if (b > a) bulk_g2s(dst, p.k + a, static_cast<uint32_t>(b - a), &b_raw[st]);
-          }
-        } else {
-          if (lane == 0)
-            mbar_arrive_expect_tx(&b_raw[st], static_cast<uint32_t>(live * W::kRowBytes));
-          __syncwarp();
-          for (int r = lane; r < live; r += 32)
-            bulk_g2s(dst + r * W::kPitch, p.k + from + static_cast<int64_t>(r) * W::kRowBytes,
-                     W::kRowBytes, &b_raw[st]);
+        uint8_t* dst = sK + st * W::kStage;
+        // one piece, from the 16-byte boundary before its start; what is
+        // behind the last boundary by words
+        const int64_t a = from & ~static_cast<int64_t>(15);
+        const int64_t e = from + static_cast<int64_t>(live) * W::kRowBytes;
+        const int64_t b = e & ~static_cast<int64_t>(15);
+        if (lane < static_cast<int>(e - b) / 4)
+          *reinterpret_cast<uint32_t*>(dst + (b - a) + lane * 4) =
+              *reinterpret_cast<const uint32_t*>(p.k + b + lane * 4);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&b_raw[st], static_cast<uint32_t>(b - a));
+          if (b > a) bulk_g2s(dst, p.k + a, static_cast<uint32_t>(b - a), &b_raw[st]);
         }
       }
       return true;
@@ -194,7 +192,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     if (s_dead)
       for (int i = max(0, k - W::kStages); i < k; ++i)
         mbar_wait_bounded(&b_raw[i % W::kStages], (i / W::kStages) & 1);
-  } else if (warp == 12) {
+  } else if (warp == kWtMma) {
     // ------------------------------------------------------ products
     bool ok = true;
     int k = 0, part = 0, run = 0;
@@ -216,16 +214,20 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           ok = all_wait(&b_part[slot], (part / W::kRing) & 1);
           if (!ok) break;
           if (tc::elect_one()) {
-            const uint32_t a = tmem + slot * W::kPartCols;
+            const uint32_t d = tmem + W::kTS + buf * W::kRows;
+            if constexpr (kQ4) {
+              const uint32_t a = tmem + slot * W::kPartCols;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_f16_ts(tmem + W::kTS + buf * kWtRows, a + kk * 8,
-                             qd + i * q_block + kk * 2, idesc, i > 0 || kk > 0 ? 1u : 0u);
-            if (kQ4) {
+              for (int kk = 0; kk < 8; ++kk)   // hi, then lo
+                tc::mma_f16_ts(d, a + kk * 8, qd + i * q_block + (kk & 3) * 2, idesc,
+                               i > 0 || kk > 0 ? 1u : 0u);
+            } else {
+              const uint64_t a =
+                  tc::smem_desc_sw128(smem_u32(sK + slot * W::kPartBytes), 1024);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                tc::mma_f16_ts(tmem + W::kTS + buf * kWtRows, a + 32 + kk * 8,
-                               qd + i * q_block + kk * 2, idesc, 1u);
+                tc::mma_f16(d, a + kk * 2, qd + i * q_block + kk * 2, idesc,
+                            i > 0 || kk > 0 ? 1u : 0u);
             }
             tc::commit(&b_free[slot]);
             if (i == W::kParts - 1) tc::commit(&b_s[buf]);
@@ -245,64 +247,62 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     __syncwarp();
     mbar_wait_bounded(&b_end, 0);
   } else if (warp >= 8) {
-    // ------------------------------------------------------ rows to operands
-    const int slot = (warp & 3) * 32 + lane;   // key of the chunk
+    // ------------------------------------------------------ operands
+    // Two groups of four warps, each with every other part.
+    const int set = (warp >> 2) & 1, slot = (warp & 3) * 32 + lane;   // key of the chunk
     bool ok = true;
     int k = 0, part = 0;
-    auto take = [&]() {
+    auto take = [&]() {   // the part's place is free
       if (part >= W::kRing)
         ok = role_wait(&b_free[part % W::kRing], (part / W::kRing - 1) & 1, &s_dead);
       ok = __all_sync(0xFFFFFFFFu, ok);   // the TMEM stores are warp-wide
-      tc::fence_after_sync();
     };
-    auto give = [&]() {
-      tc::store_wait();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b_part[part % W::kRing]);
-      ++part;
-    };
-    runs([&](int h, int c0, int c1, int) {
-      for (int c = c0; ok && c < c1; ++c, ++k) {
-        const int st = k % W::kStages;
-        ok = __all_sync(0xFFFFFFFFu, role_wait(&b_raw[st], (k / W::kStages) & 1, &s_dead));
-        if (!ok) break;
-        const uint8_t* row = sRaw + st * W::kStage + slot * W::kPitch;
-        auto done = [&]() {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&b_read[st]);
-        };
-        if constexpr (kQ4) {
-          if (D < 256)   // rows of 36 or 72 bytes: the piece began at a 16-byte boundary
-            row += ((static_cast<int64_t>(h) * p.capacity + c * kWtKeys) * W::kRowBytes) & 15;
-          // a row is nine pieces of D / 16 bytes, two blocks of 18 nine words
-          constexpr int kWords = W::kRowBytes / 4;
-          uint32_t in[kWords];
-          if constexpr (D == 256) {
-#pragma unroll
-            for (int i = 0; i < 9; ++i) {
-              const uint4 v = *reinterpret_cast<const uint4*>(row + i * 16);
-              in[4 * i] = v.x, in[4 * i + 1] = v.y, in[4 * i + 2] = v.z, in[4 * i + 3] = v.w;
-            }
-          } else if constexpr (D == 128) {
-#pragma unroll
-            for (int i = 0; i < 9; ++i) {
-              const uint2 v = *reinterpret_cast<const uint2*>(row + i * 8);
-              in[2 * i] = v.x, in[2 * i + 1] = v.y;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 9; ++i) in[i] = *reinterpret_cast<const uint32_t*>(row + i * 4);
+    if constexpr (kQ4) {
+      runs([&](int h, int c0, int c1, int) {
+        for (int c = c0; ok && c < c1; ++c, ++k) {
+          if (W::kParts == 1 && (part & 1) != set) {
+            ++part;
+            continue;
           }
-          done();   // every code is in registers
+          const int st = k % W::kStages;
+          ok = __all_sync(0xFFFFFFFFu, role_wait(&b_raw[st], (k / W::kStages) & 1, &s_dead));
+          if (!ok) break;
+          // rows of 36 or 72 bytes: the piece began at a 16-byte boundary
+          const uint8_t* row = sK + st * W::kStage + slot * W::kRowBytes;
+          if (D < 256)
+            row += ((static_cast<int64_t>(h) * p.capacity + c * kWtKeys) * W::kRowBytes) & 15;
+          // A part is two blocks of 18 bytes, nine words, read by pieces of D / 16
+          // bytes (without bank conflicts: the rows are nine of them apart).
+          constexpr int kE = D / 64;                  // words of a piece
+          constexpr int kLast = (W::kParts - 1) & ~1; // first of the last two parts
 #pragma unroll
-          for (int i = 0; i < W::kParts; ++i) {
+          for (int i = 0; i < W::kParts; ++i, ++part) {
+            if ((part & 1) != set) continue;
+            constexpr int kPieces = D == 256 ? 3 : D == 128 ? 5 : 9;
+            const int p0 = 9 * i / kE;                // the piece with the part's first word
+            uint32_t in[kPieces * kE + 1];
+#pragma unroll
+            for (int e = 0; e < kPieces; ++e) {
+              if constexpr (D == 256) {
+                const uint4 v = *reinterpret_cast<const uint4*>(row + (p0 + e) * 16);
+                in[4 * e] = v.x, in[4 * e + 1] = v.y, in[4 * e + 2] = v.z, in[4 * e + 3] = v.w;
+              } else if constexpr (D == 128) {
+                const uint2 v = *reinterpret_cast<const uint2*>(row + (p0 + e) * 8);
+                in[2 * e] = v.x, in[2 * e + 1] = v.y;
+              } else {
+                in[e] = *reinterpret_cast<const uint32_t*>(row + (p0 + e) * 4);
+              }
+            }
+            if (i >= kLast) {   // the group's last part: every code is in registers
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&b_read[st]);
+            }
+            const uint32_t* words = in + (9 * i - p0 * kE);
             uint32_t hi[32], lo[32];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              // words of the block: scale and codes are 2 bytes apart from words in
-              // the first of the two
-              const uint32_t* w = in + 9 * i + 4 * b;
+              // codes follow the scale: words of the first block are 2 bytes off
+              const uint32_t* w = words + 4 * b;
               const uint32_t sc = b == 0 ? w[0] & 0xFFFFu : w[0] >> 16;
               const uint32_t d2 = sc | (sc << 16);
               const __half2 d = *reinterpret_cast<const __half2*>(&d2);
@@ -313,8 +313,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   // 0x6400 | code is 1024 + code
-                  const uint32_t y = ((x >> (e == 0 ? 0 : e == 1 ? 4 : e == 2 ? 8 : 12)) &
-                                      0x000F000Fu) | 0x64006400u;
+                  const uint32_t y = ((x >> (4 * e)) & 0x000F000Fu) | 0x64006400u;
                   const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
                   const __half2 a = __hmul2(v, d);
                   const __half2 r = __hfma2(v, d, __hneg2(a));
@@ -325,30 +324,60 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             }
             take();
             if (!ok) break;
+            tc::fence_after_sync();
             const uint32_t t = tmem + lanes + (part % W::kRing) * W::kPartCols;
             tc::TmemIo<32>::store(t, hi);
             tc::TmemIo<32>::store(t + 32, lo);
-            give();
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < W::kParts; ++i) {
-            uint32_t v[32];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint4 x = *reinterpret_cast<const uint4*>(row + i * 128 + j * 16);
-              v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
-            }
-            if (i == W::kParts - 1) done();
-            take();
-            if (!ok) break;
-            tc::TmemIo<32>::store(tmem + lanes + (part % W::kRing) * W::kPartCols, v);
-            give();
+            tc::store_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b_part[part % W::kRing]);
           }
         }
-      }
-      return ok;
-    });
+        return ok;
+      });
+    } else {
+      // A part: 128 rows of 128 bytes, eight 16-byte pieces a thread; a group
+      // has up to kLag + 1 parts in flight.
+      constexpr int kLag = W::kRing / 2 - 1;
+      int issued = 0, given = 0;   // of the group's parts
+      auto give = [&]() {          // this thread's oldest copies have landed
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_part[(2 * given + set) % W::kRing]);
+        ++given;
+      };
+      const int t = (warp & 3) * 32 + lane;
+      runs([&](int h, int c0, int c1, int) {
+        for (int c = c0; ok && c < c1; ++c) {
+          const int live = min(kWtKeys, C - c * kWtKeys);
+          const uint8_t* src =
+              p.k + (static_cast<int64_t>(h) * p.capacity + c * kWtKeys) * W::kRowBytes;
+          for (int i = 0; i < W::kParts; ++i, ++part) {
+            if ((part & 1) != set) continue;
+            take();
+            if (!ok) break;
+            uint8_t* dst = sK + (part % W::kRing) * W::kPartBytes;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int r = (t >> 3) + e * 16, j = t & 7;
+              if (r < live)
+                cp_async16(dst + tc::sw128_offset(r, j, kWtKeys),
+                           src + static_cast<int64_t>(r) * W::kRowBytes + i * 128 + j * 16);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            ++issued;
+            if (issued > kLag) {
+              asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+              give();
+            }
+          }
+        }
+        return ok;
+      });
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      while (ok && given < issued) give();
+    }
   } else {
     // ------------------------------------------------------ query rows, sums
     const int grp = warp >> 2;
@@ -356,76 +385,93 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     int k = 0, run = 0;
     runs([&](int h, int c0, int c1, int t) {
       const int r0 = t * R, live = min(R, rows - r0), tb = run & 1;
-      if (ok && run > 0)
-        ok = __all_sync(0xFFFFFFFFu, role_wait(&b_qfree, (run - 1) & 1, &s_dead));
-      // A warp takes a query row at a time: its largest magnitude becomes a
-      // power of two, the lanes' 16-byte pieces go to the operand.
-      for (int r = warp; ok && r < R; r += 8) {
-        float slope = 0.0f, off = -INFINITY;
-        int first = 0, last = -1;
-        uint2 a = make_uint2(0, 0), b = a;
-        uint32_t m = 0;
-        if (r < live) {
-          const int s = (r0 + r) / p.group, g = (r0 + r) - s * p.group;
-          int node = p.path ? p.path[s] : s;
-          if (node < 0 || node >= p.n_rows) {
-            if (lane == 0) report(p.status, DFV_DEV_BAD_PATH);
-            node = -1;
-          }
-          if (node >= 0) {
-            const int64_t row = static_cast<int64_t>(node) * p.hq + h * p.group + g;
-            // places 8 lane .. of the K order (Q4_0), or as they are
-            const __nv_bfloat16* src = p.q + row * D;
-            if (lane < D / 8) {
-              if (kQ4) {
-                const __nv_bfloat16* w = src + (lane >> 2) * 32 + (lane & 3) * 4;
-                a = *reinterpret_cast<const uint2*>(w);
-                b = *reinterpret_cast<const uint2*>(w + 16);
+      // Query rows: D / 8 lanes each, kBatch of a lane's rows loaded together.
+      // The largest magnitude of a row becomes a power of two.
+      constexpr int kLanes = D / 8, kPerStep = 8 * 32 / kLanes, kBatch = 4;
+      const int piece = lane % kLanes;
+      for (int rb = 0; rb < R; rb += kBatch * kPerStep) {
+        uint2 a[kBatch], b[kBatch];
+        float l[kBatch];
+        int s[kBatch];
+        bool bad[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = rb + i * kPerStep + warp * (32 / kLanes) + lane / kLanes;
+          a[i] = b[i] = make_uint2(0, 0);
+          l[i] = INFINITY;
+          s[i] = -1;
+          bad[i] = false;
+          if (r < live) {
+            const int step = (r0 + r) / p.group, g = (r0 + r) - step * p.group;
+            const int node = p.path ? p.path[step] : step;
+            bad[i] = node < 0 || node >= p.n_rows;
+            if (!bad[i]) {
+              const int64_t row = static_cast<int64_t>(node) * p.hq + h * p.group + g;
+              const __nv_bfloat16* src = p.q + row * D;
+              if (kQ4) {   // the places of a code word's dims
+                const __nv_bfloat16* w = src + (piece >> 2) * 32 + (piece & 3) * 4;
+                a[i] = *reinterpret_cast<const uint2*>(w);
+                b[i] = *reinterpret_cast<const uint2*>(w + 16);
               } else {
-                const uint4 v = *reinterpret_cast<const uint4*>(src + lane * 8);
-                a = make_uint2(v.x, v.y);
-                b = make_uint2(v.z, v.w);
+                const uint4 v = *reinterpret_cast<const uint4*>(src + piece * 8);
+                a[i] = make_uint2(v.x, v.y);
+                b[i] = make_uint2(v.z, v.w);
               }
-              m = __vmaxu2(__vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu),
-                           __vmaxu2(b.x & 0x7FFF7FFFu, b.y & 0x7FFF7FFFu));
-              m = max(m & 0xFFFFu, m >> 16);
-            }
-            m = __reduce_max_sync(0xFFFFFFFFu, m);
-            const float l = p.lse[row];
-            if (m >= 0x7F80u || !(fabsf(l) < INFINITY)) {
-              // a row that is not finite counts for nothing
-              if (lane == 0) report(p.status, DFV_DEV_NONFINITE);
-              a = b = make_uint2(0, 0);
-              m = 0;
-            } else {
-              off = -l * 1.44269504f;
-              last = at0 + s;
-              first = p.window > 0 ? at0 + s - p.window + 1 : 0;
+              l[i] = p.lse[row];
+              s[i] = step;
             }
           }
         }
-        const int e = max(static_cast<int>(m >> 7), 40);   // largest magnitude below 2^(e - 126)
-        const float f = pow2i(141 - e);                    // to below 2^15
-        if (off > -INFINITY) slope = p.scale * 1.44269504f * pow2i(e - 141);
-        if (lane < D / 8) {
-          auto half2_of = [&](uint32_t lo16, uint32_t hi16) {
-            return pack_half2(__uint_as_float(lo16 << 16) * f, __uint_as_float(hi16 << 16) * f);
-          };
-          uint4 o;
-          if (kQ4)   // dims {0, 2, 16, 18, 1, 3, 17, 19} of the word
-            o = make_uint4(half2_of(a.x & 0xFFFFu, a.y & 0xFFFFu),
-                           half2_of(b.x & 0xFFFFu, b.y & 0xFFFFu), half2_of(a.x >> 16, a.y >> 16),
-                           half2_of(b.x >> 16, b.y >> 16));
-          else
-            o = make_uint4(half2_of(a.x & 0xFFFFu, a.x >> 16), half2_of(a.y & 0xFFFFu, a.y >> 16),
-                           half2_of(b.x & 0xFFFFu, b.x >> 16), half2_of(b.y & 0xFFFFu, b.y >> 16));
-          *reinterpret_cast<uint4*>(sQ + tc::sw128_offset(r, lane, R)) = o;
-        }
-        if (lane == 0) {
-          s_slope[tb][r] = slope;
-          s_off[tb][r] = off;
-          s_first[tb][r] = first;
-          s_last[tb][r] = last;
+        // the last run's products have read theirs
+        if (rb == 0 && ok && run > 0)
+          ok = __all_sync(0xFFFFFFFFu, role_wait(&b_qfree, (run - 1) & 1, &s_dead));
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = rb + i * kPerStep + warp * (32 / kLanes) + lane / kLanes;
+          if (rb + i * kPerStep >= R) break;
+          uint32_t m = __vmaxu2(__vmaxu2(a[i].x & 0x7FFF7FFFu, a[i].y & 0x7FFF7FFFu),
+                                __vmaxu2(b[i].x & 0x7FFF7FFFu, b[i].y & 0x7FFF7FFFu));
+          m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          float slope = 0.0f, off = -INFINITY;
+          int first = 0, last = -1;
+          if (bad[i] && piece == 0) report(p.status, DFV_DEV_BAD_PATH);
+          if (s[i] >= 0 && (m >= 0x7F80u || !(fabsf(l[i]) < INFINITY))) {
+            // a row that is not finite counts for nothing
+            if (piece == 0) report(p.status, DFV_DEV_NONFINITE);
+            a[i] = b[i] = make_uint2(0, 0);
+            m = 0;
+          } else if (s[i] >= 0) {
+            off = -l[i] * 1.44269504f;
+            last = at0 + s[i];
+            first = p.window > 0 ? at0 + s[i] - p.window + 1 : 0;
+          }
+          const int e = max(static_cast<int>(m >> 7), 40);   // largest magnitude below 2^(e - 126)
+          const float f = pow2i(141 - e);                    // to below 2^15
+          if (off > -INFINITY) slope = p.scale * 1.44269504f * pow2i(e - 141);
+          if (r < R) {
+            auto half2_of = [&](uint32_t lo16, uint32_t hi16) {
+              return pack_half2(__uint_as_float(lo16 << 16) * f, __uint_as_float(hi16 << 16) * f);
+            };
+            const uint2 x = a[i], y = b[i];
+            uint4 o;
+            if (kQ4)   // dims {0, 2, 16, 18, 1, 3, 17, 19} of the word
+              o = make_uint4(half2_of(x.x & 0xFFFFu, x.y & 0xFFFFu),
+                             half2_of(y.x & 0xFFFFu, y.y & 0xFFFFu),
+                             half2_of(x.x >> 16, x.y >> 16), half2_of(y.x >> 16, y.y >> 16));
+            else
+              o = make_uint4(half2_of(x.x & 0xFFFFu, x.x >> 16), half2_of(x.y & 0xFFFFu, x.y >> 16),
+                             half2_of(y.x & 0xFFFFu, y.x >> 16), half2_of(y.y & 0xFFFFu, y.y >> 16));
+            *reinterpret_cast<uint4*>(sQ + tc::sw128_offset(r, piece, R)) = o;
+            if (piece == 0) {
+              s_slope[tb][r] = slope;
+              s_off[tb][r] = off;
+              s_first[tb][r] = first;
+              s_last[tb][r] = last;
+            }
+          }
         }
       }
       fence_proxy_async_smem();
@@ -450,16 +496,17 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, role_wait(&b_s[grp], (k >> 1) & 1, &s_dead));
         if (!ok) break;
         tc::fence_after_sync();
-        const uint32_t ts = tmem + lanes + W::kTS + grp * kWtRows;
+        const uint32_t ts = tmem + lanes + W::kTS + grp * W::kRows;
         // every row sees the whole chunk: up to row 0's own place, from the last row's window on
         const bool whole = (c + 1) * kWtKeys <= at0 + 1 &&
                            (p.window == 0 || c * kWtKeys >= C - p.window);
         float s0 = 0.0f, s1 = 0.0f;
-        for (int r = 0; r < R; r += 16) {
-          uint32_t x[16];
-          tc::TmemIo<16>::load(ts + r, x);
+        auto add = [&](auto columns, int r) {
+          constexpr int kN = decltype(columns)::value;
+          uint32_t x[kN];
+          tc::TmemIo<kN>::load(ts + r, x);
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
+          for (int i = 0; i < kN; i += 4) {
             const float4 f = *reinterpret_cast<const float4*>(slope + r + i);
             const float4 o = *reinterpret_cast<const float4*>(off + r + i);
             float y0, y1, y2, y3;
@@ -477,7 +524,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             add2(s0, s1, s0, s1, y0, y1);
             add2(s0, s1, s0, s1, y2, y3);
           }
-        }
+        };
+        int r = 0;
+        for (; r + 32 <= R; r += 32) add(Columns<32>(), r);
+        if (r < R) add(Columns<16>(), r);
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_sfree[grp]);
@@ -501,7 +551,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kWtMma) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
