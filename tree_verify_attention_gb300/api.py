@@ -77,6 +77,18 @@ def _dev(t, name, dtypes, numel=None):
     return t
 
 
+def _ptr(t, name, dtype, numel, index):
+    """Address of a contiguous tensor of ``dtype`` on device ``index`` with at
+    least ``numel`` elements; None for None."""
+    if t is None:
+        return None
+    if (t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+            and t.numel() >= numel):
+        return t.data_ptr()
+    _dev(t, name, (dtype,), numel)
+    raise DfvError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
 _BF16 = (torch.bfloat16, torch.int16)
 _I32 = (torch.int32,)
 _F32 = (torch.float32,)
@@ -141,7 +153,7 @@ class KVCache:
         _check(lib().dfv_kv_read_rows(
             h, d, self.kv_format, self.capacity, pos0, n, self.k.data_ptr(), self.v.data_ptr(),
             k_out.data_ptr(), v_out.data_ptr(),
-            DTYPE_F32 if k_out.dtype == torch.float32 else DTYPE_BF16, st[r], st[hd],
+            DTYPE_F32 if k_out.dtype is torch.float32 else DTYPE_BF16, st[r], st[hd],
             _stream(stream, index)), "dfv_kv_read_rows")
 
 
@@ -478,23 +490,22 @@ def kv_weights(cache, q, lse, weights, prev=None, decay=1.0, path=None, accept_l
     h, cap = cache.n_kv_heads, cache.capacity
     if d != cache.head_dim:
         raise DfvError(f"q has head_dim {d}, the cache {cache.head_dim}")
-    _dev(lse, "lse", _F32, n * hq)
     for t, name in ((weights, "weights"), (prev, "prev")):
-        if t is None and name == "prev":
-            continue
-        _dev(t, name, _F32)
-        if tuple(t.shape) != (h, cap):
+        if t is not None and tuple(t.shape) != (h, cap):
             raise DfvError(f"{name} has shape {tuple(t.shape)}, expected {(h, cap)}")
-    if path is not None:
-        _dev(path, "path", _I32, n)
-    if accept_len is not None:
-        _dev(accept_len, "accept_len", _I32, 1)
+    if weights is None or lse is None:
+        raise DfvError("weights and lse are required")
     index = q.get_device()
-    _same_device(index, cache.k, lse, weights, prev, path, accept_len, status)
+    if index != torch._C._cuda_getDevice() or cache.k.get_device() != index:
+        _same_device(index, cache.k)
     _check(lib().dfv_kv_weights(
         n, hq, h, d, window, cache.kv_format, cap, cache.ctx_len.data_ptr(), cache.k.data_ptr(),
-        q.data_ptr(), lse.data_ptr(), _p(path), _p(accept_len), float(scale), float(decay),
-        _p(prev), weights.data_ptr(), _p(status), _stream(stream, index)), "dfv_kv_weights")
+        q.data_ptr(), _ptr(lse, "lse", torch.float32, n * hq, index),
+        _ptr(path, "path", torch.int32, n, index),
+        _ptr(accept_len, "accept_len", torch.int32, 1, index), scale, decay,
+        _ptr(prev, "prev", torch.float32, 0, index),
+        _ptr(weights, "weights", torch.float32, 0, index),
+        _ptr(status, "status", torch.int32, 1, index), _stream(stream, index)), "dfv_kv_weights")
 
 
 def kv_evict(cache, weights, into, kept, sinks=0, recent=0, weights_out=None, status=None,
@@ -508,36 +519,34 @@ def kv_evict(cache, weights, into, kept, sinks=0, recent=0, weights_out=None, st
     the kept rows' weights."""
     _kv_cache(cache, "cache")
     _kv_cache(into, "into")
-    h, d = cache.n_kv_heads, cache.head_dim
+    h, d, cap, into_cap = cache.n_kv_heads, cache.head_dim, cache.capacity, into.capacity
     if (into.n_kv_heads, into.head_dim, into.fmt) != (h, d, cache.fmt):
         raise DfvError("into must be a cache of the same heads and format")
-    if into is cache or into.k.data_ptr() == cache.k.data_ptr():
+    k_src, k_dst, index = cache.k.data_ptr(), into.k.data_ptr(), cache.k.get_device()
+    if k_src == k_dst:
         raise DfvError("into must be another cache")
-    _dev(weights, "weights", _F32)
-    if tuple(weights.shape) != (h, cache.capacity):
-        raise DfvError(f"weights has shape {tuple(weights.shape)}, expected "
-                       f"{(h, cache.capacity)}")
-    _dev(kept, "kept", _I32)
-    if kept.dim() != 2 or kept.shape[0] != h or not 1 <= kept.shape[1] <= into.capacity:
-        raise DfvError(f"kept must be [{h}, K], K in [1, {into.capacity}]")
+    if index != torch._C._cuda_getDevice() or into.k.get_device() != index:
+        _same_device(index, into.k)
+    if tuple(weights.shape) != (h, cap):
+        raise DfvError(f"weights has shape {tuple(weights.shape)}, expected {(h, cap)}")
+    if kept.dim() != 2 or kept.shape[0] != h or not 1 <= kept.shape[1] <= into_cap:
+        raise DfvError(f"kept must be [{h}, K], K in [1, {into_cap}]")
     keep = kept.shape[1]
     if sinks < 0 or recent < 0 or sinks + recent > keep:
         raise DfvError(f"{sinks} first and {recent} last rows of {keep}")
     if weights_out is not None:
-        _dev(weights_out, "weights_out", _F32)
-        if tuple(weights_out.shape) != (h, into.capacity):
+        if tuple(weights_out.shape) != (h, into_cap):
             raise DfvError(f"weights_out has shape {tuple(weights_out.shape)}, expected "
-                           f"{(h, into.capacity)}")
+                           f"{(h, into_cap)}")
         if weights_out.data_ptr() == weights.data_ptr():
             raise DfvError("weights_out must not be weights")
-    index = cache.k.get_device()
-    _same_device(index, into.k, weights, kept, weights_out, status)
     _check(lib().dfv_kv_evict(
-        h, d, cache.kv_format, cache.capacity, cache.ctx_len.data_ptr(), cache.dropped.data_ptr(),
-        cache.k.data_ptr(), cache.v.data_ptr(), weights.data_ptr(), keep, sinks, recent,
-        into.capacity, into.k.data_ptr(), into.v.data_ptr(), into.ctx_len.data_ptr(),
-        into.dropped.data_ptr(), _p(weights_out), kept.data_ptr(), _p(status),
-        _stream(stream, index)), "dfv_kv_evict")
+        h, d, cache.kv_format, cap, cache.ctx_len.data_ptr(), cache.dropped.data_ptr(), k_src,
+        cache.v.data_ptr(), _ptr(weights, "weights", torch.float32, 0, index), keep, sinks,
+        recent, into_cap, k_dst, into.v.data_ptr(), into.ctx_len.data_ptr(),
+        into.dropped.data_ptr(), _ptr(weights_out, "weights_out", torch.float32, 0, index),
+        _ptr(kept, "kept", torch.int32, 0, index),
+        _ptr(status, "status", torch.int32, 1, index), _stream(stream, index)), "dfv_kv_evict")
 
 
 class Sampling:
@@ -571,24 +580,25 @@ class Sampling:
                 raise DfvError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _sample_args(logits, uniform, sampling, token, logprob, status):
+def _sample_args(logits, uniform, sampling, token):
     if logits is None or not logits.is_cuda or logits.dim() != 2 or logits.dtype not in _ROWS:
         raise DfvError("logits must be a CUDA f32 or bf16 tensor [N, V]")
     n, vocab = logits.shape
-    if n and vocab > 1 and logits.stride(1) != 1:
+    row, one = logits.stride()
+    if one != 1 and n and vocab > 1:
         raise DfvError("logits rows must be contiguous")
-    _dev(uniform, "uniform", _F32, n)
-    _dev(token, "token", _I32, n)
-    if logprob is not None:
-        _dev(logprob, "logprob", _F32, n)
     if not isinstance(sampling, Sampling):
         raise DfvError("sampling must be a Sampling")
     index = logits.get_device()
-    sampling.check(n, index)
-    _same_device(index, uniform, token, logprob, status)
-    return (n, vocab, DTYPE_F32 if logits.dtype == torch.float32 else DTYPE_BF16,
-            logits.data_ptr(), logits.stride(0) if n > 1 else vocab, uniform.data_ptr(),
-            sampling.handle), index
+    if index != torch._C._cuda_getDevice():
+        _same_device(index)
+    if sampling.tensors:
+        sampling.check(n, index)
+    if uniform is None or token is None:
+        raise DfvError("uniform and token are required")
+    return (n, vocab, DTYPE_F32 if logits.dtype is torch.float32 else DTYPE_BF16,
+            logits.data_ptr(), row if n > 1 else vocab,
+            _ptr(uniform, "uniform", torch.float32, n, index), sampling.handle), index
 
 
 def sample_tokens(logits, uniform, sampling, token, logprob=None, status=None, stream=None):
@@ -599,8 +609,11 @@ def sample_tokens(logits, uniform, sampling, token, logprob=None, status=None, s
     token in index order is taken at which the running sum of the kept
     probabilities exceeds the random number. A row without a distribution gets
     -1 and NaN (DEV_NONFINITE, DEV_BAD_SAMPLING)."""
-    args, index = _sample_args(logits, uniform, sampling, token, logprob, status)
-    _check(lib().dfv_sample(*args, token.data_ptr(), _p(logprob), _p(status),
+    args, index = _sample_args(logits, uniform, sampling, token)
+    n = args[0]
+    _check(lib().dfv_sample(*args, _ptr(token, "token", torch.int32, n, index),
+                            _ptr(logprob, "logprob", torch.float32, n, index),
+                            _ptr(status, "status", torch.int32, 1, index),
                             _stream(stream, index)), "dfv_sample")
 
 
@@ -613,18 +626,23 @@ def sample_accept(logits, uniform, sampling, parent, tokens, target, accept_len,
     """:func:`greedy_accept` with drawn tokens: ``target`` [N] is drawn from
     each node's logits as by :func:`sample_tokens`, and the walk follows the
     children whose ``tokens`` are their parents' targets."""
-    args, index = _sample_args(logits, uniform, sampling, target, logprob, status)
+    args, index = _sample_args(logits, uniform, sampling, target)
     n = args[0]
-    for t, nm in ((parent, "parent"), (tokens, "tokens"), (path, "path"),
-                  (out_tokens, "out_tokens")):
-        _dev(t, nm, _I32, n)
-    _dev(accept_len, "accept_len", _I32, 1)
-    _dev(ws, "workspace", (torch.uint8,))
-    _same_device(index, parent, tokens, accept_len, path, out_tokens, ws)
+    for t, name in ((parent, "parent"), (tokens, "tokens"), (accept_len, "accept_len"),
+                    (path, "path"), (out_tokens, "out_tokens"), (ws, "workspace")):
+        if t is None:
+            raise DfvError(f"{name} is required")
     _check(lib().dfv_sample_accept(
-        *args, parent.data_ptr(), tokens.data_ptr(), target.data_ptr(), _p(logprob),
-        accept_len.data_ptr(), path.data_ptr(), out_tokens.data_ptr(), ws.data_ptr(), ws.numel(),
-        _p(status), _stream(stream, index)), "dfv_sample_accept")
+        *args, _ptr(parent, "parent", torch.int32, n, index),
+        _ptr(tokens, "tokens", torch.int32, n, index),
+        _ptr(target, "target", torch.int32, n, index),
+        _ptr(logprob, "logprob", torch.float32, n, index),
+        _ptr(accept_len, "accept_len", torch.int32, 1, index),
+        _ptr(path, "path", torch.int32, n, index),
+        _ptr(out_tokens, "out_tokens", torch.int32, n, index),
+        _ptr(ws, "workspace", torch.uint8, 0, index), ws.numel(),
+        _ptr(status, "status", torch.int32, 1, index), _stream(stream, index)),
+        "dfv_sample_accept")
 
 
 class Rope:
@@ -650,6 +668,7 @@ class Rope:
         self.head_dim, self.rot_dim, self.interleaved = head_dim, rot_dim, bool(interleaved)
         self.turns = torch.tensor([t - (t >> 63 << 64) for t in turns], dtype=torch.int64,
                                   device=device)
+        self._index, self._turns_ptr = self.turns.get_device(), self.turns.data_ptr()
 
 
 def qk_norm_rope(q, k, v, rope, q_out, k_out, v_out=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -673,53 +692,77 @@ def qk_norm_rope(q, k, v, rope, q_out, k_out, v_out=None, q_weight=None, k_weigh
     n, _, d = first.shape
     if rope.head_dim != d:
         raise DfvError(f"rope is for head_dim {rope.head_dim}, the rows have {d}")
-    if (k is None) and v is not None:
-        raise DfvError("v without k")
-    src, dst, heads, strides = _ROWS, _ROWS, [], []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
-        if x is None:
-            heads.append(0)
-            strides += [0, 0]
-            continue
-        h = (k if name == "v" else x).shape[1] if x.dim() == 3 else -1
-        st = _float_rows(x, name, (n, h, d), src)
-        _dev(out, name + "_out", dst)
-        if tuple(out.shape) != (n, h, d):
-            raise DfvError(f"{name}_out has shape {tuple(out.shape)}, expected {(n, h, d)}")
-        src, dst = (x.dtype,), (out.dtype,)    # one type for all sources, one for all outputs
-        heads.append(h)
-        strides += [st[0], st[1]]
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            if eps is None:
-                raise DfvError(f"{name} without a norm")
-            _dev(w, name, _F32, d)
-    if eps is not None and not eps >= 0:
+    index = first.get_device()
+    if index != torch._C._cuda_getDevice() or index != rope._index:
+        _same_device(index, rope.turns)
+    # one type for all sources, one for all outputs; a call of one token costs
+    # little else than these checks, so they are written out
+    src = first.dtype
+    dst = (q_out if q is not None else k_out)
+    if dst is None:
+        raise DfvError("q_out is required" if q is not None else "k_out is required")
+    dst = dst.dtype
+    if src not in _ROWS or dst not in _ROWS:
+        raise DfvError("sources and outputs must be CUDA f32 or bf16 tensors")
+    hq = hkv = sq = sqh = sk = skh = sv = svh = 0
+    pq = pk = pv = oq = ok = ov = None
+    if q is not None:
+        hq = q.shape[1]
+        sq, sqh, one = q.stride()
+        pq, oq = _row_pair(q, q_out, "q", (n, hq, d), one, src, dst, index)
+    if k is not None:
+        if k.dim() != 3:
+            raise DfvError("q and k must be [N, heads, D]")
+        hkv = k.shape[1]
+        sk, skh, one = k.stride()
+        pk, ok = _row_pair(k, k_out, "k", (n, hkv, d), one, src, dst, index)
+    if v is not None:
+        if k is None:
+            raise DfvError("v without k")
+        if v.dim() != 3:
+            raise DfvError("v must be [N, heads, D]")
+        sv, svh, one = v.stride()
+        pv, ov = _row_pair(v, v_out, "v", (n, hkv, d), one, src, dst, index)
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise DfvError("q_weight or k_weight without a norm")
+        eps = -1.0
+    elif not eps >= 0:
         raise DfvError(f"eps {eps} must be 0 or more")
     if positions is not None:
         if ctx_len is not None or dropped is not None or parent is not None:
             raise DfvError("positions are given: no ctx_len, dropped or parent beside them")
-        _dev(positions, "positions", _I32, n)
-    else:
-        _dev(ctx_len, "ctx_len", _I32, 1)
-        if dropped is not None:
-            _dev(dropped, "dropped", _I32, 1)
-        if parent is not None:
-            _dev(parent, "parent", _I32, n)
-            if n > MAX_NODES:
-                raise DfvError(f"{n} tree nodes, at most {MAX_NODES}")
-    index = first.get_device()
-    q_out, k_out, v_out = (o if x is not None else None
-                           for x, o in ((q, q_out), (k, k_out), (v, v_out)))
-    _same_device(index, q, k, v, q_out, k_out, v_out, rope.turns, q_weight, k_weight, positions,
-                 ctx_len, dropped, parent, status)
+    elif ctx_len is None:
+        raise DfvError("ctx_len or positions are required")
+    elif parent is not None and n > MAX_NODES:
+        raise DfvError(f"{n} tree nodes, at most {MAX_NODES}")
     _check(lib().dfv_qk_norm_rope(
-        n, heads[0], heads[1], d, _p(q), _p(k), _p(v),
-        DTYPE_F32 if first.dtype == torch.float32 else DTYPE_BF16, *strides,
-        _p(q_weight), _p(k_weight), -1.0 if eps is None else float(eps), rope.turns.data_ptr(),
-        rope.rot_dim, rope.interleaved, _p(positions), _p(parent), _p(ctx_len), _p(dropped),
-        _p(q_out), _p(k_out), _p(v_out), DTYPE_F32 if dst[0] == torch.float32 else DTYPE_BF16,
-        _p(status), _stream(stream, index)), "dfv_qk_norm_rope")
+        n, hq, hkv, d, pq, pk, pv, DTYPE_F32 if src is torch.float32 else DTYPE_BF16, sq, sqh, sk,
+        skh, sv, svh, _ptr(q_weight, "q_weight", torch.float32, d, index),
+        _ptr(k_weight, "k_weight", torch.float32, d, index), eps,
+        rope._turns_ptr, rope.rot_dim, rope.interleaved, _ptr(positions, "positions", torch.int32, n, index),
+        _ptr(parent, "parent", torch.int32, n, index),
+        _ptr(ctx_len, "ctx_len", torch.int32, 1, index),
+        _ptr(dropped, "dropped", torch.int32, 1, index), oq, ok, ov,
+        DTYPE_F32 if dst is torch.float32 else DTYPE_BF16,
+        _ptr(status, "status", torch.int32, 1, index), _stream(stream, index)),
+        "dfv_qk_norm_rope")
+
+
+def _row_pair(x, out, name, shape, one, src, dst, index):
+    """Addresses of rows [N, heads, D] and of the contiguous output for them."""
+    if x.dtype is not src or x.get_device() != index:
+        raise DfvError(f"{name} must be a {src} tensor on cuda:{index}")
+    if x.shape != shape:
+        raise DfvError(f"{name} has shape {tuple(x.shape)}, expected {shape}")
+    if one != 1 and x.numel():
+        raise DfvError(f"{name} rows must be contiguous")
+    if (out is None or out.dtype is not dst or out.get_device() != index
+            or not out.is_contiguous()):
+        raise DfvError(f"{name}_out must be a contiguous {dst} tensor on cuda:{index}")
+    if out.shape != shape:
+        raise DfvError(f"{name}_out has shape {tuple(out.shape)}, expected {shape}")
+    return x.data_ptr(), out.data_ptr()
 
 
 def kv_commit(cache, accept_len, path, tree_k, tree_v, status=None, stream=None):

@@ -13,38 +13,54 @@
 // float32: with 150 K tokens and sums that are off by 2^-24 one row in a
 // hundred would get its neighbour. Weights therefore are 64-bit integers in
 // units of 2^-44 of a power of two above the largest: 2^t by a table of
-// 2^(j/64) in 32 bits and a cubic for the rest, t = (x - base) log2(e) / T in
-// two floats (off by about 2^-31 of the weight). Sums of integers have no order, so every
-// pass over the row agrees with every other and nothing depends on how the row
-// is split.
+// 2^(j/32) in 32 bits and a quartic for the rest, t = (x - base) log2(e) / T in
+// two floats: off by up to 2^-29 of the weight, which many weights average out.
+// The few largest do not, so about the 24 largest tokens are weighed in 64 bits
+// throughout. Sums of integers have no order, so every pass over the row agrees
+// with every other and nothing depends on how the row is split.
 //
 // A row belongs to a cluster of 1 to 16 CTAs that keep it in shared memory:
 // it is read from memory once, and passes over it run at shared memory's rate.
 // The first CTA decides, the others carry out what it asks for. Passes:
 //
-//   1. maximum, while the row arrives;
-//   2. the sum of all weights; tokens within 2^-12 of the largest go to a list.
-//      If the list holds both cuts (a model that is reasonably sure), it is
-//      sorted in the first CTA and the token comes from it;
-//   3. otherwise counts and weights of 1024 bins of the logit, the bin with the
-//      cut, its tokens sorted (a bin of more than 512 is cut by its keys'
-//      bits; equal keys are counted in index order);
+//   1. maximum, while the row arrives, and the maxima of groups of tokens, about
+//      twice as many as top-k says (up to 256; 24 without it): the k-th largest
+//      of these is reached by k tokens at least, and by not many more;
+//   2. top-k of up to 256: the tokens that reach that bound, into a list. Else
+//      the sum of all weights, a list of the tokens within 2^-12 of the largest,
+//      and counts of every eighth piece of the row by bins of the logit.
+//      A list that holds both cuts (a model that is reasonably sure) is sorted
+//      in the first CTA, and the token comes from it;
+//   3. otherwise the counts give a window for the cut: the tokens above it are
+//      weighed, the ones in it gathered in index order, and what follows runs
+//      over these alone (over the whole row where they are too many or the cut
+//      lies elsewhere): counts and weights by bins of the logit, the bin with the
+//      cut, its tokens sorted (a bin of more than 512 is cut by its keys' bits;
+//      equal keys are counted in index order);
 //   4. the sum of the kept weights per warp, and the warp with the token once
 //      more.
 //
-// Without top-k and top-p pass 2 is pass 4.
+// Without top-k and top-p pass 2 is pass 4. Pass 2 is the dearest: about 20
+// cycles of a scheduler for a weight of 32 lanes, most of them on integers.
 
 #include <atomic>
 #include <climits>
 
 #include "common.cuh"
+#include "tc.cuh"
 
 namespace dfv {
 
 constexpr int kSmpThreads = 512;
 constexpr int kSmpWarps = kSmpThreads / 32;
-constexpr int kSmpBins = 1024;
+constexpr int kSmpBins = kSmpThreads;
+constexpr int kSmpBinBits = 9;
 constexpr int kSmpList = kSmpThreads;      // one sorted token a thread
+constexpr int kSmpTopMost = 256;           // top-k by group maxima
+constexpr int kSmpHeavy = 24;              // tokens weighed in 64 bits, about
+constexpr int kSmpGroups = 1024;           // of them, at most
+constexpr int kSmpGathered = 384;          // of a warp
+constexpr int kSmpSample = 8;
 constexpr int kSmpMaxCluster = 16;
 constexpr int kSmpMaxVocab = 1 << 19;      // sums of weights stay below 2^63
 constexpr float kSmpMinT = 0x1p-100f;      // below: greedy
@@ -65,16 +81,16 @@ struct SampleParams {
   int slice_vecs;    // 16-byte vectors of shared memory for the slice
 };
 
-// round(2^(31 + j / 64))
-__constant__ uint32_t kSmpExp2[64] = {
-    0x80000000u, 0x8164D1F4u, 0x82CD8699u, 0x843A28C4u, 0x85AAC368u, 0x871F6197u, 0x88980E81u, 0x8A14D575u,
-    0x8B95C1E4u, 0x8D1ADF5Bu, 0x8EA4398Bu, 0x9031DC43u, 0x91C3D374u, 0x935A2B2Fu, 0x94F4EFA9u, 0x96942D37u,
-    0x9837F052u, 0x99E04593u, 0x9B8D39BAu, 0x9D3ED9A7u, 0x9EF53261u, 0xA0B05110u, 0xA2704303u, 0xA43515AEu,
-    0xA5FED6AAu, 0xA7CD93B5u, 0xA9A15AB5u, 0xAB7A39B6u, 0xAD583EEAu, 0xAF3B78ADu, 0xB123F582u, 0xB311C413u,
-    0xB504F334u, 0xB6FD91E3u, 0xB8FBAF47u, 0xBAFF5AB2u, 0xBD08A39Fu, 0xBF1799B6u, 0xC12C4CCAu, 0xC346CCDAu,
-    0xC5672A11u, 0xC78D74C9u, 0xC9B9BD86u, 0xCBEC14FFu, 0xCE248C15u, 0xD06333DBu, 0xD2A81D92u, 0xD4F35AACu,
-    0xD744FCCBu, 0xD99D15C2u, 0xDBFBB798u, 0xDE60F482u, 0xE0CCDEECu, 0xE33F8973u, 0xE5B906E7u, 0xE8396A50u,
-    0xEAC0C6E8u, 0xED4F301Fu, 0xEFE4B99Cu, 0xF281773Cu, 0xF5257D15u, 0xF7D0DF73u, 0xFA83B2DBu, 0xFD3E0C0Du,
+// round(2^(63 + j / 32))
+__constant__ uint64_t kSmpExp2[32] = {
+    0x8000000000000000ull, 0x82CD8698AC2BA1D7ull, 0x85AAC367CC487B15ull, 0x88980E8092DA8527ull,
+    0x8B95C1E3EA8BD6E7ull, 0x8EA4398B45CD53C0ull, 0x91C3D373AB11C336ull, 0x94F4EFA8FEF70961ull,
+    0x9837F0518DB8A96Full, 0x9B8D39B9D54E5539ull, 0x9EF5326091A111AEull, 0xA27043030C496819ull,
+    0xA5FED6A9B15138EAull, 0xA9A15AB4EA7C0EF8ull, 0xAD583EEA42A14AC6ull, 0xB123F581D2AC2590ull,
+    0xB504F333F9DE6484ull, 0xB8FBAF4762FB9EE9ull, 0xBD08A39F580C36BFull, 0xC12C4CCA66709456ull,
+    0xC5672A115506DADDull, 0xC9B9BD866E2F27A3ull, 0xCE248C151F8480E4ull, 0xD2A81D91F12AE45Aull,
+    0xD744FCCAD69D6AF4ull, 0xDBFBB797DAF23755ull, 0xE0CCDEEC2A94E111ull, 0xE5B906E77C8348A8ull,
+    0xEAC0C6E7DD24392Full, 0xEFE4B99BDCDAF5CBull, 0xF5257D152486CC2Cull, 0xFA83B2DB722A033Aull,
 };
 
 enum SmpState {
@@ -82,43 +98,51 @@ enum SmpState {
 };
 
 enum SmpOp {
-  kOpDone, kOpHistLogit, kOpGatherLogit, kOpRangeLogit, kOpHistKey, kOpGatherKey, kOpCountEqual,
-  kOpFindEqual, kOpSum, kOpPick
+  kOpDone, kOpCompact, kOpHistLogit, kOpGatherLogit, kOpRangeLogit, kOpHistKey, kOpGatherKey,
+  kOpCountEqual, kOpFindEqual, kOpSum, kOpPick
 };
 
 struct SmpCmd {
   int op, bin, shift, rank, warp, nth;
+  int gathered;          // over the gathered tokens
+  float from, upto;      // gather the tokens of logits in [from, upto)
   uint32_t khi, klo;     // keys, both included
   uint64_t target, total;
 };
 
 struct SmpSmem {
   uint32_t cnt[kSmpBins], mlo[kSmpBins], mhi[kSmpBins];   // a bin's count and weight
-  uint64_t buf[kSmpList];      // this CTA's list
-  uint64_t keys[kSmpList];     // first CTA: the cluster's
-  uint64_t sorted[kSmpList], run[kSmpList];   // in order, and running weights
-  uint32_t table[64];
+  uint64_t buf[kSmpList];      // this CTA's list; first CTA: then the cluster's
+  union {
+    uint64_t sorted[kSmpList];   // in order
+    float gmax[kSmpGroups];      // before: the cluster's group maxima
+  };
+  uint64_t run[kSmpList];      // running weights
+  uint32_t sampled[kSmpBins];  // counts of every eighth piece
+  uint16_t gathered[kSmpWarps][kSmpGathered];   // places in the slice, ascending
+  uint32_t table[32];          // 2^(31 + j / 32): an entry a bank
+  float ftable[32];            // 2^(j / 32)
   uint64_t wtot[2][kSmpWarps];
   float wmax[kSmpWarps];
   float xmax[kSmpMaxCluster];
   // first CTA: what the others report
-  uint64_t xsum[kSmpMaxCluster * kSmpWarps];
+  uint64_t xsum[kSmpMaxCluster * kSmpWarps], xlmass[kSmpMaxCluster * kSmpWarps];
   uint32_t xcnt[kSmpMaxCluster * kSmpWarps];
   int xlist[kSmpMaxCluster];
   uint32_t xlo[kSmpMaxCluster], xhi[kSmpMaxCluster];
-  uint32_t found;
+  uint32_t found, over;        // a place; warps whose gathered tokens did not fit
   // parameters of the row
-  float t_inv_hi, t_inv_lo, temperature, top_p, min_p, u;
-  double ln_min;
+  float t_inv_hi, t_inv_lo, temperature, top_p, u, ln_hi, ln_lo;
   int top_k, bad;
   int list_n;
-  uint32_t lo, hi, first;
+  float bound;
+  uint32_t lo, hi;
   SmpCmd cmd;
   // first CTA: a search, its hit, and the cut so far with the weight up to it
   bool by_mass;
-  int hit;
+  int hit, hit2, list_all;
   uint32_t hit_cnt;
-  uint64_t target, acc_cnt, acc_mass, need, mass;
+  uint64_t target, acc_cnt, acc_mass, need, mass, binned;
   uint32_t cut_key;
   int cut_index;
   float result_logprob;
@@ -145,6 +169,9 @@ template <> struct SmpVec<float> {
     return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
   }
   static __device__ __forceinline__ float low() { return -INFINITY; }
+  static __device__ __forceinline__ float2 pair(const void* x, int i) {
+    return static_cast<const float2*>(x)[i];
+  }
 };
 template <> struct SmpVec<__nv_bfloat16> {
   static constexpr int kN = 8;
@@ -153,6 +180,10 @@ template <> struct SmpVec<__nv_bfloat16> {
     return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
   }
   static __device__ __forceinline__ __nv_bfloat16 low() { return __float2bfloat16(-INFINITY); }
+  static __device__ __forceinline__ float2 pair(const void* x, int i) {
+    const uint32_t w = static_cast<const uint32_t*>(x)[i];
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
 };
 
 // Cluster barrier, and addresses of the same variable in another CTA.
@@ -185,6 +216,40 @@ __device__ __forceinline__ uint64_t smp_warp_scan(uint64_t v, int lane) {   // i
     if (lane >= o) v += w;
   }
   return v;
+}
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 smp_add2(float2 a, float2 b) {
+  add2(a.x, a.y, a.x, a.y, b.x, b.y);
+  return a;
+}
+__device__ __forceinline__ float2 smp_fma2(float2 a, float2 b, float2 c) {
+  fma2(c.x, c.y, a.x, a.y, b.x, b.y, c.x, c.y);
+  return c;
+}
+__device__ __forceinline__ float2 smp_both(float x) { return make_float2(x, x); }
+
+// 2^(k / 32 + f + g) in 64 bits, |f + g| <= 2^-6, in the units that `s` gives the
+// other weights. The series of 2^r - 1 by
+// Horner's rule in 64-bit fractions, up to r^6 (the next term is below 2^-54).
+__device__ __noinline__ uint64_t smp_heavy_weight(float f, float g, int k, uint32_t s) {
+  const int64_t r = __float2ll_rn(f * 0x1p60f) + __float2ll_rn(g * 0x1p60f);
+  const bool neg = r < 0;
+  const uint64_t a = __umul64hi(static_cast<uint64_t>(neg ? -r : r) << 3,
+                                0xB17217F7D1CF79ACull);   // |r| ln2, times 2^63
+  // 1 + z + z^2 / 2! ..., z = +-a: sums of magnitudes by sign, times 2^63
+  uint64_t even = 0, odd = a, power = a;
+#pragma unroll
+  for (int i = 2; i <= 6; ++i) {
+    power = (__umul64hi(power, a) << 1) / static_cast<uint64_t>(i);
+    if (i & 1) odd += power;
+    else even += power;
+  }
+  const uint64_t one = 1ull << 63;
+  const uint64_t e = neg ? one + even - odd : one + even + odd;   // e^z, below 2^64
+  const uint64_t t = kSmpExp2[k & 31];                            // below 2^64
+  const uint64_t w = __umul64hi(t, e);                            // 2^(62 + t's fraction)
+  return s > 64 ? 0 : w >> (s - 1);
 }
 
 // ln(w / total), as far from 0 as it is where w is nearly all
@@ -269,8 +334,13 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int row = blockIdx.x / cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   smp_cluster_arrive();   // waited for before another CTA's memory is touched
-  if (tid < 64) sm.table[tid] = kSmpExp2[tid];
-  if (tid == 0) sm.list_n = 0;
+  if (tid < 32) {
+    const uint64_t t = kSmpExp2[tid];
+    sm.table[tid] = static_cast<uint32_t>((t + 0x80000000ull) >> 32);
+    sm.ftable[tid] = static_cast<float>(t) * 0x1p-63f;
+  }
+  sm.sampled[tid] = 0;
+  if (tid == 0) sm.list_n = sm.over = 0;
   grid_dep_wait();
   grid_dep_launch_dependents();   // (after the wait: see common.cuh)
 
@@ -304,16 +374,20 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     const float u = p.uniform[row];
     sm.bad = !(temp >= 0.0f) || temp == INFINITY || top_p != top_p || min_p != min_p ||
              !(u >= 0.0f && u < 1.0f);
-    const double inv = 1.4426950408889634074 / static_cast<double>(temp);
-    sm.t_inv_hi = static_cast<float>(inv);
-    sm.t_inv_lo = static_cast<float>(inv - static_cast<double>(sm.t_inv_hi));
+    // log2(e) / temperature in two floats
+    const float hi = 1.44269502f / temp;
+    sm.t_inv_hi = hi;
+    sm.t_inv_lo = (fmaf(-hi, temp, 1.44269502f) + 1.92596303e-8f) / temp;
     sm.temperature = temp;
     sm.top_p = top_p;
-    sm.min_p = fminf(min_p, 1.0f);
     sm.u = u;
     sm.top_k = p.s.top_k ? p.s.top_k[row] : p.s.top_k_all;
-    // ln(max(min_p, 2^-40))
-    sm.ln_min = sm.min_p > 0x1p-40f ? log(static_cast<double>(sm.min_p)) : -27.725887222397812377;
+    // ln(max(min(min_p, 1), 2^-40)) in two (64 bits only where it is used: an
+    // operation takes 76 cycles)
+    const double ln = min_p > 0x1p-40f ? log(static_cast<double>(fminf(min_p, 1.0f)))
+                                       : -27.725887222397812377;
+    sm.ln_hi = static_cast<float>(ln);
+    sm.ln_lo = static_cast<float>(ln - static_cast<double>(sm.ln_hi));
   }
   cp_async_wait_all();
 
@@ -333,6 +407,16 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
 #pragma unroll
     for (int e = 0; e < kV; ++e) mx = smp_max_nan(mx, SmpVec<T>::at(xs[n_vecs - 1], e));
   }
+  const bool by_k = sm.top_k > 0 && sm.top_k < p.vocab, by_p = sm.top_p < 1.0f;
+  // groups of neighbouring threads, about twice as many in the cluster as the
+  // bound that is asked of them
+  const bool by_groups = by_k && sm.top_k <= kSmpTopMost;
+  const int want = by_groups ? sm.top_k : kSmpHeavy;
+  int lanes = 32;   // of a group
+  while (lanes > 1 && cs * (kSmpThreads / lanes) < 2 * want) lanes >>= 1;
+  const int groups = kSmpThreads / lanes;   // of a CTA
+  float gm = mx;
+  for (int o = lanes >> 1; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xFFFFFFFFu, gm, o));
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(mx) : "f"(mx));
   if (lane == 0) sm.wmax[warp] = mx;
   __syncthreads();
@@ -342,6 +426,9 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
 #pragma unroll
     for (int i = 1; i < kSmpWarps; ++i) a = smp_max_nan(a, sm.wmax[i]);
     *smp_remote(&sm.xmax[rank], tid) = a;
+  }
+  if (tid % lanes == 0) {
+    for (int r = 0; r < cs; ++r) *smp_remote(&sm.gmax[rank * groups + tid / lanes], r) = gm;
   }
   smp_cluster_sync();
   float m = sm.xmax[0];
@@ -355,17 +442,18 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     }
     return;
   }
-  // Vectors of a warp are neighbours, so that warps are in index order.
-  const int per = (n_vecs + kSmpWarps - 1) / kSmpWarps;
-  const int wv0 = min(n_vecs, warp * per), wv1 = min(n_vecs, wv0 + per);
+  // Passes go by pairs of tokens, a pair a lane: their code is short, which
+  // counts for more than wide loads (what runs a few times a row comes from the
+  // instruction cache's far end). A warp's pairs are neighbours, so that warps
+  // are in index order.
+  const int n_pairs = n_vecs * (kV / 2);
+  const int per = (n_pairs + kSmpWarps - 1) / kSmpWarps;
+  const int u0 = min(n_pairs, warp * per), u1 = min(n_pairs, u0 + per);
   if (sm.temperature < kSmpMinT) {
     uint32_t best = 0xFFFFFFFFu;
-    for (int v = wv0 + lane; v < wv1; v += 32) {
-      const uint4 r = xs[v];
-#pragma unroll
-      for (int e = 0; e < kV; ++e)
-        if (SmpVec<T>::at(r, e) == m)
-          best = min(best, static_cast<uint32_t>(first + v * kV + e));
+    for (int u = u0 + lane; u < u1 && best == 0xFFFFFFFFu; u += 32) {
+      const float2 v = SmpVec<T>::pair(xs, u);
+      if (v.x == m || v.y == m) best = static_cast<uint32_t>(first + 2 * u + (v.x == m ? 0 : 1));
     }
     best = __reduce_min_sync(0xFFFFFFFFu, best);
     if (lane == 0) *smp_remote(&sm.xcnt[rank * kSmpWarps + warp], 0) = best;
@@ -379,55 +467,102 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     return;
   }
 
+  // ---- the bound that `want` tokens reach at least, the same in every CTA
+  {
+    const int all = cs * groups;
+    for (int i = tid; i < all; i += kSmpThreads) {
+      const float g = sm.gmax[i];
+      int above = 0, same = 0;
+#pragma unroll 4
+      for (int j = 0; j < all; ++j) {
+        above += sm.gmax[j] > g;
+        same += sm.gmax[j] >= g;
+      }
+      if (above < want && same >= want) sm.bound = g;   // the same value from each such thread
+    }
+    __syncthreads();
+  }
+  const float heavy = fmaxf(sm.bound, -3.4028235e38f);
+
   // ---- weights. |m| / T up to 2^12: t = x / T log2(e) itself, to 2^-36; above,
   // tokens that count lie so near the maximum that x - m is exact.
   const float chi = sm.t_inv_hi, clo = sm.t_inv_lo, temp = sm.temperature;
   const float base = fabsf(m) * chi <= 4096.0f ? 0.0f : m;
   constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: the sum's low bits are the integer
-  auto split = [&](float v, int& ki) {    // 64 t = ki + 64 r
-    const float d = v - base;
-    const float th = d * chi;
-    const float tl = fmaf(d, clo, fmaf(d, chi, -th));
-    const float k = fmaf(th, 64.0f, kMagic);
-    ki = __float_as_int(k) - 0x4B400000;
-    return fmaf(k - kMagic, -0.015625f, th) + tl;
+  // t = d log2(e) / T = k / 32 + f + g with k an integer (in the low bits of
+  // `k`) and |f| <= 2^-6, of two values at a time
+  auto split = [&](float2 v, float2& k, float2& g) {
+    const float2 d = smp_add2(v, smp_both(-base)), c = smp_both(chi);
+    const float2 th = smp_fma2(d, c, smp_both(-0.0f));
+    g = smp_fma2(d, smp_both(clo), smp_fma2(d, c, make_float2(-th.x, -th.y)));
+    k = smp_fma2(th, smp_both(32.0f), smp_both(kMagic));
+    return smp_fma2(smp_add2(k, smp_both(-kMagic)), smp_both(-0.03125f), th);
   };
-  int km;
-  split(m, km);
-  const int top = (km >> 6) + 1;   // the largest weight is in [2^43, 2^44]
-  auto weight = [&](float v) -> uint64_t {
-    int ki;
-    const float r = split(v, ki);
-    const uint32_t tj = sm.table[ki & 63];
-    // 2^31 (2^r - 1), |r| <= 2^-7: ln2, ln2^2 / 2, ln2^3 / 6; the next term is below 2^-34
-    const float q =
-        r * fmaf(r, fmaf(r, 0.055504109f * 0x1p31f, 0.24022651f * 0x1p31f), 0.69314718f * 0x1p31f);
-    const float tf = __uint_as_float(0x3F800000u | ((tj >> 8) & 0x7FFFFFu));
-    const uint32_t f = tj + static_cast<uint32_t>(__float2int_rn(tf * q));
-    // f 2^(13 - s), s = top - (ki >> 6) at least 1
-    const int s = min(max(top - (ki >> 6), 0) + 19, 63);
-    return (static_cast<uint64_t>(f) << 32) >> s;
+  // s of the maximum is 20: the largest weight is in [2^43, 2^44]
+  int top;
+  {
+    float2 k, g;
+    split(smp_both(m), k, g);
+    top = 20 + (__float_as_int(k.x) >> 5);
+  }
+  // Weights of two values, zero where `on` is not set.
+  auto weight2 = [&](float2 v, bool on0, bool on1, uint64_t& w0, uint64_t& w1) {
+    float2 k, g;
+    const float2 f = split(v, k, g), r = smp_add2(f, g);
+    // 2^31 (2^r - 1), |r| <= 2^-6: ln2^i / i!; the next term is below 2^-39
+    float2 q = smp_fma2(r, smp_both(0.0096181291f * 0x1p31f), smp_both(0.055504109f * 0x1p31f));
+    q = smp_fma2(r, q, smp_both(0.24022651f * 0x1p31f));
+    q = smp_fma2(r, q, smp_both(0.69314718f * 0x1p31f));
+    q = smp_fma2(r, q, smp_both(0.0f));
+    const int k0 = __float_as_int(k.x), k1 = __float_as_int(k.y);
+    uint32_t f0 = sm.table[k0 & 31] +
+                  static_cast<uint32_t>(__float2int_rn(sm.ftable[k0 & 31] * q.x));
+    uint32_t f1 = sm.table[k1 & 31] +
+                  static_cast<uint32_t>(__float2int_rn(sm.ftable[k1 & 31] * q.y));
+    f0 = on0 ? f0 : 0u;
+    f1 = on1 ? f1 : 0u;
+    // f 2^(32 - s), s at least 20 (PTX shifts stop at the width, C's may not)
+    const uint32_t s0 = top - (k0 >> 5), s1 = top - (k1 >> 5);
+    asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {0, %1};\n\tshr.u64 %0, a, %2;\n\t}"
+        : "=l"(w0) : "r"(f0), "r"(s0));
+    asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {0, %1};\n\tshr.u64 %0, a, %2;\n\t}"
+        : "=l"(w1) : "r"(f1), "r"(s1));
+    if (fmaxf(v.x, v.y) >= heavy) {
+      if (on0 && v.x >= heavy) w0 = smp_heavy_weight(f.x, g.x, k0, s0);
+      if (on1 && v.y >= heavy) w1 = smp_heavy_weight(f.y, g.y, k1, s1);
+    }
+  };
+  auto weight = [&](float v) {
+    uint64_t w0, w1;
+    weight2(smp_both(v), true, false, w0, w1);
+    return w0;
   };
   // below: no weight left of 2^-44; within 2^-12 of the largest; kept by min-p
   // (finite, so that -inf is below all three)
   const float tau_w = fmaxf(m - 43.0f * 0.69314718f * temp, -3.4028235e38f);
-  const float tau_l = fmaxf(m - 12.0f * 0.69314718f * temp, -3.4028235e38f);
-  float tau_0;
+  float tau_l = fmaxf(m - 12.0f * 0.69314718f * temp, -3.4028235e38f);
+  float tau_0;   // the smallest float at or above m + T ln(min-p)
   {
-    const double t0 = static_cast<double>(m) + static_cast<double>(temp) * sm.ln_min;
-    tau_0 = __double2float_ru(t0);
+    const float a = temp * sm.ln_hi, ae = fmaf(temp, sm.ln_hi, -a) + temp * sm.ln_lo;
+    const float b = m + a, bb = b - m;
+    const float be = ((m - (b - bb)) + (a - bb)) + ae;
+    tau_0 = fmaxf(be > 0.0f ? nextafterf(b, INFINITY) : b, -3.4028235e38f);
   }
   const float bin_scale = (kSmpBins - 0.5f) / (43.0f * 0.69314718f) / temp;
   auto logit_bin = [&](float v) {   // monotone: each operation is
     return min(static_cast<int>((m - v) * bin_scale), kSmpBins - 1);
   };
-  const bool by_k = sm.top_k > 0 && sm.top_k < p.vocab, by_p = sm.top_p < 1.0f;
 
-  auto each = [&](auto f) {   // f(value, row index) over this warp's vectors
-    for (int v = wv0 + lane; v < wv1; v += 32) {
-      const uint4 r = xs[v];
-#pragma unroll
-      for (int e = 0; e < kV; ++e) f(SmpVec<T>::at(r, e), first + v * kV + e);
+  // f(value, row index) over this warp's tokens, in index order over its lanes:
+  // the gathered ones, or all
+  int n_gathered = 0;
+  uint64_t above = 0;   // a lane's weight above them
+  auto each = [&](const SmpCmd& c, auto f) {
+    const int n = c.gathered ? n_gathered : (u1 - u0) * 2;
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) {
+      const int at = c.gathered ? sm.gathered[warp][i] : u0 * 2 + i;
+      f(static_cast<float>(xe[at]), first + at);
     }
   };
   auto key_of = [&](float v, int i) {
@@ -437,25 +572,55 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     const int k = atomicAdd(&sm.list_n, 1);
     if (k < kSmpList) sm.buf[k] = key_of(v, i);
   };
-  auto tell_sum = [&](uint64_t s) {
+  auto tell_sum = [&](uint64_t s, uint64_t* where) {
     s = smp_warp_sum(s);
-    if (lane == 0) *smp_remote(&sm.xsum[rank * kSmpWarps + warp], 0) = s;
+    if (lane == 0) *smp_remote(&where[rank * kSmpWarps + warp], 0) = s;
   };
 
   // ---- pass 2
-  {
-    uint64_t s = 0;
-    if (!by_k && !by_p) {
-      each([&](float v, int) { s += v >= tau_0 ? weight(v) : 0; });
-    } else {
-      each([&](float v, int i) {
-        s += v >= tau_w ? weight(v) : 0;
-        if (v >= tau_l) push(v, i);
-      });
-      __syncthreads();
-      if (tid == 0) *smp_remote(&sm.xlist[rank], 0) = sm.list_n;
+  if (by_groups) {
+    tau_l = heavy;
+#pragma unroll 1
+    for (int u = u0 + lane; u < u1; u += 32) {
+      const float2 x = SmpVec<T>::pair(xs, u);
+      if (fmaxf(x.x, x.y) >= tau_l) {
+        if (x.x >= tau_l) push(x.x, first + 2 * u);
+        if (x.y >= tau_l) push(x.y, first + 2 * u + 1);
+      }
     }
-    tell_sum(s);
+  } else {
+    uint64_t s = 0, listed = 0;   // weights of all, of the list
+    const bool filter = by_k || by_p;
+    const float from = filter ? tau_w : tau_0;
+    int turn = 0;
+#pragma unroll 2
+    for (int u = u0 + lane; u < u1; u += 32, ++turn) {
+      const float2 x = SmpVec<T>::pair(xs, u);
+      uint64_t w0, w1;
+      weight2(x, x.x >= from, x.y >= from, w0, w1);
+      s += w0 + w1;
+      if (!filter) continue;
+      if (fmaxf(x.x, x.y) >= tau_l) {
+        if (x.x >= tau_l) {
+          push(x.x, first + 2 * u);
+          listed += w0;
+        }
+        if (x.y >= tau_l) {
+          push(x.y, first + 2 * u + 1);
+          listed += w1;
+        }
+      }
+      if (turn % kSmpSample == 0) {
+        if (x.x >= tau_w) atomicAdd(&sm.sampled[logit_bin(x.x)], 1u);
+        if (x.y >= tau_w) atomicAdd(&sm.sampled[logit_bin(x.y)], 1u);
+      }
+    }
+    tell_sum(s, sm.xsum);
+    if (filter) tell_sum(listed, sm.xlmass);
+  }
+  if (by_k || by_p) {
+    __syncthreads();
+    if (tid == 0) *smp_remote(&sm.xlist[rank], 0) = sm.list_n;
   }
   smp_cluster_sync();
 
@@ -476,16 +641,57 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
   // What the first CTA asks for, carried out by all.
   auto carry_out = [&](const SmpCmd& c) {
     switch (c.op) {
+      case kOpCompact: {
+        // the window's tokens in index order, and the count and weight of those
+        // above it
+        n_gathered = 0;
+        above = 0;
+        uint32_t n_above = 0;
+#pragma unroll 1
+        for (int u = u0; u < u1; u += 32) {
+          const bool on = u + lane < u1;
+          const float2 x =
+              on ? SmpVec<T>::pair(xs, u + lane) : smp_both(-INFINITY);   // (c.from is finite)
+          const bool over0 = x.x >= c.upto, over1 = x.y >= c.upto;
+          const bool in0 = x.x >= c.from && !over0, in1 = x.y >= c.from && !over1;
+          if (over0 || over1) {
+            uint64_t w0, w1;
+            weight2(x, over0, over1, w0, w1);
+            above += w0 + w1;
+            n_above += (over0 ? 1 : 0) + (over1 ? 1 : 0);
+          }
+          const unsigned b0 = __ballot_sync(0xFFFFFFFFu, in0), b1 = __ballot_sync(0xFFFFFFFFu, in1);
+          if (b0 | b1) {
+            const unsigned below = (1u << lane) - 1u;
+            int at = n_gathered + __popc(b0 & below) + __popc(b1 & below);
+            if (in0 && at < kSmpGathered)
+              sm.gathered[warp][at] = static_cast<uint16_t>(2 * (u + lane));
+            at += in0 ? 1 : 0;
+            if (in1 && at < kSmpGathered)
+              sm.gathered[warp][at] = static_cast<uint16_t>(2 * (u + lane) + 1);
+            n_gathered += __popc(b0) + __popc(b1);
+          }
+        }
+        n_above = __reduce_add_sync(0xFFFFFFFFu, n_above);
+        if (lane == 0) *smp_remote(&sm.xcnt[rank * kSmpWarps + warp], 0) = n_above;
+        tell_sum(above, sm.xsum);
+        if (n_gathered > kSmpGathered) {
+          n_gathered = 0;
+          if (lane == 0) atomicAdd(smp_remote(&sm.over, 0), 1u);
+        }
+        __syncwarp();
+      }
+        [[fallthrough]];
       case kOpHistLogit:
       case kOpHistKey:
-        for (int b = tid; b < kSmpBins; b += kSmpThreads) sm.cnt[b] = sm.mlo[b] = sm.mhi[b] = 0;
+        sm.cnt[tid] = sm.mlo[tid] = sm.mhi[tid] = 0;
         __syncthreads();
-        if (c.op == kOpHistLogit) {
-          each([&](float v, int) {
+        if (c.op != kOpHistKey) {
+          each(c, [&](float v, int) {
             if (v >= tau_w) hist_add(logit_bin(v), v);
           });
         } else {
-          each([&](float v, int) {
+          each(c, [&](float v, int) {
             const uint32_t o = smp_order(v);
             if (o <= c.khi && o >= c.klo) hist_add((c.khi - o) >> c.shift, v);
           });
@@ -496,11 +702,11 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
         if (tid == 0) sm.list_n = 0;
         __syncthreads();
         if (c.op == kOpGatherLogit) {
-          each([&](float v, int i) {
+          each(c, [&](float v, int i) {
             if (v >= tau_w && logit_bin(v) == c.bin) push(v, i);
           });
         } else {
-          each([&](float v, int i) {
+          each(c, [&](float v, int i) {
             const uint32_t o = smp_order(v);
             if (o <= c.khi && o >= c.klo) push(v, i);
           });
@@ -515,7 +721,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
           sm.hi = hi;
         }
         __syncthreads();
-        each([&](float v, int) {
+        each(c, [&](float v, int) {
           if (v >= tau_w && logit_bin(v) == c.bin) {
             lo = min(lo, smp_order(v));
             hi = max(hi, smp_order(v));
@@ -536,7 +742,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       }
       case kOpCountEqual: {
         uint32_t n = 0;
-        each([&](float v, int) { n += smp_order(v) == c.khi; });
+        each(c, [&](float v, int) { n += smp_order(v) == c.khi; });
         n = __reduce_add_sync(0xFFFFFFFFu, n);
         if (lane == 0) *smp_remote(&sm.xcnt[rank * kSmpWarps + warp], 0) = n;
         break;
@@ -544,74 +750,69 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       case kOpFindEqual:   // the nth of a warp's equal keys
         if (rank == c.rank && warp == c.warp) {
           int before = 0;
-          for (int v = wv0; v < wv1; v += 32) {
-            int n = 0;
-            uint4 r = make_uint4(0, 0, 0, 0);
-            if (v + lane < wv1) {
-              r = xs[v + lane];
-#pragma unroll
-              for (int e = 0; e < kV; ++e) n += smp_order(SmpVec<T>::at(r, e)) == c.khi;
-            }
-            int at = before + static_cast<int>(smp_warp_scan(static_cast<uint64_t>(n), lane)) - n;
-            if (at <= c.nth && c.nth < at + n) {
-#pragma unroll
-              for (int e = 0; e < kV; ++e) {
-                if (smp_order(SmpVec<T>::at(r, e)) != c.khi) continue;
-                if (at++ == c.nth)
-                  *smp_remote(&sm.found, 0) = static_cast<uint32_t>(first + (v + lane) * kV + e);
-              }
-            }
-            before += __reduce_add_sync(0xFFFFFFFFu, n);
+          const int n = c.gathered ? n_gathered : (u1 - u0) * 2;
+          for (int i = 0; i < n; i += 32) {
+            int at = 0;
+            if (i + lane < n) at = c.gathered ? sm.gathered[warp][i + lane] : u0 * 2 + i + lane;
+            const unsigned same = __ballot_sync(
+                0xFFFFFFFFu, i + lane < n && smp_order(static_cast<float>(xe[at])) == c.khi);
+            if ((same >> lane) & 1u && before + __popc(same & ((1u << lane) - 1u)) == c.nth)
+              *smp_remote(&sm.found, 0) = static_cast<uint32_t>(first + at);
+            before += __popc(same);
           }
         }
         break;
       case kOpSum: {
-        uint64_t s = 0;
-        each([&](float v, int i) { s += kept(c, v, i) ? weight(v) : 0; });
-        tell_sum(s);
+        uint64_t s = c.gathered ? above : 0;
+        each(c, [&](float v, int i) { s += kept(c, v, i) ? weight(v) : 0; });
+        tell_sum(s, sm.xsum);
         break;
       }
-      case kOpPick:   // the token in this warp's run at which its sum exceeds the target
-        if (rank == c.rank && warp == c.warp) {
-          uint64_t before = 0;
-          int token = -1;
-          float logprob = 0.0f;
-          for (int v = wv0; v < wv1; v += 32) {
-            uint64_t s = 0;
-            uint4 r = make_uint4(0, 0, 0, 0);
-            const int i0 = first + (v + lane) * kV;
-            if (v + lane < wv1) {
-              r = xs[v + lane];
-#pragma unroll
-              for (int e = 0; e < kV; ++e) {
-                const float z = SmpVec<T>::at(r, e);
-                s += kept(c, z, i0 + e) ? weight(z) : 0;
-              }
-            }
-            const uint64_t incl = before + smp_warp_scan(s, lane);
-            const bool mine = incl - s <= c.target && c.target < incl;
-            const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
-            if (who) {
-              if (mine) {
-                uint64_t at = incl - s;
+      case kOpPick:
+        // the token at which the running sum exceeds the target, in the run of
+        // one warp: all warps of its CTA take a sixteenth of it each
+        if (rank == c.rank) {
+          const int r0 = min(n_pairs, c.warp * per), r1 = min(n_pairs, r0 + per);
+          const int part = (r1 - r0 + kSmpWarps - 1) / kSmpWarps;
+          const int q0 = min(r1, r0 + warp * part), q1 = min(r1, q0 + part);
+          auto pair_weights = [&](int u, uint64_t& w0, uint64_t& w1) {
+            w0 = w1 = 0;
+            if (u >= q1) return;
+            const float2 x = SmpVec<T>::pair(xs, u);
+            weight2(x, kept(c, x.x, first + 2 * u), kept(c, x.y, first + 2 * u + 1), w0, w1);
+          };
+          uint64_t s = 0, w0, w1;
 #pragma unroll 1
-                for (int e = 0; e < kV; ++e) {
-                  const float z = SmpVec<T>::at(r, e);
-                  const uint64_t w = kept(c, z, i0 + e) ? weight(z) : 0;
-                  if (token < 0 && c.target < at + w) {
-                    token = i0 + e;
-                    logprob = smp_log_share(w, c.total);
-                  }
-                  at += w;
-                }
-              }
-              token = __shfl_sync(0xFFFFFFFFu, token, __ffs(who) - 1);
-              logprob = __shfl_sync(0xFFFFFFFFu, logprob, __ffs(who) - 1);
-              break;
-            }
-            before = __shfl_sync(0xFFFFFFFFu, incl, 31);
+          for (int u = q0; u < q1; u += 32) {
+            pair_weights(u + lane, w0, w1);
+            s += w0 + w1;
           }
-          smp_finish(p, row, token, logprob, lane);
+          s = smp_warp_sum(s);
+          if (lane == 0) sm.wtot[0][warp] = s;
+          __syncthreads();
+          uint64_t before = 0;
+          for (int i = 0; i < warp; ++i) before += sm.wtot[0][i];
+          if (before <= c.target && c.target < before + s) {   // one warp
+#pragma unroll 1
+            for (int u = q0; u < q1; u += 32) {
+              pair_weights(u + lane, w0, w1);
+              const uint64_t incl = before + smp_warp_scan(w0 + w1, lane);
+              const uint64_t start = incl - w0 - w1;
+              const unsigned who =
+                  __ballot_sync(0xFFFFFFFFu, start <= c.target && c.target < incl);
+              if (who) {
+                const bool second = c.target >= start + w0;
+                const int src = __ffs(who) - 1;
+                const int token = __shfl_sync(
+                    0xFFFFFFFFu, first + 2 * (u + lane) + (second ? 1 : 0), src);
+                const float logprob = __shfl_sync(
+                    0xFFFFFFFFu, smp_log_share(second ? w1 : w0, c.total), src);
+                smp_finish(p, row, token, logprob, lane);
+                break;
+              }
+              before = __shfl_sync(0xFFFFFFFFu, incl, 31);
+            }
+          }
         }
         break;
       default: break;
@@ -647,13 +848,14 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       n += c;
     }
     const uint64_t key = off >= 0 ? *smp_remote(&sm.buf[off], src) : 0;
-    sm.keys[tid] = key;
+    __syncthreads();   // (this CTA's own list lay there)
+    sm.buf[tid] = key;
     sm.run[tid] = 0;
     __syncthreads();
     if (tid < n) {
       int above = 0;
 #pragma unroll 8
-      for (int i = 0; i < n; ++i) above += sm.keys[i] > key;
+      for (int i = 0; i < n; ++i) above += sm.buf[i] > key;
       sm.sorted[above] = key;
       sm.run[above] = weight(smp_value(static_cast<uint32_t>(key >> 32)));
     }
@@ -677,33 +879,23 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
   auto locate = [&]() {
     const bool by_mass = sm.by_mass;
     const uint64_t target = sm.target - (by_mass ? sm.acc_mass : sm.acc_cnt);
-    uint64_t c2[2], m2[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int b = 2 * tid + k;
-      c2[k] = m2[k] = 0;
-      for (int r = 0; r < cs; ++r) {
-        c2[k] += *smp_remote(&sm.cnt[b], r);
-        m2[k] += (static_cast<uint64_t>(*smp_remote(&sm.mhi[b], r)) << 32) +
-                 *smp_remote(&sm.mlo[b], r);
-      }
+    uint64_t c1 = 0, m1 = 0;
+    for (int r = 0; r < cs; ++r) {
+      c1 += *smp_remote(&sm.cnt[tid], r);
+      m1 += (static_cast<uint64_t>(*smp_remote(&sm.mhi[tid], r)) << 32) +
+            *smp_remote(&sm.mlo[tid], r);
     }
-    uint64_t a = c2[0] + c2[1], b = m2[0] + m2[1];
+    uint64_t a = c1, b = m1;
     if (tid == 0) sm.hit = -1;
     block_scan(a, b);
-    uint64_t ca = a - c2[0] - c2[1], ma = b - m2[0] - m2[1];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint64_t was = by_mass ? ma : ca, now = by_mass ? ma + m2[k] : ca + c2[k];
-      if (was < target && target <= now) {   // one thread's, if any
-        sm.hit = 2 * tid + k;
-        sm.hit_cnt = static_cast<uint32_t>(c2[k]);
-        sm.acc_cnt += ca;
-        sm.acc_mass += ma;
-      }
-      ca += c2[k];
-      ma += m2[k];
+    const uint64_t now = by_mass ? b : a, was = now - (by_mass ? m1 : c1);
+    if (was < target && target <= now) {   // one thread's, if any
+      sm.hit = tid;
+      sm.hit_cnt = static_cast<uint32_t>(c1);
+      sm.acc_cnt += a - c1;
+      sm.acc_mass += b - m1;
     }
+    if (tid == kSmpThreads - 1) sm.binned = b;
     __syncthreads();
   };
   // Starts the search for the cut at which the running count (weight) of the
@@ -717,6 +909,64 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     }
     c.op = kOpHistLogit;
     state = kAfterHist;
+  };
+  // The same where the list did not do, over a window around an estimate of
+  // the cut: the list's count (weight), the sampled counts below it, and an
+  // eighth of what lies below the list either way. Too many tokens in it: over
+  // all.
+  auto search_gathered = [&](SmpCmd& c, bool by_mass, uint64_t target) {
+    search(c, by_mass, target);
+    c.gathered = 0;
+    uint64_t listed = tid < cs * kSmpWarps ? sm.xlmass[tid] : 0, ignored = 0;
+    block_scan(listed, ignored);
+    listed = 0;
+    for (int i = 0; i < kSmpWarps; ++i) listed += sm.wtot[0][i];
+    // pairs of a warp's run for one that was sampled
+    const int turns = per / (32 * kSmpSample), rest = per - turns * 32 * kSmpSample;
+    const float each_one = static_cast<float>(per) / (turns * 32 + min(rest, 32));
+    uint32_t seen = 0;
+    for (int r = 0; r < cs; ++r) seen += *smp_remote(&sm.sampled[tid], r);
+    const float count = static_cast<float>(seen) * each_one;
+    // a bin's tokens, and their weight in units of 2^24; a list that is
+    // complete stands for the bins that it covers
+    const int n = sm.list_all, list_bin = n <= kSmpList ? logit_bin(tau_l) : -1;
+    const float mid = static_cast<float>(weight(m) >> 24) *
+                      tc::ex2(-43.0f / (kSmpBins - 0.5f) * (tid + 0.5f)) * count;
+    const uint64_t a0 = tid < list_bin ? 0 : tid == list_bin ? n : static_cast<uint64_t>(count);
+    const uint64_t b0 =
+        tid < list_bin ? 0 : tid == list_bin ? listed >> 24 : static_cast<uint64_t>(mid);
+    uint64_t a = a0, b = b0;
+    if (tid == 0) {
+      sm.hit = sm.hit2 = kSmpBins - 1;
+      sm.over = 0;
+    }
+    block_scan(a, b);
+    const uint64_t now = by_mass ? b : a, was = now - (by_mass ? b0 : a0);
+    const uint64_t base = list_bin < 0 ? 0 : by_mass ? listed >> 24 : n;
+    const uint64_t goal = by_mass ? target >> 24 : target;
+    const uint64_t slack = (goal > base ? (goal - base) / 8 : 0) + 2;
+    const uint64_t first_goal = goal > base + slack ? goal - slack : base + 1;
+    if (was < first_goal && first_goal <= now) {
+      sm.hit2 = tid;
+      sm.need = a - a0;
+    }
+    if ((was < goal + slack && goal + slack <= now) ||
+        (tid == kSmpThreads - 1 && now < goal + slack)) {
+      sm.hit = tid;
+      sm.hit_cnt = static_cast<uint32_t>(a);
+    }
+    if (tid == kSmpThreads - 1 && now < first_goal) sm.need = a - a0;
+    __syncthreads();
+    const int64_t inside = static_cast<int64_t>(sm.hit_cnt) - static_cast<int64_t>(sm.need);
+    if (inside + inside / 4 < kSmpGathered * kSmpWarps * cs) {
+      c.op = kOpCompact;
+      c.gathered = 1;
+      c.from = m - static_cast<float>(sm.hit + 2) / bin_scale;
+      c.upto = sm.hit2 > 1 ? m - static_cast<float>(sm.hit2 - 1) / bin_scale : INFINITY;
+      if (list_bin >= 0) c.upto = fminf(c.upto, tau_l);
+      c.from = fminf(c.from, c.upto);
+    }
+    __syncthreads();
   };
   // A list that holds every cut: the token comes from it. False: it does not.
   auto from_list = [&]() {
@@ -795,20 +1045,49 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
           sm.mass = a;            // of all tokens
           sm.cut_key = 0;         // no cut: every key is above it
           sm.cut_index = 0;
+          int n = 0;
+          for (int r = 0; r < cs; ++r) n += sm.xlist[r];
+          sm.list_all = n;
         }
         __syncthreads();
         if (!by_k && !by_p) {
           pick(c);
         } else if (from_list()) {
           c.op = kOpDone;
+        } else if (by_groups) {   // more equal tokens than the list holds
+          search(c, false, static_cast<uint64_t>(sm.top_k));
         } else {
-          search(c, !by_k, by_k ? static_cast<uint64_t>(sm.top_k) : share(sm.mass));
+          search_gathered(c, !by_k, by_k ? static_cast<uint64_t>(sm.top_k) : share(sm.mass));
         }
         return;
       }
       case kAfterHist:
-        locate();
+        if (c.gathered) {
+          // what lies above the window comes first
+          uint64_t a = tid < cs * kSmpWarps ? sm.xcnt[tid] : 0;
+          uint64_t b = tid < cs * kSmpWarps ? sm.xsum[tid] : 0;
+          block_scan(a, b);
+          if (tid == kSmpThreads - 1) {
+            sm.acc_cnt = a;
+            sm.acc_mass = b;
+          }
+          __syncthreads();
+          bool in = sm.over == 0 && sm.target > (sm.by_mass ? sm.acc_mass : sm.acc_cnt);
+          if (in) {
+            locate();
+            in = sm.hit >= 0;
+          }
+          if (!in) {   // too many, or the cut is not in the window
+            c.gathered = 0;
+            search(c, sm.by_mass, sm.target);
+            return;
+          }
+        } else {
+          locate();
+        }
         if (sm.hit < 0) {   // fewer than top_k tokens have a weight
+          __syncthreads();
+          if (tid == 0) sm.mass = sm.binned;
           found = true;
           break;
         }
@@ -884,7 +1163,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
         return;
       }
       if (span > 0) {
-        c.shift = max(0, 32 - __clz(span) - 10);
+        c.shift = max(0, 32 - __clz(span) - kSmpBinBits);
         c.op = kOpHistKey;
         state = kAfterKeyHist;
         return;
@@ -911,9 +1190,12 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       const bool more = by_p && !sm.by_mass;
       __syncthreads();
       if (more) {
-        search(c, true, share(sm.mass));
+        if (by_groups) search(c, true, share(sm.mass));
+        else search_gathered(c, true, share(sm.mass));
         return;
       }
+      // (tokens above the window may be cut by min-p: then over all)
+      if (!(tau_0 <= c.from)) c.gathered = 0;
       c.op = kOpSum;
       c.khi = sm.cut_key;
       c.nth = sm.cut_index;
@@ -940,7 +1222,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
 // Rows are cut so that two CTAs fit an SM (one's passes run while the other's
 // row arrives); few rows over as many CTAs as leave each some thousand tokens
 // (a cluster of more than eight lies in one GPC, so only for a handful of rows).
-constexpr int kSmpSliceBytes = 80 * 1024;
+constexpr int kSmpSliceBytes = 76 * 1024;
 constexpr int kSmpMostBytes = 176 * 1024;   // one CTA an SM
 
 template <typename T>
