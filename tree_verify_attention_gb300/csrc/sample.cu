@@ -60,7 +60,7 @@ constexpr int kSmpTopMost = 256;           // top-k by group maxima
 constexpr int kSmpHeavy = 24;              // tokens weighed in 64 bits, about
 constexpr int kSmpGroups = 1024;           // of them, at most
 constexpr int kSmpGathered = 384;          // of a warp
-constexpr int kSmpSample = 8;
+constexpr int kSmpSample = 8;              // turns of a warp for one whose tokens are counted
 constexpr int kSmpMaxCluster = 16;
 constexpr int kSmpMaxVocab = 1 << 19;      // sums of weights stay below 2^63
 constexpr float kSmpMinT = 0x1p-100f;      // below: greedy
@@ -105,6 +105,7 @@ enum SmpOp {
 struct SmpCmd {
   int op, bin, shift, rank, warp, nth;
   int gathered;          // over the gathered tokens
+  int under_list;        // the window ends where the list begins
   float from, upto;      // gather the tokens of logits in [from, upto)
   uint32_t khi, klo;     // keys, both included
   uint64_t target, total;
@@ -112,10 +113,11 @@ struct SmpCmd {
 
 struct SmpSmem {
   uint32_t cnt[kSmpBins], mlo[kSmpBins], mhi[kSmpBins];   // a bin's count and weight
-  uint64_t buf[kSmpList];      // this CTA's list; first CTA: then the cluster's
+  alignas(16) uint64_t buf[kSmpList];   // this CTA's list; first CTA: then the cluster's,
+                                        // then its weights in order
   union {
     uint64_t sorted[kSmpList];   // in order
-    float gmax[kSmpGroups];      // before: the cluster's group maxima
+    alignas(16) float gmax[kSmpGroups];      // before: the cluster's group maxima
   };
   uint64_t run[kSmpList];      // running weights
   uint32_t sampled[kSmpBins];  // counts of every eighth piece
@@ -474,9 +476,10 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       const float g = sm.gmax[i];
       int above = 0, same = 0;
 #pragma unroll 4
-      for (int j = 0; j < all; ++j) {
-        above += sm.gmax[j] > g;
-        same += sm.gmax[j] >= g;
+      for (int j = 0; j < all; j += 4) {   // (at least 16 groups, a power of two)
+        const float4 o = *reinterpret_cast<const float4*>(&sm.gmax[j]);
+        above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
+        same += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
       }
       if (above < want && same >= want) sm.bound = g;   // the same value from each such thread
     }
@@ -553,16 +556,20 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     return min(static_cast<int>((m - v) * bin_scale), kSmpBins - 1);
   };
 
-  // f(value, row index) over this warp's tokens, in index order over its lanes:
-  // the gathered ones, or all
+  // f(logits, row index of the first, which of the two) over this warp's tokens:
+  // the gathered ones, one a lane, or all, a pair a lane.
   int n_gathered = 0;
-  uint64_t above = 0;   // a lane's weight above them
+  uint64_t above = 0, listed = 0;   // a lane's weight above them, and in the list
   auto each = [&](const SmpCmd& c, auto f) {
-    const int n = c.gathered ? n_gathered : (u1 - u0) * 2;
+    const int n = c.gathered ? n_gathered : u1 - u0;
 #pragma unroll 1
     for (int i = lane; i < n; i += 32) {
-      const int at = c.gathered ? sm.gathered[warp][i] : u0 * 2 + i;
-      f(static_cast<float>(xe[at]), first + at);
+      if (c.gathered) {
+        const int at = sm.gathered[warp][i];
+        f(make_float2(static_cast<float>(xe[at]), -INFINITY), first + at, false);
+      } else {
+        f(SmpVec<T>::pair(xs, u0 + i), first + 2 * (u0 + i), true);
+      }
     }
   };
   auto key_of = [&](float v, int i) {
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       }
     }
   } else {
-    uint64_t s = 0, listed = 0;   // weights of all, of the list
+    uint64_t s = 0;
     const bool filter = by_k || by_p;
     const float from = filter ? tau_w : tau_0;
     int turn = 0;
@@ -624,8 +631,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
   }
   smp_cluster_sync();
 
-  auto hist_add = [&](int b, float v) {
-    const uint64_t w = weight(v);
+  auto hist_add = [&](int b, uint64_t w) {
     atomicAdd(&sm.cnt[b], 1u);
     const uint32_t lo = static_cast<uint32_t>(w);
     const uint32_t was = atomicAdd(&sm.mlo[b], lo);
@@ -645,7 +651,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
         // the window's tokens in index order, and the count and weight of those
         // above it
         n_gathered = 0;
-        above = 0;
+        above = c.under_list ? listed : 0;
         uint32_t n_above = 0;
 #pragma unroll 1
         for (int u = u0; u < u1; u += 32) {
@@ -654,7 +660,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
               on ? SmpVec<T>::pair(xs, u + lane) : smp_both(-INFINITY);   // (c.from is finite)
           const bool over0 = x.x >= c.upto, over1 = x.y >= c.upto;
           const bool in0 = x.x >= c.from && !over0, in1 = x.y >= c.from && !over1;
-          if (over0 || over1) {
+          if (!c.under_list && (over0 || over1)) {
             uint64_t w0, w1;
             weight2(x, over0, over1, w0, w1);
             above += w0 + w1;
@@ -686,31 +692,41 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       case kOpHistKey:
         sm.cnt[tid] = sm.mlo[tid] = sm.mhi[tid] = 0;
         __syncthreads();
-        if (c.op != kOpHistKey) {
-          each(c, [&](float v, int) {
-            if (v >= tau_w) hist_add(logit_bin(v), v);
-          });
-        } else {
-          each(c, [&](float v, int) {
-            const uint32_t o = smp_order(v);
-            if (o <= c.khi && o >= c.klo) hist_add((c.khi - o) >> c.shift, v);
-          });
-        }
+        each(c, [&](float2 v, int, bool) {
+          bool in0, in1;
+          int b0, b1;
+          if (c.op != kOpHistKey) {
+            in0 = v.x >= tau_w;
+            in1 = v.y >= tau_w;
+            b0 = logit_bin(v.x);
+            b1 = logit_bin(v.y);
+          } else {
+            const uint32_t o0 = smp_order(v.x), o1 = smp_order(v.y);
+            in0 = o0 <= c.khi && o0 >= c.klo;
+            in1 = o1 <= c.khi && o1 >= c.klo;
+            b0 = (c.khi - o0) >> c.shift;
+            b1 = (c.khi - o1) >> c.shift;
+          }
+          if (!in0 && !in1) return;
+          uint64_t w0, w1;
+          weight2(v, in0, in1, w0, w1);
+          if (in0) hist_add(b0, w0);
+          if (in1) hist_add(b1, w1);
+        });
         break;
       case kOpGatherLogit:
       case kOpGatherKey:
         if (tid == 0) sm.list_n = 0;
         __syncthreads();
-        if (c.op == kOpGatherLogit) {
-          each(c, [&](float v, int i) {
-            if (v >= tau_w && logit_bin(v) == c.bin) push(v, i);
-          });
-        } else {
-          each(c, [&](float v, int i) {
-            const uint32_t o = smp_order(v);
-            if (o <= c.khi && o >= c.klo) push(v, i);
-          });
-        }
+        each(c, [&](float2 v, int i, bool) {
+          auto in = [&](float z) {
+            if (c.op == kOpGatherLogit) return z >= tau_w && logit_bin(z) == c.bin;
+            const uint32_t o = smp_order(z);
+            return o <= c.khi && o >= c.klo;
+          };
+          if (in(v.x)) push(v.x, i);
+          if (in(v.y)) push(v.y, i + 1);
+        });
         __syncthreads();
         if (tid == 0) *smp_remote(&sm.xlist[rank], 0) = sm.list_n;
         break;
@@ -721,11 +737,15 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
           sm.hi = hi;
         }
         __syncthreads();
-        each(c, [&](float v, int) {
-          if (v >= tau_w && logit_bin(v) == c.bin) {
-            lo = min(lo, smp_order(v));
-            hi = max(hi, smp_order(v));
-          }
+        each(c, [&](float2 v, int, bool) {
+          auto add = [&](float z) {
+            if (z >= tau_w && logit_bin(z) == c.bin) {
+              lo = min(lo, smp_order(z));
+              hi = max(hi, smp_order(z));
+            }
+          };
+          add(v.x);
+          add(v.y);
         });
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
         hi = __reduce_max_sync(0xFFFFFFFFu, hi);
@@ -742,7 +762,9 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       }
       case kOpCountEqual: {
         uint32_t n = 0;
-        each(c, [&](float v, int) { n += smp_order(v) == c.khi; });
+        each(c, [&](float2 v, int, bool) {
+          n += (smp_order(v.x) == c.khi) + (smp_order(v.y) == c.khi);
+        });
         n = __reduce_add_sync(0xFFFFFFFFu, n);
         if (lane == 0) *smp_remote(&sm.xcnt[rank * kSmpWarps + warp], 0) = n;
         break;
@@ -764,7 +786,13 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
         break;
       case kOpSum: {
         uint64_t s = c.gathered ? above : 0;
-        each(c, [&](float v, int i) { s += kept(c, v, i) ? weight(v) : 0; });
+        each(c, [&](float2 v, int i, bool both) {
+          const bool k0 = kept(c, v.x, i), k1 = both && kept(c, v.y, i + 1);
+          if (!k0 && !k1) return;
+          uint64_t w0, w1;
+          weight2(v, k0, k1, w0, w1);
+          s += w0 + w1;
+        });
         tell_sum(s, sm.xsum);
         break;
       }
@@ -852,14 +880,20 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     sm.buf[tid] = key;
     sm.run[tid] = 0;
     __syncthreads();
+    int above = 0;
+    uint64_t w = 0;
     if (tid < n) {
-      int above = 0;
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) above += sm.buf[i] > key;
+#pragma unroll 4
+      for (int i = 0; i < n; i += 2) {   // (zeros behind the last)
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&sm.buf[i]);
+        above += (two.x > key) + (two.y > key);
+      }
+      w = weight(smp_value(static_cast<uint32_t>(key >> 32)));
       sm.sorted[above] = key;
-      sm.run[above] = weight(smp_value(static_cast<uint32_t>(key >> 32)));
+      sm.run[above] = w;
     }
     __syncthreads();
+    if (tid < n) sm.buf[above] = w;   // the weights, in order
     uint64_t a = sm.run[tid], b = 0;
     block_scan(a, b);
     sm.run[tid] = a;
@@ -912,15 +946,15 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
   };
   // The same where the list did not do, over a window around an estimate of
   // the cut: the list's count (weight), the sampled counts below it, and an
-  // eighth of what lies below the list either way. Too many tokens in it: over
-  // all.
+  // eighth of what lies below the list either way (a 48th without a complete
+  // list). Too many tokens in it: over all.
   auto search_gathered = [&](SmpCmd& c, bool by_mass, uint64_t target) {
     search(c, by_mass, target);
     c.gathered = 0;
-    uint64_t listed = tid < cs * kSmpWarps ? sm.xlmass[tid] : 0, ignored = 0;
-    block_scan(listed, ignored);
-    listed = 0;
-    for (int i = 0; i < kSmpWarps; ++i) listed += sm.wtot[0][i];
+    uint64_t in_list = tid < cs * kSmpWarps ? sm.xlmass[tid] : 0, ignored = 0;
+    block_scan(in_list, ignored);
+    in_list = 0;
+    for (int i = 0; i < kSmpWarps; ++i) in_list += sm.wtot[0][i];
     // pairs of a warp's run for one that was sampled
     const int turns = per / (32 * kSmpSample), rest = per - turns * 32 * kSmpSample;
     const float each_one = static_cast<float>(per) / (turns * 32 + min(rest, 32));
@@ -934,7 +968,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
                       tc::ex2(-43.0f / (kSmpBins - 0.5f) * (tid + 0.5f)) * count;
     const uint64_t a0 = tid < list_bin ? 0 : tid == list_bin ? n : static_cast<uint64_t>(count);
     const uint64_t b0 =
-        tid < list_bin ? 0 : tid == list_bin ? listed >> 24 : static_cast<uint64_t>(mid);
+        tid < list_bin ? 0 : tid == list_bin ? in_list >> 24 : static_cast<uint64_t>(mid);
     uint64_t a = a0, b = b0;
     if (tid == 0) {
       sm.hit = sm.hit2 = kSmpBins - 1;
@@ -942,9 +976,10 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     }
     block_scan(a, b);
     const uint64_t now = by_mass ? b : a, was = now - (by_mass ? b0 : a0);
-    const uint64_t base = list_bin < 0 ? 0 : by_mass ? listed >> 24 : n;
+    const uint64_t base = list_bin < 0 ? 0 : by_mass ? in_list >> 24 : n;
     const uint64_t goal = by_mass ? target >> 24 : target;
-    const uint64_t slack = (goal > base ? (goal - base) / 8 : 0) + 2;
+    // (a share of the whole row is known better than one of what is below a list)
+    const uint64_t slack = (goal > base ? (goal - base) / (list_bin < 0 ? 48 : 8) : 0) + 2;
     const uint64_t first_goal = goal > base + slack ? goal - slack : base + 1;
     if (was < first_goal && first_goal <= now) {
       sm.hit2 = tid;
@@ -957,13 +992,16 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     }
     if (tid == kSmpThreads - 1 && now < first_goal) sm.need = a - a0;
     __syncthreads();
+    const int64_t room = kSmpGathered * kSmpWarps * cs * 4 / 5;
     const int64_t inside = static_cast<int64_t>(sm.hit_cnt) - static_cast<int64_t>(sm.need);
-    if (inside + inside / 4 < kSmpGathered * kSmpWarps * cs) {
+    // (the list's weight is known: a window up to it costs no weights above it)
+    c.under_list = list_bin >= 0 && static_cast<int64_t>(sm.hit_cnt) - n < room;
+    if (c.under_list || inside < room) {
       c.op = kOpCompact;
       c.gathered = 1;
       c.from = m - static_cast<float>(sm.hit + 2) / bin_scale;
       c.upto = sm.hit2 > 1 ? m - static_cast<float>(sm.hit2 - 1) / bin_scale : INFINITY;
-      if (list_bin >= 0) c.upto = fminf(c.upto, tau_l);
+      if (list_bin >= 0) c.upto = c.under_list ? tau_l : fminf(c.upto, tau_l);
       c.from = fminf(c.from, c.upto);
     }
     __syncthreads();
@@ -996,14 +1034,11 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     const uint64_t target = __umul64hi(__float2ull_rz(sm.u * 0x1p64f), total);
     if (tid < keep) {
       const uint32_t mine = ~static_cast<uint32_t>(sm.sorted[tid]);
-      const uint64_t w = sm.run[tid] - (tid == 0 ? 0 : sm.run[tid - 1]);
-      uint64_t before = 0, was = 0;
+      const uint64_t w = sm.buf[tid];
+      uint64_t before = 0;
 #pragma unroll 4
-      for (int i = 0; i < keep; ++i) {
-        const uint64_t now = sm.run[i];
-        if (~static_cast<uint32_t>(sm.sorted[i]) < mine) before += now - was;
-        was = now;
-      }
+      for (int i = 0; i < keep; ++i)
+        before += ~static_cast<uint32_t>(sm.sorted[i]) < mine ? sm.buf[i] : 0;
       if (before <= target && target < before + w) {
         sm.result = static_cast<int>(mine);
         sm.result_logprob = smp_log_share(w, total);
@@ -1039,26 +1074,33 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     bool refine = false, found = false;
     switch (state) {
       case kStart: {
+        if (!by_k && !by_p) {   // no cut: every key is above it
+          if (tid == 0) sm.cut_key = sm.cut_index = 0;
+          pick(c);
+          return;
+        }
         uint64_t a = tid < cs * kSmpWarps ? sm.xsum[tid] : 0, b = 0;
         block_scan(a, b);
         if (tid == kSmpThreads - 1) {
           sm.mass = a;            // of all tokens
-          sm.cut_key = 0;         // no cut: every key is above it
-          sm.cut_index = 0;
+          sm.cut_key = sm.cut_index = 0;
           int n = 0;
           for (int r = 0; r < cs; ++r) n += sm.xlist[r];
           sm.list_all = n;
         }
         __syncthreads();
-        if (!by_k && !by_p) {
-          pick(c);
-        } else if (from_list()) {
+        const uint64_t goal = by_k ? static_cast<uint64_t>(sm.top_k) : share(sm.mass);
+        uint64_t l = tid < cs * kSmpWarps ? sm.xlmass[tid] : 0, ignored = 0;
+        block_scan(l, ignored);
+        l = 0;
+        for (int i = 0; i < kSmpWarps; ++i) l += sm.wtot[0][i];
+        // (a list of too few tokens, or too little weight, need not be sorted)
+        if ((by_groups || (by_k ? sm.list_all >= sm.top_k : l >= goal)) && from_list())
           c.op = kOpDone;
-        } else if (by_groups) {   // more equal tokens than the list holds
-          search(c, false, static_cast<uint64_t>(sm.top_k));
-        } else {
-          search_gathered(c, !by_k, by_k ? static_cast<uint64_t>(sm.top_k) : share(sm.mass));
-        }
+        else if (by_groups)   // more equal tokens than the list holds
+          search(c, false, goal);
+        else
+          search_gathered(c, !by_k, goal);
         return;
       }
       case kAfterHist:
@@ -1068,7 +1110,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
           uint64_t b = tid < cs * kSmpWarps ? sm.xsum[tid] : 0;
           block_scan(a, b);
           if (tid == kSmpThreads - 1) {
-            sm.acc_cnt = a;
+            sm.acc_cnt = c.under_list ? sm.list_all : a;
             sm.acc_mass = b;
           }
           __syncthreads();
