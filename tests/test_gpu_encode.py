@@ -201,6 +201,20 @@ def test_infinities_and_nan_stay_in_their_head():
     assert torch.equal(got[2], v)
 
 
+def test_infinities_outside_the_rotated_part():
+    """Dims that are not rotated do not meet: an infinity stays alone."""
+    d, n = 256, 3
+    for near in (False, True):
+        q, k, v = (rows(i, n, 2, d, F32) for i in range(3))
+        rope = api.Rope(d, 64, interleaved=near, device=DEV)
+        clean, got = outs(n, 2, 2, d, F32), outs(n, 2, 2, d, F32)
+        api.qk_norm_rope(q, k, v, rope, *clean, ctx_len=i32([3]), eps=None)
+        q[1, 1, 200], k[0, 0, 65] = math.inf, -math.inf
+        api.qk_norm_rope(q, k, v, rope, *got, ctx_len=i32([3]), eps=None)
+        clean[0][1, 1, 200], clean[1][0, 0, 65] = math.inf, -math.inf
+        assert all(torch.equal(a, b) for a, b in zip(got, clean))
+
+
 def test_streams_and_graphs():
     n, d = 23, 256
     q, k, v = (rows(i, n, h, d, BF16) for i, h in enumerate((24, 4, 4)))

@@ -22,10 +22,14 @@
 
 namespace dfv {
 
-constexpr int kEncWarps = 4;
+// CTAs of one warp: the SM takes the next row as soon as one is done (16411 rows
+// of 32 / 8 heads of 128: 75 us, by four warps 78).
+constexpr int kEncWarps = 1;
 
 struct EncodeParams {
-  int n_rows, hq, hkv, rot, iters, splits, per_split;
+  int n_rows, hq, hkv, rot;
+  int iters, it_k, it_v;   // of a row, the key heads' and the value heads' first
+  int splits, per_split;
   const void *q, *k, *v;
   int64_t q_row, q_head, k_row, k_head, v_row, v_head;
   const float *q_weight, *k_weight;
@@ -110,7 +114,7 @@ __device__ __forceinline__ int enc_depth(const EncodeParams& p, int row, int lan
 }
 
 template <typename TS, typename TD, int D, bool kVec>
-__global__ void __launch_bounds__(kEncWarps * 32, 4)
+__global__ void __launch_bounds__(kEncWarps * 32, 16)
     encode_kernel(const __grid_constant__ EncodeParams p, int near) {
   constexpr int kLanes = D / 16;         // lanes of a head
   constexpr int kHeads = 32 / kLanes;    // heads of a warp at a time
@@ -122,99 +126,149 @@ __global__ void __launch_bounds__(kEncWarps * 32, 4)
   grid_dep_launch_dependents();   // (after the wait: see common.cuh)
   if (row >= p.n_rows) return;
   const int64_t row64 = row;
-  const int it0 = (static_cast<int>(task) - row * p.splits) * p.per_split;
-  const int it1 = min(p.iters, it0 + p.per_split);
-  const int j = lane % kLanes;
+  const int j = lane % kLanes, mine = lane / kLanes;
   const int rl = p.rot >> 4;             // lanes with rotated pairs
   const bool turned = j < rl;
   const int ca = turned && !near ? 8 * j : 16 * j;
   const int cb = turned && !near ? 8 * (j + rl) : 16 * j + 8;
+  // This warp's iterations [it0, it1) of the row's: the query heads', the key
+  // heads', the value heads'.
+  const int it0 = (static_cast<int>(task) - row * p.splits) * p.per_split;
+  const int it1 = min(p.iters, it0 + p.per_split);
 
-  // element (head, dim 0) of the lane's head in iteration `it`, null behind the last
-  auto source = [&](int it) -> const TS* {
-    const int h = it * kHeads + lane / kLanes;
-    if (h < p.hq) return static_cast<const TS*>(p.q) + row * p.q_row + h * p.q_head;
-    if (h < p.hq + p.hkv)
-      return static_cast<const TS*>(p.k) + row * p.k_row + (h - p.hq) * p.k_head;
-    if (h < p.hq + 2 * p.hkv && p.v)
-      return static_cast<const TS*>(p.v) + row * p.v_row + (h - p.hq - p.hkv) * p.v_head;
-    return nullptr;
-  };
-  // loads of the next iterations are in flight while these are worked on
-  EncLoad<TS, kVec> xa[2][kAhead], xb[2][kAhead];
-  auto fetch = [&](int it, int s) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const TS* src = it + u < it1 ? source(it + u) : nullptr;
-      if (src) {
-        xa[s][u].load(src + ca);
-        xb[s][u].load(src + cb);
-      }
-    }
-  };
-  fetch(it0, 0);
-
-  int64_t pos;
-  if (p.positions) {
-    pos = p.positions[row];
-  } else {
-    pos = static_cast<int64_t>(*p.ctx_len) + (p.dropped ? *p.dropped : 0);
-    pos += p.parent ? enc_depth(p, row, lane) : row;
+  // A row that is one warp's is asked for at once: its loads, an iteration or two
+  // ahead, then find it on its way (78 us for 80 without).
+  if (p.splits == 1) {
+    constexpr int kLines = D * static_cast<int>(sizeof(TS)) / 128;   // of a head
+    auto ask = [&](const void* src, int64_t stride_row, int64_t stride_head, int heads) {
+      for (int i = lane; i < heads * kLines; i += 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            static_cast<const TS*>(src) + row * stride_row + (i / kLines) * stride_head +
+            (i % kLines) * (128 / static_cast<int>(sizeof(TS)))));
+    };
+    if (p.q) ask(p.q, p.q_row, p.q_head, p.hq);
+    if (p.k) ask(p.k, p.k_row, p.k_head, p.hkv);
+    if (p.v) ask(p.v, p.v_row, p.v_head, p.hkv);
   }
+
   float cs[8], sn[8];
+  if (it0 < p.it_v) {
+    int64_t pos;
+    if (p.positions) {
+      pos = p.positions[row];
+    } else {
+      pos = static_cast<int64_t>(*p.ctx_len) + (p.dropped ? *p.dropped : 0);
+      pos += p.parent ? enc_depth(p, row, lane) : row;
+    }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cs[e] = 1.0f;
-    sn[e] = 0.0f;
-    if (turned) {
-      const uint64_t t = static_cast<uint64_t>(pos) * p.turns[8 * j + e];
-      // the upper half as a signed fraction of a turn, in units of half a turn
-      sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &sn[e], &cs[e]);
+    for (int e = 0; e < 8; ++e) {
+      cs[e] = 1.0f;
+      sn[e] = 0.0f;
+      if (turned) {
+        const uint64_t t = static_cast<uint64_t>(pos) * p.turns[8 * j + e];
+        // the upper half as a signed fraction of a turn, in units of half a turn
+        sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &sn[e], &cs[e]);
+      }
     }
   }
   const bool norm = p.eps >= 0.0f;
 
-  auto work = [&](int it, int s) {
+  // Iterations [a, b) over `heads` heads at src, to dst. Loads of the next
+  // iterations are in flight while one is worked on; lanes without a head work on
+  // the last one and store nothing.
+  EncLoad<TS, kVec> xa[2][kAhead], xb[2][kAhead];
+  auto heads_of = [&](const void* src0, int64_t stride_head, void* dst0, int heads, int a, int b,
+                      auto work) {
+    if (a >= b) return;
+    const TS* src = static_cast<const TS*>(src0);
+    TD* dst = static_cast<TD*>(dst0) + row64 * heads * D;
+    auto fetch = [&](int it, int s) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (it + u >= it1) break;
-      const int h = (it + u) * kHeads + lane / kLanes;
-      const bool on = source(it + u) != nullptr;
-      float a[8], b[8];
+      for (int u = 0; u < kAhead; ++u) {
+        if (it + u >= b) break;
+        const TS* x = src + min((it + u) * kHeads + mine, heads - 1) * stride_head;
+        xa[s][u].load(x + ca);
+        xb[s][u].load(x + cb);
+      }
+    };
+    auto turn = [&](int it, int s) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (it + u >= b) break;
+        float va[8], vb[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          va[e] = xa[s][u].at(e);
+          vb[e] = xb[s][u].at(e);
+        }
+        work(va, vb);
+        const int h = (it + u) * kHeads + mine;
+        if (h < heads) {
+          enc_store(dst + h * D + ca, va);
+          enc_store(dst + h * D + cb, vb);
+        }
+      }
+    };
+    fetch(a, 0);
+    for (int it = a; it < b; it += 2 * kAhead) {
+      fetch(it + kAhead, 1);
+      turn(it, 0);
+      fetch(it + 2 * kAhead, 0);
+      turn(it + kAhead, 1);
+    }
+  };
+
+  // Norm and rotation of a head: the weights are folded into the pairs' sines and
+  // cosines, once for all heads; a = (a pa - b qa) r, b = (b pb + a qb) r, with
+  // each element's partner as b (or a) where neighbours are pairs.
+  auto turned_heads = [&](const void* src, int64_t stride_head, void* dst, int heads,
+                          const float* w, int a, int b) {
+    if (a >= b) return;
+    float pa[8], qa[8], pb[8], qb[8];
+    {
+      float wa[8], wb[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.0f;
+      if (w) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(w + ca + e);
+          const float4 g = *reinterpret_cast<const float4*>(w + cb + e);
+          wa[e] = f.x, wa[e + 1] = f.y, wa[e + 2] = f.z, wa[e + 3] = f.w;
+          wb[e] = g.x, wb[e + 1] = g.y, wb[e + 2] = g.z, wb[e + 3] = g.w;
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        a[e] = on ? xa[s][u].at(e) : 0.0f;
-        b[e] = on ? xb[s][u].at(e) : 0.0f;
+        if (near) {
+          pa[e] = wa[e] * cs[e >> 1];
+          pb[e] = wb[e] * cs[4 + (e >> 1)];
+          qa[e] = wa[e ^ 1] * ((e & 1) ? sn[e >> 1] : -sn[e >> 1]);
+          qb[e] = wb[e ^ 1] * ((e & 1) ? sn[4 + (e >> 1)] : -sn[4 + (e >> 1)]);
+        } else {
+          pa[e] = wa[e] * cs[e];
+          pb[e] = wb[e] * cs[e];
+          qa[e] = -wb[e] * sn[e];
+          qb[e] = wa[e] * sn[e];
+        }
       }
-      const bool is_v = h >= p.hq + p.hkv;
+    }
+    heads_of(src, stride_head, dst, heads, a, b, [&](float* x, float* y) {
+      float r = 1.0f;
       if (norm) {
-        float ss = 0.0f;
+        float ss = 0.0f, eps = p.eps;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(b[e], b[e], fmaf(a[e], a[e], ss));
+        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], fmaf(x[e], x[e], ss));
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float* w = h < p.hq ? p.q_weight : p.k_weight;
-        float wa[8], wb[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.0f;
-        if (w && on && !is_v) {
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(w + ca + e);
-            const float4 g = *reinterpret_cast<const float4*>(w + cb + e);
-            wa[e] = f.x, wa[e + 1] = f.y, wa[e + 2] = f.z, wa[e + 3] = f.w;
-            wb[e] = g.x, wb[e + 1] = g.y, wb[e + 2] = g.z, wb[e + 3] = g.w;
-          }
-        }
         // Squares that leave float32, or vanish in it where eps does not hide
         // them: the head is brought to [1, 2) by a power of two first, and eps
         // with it (where that leaves float32, eps is all there is).
-        float eps = p.eps;
-        const bool wide = !is_v && on && (ss > 1e37f || (ss < 1e-25f && eps < 1e-15f));
+        const bool wide = ss > 1e37f || (ss < 1e-25f && eps < 1e-15f);
         if (__any_sync(0xFFFFFFFFu, wide)) {
           float m = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(a[e]), fabsf(b[e])));
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(x[e]), fabsf(y[e])));
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1)
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -222,65 +276,62 @@ __global__ void __launch_bounds__(kEncWarps * 32, 4)
           float sc = wide && m > 0.0f && m < INFINITY ? pow2i(max(127 - e2, -126)) : 1.0f;
           if (!(eps * sc * sc < INFINITY)) sc = 1.0f;
           eps = eps * sc * sc;
-          float s2 = 0.0f;
+          ss = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            a[e] *= sc;
-            b[e] *= sc;
-            s2 = fmaf(b[e], b[e], fmaf(a[e], a[e], s2));
+            x[e] *= sc;
+            y[e] *= sc;
+            ss = fmaf(y[e], y[e], fmaf(x[e], x[e], ss));
           }
 #pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
-          ss = s2;
+          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         }
-        const float r = is_v ? 1.0f : 1.0f / sqrtf(ss * (1.0f / D) + eps);
+        r = 1.0f / sqrtf(ss * (1.0f / D) + eps);
+      }
+      float u[8], v[8];
+      if (turned && near) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          a[e] = a[e] * r * wa[e];
-          b[e] = b[e] * r * wb[e];
+          u[e] = fmaf(x[e ^ 1], qa[e], x[e] * pa[e]) * r;
+          v[e] = fmaf(y[e ^ 1], qb[e], y[e] * pb[e]) * r;
+        }
+      } else if (turned) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          u[e] = fmaf(y[e], qa[e], x[e] * pa[e]) * r;
+          v[e] = fmaf(x[e], qb[e], y[e] * pb[e]) * r;
+        }
+      } else {   // (no 0 * inf from a neighbour)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          u[e] = x[e] * pa[e] * r;
+          v[e] = y[e] * pb[e] * r;
         }
       }
-      if (turned && !is_v) {
-        if (near) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a0 = a[2 * e], a1 = a[2 * e + 1], b0 = b[2 * e], b1 = b[2 * e + 1];
-            a[2 * e] = fmaf(a0, cs[e], -a1 * sn[e]);
-            a[2 * e + 1] = fmaf(a1, cs[e], a0 * sn[e]);
-            b[2 * e] = fmaf(b0, cs[4 + e], -b1 * sn[4 + e]);
-            b[2 * e + 1] = fmaf(b1, cs[4 + e], b0 * sn[4 + e]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float a0 = a[e], b0 = b[e];
-            a[e] = fmaf(a0, cs[e], -b0 * sn[e]);
-            b[e] = fmaf(b0, cs[e], a0 * sn[e]);
-          }
-        }
+      for (int e = 0; e < 8; ++e) {
+        x[e] = u[e];
+        y[e] = v[e];
       }
-      if (on) {
-        TD* dst = h < p.hq ? static_cast<TD*>(p.q_out) + (row64 * p.hq + h) * D
-                  : !is_v ? static_cast<TD*>(p.k_out) + (row64 * p.hkv + (h - p.hq)) * D
-                          : static_cast<TD*>(p.v_out) + (row64 * p.hkv + (h - p.hq - p.hkv)) * D;
-        enc_store(dst + ca, a);
-        enc_store(dst + cb, b);
-      }
-    }
+    });
   };
-  for (int it = it0; it < it1; it += 2 * kAhead) {
-    fetch(it + kAhead, 1);
-    work(it, 0);
-    fetch(it + 2 * kAhead, 0);
-    work(it + kAhead, 1);
-  }
+  if (p.q)
+    turned_heads(static_cast<const TS*>(p.q) + row * p.q_row, p.q_head, p.q_out, p.hq, p.q_weight,
+                 it0, min(it1, p.it_k));
+  if (p.k)
+    turned_heads(static_cast<const TS*>(p.k) + row * p.k_row, p.k_head, p.k_out, p.hkv,
+                 p.k_weight, max(it0, p.it_k) - p.it_k, min(it1, p.it_v) - p.it_k);
+  if (p.v)
+    heads_of(static_cast<const TS*>(p.v) + row * p.v_row, p.v_head, p.v_out, p.hkv,
+             max(it0, p.it_v) - p.it_v, it1 - p.it_v, [](float*, float*) {});
 }
 
 template <typename TS, typename TD, int D>
 dfv_status encode_launch(EncodeParams p, bool near, cudaStream_t stream) {
-  const int heads = p.hq + (p.v ? 2 : 1) * p.hkv;
   constexpr int kHeads = 32 / (D / 16);
-  p.iters = (heads + kHeads - 1) / kHeads;
+  p.it_k = (p.hq + kHeads - 1) / kHeads;
+  p.it_v = p.it_k + (p.hkv + kHeads - 1) / kHeads;
+  p.iters = p.v ? p.it_v + (p.hkv + kHeads - 1) / kHeads : p.it_v;
   // One warp a row where that fills the GPU (the sines are computed once for
   // all of its heads); else rows are split until there are about 32 warps an SM.
   const int64_t want = (static_cast<int64_t>(sm_count()) * 32 + p.n_rows - 1) / p.n_rows;
@@ -348,7 +399,7 @@ extern "C" dfv_status dfv_qk_norm_rope(
       !aligned(k_weight, 16) || !aligned(turns, 8) || !aligned(positions, 4) ||
       !aligned(parent, 4) || !aligned(ctx_len, 4) || !aligned(dropped, 4))
     return DFV_ERR_INVALID;
-  const EncodeParams p = {n_rows, n_q_heads, n_kv_heads, rot_dim, 0, 0, 0,
+  const EncodeParams p = {n_rows, n_q_heads, n_kv_heads, rot_dim, 0, 0, 0, 0, 0,
                           n_q_heads > 0 ? q : nullptr, n_kv_heads > 0 ? k : nullptr, v,
                           q_stride_row, q_stride_head, k_stride_row, k_stride_head, v_stride_row,
                           v_stride_head, q_weight, k_weight, eps, turns, positions, parent,
