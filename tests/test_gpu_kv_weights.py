@@ -165,7 +165,16 @@ def test_accepted_nodes():
         want = torch.empty(hkv, C, device=DEV)
         at = path[:L]
         api.kv_weights(cache, q[at].contiguous(), lse[at].contiguous(), want, prev=prev)
-        assert int(st) == 0 and torch.equal(out, want)
+        assert int(st) == 0
+        if L * hq // hkv > 16:
+            assert torch.equal(out, want)
+        else:   # up to 16 rows of a head are summed in another order: each within its tolerance
+            qn, ln = (t[at].double().cpu().numpy() for t in (q, lse))
+            ref = OV.weights(qn, ln, k, prev.double().cpu().numpy())
+            had = prev.double().cpu().numpy()
+            tol = tolerance(qn, ln, k, had, 0, 1 / math.sqrt(d), d, ref)
+            for x in (out, want):
+                assert np.all(np.abs(x.double().cpu().numpy() - ref) <= tol)
     for L, now in ((0, 0), (24, 23), (-1, 0)):
         out, st = torch.empty(hkv, C, device=DEV), i32([0])
         api.kv_weights(cache, q, lse, out, prev=prev, accept_len=i32([L]), status=st)

@@ -15,6 +15,12 @@
 // exact. Query rows are scaled by a power of two each, which the exponent's
 // factor takes back.
 //
+// Up to 16 query rows of a KV head (decoding) leave TMEM room for the sums of
+// each block of 32 dims apart: then K^ is the codes' integers alone, half the
+// products and stores and a third of the conversion, and a key's block scales
+// are factors of its lane's sums (131060 keys, 4 heads of 256, 6 rows each:
+// MODEB us, by hi and lo 36.8).
+//
 // A CTA works through a run of 128-key chunks of (at most a few) heads, in parts
 // of 64 dims. Q4_0: one warp copies raw rows into a ring, two groups of four
 // convert parts in turn into TMEM, the product's A operand. F16: the two groups
@@ -33,20 +39,25 @@ constexpr int kWtKeys = 128;
 constexpr int kWtMma = 16, kWtRaw = 17;      // warps 0-7: sums, 8-15: operands
 constexpr int kWtThreads = 18 * 32;
 
-template <int D, bool kQ4>
+enum WeightMode { kModeF16, kModeSplit, kModeBlocks };   // Q4_0: hi and lo, or block by block
+
+template <int D, int kMode>
 struct WeightShape {
-  static constexpr int kRows = kQ4 || D == 256 ? 128 : 256;   // query rows of a tile, at most
+  static constexpr bool kQ4 = kMode != kModeF16, kBlocks = kMode == kModeBlocks;
+  // query rows of a tile, at most
+  static constexpr int kRows = kBlocks ? 16 : kQ4 || D == 256 ? 128 : 256;
   static constexpr int kRowBytes = kQ4 ? D / 32 * 18 : D * 2;
   static constexpr int kParts = D / 64;                       // of a chunk
-  static constexpr int kPartCols = 64;                        // Q4_0: TMEM columns, hi and lo
+  static constexpr int kPartCols = kBlocks ? 32 : 64;         // Q4_0: TMEM columns
   static constexpr int kPartBytes = kWtKeys * 128;            // F16: a tile of 64 dims
-  static constexpr int kRing = kQ4 ? 256 / kPartCols : 8;     // parts
+  static constexpr int kRing = kBlocks ? 2 * kParts : kQ4 ? 4 : 8;   // parts
   static constexpr int kStages = 4;                           // Q4_0: raw chunks
   static constexpr int kStage = (kWtKeys * kRowBytes + 16 + 127) / 128 * 128;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kBytes = kQBytes + (kQ4 ? kStages * kStage : kRing * kPartBytes) + 1024;
-  static constexpr uint32_t kTS = kQ4 ? 256 : 0;              // two buffers of kRows scores
-  static_assert(kTS + 2 * kRows <= 512, "TMEM columns");
+  static constexpr uint32_t kTS = kQ4 ? 256 : 0;              // two buffers of scores
+  static constexpr int kSCols = kBlocks ? 2 * kParts * kRows : kRows;
+  static_assert(kTS + 2 * kSCols <= 512, "TMEM columns");
   static_assert(kBytes <= 220 * 1024, "shared memory");
 };
 
@@ -71,10 +82,11 @@ struct WeightParams {
 // bytes gives pairs (bytes 0, 2 low), (0, 2 high), (1, 3 low), (1, 3 high).
 // Eight consecutive places are word w's dims 4w + {0, 2, 16, 18, 1, 3, 17, 19}.
 
-template <int D, bool kQ4>
+template <int D, int kMode>
 __global__ void __launch_bounds__(kWtThreads, 1)
     kv_weights_kernel(const __grid_constant__ WeightParams p) {
-  using W = WeightShape<D, kQ4>;
+  using W = WeightShape<D, kMode>;
+  constexpr bool kQ4 = W::kQ4, kBlocks = W::kBlocks;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
@@ -89,6 +101,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   // and the first and last position that is seen
   __shared__ __align__(16) float s_slope[2][W::kRows], s_off[2][W::kRows];
   __shared__ __align__(16) int s_first[2][W::kRows], s_last[2][W::kRows];
+  // Block scales of four chunks' keys in turn. They are written once the part's
+  // place is free: the chunk two before has been multiplied then, which waited
+  // for the sums of the chunk four before.
+  __shared__ __half s_scale[kBlocks ? 4 : 1][kBlocks ? 2 * W::kParts : 1][kBlocks ? kWtKeys : 1];
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp =
@@ -103,7 +119,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       mbar_init(&b_free[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&b_s[i], 1);
+      mbar_init(&b_s[i], kBlocks ? 2 : 1);
       mbar_init(&b_sfree[i], 4);
     }
     mbar_init(&b_q, 8);
@@ -214,8 +230,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           ok = all_wait(&b_part[slot], (part / W::kRing) & 1);
           if (!ok) break;
           if (tc::elect_one()) {
-            const uint32_t d = tmem + W::kTS + buf * W::kRows;
-            if constexpr (kQ4) {
+            const uint32_t d = tmem + W::kTS + buf * W::kSCols;
+            if constexpr (kBlocks) {
+              const uint32_t a = tmem + slot * W::kPartCols;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)   // two steps a block
+                tc::mma_f16_ts(d + (2 * i + (kk >> 1)) * W::kRows, a + kk * 8,
+                               qd + i * q_block + kk * 2, idesc, kk & 1);
+            } else if constexpr (kQ4) {
               const uint32_t a = tmem + slot * W::kPartCols;
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)   // hi, then lo
@@ -231,6 +253,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             }
             tc::commit(&b_free[slot]);
             if (i == W::kParts - 1) tc::commit(&b_s[buf]);
+            // (an arrival of its own: a commit orders the products, not the scales)
+            if (kBlocks && i == W::kParts - 1) mbar_arrive(&b_s[buf]);
           }
           __syncwarp();
         }
@@ -298,7 +322,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
               if (lane == 0) mbar_arrive(&b_read[st]);
             }
             const uint32_t* words = in + (9 * i - p0 * kE);
-            uint32_t hi[32], lo[32];
+            uint32_t hi[32], lo[kBlocks ? 1 : 32];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               // codes follow the scale: words of the first block are 2 bytes off
@@ -306,28 +330,41 @@ __global__ void __launch_bounds__(kWtThreads, 1)
               const uint32_t sc = b == 0 ? w[0] & 0xFFFFu : w[0] >> 16;
               const uint32_t d2 = sc | (sc << 16);
               const __half2 d = *reinterpret_cast<const __half2*>(&d2);
-              const __half2 bias = __float2half2_rn(1032.0f);   // 1024 + 8
+              const __half2 low = __float2half2_rn(1032.0f);    // 1024 + 8
+              const __half2 high = __float2half2_rn(1152.0f);   // 1024 + 16 * 8
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint32_t x = b == 0 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j + 1];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  // 0x6400 | code is 1024 + code
-                  const uint32_t y = ((x >> (4 * e)) & 0x000F000Fu) | 0x64006400u;
-                  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
-                  const __half2 a = __hmul2(v, d);
-                  const __half2 r = __hfma2(v, d, __hneg2(a));
-                  hi[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&a);
-                  lo[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&r);
+                  // 0x6400 | code is 1024 + code; block by block a high nibble
+                  // stays where it is: 0x6400 | code << 4 is 1024 + 16 code
+                  const bool up = kBlocks && (e & 1);
+                  const uint32_t y =
+                      up ? ((x >> (4 * e - 4)) & 0x00F000F0u) | 0x64006400u
+                         : ((x >> (4 * e)) & 0x000F000Fu) | 0x64006400u;
+                  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&y), up ? high : low);
+                  if constexpr (kBlocks) {
+                    hi[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&v);
+                  } else {
+                    const __half2 a = __hmul2(v, d);
+                    const __half2 r = __hfma2(v, d, __hneg2(a));
+                    hi[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&a);
+                    lo[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&r);
+                  }
                 }
               }
             }
             take();
             if (!ok) break;
             tc::fence_after_sync();
+            if constexpr (kBlocks) {   // (not before the place is free)
+              s_scale[k & 3][2 * i][slot] = __ushort_as_half(words[0] & 0xFFFFu);
+              s_scale[k & 3][2 * i + 1][slot] = __ushort_as_half(words[4] >> 16);
+            }
             const uint32_t t = tmem + lanes + (part % W::kRing) * W::kPartCols;
             tc::TmemIo<32>::store(t, hi);
-            tc::TmemIo<32>::store(t + 32, lo);
+            if constexpr (!kBlocks) tc::TmemIo<32>::store(t + 32, lo);
             tc::store_wait();
             tc::fence_before_sync();
             __syncwarp();
@@ -452,18 +489,21 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           const float f = pow2i(141 - e);                    // to below 2^15
           if (off > -INFINITY) slope = p.scale * 1.44269504f * pow2i(e - 141);
           if (r < R) {
-            auto half2_of = [&](uint32_t lo16, uint32_t hi16) {
+            auto half2_of = [](uint32_t lo16, uint32_t hi16, float f) {
               return pack_half2(__uint_as_float(lo16 << 16) * f, __uint_as_float(hi16 << 16) * f);
             };
+            const float g = kBlocks ? f * 0.0625f : f;   // high nibbles are 16 times as large
             const uint2 x = a[i], y = b[i];
             uint4 o;
             if (kQ4)   // dims {0, 2, 16, 18, 1, 3, 17, 19} of the word
-              o = make_uint4(half2_of(x.x & 0xFFFFu, x.y & 0xFFFFu),
-                             half2_of(y.x & 0xFFFFu, y.y & 0xFFFFu),
-                             half2_of(x.x >> 16, x.y >> 16), half2_of(y.x >> 16, y.y >> 16));
+              o = make_uint4(half2_of(x.x & 0xFFFFu, x.y & 0xFFFFu, f),
+                             half2_of(y.x & 0xFFFFu, y.y & 0xFFFFu, g),
+                             half2_of(x.x >> 16, x.y >> 16, f), half2_of(y.x >> 16, y.y >> 16, g));
             else
-              o = make_uint4(half2_of(x.x & 0xFFFFu, x.x >> 16), half2_of(x.y & 0xFFFFu, x.y >> 16),
-                             half2_of(y.x & 0xFFFFu, y.x >> 16), half2_of(y.y & 0xFFFFu, y.y >> 16));
+              o = make_uint4(half2_of(x.x & 0xFFFFu, x.x >> 16, f),
+                             half2_of(x.y & 0xFFFFu, x.y >> 16, f),
+                             half2_of(y.x & 0xFFFFu, y.x >> 16, f),
+                             half2_of(y.y & 0xFFFFu, y.y >> 16, f));
             *reinterpret_cast<uint4*>(sQ + tc::sw128_offset(r, piece, R)) = o;
             if (piece == 0) {
               s_slope[tb][r] = slope;
@@ -496,7 +536,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, role_wait(&b_s[grp], (k >> 1) & 1, &s_dead));
         if (!ok) break;
         tc::fence_after_sync();
-        const uint32_t ts = tmem + lanes + W::kTS + grp * W::kRows;
+        const uint32_t ts = tmem + lanes + W::kTS + grp * W::kSCols;
         // every row sees the whole chunk: up to row 0's own place, from the last row's window on
         const bool whole = (c + 1) * kWtKeys <= at0 + 1 &&
                            (p.window == 0 || c * kWtKeys >= C - p.window);
@@ -504,7 +544,28 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         auto add = [&](auto columns, int r) {
           constexpr int kN = decltype(columns)::value;
           uint32_t x[kN];
-          tc::TmemIo<kN>::load(ts + r, x);
+          if constexpr (kBlocks) {
+            // the blocks' sums times this key's scales, two blocks at a time
+            const int key = (warp & 3) * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < W::kParts; ++i) {
+              uint32_t z[32];
+              tc::TmemIo<32>::load(ts + i * 32, z);
+              const float d0 = __half2float(s_scale[k & 3][2 * i][key]);
+              const float d1 = __half2float(s_scale[k & 3][2 * i + 1][key]);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float a = i == 0 ? 0.0f : __uint_as_float(x[e]);
+                float b = i == 0 ? 0.0f : __uint_as_float(x[e + 1]);
+                fma2(a, b, __uint_as_float(z[e]), __uint_as_float(z[e + 1]), d0, d0, a, b);
+                fma2(a, b, __uint_as_float(z[16 + e]), __uint_as_float(z[16 + e + 1]), d1, d1, a, b);
+                x[e] = __float_as_uint(a);
+                x[e + 1] = __float_as_uint(b);
+              }
+            }
+          } else {
+            tc::TmemIo<kN>::load(ts + r, x);
+          }
 #pragma unroll
           for (int i = 0; i < kN; i += 4) {
             const float4 f = *reinterpret_cast<const float4*>(slope + r + i);
@@ -526,7 +587,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           }
         };
         int r = 0;
-        for (; r + 32 <= R; r += 32) add(Columns<32>(), r);
+        if constexpr (!kBlocks)
+          for (; r + 32 <= R; r += 32) add(Columns<32>(), r);
         if (r < R) add(Columns<16>(), r);
         tc::fence_before_sync();
         __syncwarp();
@@ -558,14 +620,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   if (tid == 0 && s_dead) report(p.status, DFV_DEV_TIMEOUT);
 }
 
-template <int D, bool kQ4>
+template <int D, int kMode>
 dfv_status weights_launch(const WeightParams& p, cudaStream_t stream) {
-  using W = WeightShape<D, kQ4>;
+  using W = WeightShape<D, kMode>;
   static std::atomic<int> allowed[64];   // per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DFV_ERR_CUDA;
   if (!allowed[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kv_weights_kernel<D, kQ4>,
+    if (cudaFuncSetAttribute(kv_weights_kernel<D, kMode>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              W::kBytes) != cudaSuccess)
       return DFV_ERR_CUDA;
@@ -583,13 +645,16 @@ dfv_status weights_launch(const WeightParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_weights_kernel<D, kQ4>, p) == cudaSuccess ? DFV_OK
+  return cudaLaunchKernelEx(&cfg, kv_weights_kernel<D, kMode>, p) == cudaSuccess ? DFV_OK
                                                                                : DFV_ERR_CUDA;
 }
 
 template <int D>
 dfv_status weights_launch_f(const WeightParams& p, bool q4, cudaStream_t stream) {
-  return q4 ? weights_launch<D, true>(p, stream) : weights_launch<D, false>(p, stream);
+  if (!q4) return weights_launch<D, kModeF16>(p, stream);
+  return static_cast<int64_t>(p.n_rows) * p.group <= WeightShape<D, kModeBlocks>::kRows
+             ? weights_launch<D, kModeBlocks>(p, stream)
+             : weights_launch<D, kModeSplit>(p, stream);
 }
 
 }  // namespace dfv
