@@ -19,7 +19,7 @@
 // each block of 32 dims apart: then K^ is the codes' integers alone, half the
 // products and stores and a third of the conversion, and a key's block scales
 // are factors of its lane's sums (131060 keys, 4 heads of 256, 6 rows each:
-// MODEB us, by hi and lo 36.8).
+// 22.8 us, by hi and lo 34).
 //
 // A CTA works through a run of 128-key chunks of (at most a few) heads, in parts
 // of 64 dims. Q4_0: one warp copies raw rows into a ring, two groups of four
@@ -47,16 +47,21 @@ struct WeightShape {
   // query rows of a tile, at most
   static constexpr int kRows = kBlocks ? 16 : kQ4 || D == 256 ? 128 : 256;
   static constexpr int kRowBytes = kQ4 ? D / 32 * 18 : D * 2;
-  static constexpr int kParts = D / 64;                       // of a chunk
-  static constexpr int kPartCols = kBlocks ? 32 : 64;         // Q4_0: TMEM columns
+  // Parts of a chunk: 64 dims, with Q4_0 as many times 64 as leave TMEM room for
+  // two parts (handing a part over costs as much as converting 64 dims: one row
+  // over 131060 keys 22.8 us, by 128 dims 25.9, by 64 30.7).
+  static constexpr int kHalves = kBlocks ? D / 64 : kQ4 && D >= 128 ? 2 : 1;
+  static constexpr int kParts = D / 64 / kHalves;
+  static constexpr int kHalfCols = kBlocks ? 32 : 64;         // Q4_0: TMEM columns
+  static constexpr int kPartCols = kHalves * kHalfCols;
   static constexpr int kPartBytes = kWtKeys * 128;            // F16: a tile of 64 dims
-  static constexpr int kRing = kBlocks ? 2 * kParts : kQ4 ? 4 : 8;   // parts
+  static constexpr int kRing = kBlocks ? 2 * kParts : kQ4 ? 256 / kPartCols : 8;   // parts
   static constexpr int kStages = 4;                           // Q4_0: raw chunks
   static constexpr int kStage = (kWtKeys * kRowBytes + 16 + 127) / 128 * 128;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kBytes = kQBytes + (kQ4 ? kStages * kStage : kRing * kPartBytes) + 1024;
   static constexpr uint32_t kTS = kQ4 ? 256 : 0;              // two buffers of scores
-  static constexpr int kSCols = kBlocks ? 2 * kParts * kRows : kRows;
+  static constexpr int kSCols = kBlocks ? D / 32 * kRows : kRows;
   static_assert(kTS + 2 * kSCols <= 512, "TMEM columns");
   static_assert(kBytes <= 220 * 1024, "shared memory");
 };
@@ -67,6 +72,7 @@ template <int kN> struct Columns {
 
 struct WeightParams {
   int n_rows, hq, hkv, group, window, capacity;
+  uint32_t group_m;   // ceil(2^32 / group) where r / group = umulhi(r, group_m) for all rows, or 0
   const int32_t* ctx_len;
   const uint8_t* k;
   const __nv_bfloat16* q;
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   // Block scales of four chunks' keys in turn. They are written once the part's
   // place is free: the chunk two before has been multiplied then, which waited
   // for the sums of the chunk four before.
-  __shared__ __half s_scale[kBlocks ? 4 : 1][kBlocks ? 2 * W::kParts : 1][kBlocks ? kWtKeys : 1];
+  __shared__ __half s_scale[kBlocks ? 4 : 1][kBlocks ? D / 32 : 1][kBlocks ? kWtKeys : 1];
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp =
@@ -231,18 +237,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           if (!ok) break;
           if (tc::elect_one()) {
             const uint32_t d = tmem + W::kTS + buf * W::kSCols;
-            if constexpr (kBlocks) {
-              const uint32_t a = tmem + slot * W::kPartCols;
+            if constexpr (kQ4) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)   // two steps a block
-                tc::mma_f16_ts(d + (2 * i + (kk >> 1)) * W::kRows, a + kk * 8,
-                               qd + i * q_block + kk * 2, idesc, kk & 1);
-            } else if constexpr (kQ4) {
-              const uint32_t a = tmem + slot * W::kPartCols;
+              for (int hh = 0; hh < W::kHalves; ++hh) {
+                const int g = i * W::kHalves + hh;   // which 64 dims
+                const uint32_t a = tmem + slot * W::kPartCols + hh * W::kHalfCols;
+                if constexpr (kBlocks) {
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)   // hi, then lo
-                tc::mma_f16_ts(d, a + kk * 8, qd + i * q_block + (kk & 3) * 2, idesc,
-                               i > 0 || kk > 0 ? 1u : 0u);
+                  for (int kk = 0; kk < 4; ++kk)   // two steps a block
+                    tc::mma_f16_ts(d + (2 * g + (kk >> 1)) * W::kRows, a + kk * 8,
+                                   qd + g * q_block + kk * 2, idesc, kk & 1);
+                } else {
+#pragma unroll
+                  for (int kk = 0; kk < 8; ++kk)   // hi, then lo
+                    tc::mma_f16_ts(d, a + kk * 8, qd + g * q_block + (kk & 3) * 2, idesc,
+                                   g > 0 || kk > 0 ? 1u : 0u);
+                }
+              }
             } else {
               const uint64_t a =
                   tc::smem_desc_sw128(smem_u32(sK + slot * W::kPartBytes), 1024);
@@ -295,76 +306,82 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           const uint8_t* row = sK + st * W::kStage + slot * W::kRowBytes;
           if (D < 256)
             row += ((static_cast<int64_t>(h) * p.capacity + c * kWtKeys) * W::kRowBytes) & 15;
-          // A part is two blocks of 18 bytes, nine words, read by pieces of D / 16
+          // 64 dims are two blocks of 18 bytes, nine words, read by pieces of D / 16
           // bytes (without bank conflicts: the rows are nine of them apart).
           constexpr int kE = D / 64;                  // words of a piece
           constexpr int kLast = (W::kParts - 1) & ~1; // first of the last two parts
 #pragma unroll
           for (int i = 0; i < W::kParts; ++i, ++part) {
             if ((part & 1) != set) continue;
-            constexpr int kPieces = D == 256 ? 3 : D == 128 ? 5 : 9;
-            const int p0 = 9 * i / kE;                // the piece with the part's first word
-            uint32_t in[kPieces * kE + 1];
+            const uint32_t t = tmem + lanes + (part % W::kRing) * W::kPartCols;
 #pragma unroll
-            for (int e = 0; e < kPieces; ++e) {
-              if constexpr (D == 256) {
-                const uint4 v = *reinterpret_cast<const uint4*>(row + (p0 + e) * 16);
-                in[4 * e] = v.x, in[4 * e + 1] = v.y, in[4 * e + 2] = v.z, in[4 * e + 3] = v.w;
-              } else if constexpr (D == 128) {
-                const uint2 v = *reinterpret_cast<const uint2*>(row + (p0 + e) * 8);
-                in[2 * e] = v.x, in[2 * e + 1] = v.y;
-              } else {
-                in[e] = *reinterpret_cast<const uint32_t*>(row + (p0 + e) * 4);
+            for (int hh = 0; hh < W::kHalves; ++hh) {
+              constexpr int kPieces = D == 256 ? 3 : D == 128 ? 5 : 9;
+              const int g = i * W::kHalves + hh;      // which 64 dims
+              const int p0 = 9 * g / kE;              // the piece with the first word
+              uint32_t in[kPieces * kE + 1];
+#pragma unroll
+              for (int e = 0; e < kPieces; ++e) {
+                if constexpr (D == 256) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(row + (p0 + e) * 16);
+                  in[4 * e] = v.x, in[4 * e + 1] = v.y, in[4 * e + 2] = v.z, in[4 * e + 3] = v.w;
+                } else if constexpr (D == 128) {
+                  const uint2 v = *reinterpret_cast<const uint2*>(row + (p0 + e) * 8);
+                  in[2 * e] = v.x, in[2 * e + 1] = v.y;
+                } else {
+                  in[e] = *reinterpret_cast<const uint32_t*>(row + (p0 + e) * 4);
+                }
               }
-            }
-            if (i >= kLast) {   // the group's last part: every code is in registers
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&b_read[st]);
-            }
-            const uint32_t* words = in + (9 * i - p0 * kE);
-            uint32_t hi[32], lo[kBlocks ? 1 : 32];
+              if (i >= kLast && hh == W::kHalves - 1) {
+                // the group's last codes are in registers
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b_read[st]);
+              }
+              const uint32_t* words = in + (9 * g - p0 * kE);
+              uint32_t hi[32], lo[kBlocks ? 1 : 32];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              // codes follow the scale: words of the first block are 2 bytes off
-              const uint32_t* w = words + 4 * b;
-              const uint32_t sc = b == 0 ? w[0] & 0xFFFFu : w[0] >> 16;
-              const uint32_t d2 = sc | (sc << 16);
-              const __half2 d = *reinterpret_cast<const __half2*>(&d2);
-              const __half2 low = __float2half2_rn(1032.0f);    // 1024 + 8
-              const __half2 high = __float2half2_rn(1152.0f);   // 1024 + 16 * 8
+              for (int b = 0; b < 2; ++b) {
+                // codes follow the scale: words of the first block are 2 bytes off
+                const uint32_t* w = words + 4 * b;
+                const uint32_t sc = b == 0 ? w[0] & 0xFFFFu : w[0] >> 16;
+                const uint32_t d2 = sc | (sc << 16);
+                const __half2 d = *reinterpret_cast<const __half2*>(&d2);
+                const __half2 low = __float2half2_rn(1032.0f);    // 1024 + 8
+                const __half2 high = __float2half2_rn(1152.0f);   // 1024 + 16 * 8
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t x = b == 0 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j + 1];
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t x = b == 0 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j + 1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  // 0x6400 | code is 1024 + code; block by block a high nibble
-                  // stays where it is: 0x6400 | code << 4 is 1024 + 16 code
-                  const bool up = kBlocks && (e & 1);
-                  const uint32_t y =
-                      up ? ((x >> (4 * e - 4)) & 0x00F000F0u) | 0x64006400u
-                         : ((x >> (4 * e)) & 0x000F000Fu) | 0x64006400u;
-                  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&y), up ? high : low);
-                  if constexpr (kBlocks) {
-                    hi[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&v);
-                  } else {
-                    const __half2 a = __hmul2(v, d);
-                    const __half2 r = __hfma2(v, d, __hneg2(a));
-                    hi[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&a);
-                    lo[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&r);
+                  for (int e = 0; e < 4; ++e) {
+                    // 0x6400 | code is 1024 + code; block by block a high nibble
+                    // stays where it is: 0x6400 | code << 4 is 1024 + 16 code
+                    const bool up = kBlocks && (e & 1);
+                    const uint32_t y = up ? ((x >> (4 * e - 4)) & 0x00F000F0u) | 0x64006400u
+                                          : ((x >> (4 * e)) & 0x000F000Fu) | 0x64006400u;
+                    const __half2 v =
+                        __hsub2(*reinterpret_cast<const __half2*>(&y), up ? high : low);
+                    if constexpr (kBlocks) {
+                      hi[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&v);
+                    } else {
+                      const __half2 a = __hmul2(v, d);
+                      const __half2 r = __hfma2(v, d, __hneg2(a));
+                      hi[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&a);
+                      lo[b * 16 + j * 4 + e] = *reinterpret_cast<const uint32_t*>(&r);
+                    }
                   }
                 }
               }
+              if (hh == 0) take();
+              if (!ok) break;
+              if (hh == 0) tc::fence_after_sync();
+              if constexpr (kBlocks) {   // (not before the place is free)
+                s_scale[k & 3][2 * g][slot] = __ushort_as_half(words[0] & 0xFFFFu);
+                s_scale[k & 3][2 * g + 1][slot] = __ushort_as_half(words[4] >> 16);
+              }
+              tc::TmemIo<32>::store(t + hh * W::kHalfCols, hi);
+              if constexpr (!kBlocks) tc::TmemIo<32>::store(t + hh * W::kHalfCols + 32, lo);
             }
-            take();
             if (!ok) break;
-            tc::fence_after_sync();
-            if constexpr (kBlocks) {   // (not before the place is free)
-              s_scale[k & 3][2 * i][slot] = __ushort_as_half(words[0] & 0xFFFFu);
-              s_scale[k & 3][2 * i + 1][slot] = __ushort_as_half(words[4] >> 16);
-            }
-            const uint32_t t = tmem + lanes + (part % W::kRing) * W::kPartCols;
-            tc::TmemIo<32>::store(t, hi);
-            if constexpr (!kBlocks) tc::TmemIo<32>::store(t + 32, lo);
             tc::store_wait();
             tc::fence_before_sync();
             __syncwarp();
@@ -426,6 +443,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       // The largest magnitude of a row becomes a power of two.
       constexpr int kLanes = D / 8, kPerStep = 8 * 32 / kLanes, kBatch = 4;
       const int piece = lane % kLanes;
+      uint32_t problems = 0;
       for (int rb = 0; rb < R; rb += kBatch * kPerStep) {
         uint2 a[kBatch], b[kBatch];
         float l[kBatch];
@@ -439,7 +457,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           s[i] = -1;
           bad[i] = false;
           if (r < live) {
-            const int step = (r0 + r) / p.group, g = (r0 + r) - step * p.group;
+            const int step = p.group_m ? static_cast<int>(__umulhi(r0 + r, p.group_m))
+                                       : (r0 + r) / p.group;
+            const int g = (r0 + r) - step * p.group;
             const int node = p.path ? p.path[step] : step;
             bad[i] = node < 0 || node >= p.n_rows;
             if (!bad[i]) {
@@ -472,22 +492,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           m = max(m & 0xFFFFu, m >> 16);
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-          float slope = 0.0f, off = -INFINITY;
-          int first = 0, last = -1;
-          if (bad[i] && piece == 0) report(p.status, DFV_DEV_BAD_PATH);
-          if (s[i] >= 0 && (m >= 0x7F80u || !(fabsf(l[i]) < INFINITY))) {
-            // a row that is not finite counts for nothing
-            if (piece == 0) report(p.status, DFV_DEV_NONFINITE);
-            a[i] = b[i] = make_uint2(0, 0);
-            m = 0;
-          } else if (s[i] >= 0) {
-            off = -l[i] * 1.44269504f;
-            last = at0 + s[i];
-            first = p.window > 0 ? at0 + s[i] - p.window + 1 : 0;
-          }
-          const int e = max(static_cast<int>(m >> 7), 40);   // largest magnitude below 2^(e - 126)
-          const float f = pow2i(141 - e);                    // to below 2^15
-          if (off > -INFINITY) slope = p.scale * 1.44269504f * pow2i(e - 141);
+          // a row that is not finite counts for nothing
+          const bool fine = s[i] >= 0 && m < 0x7F80u && fabsf(l[i]) < INFINITY;
+          if (bad[i]) problems |= DFV_DEV_BAD_PATH;
+          if (s[i] >= 0 && !fine) problems |= DFV_DEV_NONFINITE;
+          a[i] = fine ? a[i] : make_uint2(0, 0);
+          b[i] = fine ? b[i] : make_uint2(0, 0);
+          const float off = fine ? -l[i] * 1.44269504f : -INFINITY;
+          const int last = fine ? at0 + s[i] : -1;
+          const int first = p.window > 0 ? last - p.window + 1 : 0;
+          const int e = max(fine ? static_cast<int>(m >> 7) : 0, 40);   // all below 2^(e - 126)
+          const float f = pow2i(141 - e);                               // to below 2^15
+          const float slope = fine ? p.scale * 1.44269504f * pow2i(e - 141) : 0.0f;
           if (r < R) {
             auto half2_of = [](uint32_t lo16, uint32_t hi16, float f) {
               return pack_half2(__uint_as_float(lo16 << 16) * f, __uint_as_float(hi16 << 16) * f);
@@ -514,6 +530,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           }
         }
       }
+      if (problems) report(p.status, problems);
       fence_proxy_async_smem();
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&b_q);
@@ -540,7 +557,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // every row sees the whole chunk: up to row 0's own place, from the last row's window on
         const bool whole = (c + 1) * kWtKeys <= at0 + 1 &&
                            (p.window == 0 || c * kWtKeys >= C - p.window);
-        float s0 = 0.0f, s1 = 0.0f;
+        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
         auto add = [&](auto columns, int r) {
           constexpr int kN = decltype(columns)::value;
           uint32_t x[kN];
@@ -548,7 +565,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             // the blocks' sums times this key's scales, two blocks at a time
             const int key = (warp & 3) * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < W::kParts; ++i) {
+            for (int i = 0; i < D / 64; ++i) {
               uint32_t z[32];
               tc::TmemIo<32>::load(ts + i * 32, z);
               const float d0 = __half2float(s_scale[k & 3][2 * i][key]);
@@ -583,7 +600,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
               y3 = j >= a.w && j <= b.w ? y3 : 0.0f;
             }
             add2(s0, s1, s0, s1, y0, y1);
-            add2(s0, s1, s0, s1, y2, y3);
+            add2(s2, s3, s2, s3, y2, y3);
           }
         };
         int r = 0;
@@ -593,7 +610,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_sfree[grp]);
-        if (j < C) *dst = had + (s0 + s1);
+        if (j < C) *dst = had + ((s0 + s1) + (s2 + s3));
       }
       ++run;
       return true;
@@ -679,8 +696,14 @@ extern "C" dfv_status dfv_kv_weights(int n_rows, int n_q_heads, int n_kv_heads, 
       !aligned(ctx_len, 4) || !aligned(path, 4) || !aligned(accept_len, 4))
     return DFV_ERR_INVALID;
   if (scale <= 0.0f) scale = head_dim == 64 ? 0.125f : head_dim == 256 ? 0.0625f : 0.08838834765f;
+  const uint32_t group = static_cast<uint32_t>(n_q_heads / n_kv_heads);
+  // (exact while rows * group stays below 2^32)
+  const uint32_t group_m =
+      group == 1 || static_cast<uint64_t>(n_rows) * group * group >= 1ull << 32
+          ? 0u
+          : static_cast<uint32_t>(((1ull << 32) + group - 1) / group);
   const WeightParams p = {n_rows, n_q_heads, n_kv_heads, n_q_heads / n_kv_heads, window,
-                          cache_capacity, ctx_len, static_cast<const uint8_t*>(k_cache),
+                          cache_capacity, group_m, ctx_len, static_cast<const uint8_t*>(k_cache),
                           static_cast<const __nv_bfloat16*>(q), lse, path, accept_len, scale,
                           decay, prev, weights, status};
   const bool q4 = kv_format == DFV_KV_Q4_0;
