@@ -559,9 +559,10 @@ dfv_status dfv_qk_norm_rope(int n_rows, int n_q_heads, int n_kv_heads, int head_
  *   token[i]  the first index, in index order, at which the running sum of the
  *          kept w exceeds u times their total M;  logprob[i] = ln(w / M)
  *
- * Weights are exact to about 2^-31 and summed as integers, so a result does
- * not depend on how the work is split, and a border between two tokens is off
- * by about 2^-31 of the total. logprob is ln(w / M) to f32.
+ * A weight is off by less than 2^-29 of itself (the largest ones by 2^-35) and
+ * 2^-43 of the largest. Weights are summed as integers, so a result does not
+ * depend on how the work is split, and a border between two tokens lies within
+ * 2^-30 + vocab * 2^-43 of its place in [0, 1). logprob is ln(w / M) to f32.
  *
  * temperature 0 (below 2^-100): the lowest index of the maximum, logprob 0.
  * top_k <= 0 or >= vocab, top_p >= 1, min_p <= 0: off; top_p <= 0 keeps the

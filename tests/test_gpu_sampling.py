@@ -1,10 +1,10 @@
 """Tokens drawn on the GPU against the float64 definition
 (``oracle/sampling.py``).
 
-Tolerances. A weight is off by at most 2^-30 of itself (2^t: the table's 2^-32,
-the cubic's and the two floats' 2^-31) and one unit, which is at most 2^-43 of
-the largest; so a border between two tokens, relative to the total, moves by
-less than 2^-29 + V 2^-43. Tokens have to be equal wherever the float64 draw is
+Tolerances. A weight is off by at most 2^-29 of itself (2^t: the table's 2^-32,
+the quartic's and the two floats' 2^-30) and one unit, which is at most 2^-43 of
+the largest; a border with the part p of the total below it moves by p (1 - p)
+2 2^-29 and V units, less than 2^-29 + V 2^-43. Tokens have to be equal wherever the float64 draw is
 further than that from a border; a row that is nearer says nothing. Of rows with
 k borders at most 2 k (2^-29 + V 2^-43) are, and with top-p as many more as that
 distance is a part of the token at the cut: 2e-8 of 2e-6 for the longest rows

@@ -31,6 +31,7 @@ DEV_TIMEOUT = 0x20
 DEV_NONFINITE = 0x40
 DEV_BAD_TOKEN = 0x80
 DEV_BAD_SAMPLING = 0x100
+MAX_SAMPLE_VOCAB = 1 << 19
 
 KV8_BLOCK = 64       # positions that share a scale in an Int8Cache
 MAX_TOP = 32         # alternatives token_logprobs can return
@@ -495,6 +496,8 @@ def kv_weights(cache, q, lse, weights, prev=None, decay=1.0, path=None, accept_l
             raise DfvError(f"{name} has shape {tuple(t.shape)}, expected {(h, cap)}")
     if weights is None or lse is None:
         raise DfvError("weights and lse are required")
+    if not 0 <= window < 1 << 31:
+        raise DfvError(f"window {window} is out of range")
     index = q.get_device()
     if index != torch._C._cuda_getDevice() or cache.k.get_device() != index:
         _same_device(index, cache.k)
@@ -566,7 +569,7 @@ class Sampling:
                 continue
             if x != x or (name == "temperature" and not 0 <= x < math.inf):
                 raise DfvError(f"{name} {x} is out of range")
-            values.append((None, max(0, min(int(x), 2 ** 31 - 1)) if name == "top_k"
+            values.append((None, int(max(0, min(x, 2 ** 31 - 1))) if name == "top_k"
                            else float(x)))
         self._struct = _lib.SamplingStruct(*(v[0] for v in values), *(v[1] for v in values))
         self.handle = ctypes.addressof(self._struct)
@@ -587,6 +590,8 @@ def _sample_args(logits, uniform, sampling, token):
     row, one = logits.stride()
     if one != 1 and n and vocab > 1:
         raise DfvError("logits rows must be contiguous")
+    if vocab > MAX_SAMPLE_VOCAB:
+        raise DfvError(f"{vocab} logits a row, at most {MAX_SAMPLE_VOCAB}")
     if not isinstance(sampling, Sampling):
         raise DfvError("sampling must be a Sampling")
     index = logits.get_device()
@@ -740,7 +745,8 @@ def qk_norm_rope(q, k, v, rope, q_out, k_out, v_out=None, q_weight=None, k_weigh
         n, hq, hkv, d, pq, pk, pv, DTYPE_F32 if src is torch.float32 else DTYPE_BF16, sq, sqh, sk,
         skh, sv, svh, _ptr(q_weight, "q_weight", torch.float32, d, index),
         _ptr(k_weight, "k_weight", torch.float32, d, index), eps,
-        rope._turns_ptr, rope.rot_dim, rope.interleaved, _ptr(positions, "positions", torch.int32, n, index),
+        rope._turns_ptr, rope.rot_dim, rope.interleaved,
+        _ptr(positions, "positions", torch.int32, n, index),
         _ptr(parent, "parent", torch.int32, n, index),
         _ptr(ctx_len, "ctx_len", torch.int32, 1, index),
         _ptr(dropped, "dropped", torch.int32, 1, index), oq, ok, ov,
@@ -815,6 +821,8 @@ class VerifyStep:
     numbers): ``argmax`` holds the drawn tokens, ``draw_logprob`` their log
     probabilities. The step is then attention, draw with walk, and commit,
     launched one after the other, over any cache (not pipelined)."""
+
+    sampling = None
 
     def __init__(self, n_nodes, n_q_heads, n_kv_heads, head_dim, window, capacity, vocab,
                  max_depth=16, device="cuda", pipelined=False, fmt="q4_0", top=None,
@@ -937,5 +945,5 @@ class VerifyStep:
         # a step takes any shape of n * vocab logits
         n, vocab = self.shape[0], self.shape[-1]
         logits = logits.view(-1)[:n * vocab].view(n, vocab)
-        token_logprobs(_as_bf16(logits), self.argmax, self.logprob, self.entropy, self.top_ids, self.top_logprobs,
-                       status=self.status, stream=stream)
+        token_logprobs(_as_bf16(logits), self.argmax, self.logprob, self.entropy, self.top_ids,
+                       self.top_logprobs, status=self.status, stream=stream)
