@@ -107,6 +107,7 @@ struct SmpCmd {
   int gathered;          // over the gathered tokens
   int under_list;        // the window ends where the list begins
   float from, upto;      // gather the tokens of logits in [from, upto)
+  float bin0, bins;      // bin of a logit v: (bin0 - v) bins
   uint32_t khi, klo;     // keys, both included
   uint64_t target, total;
 };
@@ -555,6 +556,11 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
   auto logit_bin = [&](float v) {   // monotone: each operation is
     return min(static_cast<int>((m - v) * bin_scale), kSmpBins - 1);
   };
+  // of a search: the window's logits, or all, over all bins (a window of equal
+  // logits has one: 0 times infinity converts to 0)
+  auto command_bin = [](const SmpCmd& c, float v) {
+    return min(static_cast<int>((c.bin0 - v) * c.bins), kSmpBins - 1);
+  };
 
   // f(logits, row index of the first, which of the two) over this warp's tokens:
   // the gathered ones, one a lane, or all, a pair a lane.
@@ -698,8 +704,8 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
           if (c.op != kOpHistKey) {
             in0 = v.x >= tau_w;
             in1 = v.y >= tau_w;
-            b0 = logit_bin(v.x);
-            b1 = logit_bin(v.y);
+            b0 = command_bin(c, v.x);
+            b1 = command_bin(c, v.y);
           } else {
             const uint32_t o0 = smp_order(v.x), o1 = smp_order(v.y);
             in0 = o0 <= c.khi && o0 >= c.klo;
@@ -720,7 +726,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
         __syncthreads();
         each(c, [&](float2 v, int i, bool) {
           auto in = [&](float z) {
-            if (c.op == kOpGatherLogit) return z >= tau_w && logit_bin(z) == c.bin;
+            if (c.op == kOpGatherLogit) return z >= tau_w && command_bin(c, z) == c.bin;
             const uint32_t o = smp_order(z);
             return o <= c.khi && o >= c.klo;
           };
@@ -739,7 +745,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
         __syncthreads();
         each(c, [&](float2 v, int, bool) {
           auto add = [&](float z) {
-            if (z >= tau_w && logit_bin(z) == c.bin) {
+            if (z >= tau_w && command_bin(c, z) == c.bin) {
               lo = min(lo, smp_order(z));
               hi = max(hi, smp_order(z));
             }
@@ -942,6 +948,8 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       sm.acc_cnt = sm.acc_mass = 0;
     }
     c.op = kOpHistLogit;
+    c.bin0 = m;
+    c.bins = bin_scale;
     state = kAfterHist;
   };
   // The same where the list did not do, over a window around an estimate of
@@ -1003,6 +1011,8 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       c.upto = sm.hit2 > 1 ? m - static_cast<float>(sm.hit2 - 1) / bin_scale : INFINITY;
       if (list_bin >= 0) c.upto = c.under_list ? tau_l : fminf(c.upto, tau_l);
       c.from = fminf(c.from, c.upto);
+      c.bin0 = fminf(c.upto, m);
+      c.bins = (kSmpBins - 0.5f) / (c.bin0 - c.from);
     }
     __syncthreads();
   };
