@@ -150,7 +150,9 @@ class KVCache:
         if _float_rows(v_out, "v_out", shape, (k_out.dtype,)) != st:
             raise DfvError("k_out and v_out must have the same strides")
         index = self.k.get_device()
-        _same_device(index, k_out, v_out)
+        if (index != torch._C._cuda_getDevice() or k_out.get_device() != index
+                or v_out.get_device() != index):
+            _same_device(index, k_out, v_out)
         _check(lib().dfv_kv_read_rows(
             h, d, self.kv_format, self.capacity, pos0, n, self.k.data_ptr(), self.v.data_ptr(),
             k_out.data_ptr(), v_out.data_ptr(),

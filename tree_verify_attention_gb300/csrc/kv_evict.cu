@@ -5,14 +5,20 @@
 // of the others the ones with the largest weight (ties to the lowest position);
 // the rows keep their order and move bit for bit to another cache.
 //
-// The selection is an exact radix select: three histograms of 11, 11 and 10
-// bits of the weights' ordered bits find the smallest kept weight and how many
-// equal ones are kept; a last pass counts in position order and writes the list.
-// A head belongs to a cluster of up to 8 CTAs, each with its own run of
-// positions, held in registers up to 131072 of them; they add their histograms
+// The selection is an exact radix select: histograms of 11, 8, 8 and 5 bits of
+// the weights' ordered bits find the smallest kept weight and how many equal ones
+// are kept (it ends early where a whole bin stays; with 11 bits in the second one
+// most of 2048 bins went to all CTAs, 4 us more for 131072 positions); a last pass
+// counts in position order and writes the list. Pinned positions have the largest
+// order of all.
+// A head belongs to a cluster of up to 16 CTAs, each with its own run of
+// positions, held in shared memory up to 16384 of them; they add their histograms
 // up in each other's shared memory, so nothing goes through memory and no counter
-// has to be reset. It is bound by latency: four rounds of a few us. The copy is a
-// gather of whole rows and bound by memory.
+// has to be reset. It is bound by latency: up to five rounds of about 2 us (4 heads
+// of 131072 positions: 15 us; of 4097: 8). The copy is a gather of whole rows and
+// bound by memory, as is reading back (32768 rows of 4 heads of 256: 17 and 33 us).
+
+#include <atomic>
 
 #include "common.cuh"
 
@@ -20,8 +26,7 @@ namespace dfv {
 
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kEvBins = 2048;
-constexpr int kEvMaxCluster = 8;
+constexpr int kEvBins = 2048, kEvMore = 256;   // of the first pass, of a later one
 
 struct EvictParams {
   int capacity, keep, sinks, recent, dst_capacity;
@@ -33,11 +38,16 @@ struct EvictParams {
   uint32_t* status;
 };
 
-// Larger for larger weights; -0 equals +0, a NaN is below everything.
+// Larger for larger weights; -0 equals +0, a NaN is below everything. The
+// order of a number is in [0x7FFFFF, 0xFF800000], from which it comes back.
+constexpr uint32_t kEvNan = 1, kEvPinned = 0xFFFFFFFFu, kEvNone = 0;
 __device__ __forceinline__ uint32_t ev_order(float w) {
   const uint32_t u = __float_as_uint(w + 0.0f);
   const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return w == w ? o : 0u;
+  return w == w ? o : kEvNan;
+}
+__device__ __forceinline__ float ev_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
 __device__ __forceinline__ int ev_ctx(const EvictParams& p, bool tell) {
@@ -56,21 +66,22 @@ __device__ __forceinline__ void ev_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// A thread's weights stay in registers where its run is that short.
+// A thread's orders stay in shared memory where its run is that short.
 constexpr int kEvHeld = 16;
+constexpr int kEvHeldBytes = kEvHeld * kEvThreads * 4;
 
 template <bool kHeld>
 __global__ void __launch_bounds__(kEvThreads, 1)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
   __shared__ uint32_t s_hist[kEvBins];        // this CTA's
-  __shared__ __align__(8) uint32_t s_all[3][kEvBins];      // the cluster's, one for each pass
+  __shared__ __align__(8) uint32_t s_all[kEvBins + 3 * kEvMore];   // the cluster's, by pass
   __shared__ uint32_t s_warp[2][kEvWarps], s_before[2];
-  __shared__ uint32_t s_bin, s_above;
+  __shared__ uint32_t s_bin, s_above, s_inside;
   int cs, rank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int h = blockIdx.x / cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int b = tid; b < 3 * kEvBins; b += kEvThreads) s_all[0][b] = 0;
+  for (int b = tid; b < kEvBins + 3 * kEvMore; b += kEvThreads) s_all[b] = 0;
   if (tid < 2) s_before[tid] = 0;
   ev_cluster_sync();   // everyone's sums are zero
   grid_dep_wait();
@@ -83,34 +94,31 @@ __global__ void __launch_bounds__(kEvThreads, 1)
   }
   const float* w = p.weights + static_cast<int64_t>(h) * p.capacity;
   int32_t* kept = p.kept + static_cast<int64_t>(h) * p.keep;
-  // positions [s0, s1) compete for `need` places
+  // Pinned positions count as the largest of all: together they are at most
+  // `need`, so that a position's place depends on its order alone.
   const bool all = C <= p.keep;
-  const int s0 = all ? C : p.sinks, s1 = all ? C : C - p.recent;
-  uint32_t need = all ? 0 : static_cast<uint32_t>(p.keep - p.sinks - p.recent);
+  const int s0 = p.sinks, s1 = C - p.recent;
+  uint32_t need = all ? 0 : static_cast<uint32_t>(p.keep);
   // each CTA has a run of positions, each of its warps a run of that
   const int lo = static_cast<int>(static_cast<int64_t>(C) * rank / cs);
   const int hi = static_cast<int>(static_cast<int64_t>(C) * (rank + 1) / cs);
   const int steps = ((hi - lo + kEvWarps - 1) / kEvWarps + 31) / 32;
   const int j0 = min(hi, lo + warp * steps * 32), j1 = min(hi, j0 + steps * 32);
-  float held[kHeld ? kEvHeld : 1];
+  auto order = [&](int i) {
+    const int j = j0 + i * 32 + lane;
+    const uint32_t o = ev_order(w[min(j, C - 1)]);   // (no branch: loads in a row)
+    return j >= j1 ? kEvNone : j < s0 || j >= s1 ? kEvPinned : o;
+  };
+  extern __shared__ uint32_t s_held[];   // [step][thread]
   if constexpr (kHeld) {
-#pragma unroll
-    for (int i = 0; i < kEvHeld; ++i) {
-      const int j = j0 + i * 32 + lane;
-      held[i] = j < j1 ? w[j] : 0.0f;
-    }
+#pragma unroll 8
+    for (int i = 0; i < steps; ++i) s_held[i * kEvThreads + tid] = order(i);
   }
-  auto each = [&](auto f) {   // f(position, weight): every lane of the warp, j >= j1 too
-    if constexpr (kHeld) {
-#pragma unroll
-      for (int i = 0; i < kEvHeld; ++i)
-        if (i < steps) f(j0 + i * 32 + lane, held[i]);
-    } else {
+  auto each = [&](auto f) {   // f(step, order): every lane of the warp
 #pragma unroll 4
-      for (int i = 0; i < steps; ++i) {
-        const int j = j0 + i * 32 + lane;
-        f(j, j < j1 ? w[j] : 0.0f);
-      }
+    for (int i = 0; i < steps; ++i) {
+      if constexpr (kHeld) f(i, s_held[i * kEvThreads + tid]);
+      else f(i, order(i));
     }
   };
   // Sum over the warps before this one, and over all; s_warp[k] holds each warp's.
@@ -126,32 +134,32 @@ __global__ void __launch_bounds__(kEvThreads, 1)
     return __shfl_sync(0xFFFFFFFFu, v - mine, warp);
   };
 
-  // ---- the smallest kept weight, 11, 11 and 10 bits at a time
-  uint32_t prefix = 0xFFFFFFFFu;   // no place: nothing reaches it
+  // ---- the smallest kept order, 11, 8, 8 and 5 bits at a time
+  uint32_t prefix = 0;   // (all: every order is above it)
   if (need > 0) {
-    prefix = 0;
     int known = 0;   // leading bits of `prefix` that are found
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int bits = pass < 2 ? 11 : 10, shift = 32 - known - bits;
-      for (int b = tid; b < kEvBins; b += kEvThreads) s_hist[b] = 0;
+    for (int pass = 0; known < 32; ++pass) {
+      const int bits = pass == 0 ? 11 : pass < 3 ? 8 : 5, shift = 32 - known - bits;
+      const int bins = 1 << bits;
+      uint32_t* sums = s_all + (pass == 0 ? 0 : kEvBins + (pass - 1) * kEvMore);
+      for (int b = tid; b < bins; b += kEvThreads) s_hist[b] = 0;
       __syncthreads();
-      each([&](int j, float x) {
-        const uint32_t o = ev_order(x);
-        if (j < j1 && j >= s0 && j < s1 &&
-            (known == 0 || (o >> (32 - known)) == (prefix >> (32 - known))))
-          atomicAdd(&s_hist[(o >> shift) & ((1u << bits) - 1u)], 1u);
+      const uint32_t mask = pass == 0 ? 0 : 0xFFFFFFFFu << (32 - known);
+      each([&](int, uint32_t o) {   // (kEvNone is in a lower bin than any, or below in the same)
+        if ((o & mask) == prefix) atomicAdd(&s_hist[(o >> shift) & (bins - 1)], 1u);
       });
       __syncthreads();
-      // few bins are not empty: they are added up in every CTA
-      for (int b = tid; b < kEvBins; b += kEvThreads) {
+      // few of the first pass's bins are not empty: they are added up in every CTA
+      for (int b = tid; b < bins; b += kEvThreads) {
         const uint32_t v = s_hist[b];
         if (v)
-          for (int r = 0; r < cs; ++r) ev_remote_add(&s_all[pass][b], v, r);
+          for (int r = 0; r < cs; ++r) ev_remote_add(&sums[b], v, r);
       }
       ev_cluster_sync();
       // bins from the largest down, two a thread: where the count reaches `need`
-      const uint2 two = *reinterpret_cast<const uint2*>(&s_all[pass][kEvBins - 2 - 2 * tid]);
+      uint2 two = make_uint2(0, 0);
+      if (2 * tid < bins) two = *reinterpret_cast<const uint2*>(&sums[bins - 2 - 2 * tid]);
       const uint32_t c[2] = {two.y, two.x};
       uint32_t sum = c[0] + c[1];
 #pragma unroll
@@ -166,8 +174,9 @@ __global__ void __launch_bounds__(kEvThreads, 1)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (above < need && need <= above + c[k]) {   // one thread's
-          s_bin = kEvBins - 1 - (2 * tid + k);
+          s_bin = bins - 1 - (2 * tid + k);
           s_above = above;
+          s_inside = c[k];
         }
         above += c[k];
       }
@@ -175,24 +184,23 @@ __global__ void __launch_bounds__(kEvThreads, 1)
       need -= s_above;
       prefix |= s_bin << shift;
       known += bits;
+      if (need == s_inside && prefix > 0) {   // the whole bin stays: all above what is below it
+        prefix -= 1;
+        need = 0;
+        break;
+      }
     }
   }
-  // Now `need` of the weights that equal the smallest kept one stay.
+  // What is above `prefix` stays, and the first `need` of what equals it.
 
   // ---- the list, in position order
-  auto classify = [&](int j, float x, bool& over, bool& same) {
-    const bool in = j < j1, pinned = in && (j < s0 || j >= s1);
-    const uint32_t o = ev_order(x);
-    over = pinned || (in && need > 0 && o > prefix);
-    same = !pinned && in && need > 0 && o == prefix;
-  };
   uint32_t n_over = 0, n_same = 0;
-  each([&](int j, float x) {
-    bool over, same;
-    classify(j, x, over, same);
-    n_over += __popc(__ballot_sync(0xFFFFFFFFu, over));
-    n_same += __popc(__ballot_sync(0xFFFFFFFFu, same));
+  each([&](int, uint32_t o) {
+    n_over += o > prefix ? 1 : 0;
+    n_same += o == prefix ? 1 : 0;
   });
+  n_over = __reduce_add_sync(0xFFFFFFFFu, n_over);
+  n_same = __reduce_add_sync(0xFFFFFFFFu, n_same);
   __syncthreads();   // s_warp has been read
   if (lane == 0) {
     s_warp[0][warp] = n_over;
@@ -210,19 +218,22 @@ __global__ void __launch_bounds__(kEvThreads, 1)
   at_over += s_before[0];
   at_same += s_before[1];
   float* out = p.weights_out ? p.weights_out + static_cast<int64_t>(h) * p.dst_capacity : nullptr;
-  each([&](int j, float x) {
-    bool over, same;
-    classify(j, x, over, same);
+  each([&](int i, uint32_t o) {
+    const bool over = o > prefix, same = o == prefix;
     const unsigned bo = __ballot_sync(0xFFFFFFFFu, over), bs = __ballot_sync(0xFFFFFFFFu, same);
     const unsigned below = (1u << lane) - 1u;
-    const uint32_t eo = at_over + __popc(bo & below), es = at_same + __popc(bs & below);
+    uint32_t es = at_same;
+    if (bs) {   // hardly ever
+      es += __popc(bs & below);
+      at_same += __popc(bs);
+    }
     if (over || (same && es < need)) {
-      const uint32_t at = eo + min(es, need);
+      const uint32_t at = at_over + __popc(bo & below) + min(es, need);
+      const int j = j0 + i * 32 + lane;
       kept[at] = j;
-      if (out) out[at] = x;
+      if (out) out[at] = o == kEvPinned || o == kEvNan ? w[j] : ev_value(o);
     }
     at_over += __popc(bo);
-    at_same += __popc(bs);
   });
 }
 
@@ -366,8 +377,9 @@ __global__ void __launch_bounds__(256) read_rows_kernel(const __grid_constant__ 
 
 template <typename F, typename P>
 dfv_status launch_after(F* kernel, const P& p, dim3 grid, int threads, cudaStream_t stream,
-                        int cluster = 1) {
+                        int cluster = 1, int smem = 0) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
@@ -429,14 +441,35 @@ extern "C" dfv_status dfv_kv_evict(int n_kv_heads, int head_dim, int kv_format,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const EvictParams e = {cache_capacity, keep, sinks, recent, dst_capacity, ctx_len, dropped,
                          weights, kept, weights_out, dst_ctx_len, dst_dropped, status};
-  // a CTA for about 8192 positions of a head, eight at most
+  // A CTA for about 2048 positions of a head, eight at most; for few heads
+  // sixteen (such a cluster lies in one GPC, so only some run at a time: select
+  // and copy of one head of 131072 positions 15.2 us, by eight 18.1; of eight
+  // heads 28.5 and 20.2).
+  const int most = n_kv_heads <= 4 ? 16 : 8;
   int cs = 1;
-  while (cs < kEvMaxCluster && cache_capacity > cs * 8192) cs <<= 1;
+  while (cs < most && cache_capacity > cs * 2048) cs <<= 1;
+  static std::atomic<int> configured[64];   // per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DFV_ERR_CUDA;
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(evict_select_kernel<true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kEvHeldBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(evict_select_kernel<true>,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(evict_select_kernel<false>,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return DFV_ERR_CUDA;
+    configured[dev].store(1, std::memory_order_release);
+  }
   // (a warp's run is rounded up to whole steps of 32)
-  const bool held = cache_capacity <= cs * kEvThreads * kEvHeld;
-  dfv_status st =
-      held ? launch_after(evict_select_kernel<true>, e, dim3(n_kv_heads * cs), kEvThreads, s, cs)
-           : launch_after(evict_select_kernel<false>, e, dim3(n_kv_heads * cs), kEvThreads, s, cs);
+  const int run = (cache_capacity - 1) / cs + 1;
+  const int steps = ((run - 1) / kEvWarps + 32) / 32;
+  const dim3 grid(n_kv_heads * cs);
+  const dfv_status st =
+      steps <= kEvHeld ? launch_after(evict_select_kernel<true>, e, grid, kEvThreads, s, cs,
+                                      steps * kEvThreads * 4)
+                       : launch_after(evict_select_kernel<false>, e, grid, kEvThreads, s, cs);
   if (st != DFV_OK) return st;
   const MoveParams m = {n_kv_heads, cache_capacity, dst_capacity, keep, ctx_len, kept,
                         static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
