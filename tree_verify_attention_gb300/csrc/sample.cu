@@ -870,6 +870,12 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       b += sm.wtot[1][i];
     }
   };
+  // Sum of what the cluster's warps reported: every warp for itself.
+  auto reported = [&](const auto* x) {
+    uint64_t v = 0;
+    for (int i = lane; i < cs * kSmpWarps; i += 32) v += x[i];
+    return smp_warp_sum(v);
+  };
   // The cluster's list (at most kSmpList keys), sorted, with running weights.
   auto collect = [&]() {
     int n = 0, src = 0, off = -1;
@@ -959,10 +965,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
   auto search_gathered = [&](SmpCmd& c, bool by_mass, uint64_t target) {
     search(c, by_mass, target);
     c.gathered = 0;
-    uint64_t in_list = tid < cs * kSmpWarps ? sm.xlmass[tid] : 0, ignored = 0;
-    block_scan(in_list, ignored);
-    in_list = 0;
-    for (int i = 0; i < kSmpWarps; ++i) in_list += sm.wtot[0][i];
+    const uint64_t in_list = reported(sm.xlmass);
     // pairs of a warp's run for one that was sampled
     const int turns = per / (32 * kSmpSample), rest = per - turns * 32 * kSmpSample;
     const float each_one = static_cast<float>(per) / (turns * 32 + min(rest, 32));
@@ -1089,9 +1092,8 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
           pick(c);
           return;
         }
-        uint64_t a = tid < cs * kSmpWarps ? sm.xsum[tid] : 0, b = 0;
-        block_scan(a, b);
-        if (tid == kSmpThreads - 1) {
+        const uint64_t a = reported(sm.xsum);
+        if (tid == 0) {
           sm.mass = a;            // of all tokens
           sm.cut_key = sm.cut_index = 0;
           int n = 0;
@@ -1100,10 +1102,7 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
         }
         __syncthreads();
         const uint64_t goal = by_k ? static_cast<uint64_t>(sm.top_k) : share(sm.mass);
-        uint64_t l = tid < cs * kSmpWarps ? sm.xlmass[tid] : 0, ignored = 0;
-        block_scan(l, ignored);
-        l = 0;
-        for (int i = 0; i < kSmpWarps; ++i) l += sm.wtot[0][i];
+        const uint64_t l = by_groups ? 0 : reported(sm.xlmass);
         // (a list of too few tokens, or too little weight, need not be sorted)
         if ((by_groups || (by_k ? sm.list_all >= sm.top_k : l >= goal)) && from_list())
           c.op = kOpDone;
@@ -1116,10 +1115,8 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
       case kAfterHist:
         if (c.gathered) {
           // what lies above the window comes first
-          uint64_t a = tid < cs * kSmpWarps ? sm.xcnt[tid] : 0;
-          uint64_t b = tid < cs * kSmpWarps ? sm.xsum[tid] : 0;
-          block_scan(a, b);
-          if (tid == kSmpThreads - 1) {
+          const uint64_t a = reported(sm.xcnt), b = reported(sm.xsum);
+          if (tid == 0) {
             sm.acc_cnt = c.under_list ? sm.list_all : a;
             sm.acc_mass = b;
           }
