@@ -22,10 +22,15 @@
 // 22.8 us, by hi and lo 34).
 //
 // A CTA works through a run of 128-key chunks of (at most a few) heads, in parts
-// of 64 dims. Q4_0: one warp copies raw rows into a ring, two groups of four
+// of up to 256 dims. Q4_0: one warp copies raw rows into a ring, two groups of four
 // convert parts in turn into TMEM, the product's A operand. F16: the two groups
 // copy parts straight into swizzled tiles, A from shared memory. One warp
 // issues the products; two groups of four warps take turns at the chunks' sums.
+//
+// Bound by issue: hand-offs and conversion for few rows (one row over 131060
+// Q4_0 keys, 4 heads of 256: 22.5 us, 3.4 TB/s; nine rows over 61440
+// 17.4), the sums for many (65 nodes, 32 / 8 heads of 128, 32791 F16
+// keys: 37 us, 24 % of the products' rate).
 
 #include <atomic>
 
@@ -39,29 +44,34 @@ constexpr int kWtKeys = 128;
 constexpr int kWtMma = 16, kWtRaw = 17;      // warps 0-7: sums, 8-15: operands
 constexpr int kWtThreads = 18 * 32;
 
-enum WeightMode { kModeF16, kModeSplit, kModeBlocks };   // Q4_0: hi and lo, or block by block
+// F16 (rows by slices or not); Q4_0: hi and lo, or block by block
+enum WeightMode { kModeF16, kModeSliced, kModeSplit, kModeBlocks };
 
 template <int D, int kMode>
 struct WeightShape {
-  static constexpr bool kQ4 = kMode != kModeF16, kBlocks = kMode == kModeBlocks;
-  // query rows of a tile, at most
-  static constexpr int kRows = kBlocks ? 16 : kQ4 || D == 256 ? 128 : 256;
+  static constexpr bool kQ4 = kMode == kModeSplit || kMode == kModeBlocks;
+  static constexpr bool kBlocks = kMode == kModeBlocks, kSliced = kMode == kModeSliced;
+  // Query rows of a tile, at most. Sliced: in up to three slices of 128 columns
+  // of scores, so that K is read once for as many rows as fit shared memory (260
+  // rows of a head, 61440 F16 keys: 73 us, in two tiles 78).
+  static constexpr int kRows = kBlocks ? 16 : kQ4 || D == 256 ? 128 : kSliced ? 288 : 256;
   static constexpr int kRowBytes = kQ4 ? D / 32 * 18 : D * 2;
-  // Parts of a chunk: 64 dims, with Q4_0 as many times 64 as leave TMEM room for
-  // two parts (handing a part over costs as much as converting 64 dims: one row
-  // over 131060 keys 22.8 us, by 128 dims 25.9, by 64 30.7).
-  static constexpr int kHalves = kBlocks ? D / 64 : kQ4 && D >= 128 ? 2 : 1;
+  // Parts of a chunk: with Q4_0 as many times 64 dims as leave TMEM room for two
+  // parts, F16 128 dims (handing a part over costs as much as converting 64 dims:
+  // one row over 131060 keys 22.8 us, by 128 dims 25.9, by 64 30.7).
+  static constexpr int kHalves = kBlocks ? D / 64 : D >= 128 ? 2 : 1;
   static constexpr int kParts = D / 64 / kHalves;
   static constexpr int kHalfCols = kBlocks ? 32 : 64;         // Q4_0: TMEM columns
   static constexpr int kPartCols = kHalves * kHalfCols;
-  static constexpr int kPartBytes = kWtKeys * 128;            // F16: a tile of 64 dims
-  static constexpr int kRing = kBlocks ? 2 * kParts : kQ4 ? 256 / kPartCols : 8;   // parts
+  static constexpr int kPartBytes = kHalves * kWtKeys * 128;  // F16: tiles of 64 dims
+  static constexpr int kRing = kBlocks ? 2 * kParts : kQ4 ? 256 / kPartCols : 8 / kHalves;
   static constexpr int kStages = 4;                           // Q4_0: raw chunks
   static constexpr int kStage = (kWtKeys * kRowBytes + 16 + 127) / 128 * 128;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kBytes = kQBytes + (kQ4 ? kStages * kStage : kRing * kPartBytes) + 1024;
-  static constexpr uint32_t kTS = kQ4 ? 256 : 0;              // two buffers of scores
-  static constexpr int kSCols = kBlocks ? D / 32 * kRows : kRows;
+  // Scores: two buffers; sliced as many slices as fit, at most eight
+  static constexpr uint32_t kTS = kQ4 ? 256 : 0;
+  static constexpr int kSCols = kBlocks ? D / 32 * kRows : kSliced ? 128 : kRows;
   static_assert(kTS + 2 * kSCols <= 512, "TMEM columns");
   static_assert(kBytes <= 220 * 1024, "shared memory");
 };
@@ -92,14 +102,14 @@ template <int D, int kMode>
 __global__ void __launch_bounds__(kWtThreads, 1)
     kv_weights_kernel(const __grid_constant__ WeightParams p) {
   using W = WeightShape<D, kMode>;
-  constexpr bool kQ4 = W::kQ4, kBlocks = W::kBlocks;
+  constexpr bool kQ4 = W::kQ4, kBlocks = W::kBlocks, kSliced = W::kSliced;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
   uint8_t* sK = smem + W::kQBytes;                    // raw rows, or tiles
   __shared__ uint64_t b_raw[4], b_read[4];            // raw rows landed, read
   __shared__ uint64_t b_part[8], b_free[8];           // operand part written, multiplied
-  __shared__ uint64_t b_s[2], b_sfree[2];             // scores there, read
+  __shared__ uint64_t b_s[8], b_sfree[8];             // scores there, read
   __shared__ uint64_t b_q, b_qfree, b_end;            // query rows there, multiplied
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_dead;
@@ -124,7 +134,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       mbar_init(&b_part[i], 4);
       mbar_init(&b_free[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 8; ++i) {
       mbar_init(&b_s[i], kBlocks ? 2 : 1);
       mbar_init(&b_sfree[i], 4);
     }
@@ -152,8 +162,19 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   }
   const int rows = n * p.group;                       // query rows of a KV head
   const int tiles = (rows + W::kRows - 1) / W::kRows;
-  // columns of a tile, balanced, in steps of 16
-  const int R = tiles == 0 ? 16 : ((rows + tiles - 1) / tiles + 15) / 16 * 16;
+  // slices of a tile, and their columns, balanced, in steps of 16
+  const int tile_rows = tiles == 0 ? 1 : (rows + tiles - 1) / tiles;
+  const int slices = kSliced ? (tile_rows + 127) / 128 : 1;
+  const int RS = ((tile_rows + slices - 1) / slices + 15) / 16 * 16, R = slices * RS;
+  // places of slices of scores, taken in turn: slice number i has place i % places
+  const uint32_t places = kSliced ? min(8, 512 / RS) : 2;
+  const uint32_t place_cols = kSliced ? RS : W::kSCols;
+  // place and turn (how often it was taken) of a chunk's first slice, from
+  // those of a chunk before, and of the next slice
+  auto skip = [&](uint32_t& place, uint32_t& turn, int by) {
+    place += by;
+    while (place >= places) place -= places, ++turn;
+  };
   // positions: row s stands at C - n + s; chunks [fc, lc) are seen by some row
   const int at0 = C - n;
   const int lc = tiles == 0 ? 0 : (C + kWtKeys - 1) / kWtKeys;
@@ -218,7 +239,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     // ------------------------------------------------------ products
     bool ok = true;
     int k = 0, part = 0, run = 0;
-    const uint32_t idesc = tc::idesc_f16(128, 0) | (static_cast<uint32_t>(R >> 3) << 17);
+    uint32_t place0 = 0, turn0 = 0;   // of the chunk's first slice
+    const uint32_t idesc = tc::idesc_f16(128, 0) | (static_cast<uint32_t>(RS >> 3) << 17);
     const uint64_t qd = tc::smem_desc_sw128(smem_u32(sQ), 1024);
     const uint64_t q_block = static_cast<uint64_t>(R * 128) >> 4;   // 64 dims of all rows
     auto all_wait = [&](uint64_t* bar, uint32_t parity) {
@@ -229,46 +251,57 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     runs([&](int, int c0, int c1, int) {
       ok = all_wait(&b_q, run & 1);
       for (int c = c0; ok && c < c1; ++c, ++k) {
-        const int buf = k & 1;
-        if (k >= 2) ok = all_wait(&b_sfree[buf], ((k >> 1) - 1) & 1);
+        if constexpr (!kSliced) place0 = k & 1, turn0 = k >> 1;
         for (int i = 0; ok && i < W::kParts; ++i, ++part) {
           const int slot = part % W::kRing;
-          ok = all_wait(&b_part[slot], (part / W::kRing) & 1);
-          if (!ok) break;
-          if (tc::elect_one()) {
-            const uint32_t d = tmem + W::kTS + buf * W::kSCols;
-            if constexpr (kQ4) {
+          uint32_t place = place0, turn = turn0;
+          // (a chunk's slices are at most as many as the places)
+          for (int sl = 0; ok && sl < slices; ++sl) {
+            if (i == 0 && turn > 0) ok = all_wait(&b_sfree[place], (turn - 1) & 1);
+            if (ok && sl == 0) ok = all_wait(&b_part[slot], (part / W::kRing) & 1);
+            if (!ok) break;
+            if (tc::elect_one()) {
+              const uint32_t d = tmem + W::kTS + place * place_cols;
+              if constexpr (kQ4) {
 #pragma unroll
-              for (int hh = 0; hh < W::kHalves; ++hh) {
-                const int g = i * W::kHalves + hh;   // which 64 dims
-                const uint32_t a = tmem + slot * W::kPartCols + hh * W::kHalfCols;
-                if constexpr (kBlocks) {
+                for (int hh = 0; hh < W::kHalves; ++hh) {
+                  const int g = i * W::kHalves + hh;   // which 64 dims
+                  const uint32_t a = tmem + slot * W::kPartCols + hh * W::kHalfCols;
+                  if constexpr (kBlocks) {
 #pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)   // two steps a block
-                    tc::mma_f16_ts(d + (2 * g + (kk >> 1)) * W::kRows, a + kk * 8,
-                                   qd + g * q_block + kk * 2, idesc, kk & 1);
-                } else {
+                    for (int kk = 0; kk < 4; ++kk)   // two steps a block
+                      tc::mma_f16_ts(d + (2 * g + (kk >> 1)) * W::kRows, a + kk * 8,
+                                     qd + g * q_block + kk * 2, idesc, kk & 1);
+                  } else {
 #pragma unroll
-                  for (int kk = 0; kk < 8; ++kk)   // hi, then lo
-                    tc::mma_f16_ts(d, a + kk * 8, qd + g * q_block + (kk & 3) * 2, idesc,
-                                   g > 0 || kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < 8; ++kk)   // hi, then lo
+                      tc::mma_f16_ts(d, a + kk * 8, qd + g * q_block + (kk & 3) * 2, idesc,
+                                     g > 0 || kk > 0 ? 1u : 0u);
+                  }
+                }
+              } else {
+                const uint64_t a0 =
+                    tc::smem_desc_sw128(smem_u32(sK + slot * W::kPartBytes), 1024);
+#pragma unroll
+                for (int hh = 0; hh < W::kHalves; ++hh) {
+                  const int g = i * W::kHalves + hh;   // which 64 dims
+                  const uint64_t a = a0 + hh * (kWtKeys * 128 >> 4);
+                  const uint64_t q = qd + g * q_block + sl * RS * 8;
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    tc::mma_f16(d, a + kk * 2, q + kk * 2, idesc, g > 0 || kk > 0 ? 1u : 0u);
                 }
               }
-            } else {
-              const uint64_t a =
-                  tc::smem_desc_sw128(smem_u32(sK + slot * W::kPartBytes), 1024);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc::mma_f16(d, a + kk * 2, qd + i * q_block + kk * 2, idesc,
-                            i > 0 || kk > 0 ? 1u : 0u);
+              if (sl == slices - 1) tc::commit(&b_free[slot]);
+              if (i == W::kParts - 1) tc::commit(&b_s[place]);
+              // (an arrival of its own: a commit orders the products, not the scales)
+              if (kBlocks && i == W::kParts - 1) mbar_arrive(&b_s[place]);
             }
-            tc::commit(&b_free[slot]);
-            if (i == W::kParts - 1) tc::commit(&b_s[buf]);
-            // (an arrival of its own: a commit orders the products, not the scales)
-            if (kBlocks && i == W::kParts - 1) mbar_arrive(&b_s[buf]);
+            __syncwarp();
+            if constexpr (kSliced) skip(place, turn, 1);
           }
-          __syncwarp();
         }
+        if constexpr (kSliced) skip(place0, turn0, slices);
       }
       if (!ok) return false;
       if (tc::elect_one()) tc::commit(&b_qfree);
@@ -413,11 +446,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (!ok) break;
             uint8_t* dst = sK + (part % W::kRing) * W::kPartBytes;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = (t >> 3) + e * 16, j = t & 7;
+            for (int e = 0; e < 8 * W::kHalves; ++e) {
+              const int r = (t >> 3) + e % 8 * 16, j = (t & 7) + e / 8 * 8;
               if (r < live)
                 cp_async16(dst + tc::sw128_offset(r, j, kWtKeys),
-                           src + static_cast<int64_t>(r) * W::kRowBytes + i * 128 + j * 16);
+                           src + static_cast<int64_t>(r) * W::kRowBytes +
+                               i * (W::kHalves * 128) + j * 16);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             ++issued;
@@ -437,6 +471,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const int grp = warp >> 2;
     bool ok = true;
     int k = 0, run = 0;
+    uint32_t place = 0, turn = 0;
+    skip(place, turn, grp * slices);
     runs([&](int h, int c0, int c1, int t) {
       const int r0 = t * R, live = min(R, rows - r0), tb = run & 1;
       // Query rows: D / 8 lanes each, kBatch of a lane's rows loaded together.
@@ -444,6 +480,25 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       constexpr int kLanes = D / 8, kPerStep = 8 * 32 / kLanes, kBatch = 4;
       const int piece = lane % kLanes;
       uint32_t problems = 0;
+      // The tile's power of two, 2^4 above its first row's: rows within 2^-8 to 1
+      // of it have that one (their elements are exact down to 2^-24 of the row's
+      // largest), and where all have, the exponent's slope stays in a register
+      // (65 rows, 32 / 8 heads of 128 over 61440 F16 keys: 77 us, slopes read for
+      // every column 82).
+      int e_tile = 40;
+      bool own = false;   // some row has another one
+      if (!kBlocks) {
+        const int step = r0 / p.group, g = r0 - step * p.group;
+        const int node = p.path ? p.path[step] : step;
+        if (node >= 0 && node < p.n_rows) {
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              p.q + (static_cast<int64_t>(node) * p.hq + h * p.group + g) * D + piece * 8);
+          uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+          m = max(m & 0xFFFFu, m >> 16);
+          e_tile = max(min(static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, m) >> 7) + 4, 254), 40);
+        }
+      }
       for (int rb = 0; rb < R; rb += kBatch * kPerStep) {
         uint2 a[kBatch], b[kBatch];
         float l[kBatch];
@@ -501,9 +556,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           const float off = fine ? -l[i] * 1.44269504f : -INFINITY;
           const int last = fine ? at0 + s[i] : -1;
           const int first = p.window > 0 ? last - p.window + 1 : 0;
-          const int e = max(fine ? static_cast<int>(m >> 7) : 0, 40);   // all below 2^(e - 126)
+          int e = max(fine ? static_cast<int>(m >> 7) : 0, 40);   // all below 2^(e - 126)
+          if (!kBlocks) {
+            if (!fine || (e <= e_tile && e >= e_tile - 8)) e = e_tile;
+            else own = true;
+          }
           const float f = pow2i(141 - e);                               // to below 2^15
-          const float slope = fine ? p.scale * 1.44269504f * pow2i(e - 141) : 0.0f;
+          const float slope = p.scale * 1.44269504f * pow2i(e - 141);
           if (r < R) {
             auto half2_of = [](uint32_t lo16, uint32_t hi16, float f) {
               return pack_half2(__uint_as_float(lo16 << 16) * f, __uint_as_float(hi16 << 16) * f);
@@ -538,6 +597,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       // run, whatever their waits gave, and end together.
       ok = named_sync_and(1, 256, ok);
       if (!ok) return false;
+      const bool same = kBlocks || named_sync_and(1, 256, !own);
+      const float slope_all = p.scale * 1.44269504f * pow2i(e_tile - 141);
       const float* slope = s_slope[tb];
       const float* off = s_off[tb];
       for (int c = c0; ok && c < c1; ++c, ++k) {
@@ -550,16 +611,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           else if (p.prev && j < at0)
             had = p.decay * p.prev[static_cast<int64_t>(h) * p.capacity + j];
         }
-        ok = __all_sync(0xFFFFFFFFu, role_wait(&b_s[grp], (k >> 1) & 1, &s_dead));
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t ts = tmem + lanes + W::kTS + grp * W::kSCols;
         // every row sees the whole chunk: up to row 0's own place, from the last row's window on
         const bool whole = (c + 1) * kWtKeys <= at0 + 1 &&
                            (p.window == 0 || c * kWtKeys >= C - p.window);
         float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-        auto add = [&](auto columns, int r) {
+        uint32_t ts = 0;   // column 0 of the tile, were the slice's neighbours beside it
+        auto add = [&](auto columns, auto plain, int r) {
           constexpr int kN = decltype(columns)::value;
+          constexpr bool kPlain = decltype(plain)::value != 0;
           uint32_t x[kN];
           if constexpr (kBlocks) {
             // the blocks' sums times this key's scales, two blocks at a time
@@ -585,13 +644,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < kN; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(slope + r + i);
+            const float4 f = kPlain && !kBlocks
+                                 ? make_float4(slope_all, slope_all, slope_all, slope_all)
+                                 : *reinterpret_cast<const float4*>(slope + r + i);
             const float4 o = *reinterpret_cast<const float4*>(off + r + i);
             float y0, y1, y2, y3;
             fma2(y0, y1, __uint_as_float(x[i]), __uint_as_float(x[i + 1]), f.x, f.y, o.x, o.y);
             fma2(y2, y3, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]), f.z, f.w, o.z, o.w);
             y0 = tc::ex2(y0), y1 = tc::ex2(y1), y2 = tc::ex2(y2), y3 = tc::ex2(y3);
-            if (!whole) {
+            if constexpr (!kPlain) {
               const int4 a = *reinterpret_cast<const int4*>(s_first[tb] + r + i);
               const int4 b = *reinterpret_cast<const int4*>(s_last[tb] + r + i);
               y0 = j >= a.x && j <= b.x ? y0 : 0.0f;
@@ -603,13 +664,29 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             add2(s2, s3, s2, s3, y2, y3);
           }
         };
-        int r = 0;
-        if constexpr (!kBlocks)
-          for (; r + 32 <= R; r += 32) add(Columns<32>(), r);
-        if (r < R) add(Columns<16>(), r);
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_sfree[grp]);
+        for (int sl = 0; ok && sl < slices; ++sl) {
+          ok = __all_sync(0xFFFFFFFFu, role_wait(&b_s[place], turn & 1, &s_dead));
+          if (!ok) break;
+          tc::fence_after_sync();
+          ts = tmem + lanes + W::kTS + place * place_cols - sl * RS;
+          auto add_all = [&](auto plain) {
+            int r = sl * RS;
+            const int end = r + RS;
+            if constexpr (!kBlocks)
+              for (; r + 32 <= end; r += 32) add(Columns<32>(), plain, r);
+            if (r < end) add(Columns<16>(), plain, r);
+          };
+          // (the same rows: 57 us, with the test of `whole` within the loop 73)
+          if (whole && same) add_all(Columns<1>());
+          else add_all(Columns<0>());
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b_sfree[place]);
+          if constexpr (kSliced) skip(place, turn, 1);
+        }
+        if constexpr (kSliced) skip(place, turn, slices);   // the other group's
+        else ++turn;
+        if (!ok) break;
         if (j < C) *dst = had + ((s0 + s1) + (s2 + s3));
       }
       ++run;
@@ -668,10 +745,13 @@ dfv_status weights_launch(const WeightParams& p, cudaStream_t stream) {
 
 template <int D>
 dfv_status weights_launch_f(const WeightParams& p, bool q4, cudaStream_t stream) {
-  if (!q4) return weights_launch<D, kModeF16>(p, stream);
-  return static_cast<int64_t>(p.n_rows) * p.group <= WeightShape<D, kModeBlocks>::kRows
-             ? weights_launch<D, kModeBlocks>(p, stream)
-             : weights_launch<D, kModeSplit>(p, stream);
+  const int64_t rows = static_cast<int64_t>(p.n_rows) * p.group;
+  if (q4)
+    return rows <= WeightShape<D, kModeBlocks>::kRows ? weights_launch<D, kModeBlocks>(p, stream)
+                                                      : weights_launch<D, kModeSplit>(p, stream);
+  if constexpr (D < 256)
+    if (rows > WeightShape<D, kModeF16>::kRows) return weights_launch<D, kModeSliced>(p, stream);
+  return weights_launch<D, kModeF16>(p, stream);
 }
 
 }  // namespace dfv
