@@ -535,7 +535,8 @@ dfv_status dfv_token_logprobs(int n_rows, int vocab, int logits_dtype, const voi
  *   q_out, k_out, v_out  device f32 or bf16 (dst_dtype), [n_rows][heads][D],
  *              16-byte aligned; each may be its source itself if that has the
  *              same type and layout, and overlaps nothing else
- * One launch, no workspace.
+ * One launch, no workspace. (Its outputs are no inputs for a DFV_STEP_PIPELINED
+ * call right behind it: see the flag.)
  * ---------------------------------------------------------------------- */
 dfv_status dfv_qk_norm_rope(int n_rows, int n_q_heads, int n_kv_heads, int head_dim,
                             const void* q, const void* k, const void* v, int src_dtype,
@@ -640,8 +641,9 @@ dfv_status dfv_sample_accept(int n_nodes, int vocab, int logits_dtype, const voi
  *                `weights` itself
  *   weights      device f32 [Hkv][cache_capacity]; entries from C on are left
  *                as they were
- * Products are exact, sums f32 in a fixed order: a weight is off by about 2^-19
- * of itself at |lse| of 30. Cached K values must stay within the binary16 range.
+ * Products are exact for elements down to 2^-24 of a query row's largest, sums
+ * f32 in a fixed order: a weight is off by about 2^-19 of itself at |lse| of 30.
+ * Cached K values must stay within the binary16 range.
  * One launch, no workspace.
  * ---------------------------------------------------------------------- */
 dfv_status dfv_kv_weights(int n_rows, int n_q_heads, int n_kv_heads, int head_dim, int window,
