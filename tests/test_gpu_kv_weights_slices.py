@@ -78,3 +78,11 @@ def test_a_first_row_without_a_magnitude(fmt, row):
     got = out.double().cpu().numpy()
     assert int(st) == (0 if row == 0 else api.DEV_NONFINITE)
     assert np.all(np.abs(got - ref) <= tol), np.max(np.abs(got - ref) / tol)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q4_0"])
+@pytest.mark.parametrize("window", [1, 4, 299, 300, 301, (1 << 31) - 1])
+def test_windows_about_the_capacity(fmt, window):
+    """Also with more rows than keys, whose first ones stand before position 0."""
+    for C, n in ((5, 12), (300, 7)):
+        check(8 + C, 2, 4, 64, C, fmt, n, cap=300, window=window)

@@ -776,6 +776,7 @@ extern "C" dfv_status dfv_kv_weights(int n_rows, int n_q_heads, int n_kv_heads, 
       !aligned(ctx_len, 4) || !aligned(path, 4) || !aligned(accept_len, 4))
     return DFV_ERR_INVALID;
   if (scale <= 0.0f) scale = head_dim == 64 ? 0.125f : head_dim == 256 ? 0.0625f : 0.08838834765f;
+  if (window >= cache_capacity) window = 0;   // (hides nothing; and no difference overflows)
   const uint32_t group = static_cast<uint32_t>(n_q_heads / n_kv_heads);
   // (exact while rows * group stays below 2^32)
   const uint32_t group_m =
