@@ -427,3 +427,36 @@ def test_refusals():
         api.VerifyStep(4, 4, 2, 64, 0, 100, 100, sampling=1.0)
     assert torch.all(t == -7)
     api.sample_tokens(x[:0], u[:0], s, t[:0])
+
+
+def test_steps_over_bit_patterns():
+    """bf16 logits given as int16, as the greedy step takes them; and rows that
+    have no distribution, whose scores are NaN."""
+    n, hq, hkv, d, v, cap = 5, 4, 2, 64, 600, 50
+    q, tk = torch.zeros(n, hq, d, dtype=torch.bfloat16, device=DEV), torch.zeros(
+        n, hkv, d, dtype=torch.bfloat16, device=DEV)
+    x, u = make(3, n, v, torch.bfloat16)
+    x[2, 5] = math.nan
+    parent = torch.tensor([-1, 0, 1, 2, 3], dtype=torch.int32, device=DEV)
+    tokens = torch.zeros(n, dtype=torch.int32, device=DEV)
+    got = []
+    for y in (x, x.view(torch.int16)):
+        step = api.VerifyStep(n, hq, hkv, d, 0, cap, v, sampling=api.Sampling(top_p=0.9), top=2)
+        step.run(api.KVCache(hkv, d, cap), q, tk, tk, parent, tokens, y, uniform=u)
+        got.append([step.argmax, step.path, step.accept_len, step.status])
+        assert int(step.argmax[2]) == -1 and torch.isnan(step.draw_logprob[2])
+        assert int(step.status) & api.DEV_NONFINITE
+        good = torch.tensor([0, 1, 3, 4], device=DEV)
+        assert torch.all(step.argmax[good] >= 0) and torch.all(torch.isfinite(step.logprob[good]))
+        assert torch.isnan(step.logprob[2])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("t", [1e-30, 1e-6, 1e6, 3e38])
+def test_extreme_temperatures(t):
+    """All the mass on the maximum, or on all alike."""
+    x, u = make(9, 6, 5000, torch.float32)
+    tok, _ = check(x, u, temperature=t, few=0)
+    check(x * 1e30, u, temperature=t, few=0)
+    if t < 1:
+        assert np.array_equal(tok, x.argmax(1).cpu().numpy())
