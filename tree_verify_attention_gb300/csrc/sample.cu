@@ -47,7 +47,7 @@
 // work on weights (about 30 cycles of a scheduler for 32 lanes, in passes 2 and 3)
 // and, for few rows, by the chain of decisions in the first CTA. 1024 rows of
 // 151936 bf16 logits: greedy 115 us, no cut 297, top-k 50 223, top-p 0.9 at 0.7
-// 321, top-p 0.95 787; 23 rows 7, 19, 14, 20, 45; one f32 row 6, 14, 14, 16, 34.
+// 303, top-p 0.95 779; 23 rows 7, 19, 14, 20, 45; one f32 row 6, 14, 14, 15, 34.
 
 #include <atomic>
 #include <climits>
@@ -97,6 +97,10 @@ __constant__ uint64_t kSmpExp2[32] = {
     0xC5672A115506DADDull, 0xC9B9BD866E2F27A3ull, 0xCE248C151F8480E4ull, 0xD2A81D91F12AE45Aull,
     0xD744FCCAD69D6AF4ull, 0xDBFBB797DAF23755ull, 0xE0CCDEEC2A94E111ull, 0xE5B906E77C8348A8ull,
     0xEAC0C6E7DD24392Full, 0xEFE4B99BDCDAF5CBull, 0xF5257D152486CC2Cull, 0xFA83B2DB722A033Aull,
+};
+
+template <bool kOn> struct SmpFlag {
+  static constexpr bool value = kOn;
 };
 
 enum SmpState {
@@ -517,8 +521,9 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     split(smp_both(m), k, g);
     top = 20 + (__float_as_int(k.x) >> 5);
   }
-  // Weights of two values, zero where `on` is not set.
-  auto weight2 = [&](float2 v, bool on0, bool on1, uint64_t& w0, uint64_t& w1) {
+  // Weights of two values, zero where `on` is not set; the largest tokens' are
+  // put right if `heavies` says so.
+  auto weights_of = [&](float2 v, bool on0, bool on1, uint64_t& w0, uint64_t& w1, auto heavies) {
     float2 k, g;
     const float2 f = split(v, k, g), r = smp_add2(f, g);
     // 2^31 (2^r - 1), |r| <= 2^-6: ln2^i / i!; the next term is below 2^-39
@@ -539,10 +544,13 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
         : "=l"(w0) : "r"(f0), "r"(s0));
     asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {0, %1};\n\tshr.u64 %0, a, %2;\n\t}"
         : "=l"(w1) : "r"(f1), "r"(s1));
-    if (fmaxf(v.x, v.y) >= heavy) {
+    if (decltype(heavies)::value && fmaxf(v.x, v.y) >= heavy) {
       if (on0 && v.x >= heavy) w0 = smp_heavy_weight(f.x, g.x, k0, s0);
       if (on1 && v.y >= heavy) w1 = smp_heavy_weight(f.y, g.y, k1, s1);
     }
+  };
+  auto weight2 = [&](float2 v, bool on0, bool on1, uint64_t& w0, uint64_t& w1) {
+    weights_of(v, on0, on1, w0, w1, SmpFlag<true>());
   };
   auto weight = [&](float v) {
     uint64_t w0, w1;
@@ -613,25 +621,35 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     uint64_t s = 0;
     const bool filter = by_k || by_p;
     const float from = filter ? tau_w : tau_0;
-    int turn = 0;
-#pragma unroll 2
-    for (int u = u0 + lane; u < u1; u += 32, ++turn) {
-      const float2 x = SmpVec<T>::pair(xs, u);
-      uint64_t w0, w1;
+    // the largest and the listed tokens are few: one test for two pairs
+    const float rare = filter ? fminf(heavy, tau_l) : heavy;
+    auto fix = [&](float2 x, int u, uint64_t& w0, uint64_t& w1) {
+      if (!(fmaxf(x.x, x.y) >= rare)) return;
       weight2(x, x.x >= from, x.y >= from, w0, w1);
-      s += w0 + w1;
-      if (!filter) continue;
-      if (fmaxf(x.x, x.y) >= tau_l) {
-        if (x.x >= tau_l) {
-          push(x.x, first + 2 * u);
-          listed += w0;
-        }
-        if (x.y >= tau_l) {
-          push(x.y, first + 2 * u + 1);
-          listed += w1;
-        }
+      if (filter && x.x >= tau_l) {
+        push(x.x, first + 2 * u);
+        listed += w0;
       }
-      if (turn % kSmpSample == 0) {
+      if (filter && x.y >= tau_l) {
+        push(x.y, first + 2 * u + 1);
+        listed += w1;
+      }
+    };
+    int turn = 0;
+#pragma unroll 1
+    for (int u = u0 + lane; u < u1; u += 64, turn += 2) {
+      const bool two = u + 32 < u1;
+      const float2 x = SmpVec<T>::pair(xs, u);
+      const float2 y = two ? SmpVec<T>::pair(xs, u + 32) : smp_both(-INFINITY);
+      uint64_t w0, w1, w2, w3;
+      weights_of(x, x.x >= from, x.y >= from, w0, w1, SmpFlag<false>());
+      weights_of(y, y.x >= from, y.y >= from, w2, w3, SmpFlag<false>());
+      if (fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)) >= rare) {
+        fix(x, u, w0, w1);
+        fix(y, u + 32, w2, w3);
+      }
+      s += (w0 + w1) + (w2 + w3);
+      if (filter && turn % kSmpSample == 0) {
         if (x.x >= tau_w) atomicAdd(&sm.sampled[logit_bin(x.x)], 1u);
         if (x.y >= tau_w) atomicAdd(&sm.sampled[logit_bin(x.y)], 1u);
       }
