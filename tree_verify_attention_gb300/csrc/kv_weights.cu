@@ -30,7 +30,7 @@
 // Bound by issue: hand-offs and conversion for few rows (one row over 131060
 // Q4_0 keys, 4 heads of 256: 22.5 us, 3.4 TB/s; nine rows over 61440
 // 17.4), the sums for many (65 nodes, 32 / 8 heads of 128, 32791 F16
-// keys: 37 us, 24 % of the products' rate).
+// keys: 37 us, 24 % of the products' rate; 6 of them build the query rows).
 
 #include <atomic>
 
@@ -51,9 +51,10 @@ template <int D, int kMode>
 struct WeightShape {
   static constexpr bool kQ4 = kMode == kModeSplit || kMode == kModeBlocks;
   static constexpr bool kBlocks = kMode == kModeBlocks, kSliced = kMode == kModeSliced;
-  // Query rows of a tile, at most. Sliced: in up to three slices of 128 columns
-  // of scores, so that K is read once for as many rows as fit shared memory (260
-  // rows of a head, 61440 F16 keys: 73 us, in two tiles 78).
+  // Query rows of a tile, at most. Sliced: in two slices of scores, three of
+  // which are in TMEM, so that K is read once for as many rows as fit shared memory
+  // (260 rows of a head, 61440 F16 keys: 54 us, in three slices 57; before the
+  // sums were faster, 73 for 78 in two tiles).
   static constexpr int kRows = kBlocks ? 16 : kQ4 || D == 256 ? 128 : kSliced ? 288 : 256;
   static constexpr int kRowBytes = kQ4 ? D / 32 * 18 : D * 2;
   // Parts of a chunk: with Q4_0 as many times 64 dims as leave TMEM room for two
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   const int tiles = (rows + W::kRows - 1) / W::kRows;
   // slices of a tile, and their columns, balanced, in steps of 16
   const int tile_rows = tiles == 0 ? 1 : (rows + tiles - 1) / tiles;
-  const int slices = kSliced ? (tile_rows + 127) / 128 : 1;
+  const int slices = kSliced ? (tile_rows + 255) / 256 : 1;
   const int RS = ((tile_rows + slices - 1) / slices + 15) / 16 * 16, R = slices * RS;
   // places of slices of scores, taken in turn: slice number i has place i % places
   const uint32_t places = kSliced ? min(8, 512 / RS) : 2;
@@ -506,33 +507,28 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         bool bad[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
+          // (no branches: a batch's loads are in flight together)
           const int r = rb + i * kPerStep + warp * (32 / kLanes) + lane / kLanes;
-          a[i] = b[i] = make_uint2(0, 0);
-          l[i] = INFINITY;
-          s[i] = -1;
-          bad[i] = false;
-          if (r < live) {
-            const int step = p.group_m ? static_cast<int>(__umulhi(r0 + r, p.group_m))
-                                       : (r0 + r) / p.group;
-            const int g = (r0 + r) - step * p.group;
-            const int node = p.path ? p.path[step] : step;
-            bad[i] = node < 0 || node >= p.n_rows;
-            if (!bad[i]) {
-              const int64_t row = static_cast<int64_t>(node) * p.hq + h * p.group + g;
-              const __nv_bfloat16* src = p.q + row * D;
-              if (kQ4) {   // the places of a code word's dims
-                const __nv_bfloat16* w = src + (piece >> 2) * 32 + (piece & 3) * 4;
-                a[i] = *reinterpret_cast<const uint2*>(w);
-                b[i] = *reinterpret_cast<const uint2*>(w + 16);
-              } else {
-                const uint4 v = *reinterpret_cast<const uint4*>(src + piece * 8);
-                a[i] = make_uint2(v.x, v.y);
-                b[i] = make_uint2(v.z, v.w);
-              }
-              l[i] = p.lse[row];
-              s[i] = step;
-            }
+          const uint32_t at = r0 + min(r, live - 1);
+          const int step = p.group_m ? static_cast<int>(__umulhi(at, p.group_m))
+                                     : static_cast<int>(at) / p.group;
+          const int g = static_cast<int>(at) - step * p.group;
+          const int node = p.path ? p.path[step] : step;
+          const bool there = node >= 0 && node < p.n_rows;
+          bad[i] = r < live && !there;
+          s[i] = r < live && there ? step : -1;
+          const int64_t row = static_cast<int64_t>(there ? node : 0) * p.hq + h * p.group + g;
+          const __nv_bfloat16* src = p.q + row * D;
+          if (kQ4) {   // the places of a code word's dims
+            const __nv_bfloat16* w = src + (piece >> 2) * 32 + (piece & 3) * 4;
+            a[i] = *reinterpret_cast<const uint2*>(w);
+            b[i] = *reinterpret_cast<const uint2*>(w + 16);
+          } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + piece * 8);
+            a[i] = make_uint2(v.x, v.y);
+            b[i] = make_uint2(v.z, v.w);
           }
+          l[i] = p.lse[row];
         }
         // the last run's products have read theirs
         if (rb == 0 && ok && run > 0)
