@@ -494,7 +494,7 @@ def kv_weights(cache, q, lse, weights, prev=None, decay=1.0, path=None, accept_l
     if d != cache.head_dim:
         raise DfvError(f"q has head_dim {d}, the cache {cache.head_dim}")
     for t, name in ((weights, "weights"), (prev, "prev")):
-        if t is not None and tuple(t.shape) != (h, cap):
+        if t is not None and t.shape != (h, cap):
             raise DfvError(f"{name} has shape {tuple(t.shape)}, expected {(h, cap)}")
     if weights is None or lse is None:
         raise DfvError("weights and lse are required")
@@ -532,15 +532,15 @@ def kv_evict(cache, weights, into, kept, sinks=0, recent=0, weights_out=None, st
         raise DfvError("into must be another cache")
     if index != torch._C._cuda_getDevice() or into.k.get_device() != index:
         _same_device(index, into.k)
-    if tuple(weights.shape) != (h, cap):
+    if weights.shape != (h, cap):
         raise DfvError(f"weights has shape {tuple(weights.shape)}, expected {(h, cap)}")
-    if kept.dim() != 2 or kept.shape[0] != h or not 1 <= kept.shape[1] <= into_cap:
+    keep = kept.shape[-1] if kept.dim() == 2 else 0
+    if kept.shape != (h, keep) or not 1 <= keep <= into_cap:
         raise DfvError(f"kept must be [{h}, K], K in [1, {into_cap}]")
-    keep = kept.shape[1]
     if sinks < 0 or recent < 0 or sinks + recent > keep:
         raise DfvError(f"{sinks} first and {recent} last rows of {keep}")
     if weights_out is not None:
-        if tuple(weights_out.shape) != (h, into_cap):
+        if weights_out.shape != (h, into_cap):
             raise DfvError(f"weights_out has shape {tuple(weights_out.shape)}, expected "
                            f"{(h, into_cap)}")
         if weights_out.data_ptr() == weights.data_ptr():

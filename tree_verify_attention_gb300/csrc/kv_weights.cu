@@ -30,7 +30,7 @@
 // Bound by issue: hand-offs and conversion for few rows (one row over 131060
 // Q4_0 keys, 4 heads of 256: 22.5 us, 3.4 TB/s; nine rows over 61440
 // 17.4), the sums for many (65 nodes, 32 / 8 heads of 128, 32791 F16
-// keys: 37 us, 24 % of the products' rate; 6 of them build the query rows).
+// keys: 35 us, 25 % of the products' rate; 6 of them build the query rows).
 
 #include <atomic>
 
