@@ -1,6 +1,6 @@
 """Draws from rows whose order in the vocabulary misleads counts that are taken
 from a part of it: the result is the definition's all the same (tolerances as in
-``test_gpu_sampling.py``)."""
+``test_gpu_sampling.py``; of a call's rows one may lie on a border)."""
 
 import pytest
 import torch
@@ -39,8 +39,6 @@ def ordered(kind, n, v, g):
                                   "flat", "alternating"])
 def test_orders(kind, dtype):
     g = torch.Generator().manual_seed(len(kind))
-    # rows near a border: three in a hundred at most (the module's estimate, times the
-    # steps of `flat`, where a cut lies within equal tokens)
     for n, v in ((3, 60011), (90, 30007)):
         x = ordered(kind, n, v, g).to(dtype).to(DEV)
         u = torch.rand(n, generator=g).to(DEV)
