@@ -688,8 +688,8 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
 #pragma unroll 1
         for (int u = u0; u < u1; u += 32) {
           const bool on = u + lane < u1;
-          const float2 x =
-              on ? SmpVec<T>::pair(xs, u + lane) : smp_both(-INFINITY);   // (c.from is finite)
+          // (behind the run: neither in the window nor above it, whatever its bounds)
+          const float2 x = on ? SmpVec<T>::pair(xs, u + lane) : smp_both(NAN);
           const bool over0 = x.x >= c.upto, over1 = x.y >= c.upto;
           const bool in0 = x.x >= c.from && !over0, in1 = x.y >= c.from && !over1;
           if (!c.under_list && (over0 || over1)) {
@@ -1058,8 +1058,12 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
     if (c.under_list || inside < room) {
       c.op = kOpCompact;
       c.gathered = 1;
-      c.from = m - static_cast<float>(sm.hit + 2) / bin_scale;
-      c.upto = sm.hit2 > 1 ? m - static_cast<float>(sm.hit2 - 1) / bin_scale : INFINITY;
+      // (finite, so that -inf stays below: 513 bins are 29.9 T, beyond float32
+      // for temperatures above 1.1e37)
+      c.from = fmaxf(m - static_cast<float>(sm.hit + 2) / bin_scale, -3.4028235e38f);
+      c.upto = sm.hit2 > 1
+                   ? fmaxf(m - static_cast<float>(sm.hit2 - 1) / bin_scale, -3.4028235e38f)
+                   : INFINITY;
       if (list_bin >= 0) c.upto = c.under_list ? tau_l : fminf(c.upto, tau_l);
       c.from = fminf(c.from, c.upto);
       c.bin0 = fminf(c.upto, m);
