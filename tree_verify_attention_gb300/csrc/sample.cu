@@ -334,7 +334,10 @@ __device__ void smp_finish(const SampleParams& p, int row, int token, float logp
       }
     }
   }
-  if (__shfl_sync(0xFFFFFFFFu, last, 0)) smp_walk(p, lane);
+  if (__shfl_sync(0xFFFFFFFFu, last, 0)) {
+    __syncwarp();   // what lane 0 has acquired is every lane's (a shuffle orders no memory)
+    smp_walk(p, lane);
+  }
 }
 
 template <typename T>
