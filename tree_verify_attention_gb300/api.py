@@ -117,7 +117,8 @@ class KVCache:
     K and V byte tensors [Hkv, capacity, row bytes], the committed length
     (device int32), and ``dropped``, the number of positions by which its rows
     lie below their place in the sequence (device int32; 0 until
-    :func:`kv_evict` has moved rows into it)."""
+    :func:`kv_evict` has moved rows into it, and again after a :meth:`fill` from
+    position 0; who sets ``ctx_len`` back by hand sets it back too)."""
 
     def __init__(self, n_kv_heads, head_dim, capacity, device="cuda", fmt="q4_0"):
         self.n_kv_heads, self.head_dim, self.capacity = n_kv_heads, head_dim, capacity
@@ -131,12 +132,15 @@ class KVCache:
 
     def fill(self, k_rows, v_rows, pos0=0, stream=None):
         """Encode float rows [Hkv, n, D] (f32 or bf16) into positions
-        [pos0, pos0 + n) and set the committed length to pos0 + n."""
+        [pos0, pos0 + n) and set the committed length to pos0 + n. With pos0 =
+        0 another sequence begins: ``dropped`` is 0 again."""
         n = k_rows.shape[1]
         for src, dst in ((k_rows, self.k), (v_rows, self.v)):
             kv_quantize_rows(dst, src, pos0, self.n_kv_heads, self.head_dim, self.capacity,
                              head_major=True, stream=stream, fmt=self.fmt)
         self.ctx_len.fill_(pos0 + n)
+        if pos0 == 0:
+            self.dropped.zero_()
 
     def read(self, pos0, n, k_out, v_out, head_major=False, stream=None):
         """The values of rows [pos0, pos0 + n) into k_out and v_out, [n, Hkv,
