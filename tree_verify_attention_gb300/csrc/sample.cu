@@ -84,7 +84,6 @@ struct SampleParams {
   const int32_t *parent, *tokens;
   int32_t *accept_len, *path, *out_tokens;
   unsigned int* ticket;
-  int slice_vecs;    // 16-byte vectors of shared memory for the slice
 };
 
 // round(2^(63 + j / 32))
@@ -1327,7 +1326,14 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
 // row arrives); few rows over as many CTAs as leave each some thousand tokens
 // (a cluster of more than eight lies in one GPC, so only for a handful of rows).
 constexpr int kSmpSliceBytes = 76 * 1024;
-constexpr int kSmpMostBytes = 176 * 1024;   // one CTA an SM
+// The longest slice, with a head's and a tail's vector: of float32 by sixteen CTAs.
+constexpr int kSmpMostBytes =
+    ((kSmpMaxVocab / 4 + 2 + kSmpMaxCluster - 1) / kSmpMaxCluster + 2) * 16;
+constexpr int kSmpFixed = static_cast<int>((sizeof(SmpSmem) + 127) / 128 * 128);
+static_assert(kSmpSliceBytes <= kSmpMostBytes && kSmpFixed + kSmpMostBytes <= 227 * 1024,
+              "a slice fits an SM");
+static_assert(kSmpSliceBytes / 2 <= 1 << 16 && kSmpMostBytes / 4 <= 1 << 16,
+              "gathered places are 16-bit (longer slices than kSmpSliceBytes are float32)");
 
 template <typename T>
 dfv_status sample_launch(SampleParams p, cudaStream_t stream) {
@@ -1339,16 +1345,13 @@ dfv_status sample_launch(SampleParams p, cudaStream_t stream) {
   while (cs < kSmpMaxCluster &&
          (slice() * 16 > kSmpSliceBytes || (cs < most && p.vocab > cs * 8192)))
     cs <<= 1;
-  if (slice() * 16 > kSmpMostBytes) return DFV_ERR_UNSUPPORTED;
-  p.slice_vecs = static_cast<int>(slice());
-  const int smem = static_cast<int>((sizeof(SmpSmem) + 127) / 128 * 128) + p.slice_vecs * 16;
+  const int smem = kSmpFixed + static_cast<int>(slice()) * 16;
   static std::atomic<int> allowed[64];   // per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DFV_ERR_CUDA;
   if (!allowed[dev].load(std::memory_order_acquire)) {
-    constexpr int kMost = static_cast<int>((sizeof(SmpSmem) + 127) / 128 * 128) + kSmpMostBytes;
     if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMost) != cudaSuccess ||
+                             kSmpFixed + kSmpMostBytes) != cudaSuccess ||
         cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed,
                              1) != cudaSuccess)
       return DFV_ERR_CUDA;
