@@ -512,7 +512,8 @@ dfv_status dfv_token_logprobs(int n_rows, int vocab, int logits_dtype, const voi
  *   the first rot_dim dims of y in pairs (a, b):
  *   (a cos t - b sin t, b cos t + a sin t), t = position * frequency of the pair
  *
- * computed in f32 (angles exact to 2^-26 of a turn at any position), rounded
+ * computed in f32 (the angle position * turns within 2^-25 of a turn at any
+ * position; what an entry of `turns` is off by counts position times), rounded
  * once.
  *
  *   q, k, v    device f32 or bf16 (src_dtype), element (row r, head h, dim c)

@@ -6,6 +6,8 @@ non-OK status. No compute happens here.
 """
 
 import ctypes
+import decimal
+import fractions
 import math
 
 import torch
@@ -656,12 +658,32 @@ def sample_accept(logits, uniform, sampling, parent, tokens, target, accept_len,
         "dfv_sample_accept")
 
 
+# 2 pi to 80 digits
+_TWO_PI = 2 * fractions.Fraction(
+    "3.1415926535897932384626433832795028841971693993751058209749445923078164062862090")
+
+
+def _turns(base, rot_dim):
+    """base ** (-2 i / rot_dim) / (2 pi) for i < rot_dim / 2, modulo 1, times 2^64,
+    to the nearest integer."""
+    if not base > 0:
+        raise DfvError(f"base {base} must be positive")
+    with decimal.localcontext(decimal.Context(prec=80)):
+        step = decimal.Decimal(base) ** (decimal.Decimal(-2) / rot_dim)
+        freq = [decimal.Decimal(1)]
+        while len(freq) < rot_dim // 2:
+            freq.append(freq[-1] * step)
+    return [round(fractions.Fraction(f) / _TWO_PI * 2 ** 64) % 2 ** 64 for f in freq]
+
+
 class Rope:
     """Frequencies of the position rotation of :func:`qk_norm_rope`: the first
     ``rot_dim`` dims of a head (all by default) turn in pairs, pair i by
     ``base ** (-2 i / rot_dim)`` rad per position, or by ``inv_freq[i]``
     (rot_dim / 2 numbers). Pairs are dims (i, i + rot_dim / 2), or (2 i, 2 i + 1)
-    with ``interleaved``. Kept as turns per position in 64-bit fractions."""
+    with ``interleaved``. Kept as turns per position in 64-bit fractions: from
+    ``base`` off by 2^-65, so angles are as exact at position 2^31 as at 1; from
+    ``inv_freq``, which are doubles and divided as such, by 2^-52 of themselves."""
 
     def __init__(self, head_dim, rot_dim=None, base=10000.0, inv_freq=None, interleaved=False,
                  device="cuda"):
@@ -671,11 +693,13 @@ class Rope:
         if not 0 <= rot_dim <= head_dim or rot_dim % 16:
             raise DfvError(f"rot_dim {rot_dim} is not a multiple of 16 in [0, {head_dim}]")
         if inv_freq is None:
-            inv_freq = [float(base) ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
-        inv_freq = [float(f) for f in inv_freq]
-        if len(inv_freq) != rot_dim // 2 or not all(math.isfinite(f) for f in inv_freq):
-            raise DfvError(f"inv_freq must be {rot_dim // 2} finite numbers")
-        turns = [int(math.fmod(f / (2.0 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in inv_freq]
+            turns = _turns(float(base), rot_dim) if rot_dim else []
+        else:
+            inv_freq = [float(f) for f in inv_freq]
+            if len(inv_freq) != rot_dim // 2 or not all(math.isfinite(f) for f in inv_freq):
+                raise DfvError(f"inv_freq must be {rot_dim // 2} finite numbers")
+            turns = [int(math.fmod(f / (2.0 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64
+                     for f in inv_freq]
         self.head_dim, self.rot_dim, self.interleaved = head_dim, rot_dim, bool(interleaved)
         self.turns = torch.tensor([t - (t >> 63 << 64) for t in turns], dtype=torch.int64,
                                   device=device)

@@ -16,7 +16,8 @@
 // Angles: pos * freq in 32 bits would be off by 2^-8 rad at position 131072.
 // The table holds turns per position as a 64-bit binary fraction, so the
 // integer product pos * turns, modulo 2^64, is the angle's fraction of a turn,
-// off by at most pos * 2^-65 of one; its upper 32 bits go to sincospi.
+// exact for the table's entry; one rounded to the nearest 2^-64 adds |pos| * 2^-65.
+// The upper 32 bits go to sincospi, as 24: 2^-32 and 2^-26 of a turn.
 
 #include "common.cuh"
 
