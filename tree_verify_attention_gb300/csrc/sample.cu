@@ -1322,14 +1322,15 @@ __global__ void __launch_bounds__(kSmpThreads, 2)
   }
 }
 
-// Rows are cut so that two CTAs fit an SM (one's passes run while the other's
-// row arrives); few rows over as many CTAs as leave each some thousand tokens
-// (a cluster of more than eight lies in one GPC, so only for a handful of rows).
-constexpr int kSmpSliceBytes = 76 * 1024;
+constexpr int kSmpFixed = static_cast<int>((sizeof(SmpSmem) + 127) / 128 * 128);
+// Rows are cut so that two CTAs fit an SM of 228 KB, 1 KB of each CTA's reserved
+// (one's passes run while the other's row arrives: 1024 rows of 154600, normal
+// logits of deviation 2, top-p 0.95: 1501 us by eight such, by four that fill an
+// SM each 1728; without a cut 454 and 450).
+constexpr int kSmpSliceBytes = (228 * 1024 / 2 - 1024 - kSmpFixed) / 16 * 16;
 // The longest slice, with a head's and a tail's vector: of float32 by sixteen CTAs.
 constexpr int kSmpMostBytes =
     ((kSmpMaxVocab / 4 + 2 + kSmpMaxCluster - 1) / kSmpMaxCluster + 2) * 16;
-constexpr int kSmpFixed = static_cast<int>((sizeof(SmpSmem) + 127) / 128 * 128);
 static_assert(kSmpSliceBytes <= kSmpMostBytes && kSmpFixed + kSmpMostBytes <= 227 * 1024,
               "a slice fits an SM");
 static_assert(kSmpSliceBytes / 2 <= 1 << 16 && kSmpMostBytes / 4 <= 1 << 16,
@@ -1339,6 +1340,12 @@ template <typename T>
 dfv_status sample_launch(SampleParams p, cudaStream_t stream) {
   constexpr int kV = SmpVec<T>::kN;
   const int64_t vecs = p.vocab / kV + 2;
+  // Few rows over as many CTAs as leave each 4096 tokens at least. Sixteen, which
+  // lie in one GPC, for a handful of rows alone (4 rows of 151936 as above: 39 us,
+  // by eight 45; 8 rows 48 and 45), eight and four as long as two CTAs an SM hold
+  // them all (23 rows: 57, by four 63; 65 rows of 32000 by four 41, by one 58).
+  // Not all of such clusters fit at the limits themselves: 37 rows take 91, by
+  // four 80, 75 rows of 32000 65, by one 58.
   const int most = p.n_rows <= 4 ? 16 : p.n_rows <= 37 ? 8 : p.n_rows <= 75 ? 4 : 1;
   int cs = 1;
   auto slice = [&]() { return (vecs + cs - 1) / cs + 2; };   // head and tail vectors beside
