@@ -61,3 +61,19 @@ def test_rows_behind_the_ones_that_stayed():
     assert int(cache.ctx_len) == KEEP + 20 and int(cache.dropped) == 50
     cache.fill(*rows(6, 1))
     assert int(cache.ctx_len) == 1 and int(cache.dropped) == 0
+
+
+def test_on_another_stream():
+    """The length and the count follow the rows on the stream that was given,
+    whatever the current one is at."""
+    cache, side = evicted("q4_0"), torch.cuda.Stream()
+    k, v = rows(7, 40)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)        # some 50 ms of the current stream
+    cache.fill(k, v, stream=side)
+    with torch.cuda.stream(side):
+        got = torch.cat([cache.ctx_len, cache.dropped])
+    side.synchronize()
+    assert got.tolist() == [40, 0]
+    torch.cuda.synchronize()
+    assert int(cache.ctx_len) == 40 and int(cache.dropped) == 0

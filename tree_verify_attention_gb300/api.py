@@ -140,9 +140,10 @@ class KVCache:
         for src, dst in ((k_rows, self.k), (v_rows, self.v)):
             kv_quantize_rows(dst, src, pos0, self.n_kv_heads, self.head_dim, self.capacity,
                              head_major=True, stream=stream, fmt=self.fmt)
-        self.ctx_len.fill_(pos0 + n)
-        if pos0 == 0:
-            self.dropped.zero_()
+        with torch.cuda.stream(stream):   # (None: the current one)
+            self.ctx_len.fill_(pos0 + n)
+            if pos0 == 0:
+                self.dropped.zero_()
 
     def read(self, pos0, n, k_out, v_out, head_major=False, stream=None):
         """The values of rows [pos0, pos0 + n) into k_out and v_out, [n, Hkv,
