@@ -7,7 +7,6 @@ non-OK status. No compute happens here.
 
 import ctypes
 import decimal
-import fractions
 import math
 
 import torch
@@ -659,22 +658,23 @@ def sample_accept(logits, uniform, sampling, parent, tokens, target, accept_len,
         "dfv_sample_accept")
 
 
-# 2 pi to 80 digits
-_TWO_PI = 2 * fractions.Fraction(
-    "3.1415926535897932384626433832795028841971693993751058209749445923078164062862090")
+_PI = "3.1415926535897932384626433832795028841971693993751058209749445923078164062862090"
 
 
 def _turns(base, rot_dim):
     """base ** (-2 i / rot_dim) / (2 pi) for i < rot_dim / 2, modulo 1, times 2^64,
-    to the nearest integer."""
+    to the nearest integer (80 digits; doubles would be off by some hundred)."""
     if not base > 0:
         raise DfvError(f"base {base} must be positive")
     with decimal.localcontext(decimal.Context(prec=80)):
-        step = decimal.Decimal(base) ** (decimal.Decimal(-2) / rot_dim)
-        freq = [decimal.Decimal(1)]
-        while len(freq) < rot_dim // 2:
-            freq.append(freq[-1] * step)
-    return [round(fractions.Fraction(f) / _TWO_PI * 2 ** 64) % 2 ** 64 for f in freq]
+        # in units of 2^-192
+        step = int(decimal.Decimal(base) ** (decimal.Decimal(-2) / rot_dim) * 2 ** 192)
+        turn = int(2 ** 255 / decimal.Decimal(_PI))
+    turns = []
+    for _ in range(rot_dim // 2):
+        turns.append((turn + (1 << 191) >> 192) % 2 ** 64)
+        turn = turn * step >> 192
+    return turns
 
 
 class Rope:
