@@ -562,9 +562,10 @@ dfv_status dfv_qk_norm_rope(int n_rows, int n_q_heads, int n_kv_heads, int head_
  *          kept w exceeds u times their total M;  logprob[i] = ln(w / M)
  *
  * A weight is off by less than 2^-29 of itself (the largest ones by 2^-35) and
- * 2^-43 of the largest. Weights are summed as integers, so a result does not
- * depend on how the work is split, and a border between two tokens lies within
- * 2^-30 + vocab * 2^-43 of its place in [0, 1). logprob is ln(w / M) to f32.
+ * 2^-43 of the largest (temperatures above 2^100, whose reciprocal loses bits:
+ * 2^-21). Weights are summed as integers, so a result does not depend on how the
+ * work is split, and a border between two tokens lies within 2^-30 + vocab *
+ * 2^-43 of its place in [0, 1). logprob is ln(w / M) to f32.
  *
  * temperature 0 (below 2^-100): the lowest index of the maximum, logprob 0.
  * top_k <= 0 or >= vocab, top_p >= 1, min_p <= 0: off; top_p <= 0 keeps the
@@ -642,7 +643,7 @@ dfv_status dfv_sample_accept(int n_nodes, int vocab, int logits_dtype, const voi
  *                `weights` itself
  *   weights      device f32 [Hkv][cache_capacity]; entries from C on are left
  *                as they were
- * Products are exact for elements down to 2^-24 of a query row's largest, sums
+ * Products are exact for elements down to 2^-23 of a query row's largest, sums
  * f32 in a fixed order: a weight is off by about 2^-19 of itself at |lse| of 30.
  * Cached K values must stay within the binary16 range.
  * One launch, no workspace.

@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int piece = lane % kLanes;
       uint32_t problems = 0;
       // The tile's power of two, 2^4 above its first row's: rows within 2^-8 to 1
-      // of it have that one (their elements are exact down to 2^-24 of the row's
+      // of it have that one (their elements are exact down to 2^-23 of the row's
       // largest), and where all have, the exponent's slope stays in a register
       // (65 rows, 32 / 8 heads of 128 over 61440 F16 keys: 77 us, slopes read for
       // every column 82).
